@@ -70,12 +70,16 @@ extern "C" {
 #define PA_DTYPE_BF16 2
 #define PA_DTYPE_E4M3 3   /* 8-bit cache storage (see the _fp8 calls); also   */
                           /* accepted by pa_copy_blocks                        */
+#define PA_DTYPE_INT4 4   /* 4-bit cache storage (see the _int4 calls), as      */
+                          /* pa_paged_kv_evict takes it                        */
 
 /* ---- device error bits (pa_get_device_error) ------------------------------ */
 #define PA_DEVERR_SLOT       0x1u  /* slot not -1 and outside [0, NB*bs)          */
 #define PA_DEVERR_BLOCK_ID   0x2u  /* live table entry outside [0, num_blocks)    */
 #define PA_DEVERR_CONTEXT    0x4u  /* context_len < 0, > max_blocks_per_seq*bs,   */
-                                   /* or > max_context_len                        */
+                                   /* > max_context_len or > mass_len; eviction:  */
+                                   /* a keep_len < 0, or more kept tokens than    */
+                                   /* the outputs hold                            */
 #define PA_DEVERR_COPY_PAIR  0x8u  /* copy pair id outside [0, num_blocks)        */
 #define PA_DEVERR_WAIT       0x10u /* an internal pipeline wait hit its bound     */
 
@@ -409,6 +413,141 @@ int pa_paged_attention_decode_fp8_append(void *out, const void *q, const void *k
                                          int head_dim, int block_size, int64_t num_blocks, float scale,
                                          float k_scale, float v_scale, int max_context_len, int partition_size,
                                          void *workspace, size_t workspace_bytes, int dtype, void *stream);
+
+/* ---- 4-bit KV cache --------------------------------------------------------
+ * Not on the pages [P1-P3]; an extension that quarters the bytes a decode step
+ * reads. Per token and kv head, a K row and a V row of head_dim (64 or 128)
+ * channels are held as 4-bit codes with a float16 scale and zero each:
+ *   key_cache, value_cache : uint8 [num_blocks, num_kv_heads, block_size, head_dim / 2],
+ *                            channel 2i in the low half of byte i, 2i + 1 in the high
+ *   kv_params              : float16 [num_blocks, num_kv_heads, block_size, 4] =
+ *                            (K scale, K zero, V scale, V zero)
+ * A channel stands for code * scale + zero. A block's rows of one kv head are one
+ * contiguous run (unlike the other caches, whose blocks are token-major), so a
+ * decode fetches them with untiled bulk copies. block_size: a power of two in
+ * [8, 256]. Slots, tables and lengths are those of the other caches.
+ */
+
+/*
+ * Scatter with quantisation. [P1 write_kv; P3 B.2 for the slots, exactly as
+ * pa_paged_kv_write]
+ * For a row x, clamped to +-65504: zero = f16(min x), scale = f16((max x - min x) / 15),
+ * code = clamp(rint((x - zero) / scale), 0, 15) with the difference and the quotient in
+ * float32 (IEEE division) and rint to even; 0 where scale is 0 (a constant row reads as
+ * its zero). A row that holds a NaN gets NaN parameters: all of it reads as NaN.
+ * k, v: [num_tokens, num_kv_heads, head_dim] of src_dtype (PA_DTYPE_F32, _F16 or _BF16).
+ * Slot rules and errors as pa_paged_kv_write.
+ */
+int pa_paged_kv_write_int4(const void *k, const void *v, const int32_t *slot_mapping, int64_t num_tokens,
+                           void *key_cache, void *value_cache, void *kv_params, int64_t num_blocks, int block_size,
+                           int num_kv_heads, int head_dim, int src_dtype, void *stream);
+
+/*
+ * Read-back: k[t], v[t] = the values held at slot_mapping[t], computed in float32 (one
+ * rounding) and rounded to dst_dtype (PA_DTYPE_F32, _F16 or _BF16). A token of slot -1, or of a slot out of range (which
+ * sets PA_DEVERR_SLOT), keeps its row of k and v as it was. Slots may repeat. Read into
+ * a [num_blocks', block_size', num_kv_heads, head_dim] buffer, a cached context can be
+ * attended by pa_paged_attention_prefill.
+ */
+int pa_paged_kv_read_int4(void *k, void *v, const int32_t *slot_mapping, int64_t num_tokens, const void *key_cache,
+                          const void *value_cache, const void *kv_params, int64_t num_blocks, int block_size,
+                          int num_kv_heads, int head_dim, int dst_dtype, void *stream);
+
+/* pa_copy_blocks for a 4-bit cache: codes and parameters of whole blocks. */
+int pa_copy_blocks_int4(void *key_cache, void *value_cache, void *kv_params, const int32_t *src_dst_pairs,
+                        int64_t num_pairs, int64_t num_blocks, int block_size, int num_kv_heads, int head_dim,
+                        void *stream);
+
+/* The partition size a 4-bit decode call uses: partition_size itself when it is not 0,
+ * else the automatic choice. */
+int pa_decode_int4_partition_size(int num_seqs, int num_kv_heads, int max_context_len, int partition_size);
+
+/* Bytes of workspace pa_paged_attention_decode_int4 needs for these sizes; with_mass
+ * non-zero: for a call that accumulates weights. May be 0 without. */
+size_t pa_decode_int4_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                      int max_context_len, int partition_size, int with_mass);
+
+/*
+ * Decode attention over a 4-bit cache. [P2 demo 2, eq. 4, as
+ * pa_paged_attention_decode]
+ *
+ *   out[b,h,:] = sum_t softmax_t(scale * q[b,h,:] . K[b,t,h/G,:]) * V[b,t,h/G,:]
+ *
+ * with K and V the values held (code * scale + zero, unrounded). q and out:
+ * [num_seqs, num_heads, head_dim], PA_DTYPE_BF16 or PA_DTYPE_F16; head_dim 64 or 128,
+ * num_heads / num_kv_heads <= 16. mass (NULL: none): float32 [num_seqs, num_kv_heads,
+ * mass_len], accumulated as by pa_paged_attention_decode_scored, out staying the same.
+ * Parameters of the slots past a context's end are never used, whatever they hold; a
+ * NaN parameter inside a context makes the outputs of its heads NaN. Partitions,
+ * max_context_len, the workspace (size from pa_decode_int4_workspace_bytes; NULL =
+ * cudaMallocAsync on the stream) and the device error bits are those of
+ * pa_paged_attention_decode.
+ */
+int pa_paged_attention_decode_int4(void *out, const void *q, const void *key_cache, const void *value_cache,
+                                   const void *kv_params, float *mass, int64_t mass_len, const int32_t *block_tables,
+                                   int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_heads,
+                                   int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale,
+                                   int max_context_len, int partition_size, void *workspace, size_t workspace_bytes,
+                                   int dtype, void *stream);
+
+/* ---- accumulated attention weights, and eviction by them --------------------
+ * Not on the pages [P1-P3]; an extension that keeps long caches within a budget.
+ */
+
+/* Bytes of workspace pa_paged_attention_decode_scored needs for these sizes. */
+size_t pa_decode_scored_workspace_bytes(int num_seqs, int num_heads, int head_dim, int max_context_len,
+                                        int partition_size);
+
+/*
+ * pa_paged_attention_decode that also accumulates each token's attention weight:
+ *
+ *   mass[b, kvh, t] += sum over the query heads h of kv head kvh of
+ *                      softmax_t(scale * q[b,h,:] . K[b,t,kvh,:])      for t < context_lens[b]
+ *
+ * mass: float32 [num_seqs, num_kv_heads, mass_len]; entries past a context are left as
+ * they are. The weights are added in head order, in float32 from the unrounded scores.
+ * A context longer than mass_len sets PA_DEVERR_CONTEXT and is cut to it. out is that of
+ * pa_paged_attention_decode, bit for bit, with the same arguments (caches of float32,
+ * f16 or bf16). The workspace (size from pa_decode_scored_workspace_bytes; NULL =
+ * cudaMallocAsync on the stream) holds the scores: 4 bytes per query head and token.
+ */
+int pa_paged_attention_decode_scored(void *out, const void *q, float *mass, int64_t mass_len, const void *key_cache,
+                                     const void *value_cache, const int32_t *block_tables, int max_blocks_per_seq,
+                                     const int32_t *context_lens, int num_seqs, int num_heads, int num_kv_heads,
+                                     int head_dim, int block_size, int64_t num_blocks, float scale,
+                                     int max_context_len, int partition_size, void *workspace,
+                                     size_t workspace_bytes, int dtype, void *stream);
+
+/*
+ * Evict the least attended tokens, per sequence and kv head. With c = context_lens[b],
+ * n = min(c, keep_lens[b]) and r = min(recent, n): the last r tokens stay, and of the
+ * c - r before them the n - r of the largest mass[b, kvh] (equal masses: the lower index;
+ * a NaN counts below every number). What stays keeps its order. For i < n:
+ *
+ *   kept[b, kvh, i]     = the index that token i had
+ *   mass_out[b, kvh, i] = mass[b, kvh, kept[b, kvh, i]]
+ *   the K and V rows (and 4-bit parameters) of kv head kvh of token kept[b, kvh, i] move
+ *   to position i of out_block_tables[b]
+ *
+ * and kept = -1, mass_out = 0 for i >= n, so that tokens appended later start at zero.
+ * Afterwards the sequence has n tokens, in the blocks of out_block_tables.
+ *
+ * out_block_tables [num_seqs, out_max_blocks_per_seq] names blocks of the same caches:
+ * either blocks that no sequence of the call reads, or, for eviction in place, the
+ * sequence's own blocks in their order (then mass_out may be mass itself). In place, a
+ * block that moved rows land in must not be read by another sequence (copy-on-write, or
+ * other out blocks, guarantee it). kept: int32 [num_seqs, num_kv_heads, kept_len].
+ * dtype: PA_DTYPE_F32, _F16, _BF16 or _E4M3 (caches [num_blocks, block_size,
+ * num_kv_heads, head_dim], kv_params unused; rows a multiple of 16 bytes) or PA_DTYPE_INT4.
+ * A length outside its range sets PA_DEVERR_CONTEXT and is cut; a bad block id sets
+ * PA_DEVERR_BLOCK_ID and its row is not moved.
+ */
+int pa_paged_kv_evict(int32_t *kept, int64_t kept_len, const float *mass, int64_t mass_len, float *mass_out,
+                      int64_t mass_out_len, void *key_cache, void *value_cache, void *kv_params,
+                      const int32_t *block_tables, int max_blocks_per_seq, const int32_t *out_block_tables,
+                      int out_max_blocks_per_seq, const int32_t *context_lens, const int32_t *keep_lens, int recent,
+                      int num_seqs, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, int dtype,
+                      void *stream);
 
 /*
  * Synchronise `stream`, then read and clear the current device's error word.

@@ -19,12 +19,23 @@ Entry points (same names as the C ABI, without the ``pa_`` prefix):
   paged_kv_write_fp8(k, v, slot_mapping, key_cache, value_cache, k_scale, v_scale)
   paged_attention_decode_fp8(out, q, key_cache, value_cache, block_tables,
                              context_lens, scale, k_scale, v_scale)
+  paged_kv_write_int4(k, v, slot_mapping, key_cache, value_cache, kv_params)
+  paged_kv_read_int4(k, v, slot_mapping, key_cache, value_cache, kv_params)
+  paged_attention_decode_int4(out, q, key_cache, value_cache, kv_params,
+                              block_tables, context_lens, scale, mass=None)
+  paged_attention_decode_scored(out, q, mass, key_cache, value_cache,
+                                block_tables, context_lens, scale)
+  paged_kv_evict(kept, mass, mass_out, key_cache, value_cache, block_tables,
+                 out_block_tables, context_lens, keep_lens, recent, kv_params=None)
   get_device_error()
   BlockAllocator: the host block manager (free list, reference counts, fork,
   copy-on-write, block-table and slot-mapping export).
 Cache layout: [num_blocks, block_size, num_kv_heads, head_dim]. The _fp8 calls
 take 8-bit caches (torch.uint8 or torch.float8_e4m3fn) holding OCP FP8 E4M3
-codes with one float32 scale for K and one for V.
+codes with one float32 scale for K and one for V. The _int4 calls take caches
+[num_blocks, num_kv_heads, block_size, head_dim / 2] (torch.uint8, two codes a
+byte) with kv_params float16 [num_blocks, num_kv_heads, block_size, 4]: K scale,
+K zero, V scale, V zero of every token and kv head.
 """
 from __future__ import annotations
 
@@ -54,7 +65,7 @@ PA_ERR_UNKNOWN_SEQ = -6
 PA_ERR_WORKSPACE = -7
 PA_ERR_EXISTS = -8
 
-PA_DTYPE_F32, PA_DTYPE_F16, PA_DTYPE_BF16, PA_DTYPE_E4M3 = 0, 1, 2, 3
+PA_DTYPE_F32, PA_DTYPE_F16, PA_DTYPE_BF16, PA_DTYPE_E4M3, PA_DTYPE_INT4 = 0, 1, 2, 3, 4
 
 PA_DEVERR_SLOT = 0x1
 PA_DEVERR_BLOCK_ID = 0x2
@@ -96,6 +107,18 @@ _decl("pa_paged_attention_decode_fp8_append", [_vp, _vp, _vp, _vp, _vp, _vp, _vp
                                                _i32, _i32, _i32, _i64, _f, _f, _f, _i32, _i32, _vp, _sz, _i32, _vp])
 _decl("pa_paged_attention_prefill", [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i64, _i32, _i32, _i32, _i32,
                                      _i32, _i64, _f, _i32, _vp])
+_decl("pa_paged_kv_write_int4", [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp])
+_decl("pa_paged_kv_read_int4", [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp])
+_decl("pa_copy_blocks_int4", [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _vp])
+_decl("pa_decode_int4_partition_size", [_i32, _i32, _i32, _i32])
+_decl("pa_decode_int4_workspace_bytes", [_i32, _i32, _i32, _i32, _i32, _i32, _i32], _sz)
+_decl("pa_paged_attention_decode_int4", [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i32, _vp, _i32, _i32, _i32, _i32,
+                                         _i32, _i64, _f, _i32, _i32, _vp, _sz, _i32, _vp])
+_decl("pa_decode_scored_workspace_bytes", [_i32, _i32, _i32, _i32, _i32], _sz)
+_decl("pa_paged_attention_decode_scored", [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32,
+                                           _i32, _i64, _f, _i32, _i32, _vp, _sz, _i32, _vp])
+_decl("pa_paged_kv_evict", [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _i32,
+                            _i32, _i32, _i32, _i32, _i64, _i32, _vp])
 
 
 class PagedAttnError(RuntimeError):
@@ -429,10 +452,23 @@ def paged_attention_decode_shared(out, q, key_cache, value_cache, block_tables, 
     _check(rc, "pa_paged_attention_decode_shared")
 
 
-def copy_blocks(key_cache, value_cache, src_dst_pairs, stream=None) -> None:
-    """key_cache[dst] = key_cache[src] (and V) for each row (src, dst) of src_dst_pairs [P, 2]."""
+def copy_blocks(key_cache, value_cache, src_dst_pairs, stream=None, kv_params=None) -> None:
+    """key_cache[dst] = key_cache[src] (and V) for each row (src, dst) of src_dst_pairs [P, 2].
+
+    kv_params: that of a 4-bit cache, copied along."""
     torch = _torch()
     dev = key_cache.device
+    if kv_params is not None:
+        nb, hk, bs, d = _int4_caches(key_cache, value_cache, kv_params, dev)
+        _cuda(src_dst_pairs, "src_dst_pairs", torch.int32, dev)
+        if src_dst_pairs.dim() != 2 or src_dst_pairs.shape[1] != 2:
+            raise ValueError("src_dst_pairs must be [P, 2]")
+        with _on(dev):
+            rc = _lib.pa_copy_blocks_int4(key_cache.data_ptr(), value_cache.data_ptr(), kv_params.data_ptr(),
+                                          src_dst_pairs.data_ptr(), src_dst_pairs.shape[0], nb, bs, hk, d,
+                                          _stream_ptr(stream, dev))
+        _check(rc, "pa_copy_blocks_int4")
+        return
     _cuda(key_cache, "key_cache")
     _cuda(value_cache, "value_cache", key_cache.dtype, dev)
     _cuda(src_dst_pairs, "src_dst_pairs", torch.int32, dev)
@@ -555,6 +591,208 @@ def paged_attention_decode_fp8_append(out, q, k_new, v_new, slot_mapping, key_ca
                                                        float(k_scale), float(v_scale), int(max_context_len),
                                                        int(partition_size), ws_ptr, ws_bytes, _dtype_code(q), sp)
     _check(rc, "pa_paged_attention_decode_fp8_append")
+
+
+def _int4_caches(key_cache, value_cache, kv_params, dev):
+    """Checks the tensors of a 4-bit cache; (num_blocks, num_kv_heads, block_size, head_dim)."""
+    torch = _torch()
+    _cuda(key_cache, "key_cache", torch.uint8)
+    _cuda(value_cache, "value_cache", torch.uint8, dev)
+    _cuda(kv_params, "kv_params", torch.float16, dev)
+    if key_cache.dim() != 4 or value_cache.shape != key_cache.shape:
+        raise ValueError("key_cache and value_cache must be [num_blocks, num_kv_heads, block_size, head_dim / 2]")
+    nb, hk, bs, half = key_cache.shape
+    if tuple(kv_params.shape) != (nb, hk, bs, 4):
+        raise ValueError(f"kv_params must be [{nb}, {hk}, {bs}, 4]")
+    return nb, hk, bs, 2 * half
+
+
+def _int4_rows(k, v, slot_mapping, hk, d, dev):
+    torch = _torch()
+    _cuda(k, "k", None, dev)
+    _cuda(v, "v", k.dtype, dev)
+    _cuda(slot_mapping, "slot_mapping", torch.int32, dev)
+    if slot_mapping.dim() != 1:
+        raise ValueError("slot_mapping must be [T]")
+    T = slot_mapping.shape[0]
+    if tuple(k.shape) != (T, hk, d) or tuple(v.shape) != (T, hk, d):
+        raise ValueError(f"k/v must be [{T}, {hk}, {d}]")
+    return T
+
+
+def paged_kv_write_int4(k, v, slot_mapping, key_cache, value_cache, kv_params, stream=None) -> None:
+    """Scatter k/v [T, Hk, D] (fp32/fp16/bf16) into 4-bit caches [NB, Hk, bs, D / 2] with
+    kv_params [NB, Hk, bs, 4] at slot_mapping[T]: per row, zero = f16(min), scale =
+    f16((max - min) / 15), code = the nearest of (x - zero) / scale in 0..15."""
+    dev = key_cache.device
+    nb, hk, bs, d = _int4_caches(key_cache, value_cache, kv_params, dev)
+    T = _int4_rows(k, v, slot_mapping, hk, d, dev)
+    with _on(dev):
+        rc = _lib.pa_paged_kv_write_int4(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), T, key_cache.data_ptr(),
+                                         value_cache.data_ptr(), kv_params.data_ptr(), nb, bs, hk, d, _dtype_code(k),
+                                         _stream_ptr(stream, dev))
+    _check(rc, "pa_paged_kv_write_int4")
+
+
+def paged_kv_read_int4(k, v, slot_mapping, key_cache, value_cache, kv_params, stream=None) -> None:
+    """The inverse: k[t], v[t] [T, Hk, D] (fp32/fp16/bf16) = the values held at
+    slot_mapping[t]; rows of slot -1 stay as they are."""
+    dev = key_cache.device
+    nb, hk, bs, d = _int4_caches(key_cache, value_cache, kv_params, dev)
+    T = _int4_rows(k, v, slot_mapping, hk, d, dev)
+    with _on(dev):
+        rc = _lib.pa_paged_kv_read_int4(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), T, key_cache.data_ptr(),
+                                        value_cache.data_ptr(), kv_params.data_ptr(), nb, bs, hk, d, _dtype_code(k),
+                                        _stream_ptr(stream, dev))
+    _check(rc, "pa_paged_kv_read_int4")
+
+
+def _mass(mass, name, B, hk, dev):
+    torch = _torch()
+    _cuda(mass, name, torch.float32, dev)
+    if mass.dim() != 3 or tuple(mass.shape[:2]) != (B, hk):
+        raise ValueError(f"{name} must be [{B}, {hk}, length]")
+    return mass.shape[2]
+
+
+def decode_int4_partition_size(num_seqs: int, num_kv_heads: int, max_context_len: int,
+                               partition_size: int = 0) -> int:
+    """Partition size (tokens) a 4-bit decode call uses: partition_size, or the automatic choice for 0."""
+    return int(_lib.pa_decode_int4_partition_size(num_seqs, num_kv_heads, max_context_len, partition_size))
+
+
+def decode_int4_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                max_context_len: int, partition_size: int = 0, with_mass: bool = False) -> int:
+    return int(_lib.pa_decode_int4_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len,
+                                                   partition_size, int(with_mass)))
+
+
+def paged_attention_decode_int4(out, q, key_cache, value_cache, kv_params, block_tables, context_lens, scale: float,
+                                max_context_len: int = 0, partition_size: int = 0, workspace=None, mass=None,
+                                stream=None) -> None:
+    """Decode attention over 4-bit caches [NB, Hk, bs, D / 2] with kv_params [NB, Hk, bs, 4].
+
+    q, out [B, H, D] bf16 or fp16. mass: optional float32 [B, Hk, M], to which each token's
+    weight is added (see paged_attention_decode_scored). Other arguments as
+    paged_attention_decode."""
+    torch = _torch()
+    dev = key_cache.device
+    nb, hk, bs, d = _int4_caches(key_cache, value_cache, kv_params, dev)
+    _cuda(q, "q", None, dev)
+    _cuda(out, "out", q.dtype, dev)
+    _cuda(block_tables, "block_tables", torch.int32, dev)
+    _cuda(context_lens, "context_lens", torch.int32, dev)
+    B, H, D = q.shape
+    if D != d or tuple(out.shape) != (B, H, D):
+        raise ValueError("q/out must be [B, H, head_dim]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(context_lens.shape) != (B,):
+        raise ValueError("block_tables must be [B, MB] and context_lens [B]")
+    mb = block_tables.shape[1]
+    mass_ptr, mass_len = None, 0
+    if mass is not None:
+        mass_len = _mass(mass, "mass", B, hk, dev)
+        mass_ptr = mass.data_ptr()
+    sp = _stream_ptr(stream, dev)
+    need = decode_int4_workspace_bytes(B, H, hk, D, max_context_len or mb * bs, partition_size, mass is not None)
+    ws_ptr, ws_bytes = None, 0
+    if need:
+        if workspace is None:
+            workspace = _workspace(dev, sp, need)
+        _cuda(workspace, "workspace", torch.uint8, dev)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
+    with _on(dev):
+        rc = _lib.pa_paged_attention_decode_int4(out.data_ptr(), q.data_ptr(), key_cache.data_ptr(),
+                                                 value_cache.data_ptr(), kv_params.data_ptr(), mass_ptr, mass_len,
+                                                 block_tables.data_ptr(), mb, context_lens.data_ptr(), B, H, hk, D, bs,
+                                                 nb, float(scale), int(max_context_len), int(partition_size), ws_ptr,
+                                                 ws_bytes, _dtype_code(q), sp)
+    _check(rc, "pa_paged_attention_decode_int4")
+
+
+def decode_scored_workspace_bytes(num_seqs: int, num_heads: int, head_dim: int, max_context_len: int,
+                                  partition_size: int = 0) -> int:
+    return int(_lib.pa_decode_scored_workspace_bytes(num_seqs, num_heads, head_dim, max_context_len,
+                                                     partition_size))
+
+
+def paged_attention_decode_scored(out, q, mass, key_cache, value_cache, block_tables, context_lens, scale: float,
+                                  max_context_len: int = 0, partition_size: int = 0, workspace=None,
+                                  stream=None) -> None:
+    """paged_attention_decode that also adds each token's attention weight, summed over the
+    query heads of its kv head, to mass float32 [B, Hk, M]. Entries past a context stay."""
+    torch = _torch()
+    dev = key_cache.device
+    _cuda(key_cache, "key_cache")
+    _cuda(value_cache, "value_cache", key_cache.dtype, dev)
+    _cuda(q, "q", key_cache.dtype, dev)
+    _cuda(out, "out", key_cache.dtype, dev)
+    _cuda(block_tables, "block_tables", torch.int32, dev)
+    _cuda(context_lens, "context_lens", torch.int32, dev)
+    nb, bs, hk, d = key_cache.shape
+    if value_cache.shape != key_cache.shape:
+        raise ValueError("value_cache shape differs from key_cache")
+    B, H, D = q.shape
+    if D != d or tuple(out.shape) != (B, H, D):
+        raise ValueError("q/out must be [B, H, head_dim]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(context_lens.shape) != (B,):
+        raise ValueError("block_tables must be [B, MB] and context_lens [B]")
+    mass_len = _mass(mass, "mass", B, hk, dev)
+    mb = block_tables.shape[1]
+    sp = _stream_ptr(stream, dev)
+    need = decode_scored_workspace_bytes(B, H, D, max_context_len or mb * bs, partition_size)
+    if workspace is None:
+        workspace = _workspace(dev, sp, need)
+    _cuda(workspace, "workspace", torch.uint8, dev)
+    with _on(dev):
+        rc = _lib.pa_paged_attention_decode_scored(out.data_ptr(), q.data_ptr(), mass.data_ptr(), mass_len,
+                                                   key_cache.data_ptr(), value_cache.data_ptr(),
+                                                   block_tables.data_ptr(), mb, context_lens.data_ptr(), B, H, hk, D,
+                                                   bs, nb, float(scale), int(max_context_len), int(partition_size),
+                                                   workspace.data_ptr(), workspace.numel(), _dtype_code(key_cache),
+                                                   sp)
+    _check(rc, "pa_paged_attention_decode_scored")
+
+
+def paged_kv_evict(kept, mass, mass_out, key_cache, value_cache, block_tables, out_block_tables, context_lens,
+                   keep_lens, recent: int, kv_params=None, stream=None) -> None:
+    """Keep min(context_lens[b], keep_lens[b]) tokens of every sequence and kv head: the last
+    `recent`, and the heaviest by mass [B, Hk, M] of the others (ties: the lower index), in
+    their order. Token kept[b, h, i] (int32 [B, Hk, K]; -1 past the kept ones) becomes token
+    i: its rows move to position i of out_block_tables [B, MB'], its mass to mass_out
+    [B, Hk, M'] (0 past the kept ones). out_block_tables: blocks that no sequence of the call
+    reads, or block_tables' own blocks for eviction in place (mass_out may then be mass).
+    Caches as the decode calls take them; kv_params with 4-bit ones."""
+    torch = _torch()
+    dev = key_cache.device
+    if kv_params is not None:
+        nb, hk, bs, d = _int4_caches(key_cache, value_cache, kv_params, dev)
+        dt, par = PA_DTYPE_INT4, kv_params.data_ptr()
+    else:
+        _cuda(key_cache, "key_cache")
+        _cuda(value_cache, "value_cache", key_cache.dtype, dev)
+        if key_cache.dim() != 4 or value_cache.shape != key_cache.shape:
+            raise ValueError("key_cache and value_cache must be [num_blocks, block_size, num_kv_heads, head_dim]")
+        nb, bs, hk, d = key_cache.shape
+        dt, par = _storage_code(key_cache), None
+    for t, n in ((kept, "kept"), (block_tables, "block_tables"), (out_block_tables, "out_block_tables"),
+                 (context_lens, "context_lens"), (keep_lens, "keep_lens")):
+        _cuda(t, n, torch.int32, dev)
+    if context_lens.dim() != 1:
+        raise ValueError("context_lens must be [B]")
+    B = context_lens.shape[0]
+    if tuple(keep_lens.shape) != (B,) or block_tables.dim() != 2 or out_block_tables.dim() != 2 or \
+            block_tables.shape[0] != B or out_block_tables.shape[0] != B:
+        raise ValueError("block_tables and out_block_tables must be [B, MB], context_lens and keep_lens [B]")
+    if kept.dim() != 3 or tuple(kept.shape[:2]) != (B, hk):
+        raise ValueError(f"kept must be [{B}, {hk}, length]")
+    mass_len, out_len = _mass(mass, "mass", B, hk, dev), _mass(mass_out, "mass_out", B, hk, dev)
+    with _on(dev):
+        rc = _lib.pa_paged_kv_evict(kept.data_ptr(), kept.shape[2], mass.data_ptr(), mass_len, mass_out.data_ptr(),
+                                    out_len, key_cache.data_ptr(), value_cache.data_ptr(), par,
+                                    block_tables.data_ptr(), block_tables.shape[1], out_block_tables.data_ptr(),
+                                    out_block_tables.shape[1], context_lens.data_ptr(), keep_lens.data_ptr(),
+                                    int(recent), B, hk, d, bs, nb, dt, _stream_ptr(stream, dev))
+    _check(rc, "pa_paged_kv_evict")
 
 
 def get_device_error(stream=None, device=None) -> int:

@@ -11,6 +11,7 @@
 #include "call_range.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "kernels_compress.h"
 #include "kernels_fp8.h"
 
 namespace {
@@ -250,6 +251,67 @@ int decode_fp8_call(void *out, const void *q, const void *k_new, const void *v_n
     if (owned) cudaFreeAsync(owned, s);
     if (krc == -2) return PA_ERR_UNSUPPORTED;
     return krc == 0 ? PA_OK : PA_ERR_CUDA;
+}
+
+// Workspace of a scored decode: the split-K partials, then every partition's (max, sum)
+// pair, then the scores.
+size_t scored_workspace_bytes(int64_t B, int64_t H, int64_t D, int64_t P, int64_t max_ctx) {
+    return align256(workspace_bytes_for(B, H, D, P)) + align256((size_t)(B * H * P * 2 * 4)) +
+           (size_t)(B * H * max_ctx * 4);
+}
+
+// Workspace of a decode that may be scored (max_ctx > 0: the scores of so many tokens a
+// sequence are kept); as decode_workspace otherwise.
+int scored_workspace(pa::DecodeParams &p, int64_t P, int64_t max_ctx, void *workspace, size_t workspace_bytes,
+                     cudaStream_t s, void **owned) {
+    *owned = nullptr;
+    const int64_t B = p.num_seqs, H = p.num_heads;
+    const size_t need = scored_workspace_bytes(B, H, p.head_dim, P, max_ctx);
+    void *ws = workspace;
+    if (ws) {
+        if (workspace_bytes < need) return PA_ERR_WORKSPACE;
+        if (!aligned16(ws)) return PA_ERR_INVALID_ARG;
+    } else {
+        if (cudaMallocAsync(&ws, need, s) != cudaSuccess) return PA_ERR_CUDA;
+        *owned = ws;
+    }
+    char *at = static_cast<char *>(ws);
+    p.ws_ml = reinterpret_cast<float *>(at);
+    p.ws_o = reinterpret_cast<float *>(at + align256((size_t)(B * H * P * 2 * 4)));
+    at += align256(workspace_bytes_for(B, H, p.head_dim, P));
+    p.ws_score_ml = reinterpret_cast<float *>(at);
+    at += align256((size_t)(B * H * P * 2 * 4));
+    p.ws_logits = reinterpret_cast<float *>(at);
+    p.logits_len = (int)max_ctx;
+    return PA_OK;
+}
+
+int64_t call_max_context(int max_blocks_per_seq, int block_size, int max_context_len) {
+    return max_context_len == 0 ? (int64_t)max_blocks_per_seq * block_size : max_context_len;
+}
+
+// Validation shared by the 4-bit scatter and read-back; fills c.
+int int4_setup(pa::Int4Cache &c, const void *k, const void *v, const int32_t *slot_mapping, int64_t num_tokens,
+               void *key_cache, void *value_cache, void *kv_params, int64_t num_blocks, int block_size,
+               int num_kv_heads, int head_dim, int dtype) {
+    if (elem_size(dtype) == 0 || num_tokens < 0 || num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0 ||
+        head_dim <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (!pow2(block_size) || block_size < 8 || block_size > 256 || num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return kNothingToDo;
+    if (!k || !v || !slot_mapping || !key_cache || !value_cache || !kv_params) return PA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(key_cache) || !aligned16(value_cache) || !aligned16(kv_params))
+        return PA_ERR_INVALID_ARG;
+    if (num_blocks > INT64_MAX / ((int64_t)block_size * num_kv_heads * head_dim)) return PA_ERR_INVALID_ARG;
+    c.key = key_cache;
+    c.value = value_cache;
+    c.params = kv_params;
+    c.num_slots = num_blocks * block_size;
+    c.num_kv_heads = num_kv_heads;
+    c.head_dim = head_dim;
+    c.log2_block_size = ilog2(block_size);
+    return PA_OK;
 }
 
 }  // namespace
@@ -668,6 +730,227 @@ int pa_copy_blocks(void *key_cache, void *value_cache, const int32_t *src_dst_pa
                                err, static_cast<cudaStream_t>(stream)) != 0)
         return PA_ERR_CUDA;
     return PA_OK;
+}
+
+size_t pa_decode_scored_workspace_bytes(int num_seqs, int num_heads, int head_dim, int max_context_len,
+                                        int partition_size) {
+    if (num_seqs <= 0 || num_heads <= 0 || head_dim <= 0 || max_context_len < 0 || partition_size < 0) return 0;
+    const int part = resolve_partition(partition_size, num_seqs, max_context_len);
+    return scored_workspace_bytes(num_seqs, num_heads, head_dim, num_partitions(max_context_len, part),
+                                  max_context_len);
+}
+
+int pa_paged_attention_decode_scored(void *out, const void *q, float *mass, int64_t mass_len, const void *key_cache,
+                                     const void *value_cache, const int32_t *block_tables, int max_blocks_per_seq,
+                                     const int32_t *context_lens, int num_seqs, int num_heads, int num_kv_heads,
+                                     int head_dim, int block_size, int64_t num_blocks, float scale,
+                                     int max_context_len, int partition_size, void *workspace,
+                                     size_t workspace_bytes, int dtype, void *stream) {
+    const pa::CallRange range(__func__);
+    if (elem_size(dtype) == 0) return PA_ERR_INVALID_ARG;
+    pa::DecodeParams p{};
+    int64_t P = 0;
+    int rc = decode_setup(p, P, out, q, key_cache, value_cache, block_tables, max_blocks_per_seq, context_lens,
+                          num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                          max_context_len, partition_size);
+    if (rc == kNothingToDo) return PA_OK;
+    if (rc != PA_OK) return rc;
+    if (!mass || mass_len <= 0 || (reinterpret_cast<uintptr_t>(mass) & 3u) != 0) return PA_ERR_INVALID_ARG;
+    if (p.context_limit > mass_len) p.context_limit = (int)mass_len;
+    if ((rc = error_word(&p.err)) != PA_OK) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    void *owned = nullptr;
+    const int64_t max_ctx = call_max_context(max_blocks_per_seq, block_size, max_context_len);
+    if ((rc = scored_workspace(p, P, max_ctx, workspace, workspace_bytes, s, &owned)) != PA_OK) return rc;
+    const DecodeKernel choice = decode_kernel_choice();
+    int krc;
+    if (choice == DecodeKernel::Tc || (choice == DecodeKernel::Auto && pa::decode_tc_supported(p, dtype)))
+        krc = pa::launch_decode_tc(p, dtype, s);
+    else
+        krc = pa::launch_decode_simt(p, dtype, s);
+    if (krc == 0 && P > 1) krc = pa::launch_decode_reduce(p, dtype, s);
+    if (krc == 0) krc = pa::launch_decode_mass(p, mass, mass_len, s);
+    if (owned) cudaFreeAsync(owned, s);
+    if (krc == -2) return PA_ERR_UNSUPPORTED;
+    return krc == 0 ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_paged_kv_write_int4(const void *k, const void *v, const int32_t *slot_mapping, int64_t num_tokens,
+                           void *key_cache, void *value_cache, void *kv_params, int64_t num_blocks, int block_size,
+                           int num_kv_heads, int head_dim, int src_dtype, void *stream) {
+    const pa::CallRange range(__func__);
+    pa::Int4Cache c{};
+    int rc = int4_setup(c, k, v, slot_mapping, num_tokens, key_cache, value_cache, kv_params, num_blocks, block_size,
+                        num_kv_heads, head_dim, src_dtype);
+    if (rc == kNothingToDo) return PA_OK;
+    if (rc != PA_OK) return rc;
+    unsigned int *err = nullptr;
+    if ((rc = error_word(&err)) != PA_OK) return rc;
+    const int krc = pa::launch_kv_write_int4(k, v, src_dtype, slot_mapping, num_tokens, c, err,
+                                             static_cast<cudaStream_t>(stream));
+    if (krc == -2) return PA_ERR_UNSUPPORTED;
+    return krc == 0 ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_paged_kv_read_int4(void *k, void *v, const int32_t *slot_mapping, int64_t num_tokens, const void *key_cache,
+                          const void *value_cache, const void *kv_params, int64_t num_blocks, int block_size,
+                          int num_kv_heads, int head_dim, int dst_dtype, void *stream) {
+    const pa::CallRange range(__func__);
+    pa::Int4Cache c{};
+    int rc = int4_setup(c, k, v, slot_mapping, num_tokens, const_cast<void *>(key_cache),
+                        const_cast<void *>(value_cache), const_cast<void *>(kv_params), num_blocks, block_size,
+                        num_kv_heads, head_dim, dst_dtype);
+    if (rc == kNothingToDo) return PA_OK;
+    if (rc != PA_OK) return rc;
+    unsigned int *err = nullptr;
+    if ((rc = error_word(&err)) != PA_OK) return rc;
+    const int krc = pa::launch_kv_read_int4(k, v, dst_dtype, slot_mapping, num_tokens, c, err,
+                                            static_cast<cudaStream_t>(stream));
+    if (krc == -2) return PA_ERR_UNSUPPORTED;
+    return krc == 0 ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_copy_blocks_int4(void *key_cache, void *value_cache, void *kv_params, const int32_t *src_dst_pairs,
+                        int64_t num_pairs, int64_t num_blocks, int block_size, int num_kv_heads, int head_dim,
+                        void *stream) {
+    const pa::CallRange range(__func__);
+    if (num_pairs < 0 || num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0 || head_dim <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (!pow2(block_size) || block_size < 8 || block_size > 256) return PA_ERR_UNSUPPORTED;
+    if (num_pairs == 0) return PA_OK;
+    if (num_pairs > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    if (!key_cache || !value_cache || !kv_params || !src_dst_pairs) return PA_ERR_INVALID_ARG;
+    if (!aligned16(key_cache) || !aligned16(value_cache) || !aligned16(kv_params)) return PA_ERR_INVALID_ARG;
+    unsigned int *err = nullptr;
+    if (int rc = error_word(&err)) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t rows = (int64_t)block_size * num_kv_heads;
+    if (pa::launch_copy_blocks(key_cache, value_cache, src_dst_pairs, num_pairs, num_blocks, rows * (head_dim / 2), err,
+                               s) != 0 ||
+        pa::launch_copy_params_int4(kv_params, src_dst_pairs, num_pairs, num_blocks, rows * 8, err, s) != 0)
+        return PA_ERR_CUDA;
+    return PA_OK;
+}
+
+int pa_decode_int4_partition_size(int num_seqs, int num_kv_heads, int max_context_len, int partition_size) {
+    if (num_seqs < 0 || num_kv_heads <= 0 || max_context_len < 0 || partition_size < 0) return 0;
+    return resolve_partition(partition_size, num_seqs, max_context_len);
+}
+
+size_t pa_decode_int4_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                      int max_context_len, int partition_size, int with_mass) {
+    if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || max_context_len < 0 ||
+        partition_size < 0)
+        return 0;
+    const int part = pa_decode_int4_partition_size(num_seqs, num_kv_heads, max_context_len, partition_size);
+    const int64_t P = num_partitions(max_context_len, part);
+    return with_mass ? scored_workspace_bytes(num_seqs, num_heads, head_dim, P, max_context_len)
+                     : workspace_bytes_for(num_seqs, num_heads, head_dim, P);
+}
+
+int pa_paged_attention_decode_int4(void *out, const void *q, const void *key_cache, const void *value_cache,
+                                   const void *kv_params, float *mass, int64_t mass_len, const int32_t *block_tables,
+                                   int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_heads,
+                                   int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale,
+                                   int max_context_len, int partition_size, void *workspace, size_t workspace_bytes,
+                                   int dtype, void *stream) {
+    const pa::CallRange range(__func__);
+    if (dtype != PA_DTYPE_BF16 && dtype != PA_DTYPE_F16) return elem_size(dtype) ? PA_ERR_UNSUPPORTED
+                                                                                  : PA_ERR_INVALID_ARG;
+    pa::DecodeParams p{};
+    int64_t P = 0;
+    if (partition_size == 0 && num_seqs > 0 && num_kv_heads > 0 && max_blocks_per_seq > 0 && block_size > 0 &&
+        max_context_len >= 0) {
+        const int64_t m = call_max_context(max_blocks_per_seq, block_size, max_context_len);
+        if (m <= INT32_MAX) partition_size = pa_decode_int4_partition_size(num_seqs, num_kv_heads, (int)m, 0);
+    }
+    int rc = decode_setup(p, P, out, q, key_cache, value_cache, block_tables, max_blocks_per_seq, context_lens,
+                          num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                          max_context_len, partition_size);
+    if (rc == kNothingToDo) return PA_OK;
+    if (rc != PA_OK) return rc;
+    if (!kv_params || !aligned16(kv_params)) return PA_ERR_INVALID_ARG;
+    if (mass && (mass_len <= 0 || (reinterpret_cast<uintptr_t>(mass) & 3u) != 0)) return PA_ERR_INVALID_ARG;
+    p.kv_params = kv_params;
+    if (mass && p.context_limit > mass_len) p.context_limit = (int)mass_len;
+    if (!pa::decode_int4_supported(p, dtype)) return PA_ERR_UNSUPPORTED;
+    if ((rc = error_word(&p.err)) != PA_OK) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    void *owned = nullptr;
+    const int64_t max_ctx = call_max_context(max_blocks_per_seq, block_size, max_context_len);
+    rc = mass ? scored_workspace(p, P, max_ctx, workspace, workspace_bytes, s, &owned)
+              : decode_workspace(p, P, workspace, workspace_bytes, s, &owned);
+    if (rc != PA_OK) return rc;
+    int krc = pa::launch_decode_int4(p, dtype, s);
+    if (krc == 0 && P > 1) krc = pa::launch_decode_reduce(p, dtype, s);
+    if (krc == 0 && mass) krc = pa::launch_decode_mass(p, mass, mass_len, s);
+    if (owned) cudaFreeAsync(owned, s);
+    if (krc == -2) return PA_ERR_UNSUPPORTED;
+    return krc == 0 ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_paged_kv_evict(int32_t *kept, int64_t kept_len, const float *mass, int64_t mass_len, float *mass_out,
+                      int64_t mass_out_len, void *key_cache, void *value_cache, void *kv_params,
+                      const int32_t *block_tables, int max_blocks_per_seq, const int32_t *out_block_tables,
+                      int out_max_blocks_per_seq, const int32_t *context_lens, const int32_t *keep_lens, int recent,
+                      int num_seqs, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, int dtype,
+                      void *stream) {
+    const pa::CallRange range(__func__);
+    const bool int4 = dtype == PA_DTYPE_INT4;
+    const int es = dtype == PA_DTYPE_E4M3 ? 1 : elem_size(dtype);
+    if ((es == 0 && !int4) || num_seqs < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
+        num_blocks <= 0 || max_blocks_per_seq <= 0 || out_max_blocks_per_seq <= 0 || recent < 0 || kept_len <= 0 ||
+        mass_len <= 0 || mass_out_len <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (!pow2(block_size) || block_size > 256 || num_seqs > 65535 || num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+    if (int4 && ((head_dim != 64 && head_dim != 128) || block_size < 8)) return PA_ERR_UNSUPPORTED;
+    const int64_t row = int4 ? head_dim / 2 : (int64_t)head_dim * es;
+    if (row % 16 != 0 || row > 1 << 20) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PA_OK;
+    if (!kept || !mass || !mass_out || !key_cache || !value_cache || !block_tables || !out_block_tables ||
+        !context_lens || !keep_lens || (int4 && !kv_params))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(key_cache) || !aligned16(value_cache) || (int4 && !aligned16(kv_params)) ||
+        (reinterpret_cast<uintptr_t>(mass) & 3u) != 0 || (reinterpret_cast<uintptr_t>(mass_out) & 3u) != 0 ||
+        (reinterpret_cast<uintptr_t>(kept) & 3u) != 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_blocks > INT64_MAX / ((int64_t)block_size * num_kv_heads * row)) return PA_ERR_INVALID_ARG;
+    pa::EvictParams p{};
+    int rc = error_word(&p.err);
+    if (rc != PA_OK) return rc;
+    p.kept = kept;
+    p.mass = mass;
+    p.mass_out = mass_out;
+    p.block_tables = block_tables;
+    p.out_block_tables = out_block_tables;
+    p.context_lens = context_lens;
+    p.keep_lens = keep_lens;
+    p.kept_len = kept_len;
+    p.mass_len = mass_len;
+    p.mass_out_len = mass_out_len;
+    p.num_blocks = num_blocks;
+    p.max_blocks = max_blocks_per_seq;
+    p.out_max_blocks = out_max_blocks_per_seq;
+    const int64_t top = INT32_MAX;
+    p.context_limit = (int)std::min(top, std::min((int64_t)max_blocks_per_seq * block_size, mass_len));
+    p.keep_limit = (int)std::min({top, (int64_t)out_max_blocks_per_seq * block_size, mass_out_len, kept_len});
+    p.num_seqs = num_seqs;
+    p.num_kv_heads = num_kv_heads;
+    p.log2_block_size = ilog2(block_size);
+    p.recent = recent;
+    p.num_planes = int4 ? 3 : 2;
+    void *bases[3] = {key_cache, value_cache, kv_params};
+    for (int i = 0; i < p.num_planes; ++i) {
+        const int64_t bytes = i == 2 ? 8 : row;
+        pa::EvictPlane &pl = p.planes[i];
+        pl.base = static_cast<char *>(bases[i]);
+        pl.row_bytes = (int)bytes;
+        pl.block_stride = bytes * block_size * num_kv_heads;
+        pl.token_stride = int4 ? bytes : bytes * num_kv_heads;
+        pl.head_stride = int4 ? bytes * block_size : bytes;
+    }
+    return pa::launch_evict(p, static_cast<cudaStream_t>(stream)) == 0 ? PA_OK : PA_ERR_CUDA;
 }
 
 int pa_check_bounded_wait(int64_t limit_ns, int64_t *report, void *stream) {

@@ -48,7 +48,8 @@ struct SimtCfg {
     static_assert(kChunks >= 8, "swizzle needs at least 8 chunks per row");
 };
 
-template <typename T, int D, int GT>
+// kScore: also store the scores and every partition's (max, sum) pair (scored decode).
+template <typename T, int D, int GT, bool kScore>
 __global__ __launch_bounds__(kThreads) void decode_simt_kernel(const DecodeParams p) {
     using C = SimtCfg<T, D, GT>;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -182,6 +183,11 @@ __global__ __launch_bounds__(kThreads) void decode_simt_kernel(const DecodeParam
                 const int g = warp + 4 * hh;
                 if (g < GT) {
                     const float s = r < nvalid ? acc[hh] : -INFINITY;
+                    if constexpr (kScore) {
+                        if (r < nvalid && g < G)
+                            p.ws_logits[(((int64_t)b * p.num_kv_heads + kvh) * p.logits_len + tile_start + r) * G + g] =
+                                s;
+                    }
                     float mx = s;
 #pragma unroll
                     for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
@@ -251,6 +257,13 @@ __global__ __launch_bounds__(kThreads) void decode_simt_kernel(const DecodeParam
         }
     }
     __syncthreads();
+    if constexpr (kScore) {
+        if (tid < G) {
+            const int64_t row = (head0 + tid) * p.max_partitions + part;
+            p.ws_score_ml[2 * row] = m_s[tid];
+            p.ws_score_ml[2 * row + 1] = l_s[tid];
+        }
+    }
 
     if (nparts == 1) {
 #pragma unroll
@@ -482,10 +495,10 @@ __global__ __launch_bounds__(kReduceThreads) void decode_reduce_kernel(const Dec
     else merge_row<T, 2>(p, b, h, nparts, part_sum, ml_s);
 }
 
-template <typename T, int D, int GT>
+template <typename T, int D, int GT, bool kScore>
 int launch_simt_t(const DecodeParams &p, cudaStream_t stream) {
     using C = SimtCfg<T, D, GT>;
-    auto kern = decode_simt_kernel<T, D, GT>;
+    auto kern = decode_simt_kernel<T, D, GT, kScore>;
     static bool attr_set[kMaxDevices] = {};   // the opt-in is per device
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
@@ -498,15 +511,20 @@ int launch_simt_t(const DecodeParams &p, cudaStream_t stream) {
     return launch_pdl(kern, grid, dim3(kThreads), C::kSmem, stream, p);
 }
 
+template <typename T, int D, bool kScore>
+int launch_simt_s(const DecodeParams &p, cudaStream_t stream) {
+    const int G = p.group;
+    if (G <= 1) return launch_simt_t<T, D, 1, kScore>(p, stream);
+    if (G <= 2) return launch_simt_t<T, D, 2, kScore>(p, stream);
+    if (G <= 4) return launch_simt_t<T, D, 4, kScore>(p, stream);
+    if (G <= 8) return launch_simt_t<T, D, 8, kScore>(p, stream);
+    if (G <= 16) return launch_simt_t<T, D, 16, kScore>(p, stream);
+    return -2;
+}
+
 template <typename T, int D>
 int launch_simt_g(const DecodeParams &p, cudaStream_t stream) {
-    const int G = p.group;
-    if (G <= 1) return launch_simt_t<T, D, 1>(p, stream);
-    if (G <= 2) return launch_simt_t<T, D, 2>(p, stream);
-    if (G <= 4) return launch_simt_t<T, D, 4>(p, stream);
-    if (G <= 8) return launch_simt_t<T, D, 8>(p, stream);
-    if (G <= 16) return launch_simt_t<T, D, 16>(p, stream);
-    return -2;
+    return p.ws_logits ? launch_simt_s<T, D, true>(p, stream) : launch_simt_s<T, D, false>(p, stream);
 }
 
 template <typename T>

@@ -98,7 +98,8 @@ constexpr int kOffQ = kOffV + kStages * kKVBytes;
 constexpr int kOffP = kOffQ + kStages * kQBytes;
 constexpr int kOffRed = kOffP + 2 * kPBytes;                  // float [2][4][16]
 constexpr int kOffLRed = kOffRed + 2 * 4 * kN * 4;            // float [2][4][16] (by item parity)
-constexpr int kOffBar = kOffLRed + 2 * 4 * kN * 4;                // uint64 barriers
+constexpr int kOffXRed = kOffLRed + 2 * 4 * kN * 4;           // float [2][4][16]: the scored decode's sums
+constexpr int kOffBar = kOffXRed + 2 * 4 * kN * 4;            // uint64 barriers
 // mbarrier slots, in order; kNumBars counts them
 constexpr int kBarFull = 0;                                   // [kStages] K and Q of the stage landed
 constexpr int kBarEmpty = kBarFull + kStages;                 // [kStages]
@@ -190,7 +191,8 @@ template <> __device__ __forceinline__ float from_bits<__half>(uint16_t b) {
     return __half2float(__ushort_as_half(b));
 }
 
-template <typename T, int GT, bool kFold>
+// kScore: also store the scores and every partition's (max, sum) pair (scored decode).
+template <typename T, int GT, bool kFold, bool kScore>
 __global__ __launch_bounds__(kThreads, 1) void decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                                                                 const __grid_constant__ CUtensorMap tm_v,
                                                                 const __grid_constant__ CUtensorMap tm_q,
@@ -204,6 +206,7 @@ __global__ __launch_bounds__(kThreads, 1) void decode_tc_kernel(const __grid_con
     unsigned char *sP = smem + kOffP;
     float *red = reinterpret_cast<float *>(smem + kOffRed);
     float *lred = reinterpret_cast<float *>(smem + kOffLRed);
+    float *xred = reinterpret_cast<float *>(smem + kOffXRed);
     uint64_t *bar_base = reinterpret_cast<uint64_t *>(smem + kOffBar);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 4);
@@ -479,6 +482,7 @@ __global__ __launch_bounds__(kThreads, 1) void decode_tc_kernel(const __grid_con
         uint32_t it = 0, nfin = 0;              // tile counter; uses of the finalize barrier
         bool ok = true;
         float m_run[kC], l_part[kC], o_acc[kC], alpha_prev[kC];
+        float l_x[kC];                          // kScore: sums of the weights before their rounding
         // An item's finish (its last tile's O, the sum of l over the warps, the output)
         // is deferred until the next item's first tile has been through the softmax, so
         // the warpgroup does not wait for the last P.V at every item boundary: this is
@@ -492,7 +496,7 @@ __global__ __launch_bounds__(kThreads, 1) void decode_tc_kernel(const __grid_con
         int64_t pend_head0 = 0;
         int pend_slot = 0;
         bool pend_direct = false, pend_fold = false;
-        float pm[kC], pl[kC], po[kC], pa[kC], pfm[kC], pfl[kC], pfo[kC];
+        float pm[kC], pl[kC], po[kC], pa[kC], pfm[kC], pfl[kC], pfo[kC], px[kC];
         // this warpgroup's columns of a tile's accumulator at tensor-memory column `col`
         // (8 columns loaded; the first kC are this warpgroup's)
         auto load_cols = [&](uint32_t col, float *v) { tmem_ld8(tmem + lane_off + col + c0, v); };
@@ -514,12 +518,18 @@ __global__ __launch_bounds__(kThreads, 1) void decode_tc_kernel(const __grid_con
         // double-buffered by finish parity: one barrier per item), then the final row,
         // the join with the shared pass's partial, or this partition's partial.
         auto finish = [&](int64_t head0, int slot, bool direct, bool fold, const float *m, const float *lp,
-                          const float *acc, const float *fm, const float *fl, const float *fo) -> bool {
+                          const float *acc, const float *fm, const float *fl, const float *fo,
+                          const float *lx) -> bool {
             float *lr = lred + (nfin & 1) * 4 * kN;
+            float *xr = xred + (nfin & 1) * 4 * kN;
 #pragma unroll
             for (int u = 0; u < kC; ++u) {
                 const float ls = warp_sum(lp[u]);
                 if (lane == 0) lr[q4 * kN + c0 + u] = ls;
+                if constexpr (kScore) {
+                    const float xs = warp_sum(lx[u]);
+                    if (lane == 0) xr[q4 * kN + c0 + u] = xs;
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(fin_bar);
@@ -529,6 +539,13 @@ __global__ __launch_bounds__(kThreads, 1) void decode_tc_kernel(const __grid_con
             for (int u = 0; u < kC; ++u) {
                 const int g = c0 + u;
                 l_tot[u] = lr[g] + lr[kN + g] + lr[2 * kN + g] + lr[3 * kN + g];
+                if constexpr (kScore) {
+                    if (row == 0 && g < G) {
+                        const int64_t r = (head0 + g) * p.max_partitions + slot;
+                        p.ws_score_ml[2 * r] = m[u];
+                        p.ws_score_ml[2 * r + 1] = xr[g] + xr[kN + g] + xr[2 * kN + g] + xr[3 * kN + g];
+                    }
+                }
             }
             if (kFold && fold) {
                 // the shared pass's partial of these heads (slot 0, written before this
@@ -568,7 +585,7 @@ __global__ __launch_bounds__(kThreads, 1) void decode_tc_kernel(const __grid_con
             if (!pend) return true;
             pend = false;
             return accumulate(pend_it, po, pa) &&
-                   finish(pend_head0, pend_slot, pend_direct, pend_fold, pm, pl, po, pfm, pfl, pfo);
+                   finish(pend_head0, pend_slot, pend_direct, pend_fold, pm, pl, po, pfm, pfl, pfo, px);
         };
         for (int k = 0; k < nmy && ok; ++k) {
             const Item I = decode_order::unpack_item(items[k]);
@@ -600,6 +617,7 @@ __global__ __launch_bounds__(kThreads, 1) void decode_tc_kernel(const __grid_con
                 l_part[u] = 0.f;
                 o_acc[u] = 0.f;
                 alpha_prev[u] = 0.f;
+                if constexpr (kScore) l_x[u] = 0.f;
             }
             for (int tile = 0; tile < I.ntiles; ++tile, ++it) {
                 const int buf = it & 1, stage = it % kStages;
@@ -630,6 +648,15 @@ __global__ __launch_bounds__(kThreads, 1) void decode_tc_kernel(const __grid_con
                     ok = false;
                     break;
                 }
+                if constexpr (kScore) {
+                    // [sequence][kv head][token][head]: a thread stores its token's heads
+                    float *lg = p.ws_logits + (((int64_t)I.b * p.num_kv_heads + I.kvh) * p.logits_len + tok) * G + c0;
+                    if (valid) {
+#pragma unroll
+                        for (int u = 0; u < kC; ++u)
+                            if (c0 + u < G) lg[u] = s[u];
+                    }
+                }
                 float alpha[kC];
                 unsigned char *pb = sP + buf * kPBytes + (row >> 6) * (kN * 128);
                 const int colb = (row & 63) * 2;
@@ -640,7 +667,9 @@ __global__ __launch_bounds__(kThreads, 1) void decode_tc_kernel(const __grid_con
                     const float m_new = fmaxf(m_run[u], tmax);
                     alpha[u] = fast_exp2(m_run[u] - m_new);
                     m_run[u] = m_new;
-                    const uint16_t bits = to_bits<T>(valid ? fast_exp2(s[u] - m_new) : 0.f);
+                    const float pe = valid ? fast_exp2(s[u] - m_new) : 0.f;
+                    if constexpr (kScore) l_x[u] = fmaf(l_x[u], alpha[u], pe);
+                    const uint16_t bits = to_bits<T>(pe);
                     l_part[u] = fmaf(l_part[u], alpha[u], from_bits<T>(bits));
                     // P^T element (row n = g, column k = token) in a 128-byte swizzled K-major tile
                     unsigned char *dst = pb + g * 128 + ((((colb >> 4) ^ (g & 7)) << 4) | (colb & 15));
@@ -677,7 +706,7 @@ __global__ __launch_bounds__(kThreads, 1) void decode_tc_kernel(const __grid_con
             if (!ok) break;
             if (I.ntiles == 0) {
                 // a join with no tiles of its own (kFold): nothing to defer
-                if (!finish_pending() || !finish(head0, I.slot, I.direct, fold, m_run, l_part, o_acc, f_m, f_l, f_o)) {
+                if (!finish_pending() || !finish(head0, I.slot, I.direct, fold, m_run, l_part, o_acc, f_m, f_l, f_o, l_x)) {
                     ok = false;
                     break;
                 }
@@ -685,7 +714,7 @@ __global__ __launch_bounds__(kThreads, 1) void decode_tc_kernel(const __grid_con
             }
             if constexpr (!kDefer) {
                 if (!accumulate(it - 1, o_acc, alpha_prev) ||
-                    !finish(head0, I.slot, I.direct, fold, m_run, l_part, o_acc, f_m, f_l, f_o)) {
+                    !finish(head0, I.slot, I.direct, fold, m_run, l_part, o_acc, f_m, f_l, f_o, l_x)) {
                     ok = false;
                     break;
                 }
@@ -703,6 +732,7 @@ __global__ __launch_bounds__(kThreads, 1) void decode_tc_kernel(const __grid_con
                 pl[u] = l_part[u];
                 po[u] = o_acc[u];
                 pa[u] = alpha_prev[u];
+                if constexpr (kScore) px[u] = l_x[u];
                 if constexpr (kFold) {
                     pfm[u] = f_m[u];
                     pfl[u] = f_l[u];
@@ -744,9 +774,9 @@ bool make_q_map(CUtensorMap *m, const DecodeParams &p, CUtensorMapDataType dt) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int GT, bool kFold>
+template <typename T, int GT, bool kFold, bool kScore = false>
 int launch_tc_t(const DecodeParams &p, CUtensorMapDataType dt, cudaStream_t stream) {
-    auto kern = decode_tc_kernel<T, GT, kFold>;
+    auto kern = decode_tc_kernel<T, GT, kFold, kScore>;
     static bool attr_set[kMaxDevices] = {};
     static int num_sms[kMaxDevices] = {};
     int dev = 0;
@@ -774,6 +804,11 @@ int launch_tc_g(const DecodeParams &p, CUtensorMapDataType dt, cudaStream_t stre
         if (p.group <= 4) return launch_tc_t<T, 4, true>(p, dt, stream);
         if (p.group <= 8) return launch_tc_t<T, 8, true>(p, dt, stream);
         return -2;
+    }
+    if (p.ws_logits) {
+        if (p.group <= 4) return launch_tc_t<T, 4, false, true>(p, dt, stream);
+        if (p.group <= 8) return launch_tc_t<T, 8, false, true>(p, dt, stream);
+        return launch_tc_t<T, 16, false, true>(p, dt, stream);
     }
     if (p.group <= 4) return launch_tc_t<T, 4, false>(p, dt, stream);
     if (p.group <= 8) return launch_tc_t<T, 8, false>(p, dt, stream);
@@ -818,6 +853,10 @@ int launch_decode_tc(const DecodeParams &p, int dtype, cudaStream_t stream) {
         if (p.ws_ml) {
             c.ws_ml = p.ws_ml + rows * p.max_partitions * 2;
             c.ws_o = p.ws_o + rows * p.max_partitions * kD;
+        }
+        if (p.ws_logits) {
+            c.ws_logits = p.ws_logits + (int64_t)b0 * p.num_kv_heads * p.logits_len * p.group;
+            c.ws_score_ml = p.ws_score_ml + rows * p.max_partitions * 2;
         }
         const int rc = dtype == PA_DTYPE_BF16
                            ? launch_tc_g<__nv_bfloat16>(c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, stream)

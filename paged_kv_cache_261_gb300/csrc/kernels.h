@@ -50,6 +50,16 @@ struct DecodeParams {
     // while it runs. Not with the 8-bit kernel, whose two CTAs per SM, resident
     // early, slow that merge down more than their set-up gains.
     int chain_next;
+    // Scored decode: every score in log2 units, [num_seqs][num_kv_heads][logits_len][group],
+    // and every partition's (max, sum) pair, [B][H][P][2], those of whole rows included.
+    // The sum is of the fp32 weights; ws_ml's is of the weights as the P.V product has
+    // them (16 bits in the tensor-core kernel).
+    float *ws_logits;
+    float *ws_score_ml;
+    int logits_len;
+    // 4-bit cache: (K scale, K zero, V scale, V zero) float16,
+    // [num_blocks][num_kv_heads][block_size][4]
+    const void *kv_params;
 };
 
 // Chunked prefill: every query row of a packed chunk attends causally.

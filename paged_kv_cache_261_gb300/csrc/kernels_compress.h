@@ -1,0 +1,72 @@
+// Internal launch interface of the cache-compression operators (4-bit cache,
+// accumulated attention weights, eviction), between the C-ABI layer (capi.cu) and
+// their kernel translation units. Not part of the public ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kernels.h"
+
+namespace pa {
+
+// A 4-bit paged cache: codes [num_blocks, num_kv_heads, block_size, head_dim / 2]
+// for K and V, and params float16 [num_blocks, num_kv_heads, block_size, 4].
+struct Int4Cache {
+    void *key;
+    void *value;
+    void *params;
+    int64_t num_slots;         // num_blocks * block_size
+    int num_kv_heads;
+    int head_dim;              // 64 or 128
+    int log2_block_size;
+};
+
+int launch_kv_write_int4(const void *k, const void *v, int src_dtype, const int32_t *slot_mapping,
+                         int64_t num_tokens, const Int4Cache &c, unsigned int *err, cudaStream_t stream);
+int launch_kv_read_int4(void *k, void *v, int dst_dtype, const int32_t *slot_mapping, int64_t num_tokens,
+                        const Int4Cache &c, unsigned int *err, cudaStream_t stream);
+int launch_copy_params_int4(void *params, const int32_t *pairs, int64_t num_pairs, int64_t num_blocks,
+                            int64_t block_bytes, unsigned int *err, cudaStream_t stream);
+
+// Decode attention over a 4-bit cache (p.key_cache, p.value_cache, p.kv_params);
+// partials for multi-partition sequences go to p.ws_ml / p.ws_o. With p.ws_logits set
+// it also stores every score and every partition's (max, sum) pair.
+bool decode_int4_supported(const DecodeParams &p, int dtype);
+int launch_decode_int4(const DecodeParams &p, int dtype, cudaStream_t stream);
+
+// Adds each token's softmax weights, summed over the query heads of its kv head, to
+// mass [num_seqs, num_kv_heads, mass_len], from the scores and (max, sum) pairs that a
+// decode with p.ws_logits left in the workspace.
+int launch_decode_mass(const DecodeParams &p, float *mass, int64_t mass_len, cudaStream_t stream);
+
+// One array of rows that an eviction moves: row of (block, offset, kv head) at
+// base + block * block_stride + offset * token_stride + head * head_stride.
+struct EvictPlane {
+    char *base;
+    int64_t block_stride, token_stride, head_stride;
+    int row_bytes;             // a multiple of 8
+};
+
+struct EvictParams {
+    int32_t *kept;             // [num_seqs, num_kv_heads, kept_len]
+    const float *mass;         // [num_seqs, num_kv_heads, mass_len]
+    float *mass_out;           // [num_seqs, num_kv_heads, mass_out_len]
+    const int32_t *block_tables;
+    const int32_t *out_block_tables;
+    const int32_t *context_lens;
+    const int32_t *keep_lens;
+    unsigned int *err;
+    int64_t kept_len, mass_len, mass_out_len, num_blocks;
+    int max_blocks, out_max_blocks;
+    int context_limit;         // tokens the table and mass hold
+    int keep_limit;            // tokens the out table, mass_out and kept hold
+    int num_seqs, num_kv_heads;
+    int log2_block_size;
+    int recent;
+    int num_planes;
+    EvictPlane planes[3];
+};
+int launch_evict(const EvictParams &p, cudaStream_t stream);
+
+}  // namespace pa
