@@ -182,7 +182,7 @@ class Case:
         for b, n in enumerate(self.lens):
             ref, w, big, wv = cc.attention(qs[b], self.k[b], self.v[b], self.scale)
             dx = score_error(qs[b], self, b)
-            tol = bound(ref, w, dx, wv, self.dtype)
+            tol = bound(ref, dx, parts(self, b, w), self.dtype)
             err = np.abs(got[b] - ref)
             assert np.isfinite(got[b]).all() and (err <= tol).all(), (b, n, float((err - tol).max()), float(err.max()))
             if mass is not None:
@@ -215,13 +215,23 @@ def score_error(q, case, b):
     return a * case.scale * (case.D + 2) * 2.0 ** -23
 
 
-def bound(ref, w, dx, wv, dtype):
-    """Output bound: the final rounding; each weight off by its score's error, by 2^-11 (weights
-    times V scales enter the products as f16) and by 2^-21 (exp2, sums); the same over the
-    denominator. v_zero's share is inside wv's sum as |code * scale| + |zero| <= 3 |range|."""
-    dxm = dx.max(1, initial=0.0)[:, None]
-    rel = np.expm1(2 * dxm) + 2.0 ** -11 + 2.0 ** -20
-    return np.abs(ref) * cc.EPS[dtype] / 2 + 4 * rel * wv + cc.EPS[dtype] * 2.0 ** -14
+def parts(case, b, w):
+    """Weighted sums of what an output is added up from, [H, D]: |code * v_scale| + |v_zero|. (Not
+    of |v|: where code * scale and zero cancel, their roundings stay.)"""
+    n = case.lens[b]
+    s = cc.slots_of(case.bt[b], n, case.bs)
+    blk, off = s // case.bs, s % case.bs
+    par = np.abs(case.par[blk, :, off].astype(np.float64))                          # [n, Hk, 4]
+    a = cc.unpack(case.vc[blk, :, off]) * par[:, :, 2, None] + par[:, :, 3, None]
+    return np.einsum("hn,nhd->hd", w, np.repeat(a, case.H // case.Hk, 1))
+
+
+def bound(ref, dx, a, dtype):
+    """Output bound. Each term of an output's sum is off by its weight's error -- its own score's
+    and the sum's, e^(2 dx) -- by 2^-11 (weights times V scales enter the products as f16) and by
+    2^-20 (exp2, sums); the result is rounded once. A last term covers f16 subnormal outputs."""
+    rel = np.expm1(2 * dx.max(1, initial=0.0)[:, None]) + 2.0 ** -11 + 2.0 ** -20
+    return np.abs(ref) * cc.EPS[dtype] / 2 + (1 + cc.EPS[dtype]) * rel * a + cc.EPS[dtype] * 2.0 ** -14
 
 
 RAGGED = [1, 7, 0, 15, 16, 17, 31, 33, 64, 127, 128, 129, 300, 513, 1000, 1025]
