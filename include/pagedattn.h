@@ -458,14 +458,10 @@ int pa_copy_blocks_int4(void *key_cache, void *value_cache, void *kv_params, con
                         int64_t num_pairs, int64_t num_blocks, int block_size, int num_kv_heads, int head_dim,
                         void *stream);
 
-/* The partition size a 4-bit decode call uses: partition_size itself when it is not 0,
- * else the automatic choice. */
-int pa_decode_int4_partition_size(int num_seqs, int num_kv_heads, int max_context_len, int partition_size);
-
-/* Bytes of workspace pa_paged_attention_decode_int4 needs for these sizes; with_mass
- * non-zero: for a call that accumulates weights. May be 0 without. */
+/* Bytes of workspace pa_paged_attention_decode_int4 needs for these sizes on the current
+ * device; with_mass non-zero: for a call that accumulates weights. */
 size_t pa_decode_int4_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
-                                      int max_context_len, int partition_size, int with_mass);
+                                      int max_context_len, int with_mass);
 
 /*
  * Decode attention over a 4-bit cache. [P2 demo 2, eq. 4, as
@@ -478,8 +474,9 @@ size_t pa_decode_int4_workspace_bytes(int num_seqs, int num_heads, int num_kv_he
  * num_heads / num_kv_heads <= 16. mass (NULL: none): float32 [num_seqs, num_kv_heads,
  * mass_len], accumulated as by pa_paged_attention_decode_scored, out staying the same.
  * Parameters of the slots past a context's end are never used, whatever they hold; a
- * NaN parameter inside a context makes the outputs of its heads NaN. Partitions,
- * max_context_len, the workspace (size from pa_decode_int4_workspace_bytes; NULL =
+ * NaN parameter inside a context makes the outputs of its heads NaN. The work is cut
+ * into equal runs of tokens over the device, whatever the lengths (there is no partition
+ * size). max_context_len, the workspace (size from pa_decode_int4_workspace_bytes; NULL =
  * cudaMallocAsync on the stream) and the device error bits are those of
  * pa_paged_attention_decode.
  */
@@ -487,8 +484,8 @@ int pa_paged_attention_decode_int4(void *out, const void *q, const void *key_cac
                                    const void *kv_params, float *mass, int64_t mass_len, const int32_t *block_tables,
                                    int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_heads,
                                    int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale,
-                                   int max_context_len, int partition_size, void *workspace, size_t workspace_bytes,
-                                   int dtype, void *stream);
+                                   int max_context_len, void *workspace, size_t workspace_bytes, int dtype,
+                                   void *stream);
 
 /* ---- accumulated attention weights, and eviction by them --------------------
  * Not on the pages [P1-P3]; an extension that keeps long caches within a budget.

@@ -110,10 +110,9 @@ _decl("pa_paged_attention_prefill", [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i
 _decl("pa_paged_kv_write_int4", [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp])
 _decl("pa_paged_kv_read_int4", [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp])
 _decl("pa_copy_blocks_int4", [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _vp])
-_decl("pa_decode_int4_partition_size", [_i32, _i32, _i32, _i32])
-_decl("pa_decode_int4_workspace_bytes", [_i32, _i32, _i32, _i32, _i32, _i32, _i32], _sz)
+_decl("pa_decode_int4_workspace_bytes", [_i32, _i32, _i32, _i32, _i32, _i32], _sz)
 _decl("pa_paged_attention_decode_int4", [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i32, _vp, _i32, _i32, _i32, _i32,
-                                         _i32, _i64, _f, _i32, _i32, _vp, _sz, _i32, _vp])
+                                         _i32, _i64, _f, _i32, _vp, _sz, _i32, _vp])
 _decl("pa_decode_scored_workspace_bytes", [_i32, _i32, _i32, _i32, _i32], _sz)
 _decl("pa_paged_attention_decode_scored", [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32,
                                            _i32, _i64, _f, _i32, _i32, _vp, _sz, _i32, _vp])
@@ -655,21 +654,15 @@ def _mass(mass, name, B, hk, dev):
     return mass.shape[2]
 
 
-def decode_int4_partition_size(num_seqs: int, num_kv_heads: int, max_context_len: int,
-                               partition_size: int = 0) -> int:
-    """Partition size (tokens) a 4-bit decode call uses: partition_size, or the automatic choice for 0."""
-    return int(_lib.pa_decode_int4_partition_size(num_seqs, num_kv_heads, max_context_len, partition_size))
-
-
 def decode_int4_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
-                                max_context_len: int, partition_size: int = 0, with_mass: bool = False) -> int:
+                                max_context_len: int, with_mass: bool = False) -> int:
+    """Workspace bytes of a 4-bit decode call on the current device."""
     return int(_lib.pa_decode_int4_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len,
-                                                   partition_size, int(with_mass)))
+                                                   int(with_mass)))
 
 
 def paged_attention_decode_int4(out, q, key_cache, value_cache, kv_params, block_tables, context_lens, scale: float,
-                                max_context_len: int = 0, partition_size: int = 0, workspace=None, mass=None,
-                                stream=None) -> None:
+                                max_context_len: int = 0, workspace=None, mass=None, stream=None) -> None:
     """Decode attention over 4-bit caches [NB, Hk, bs, D / 2] with kv_params [NB, Hk, bs, 4].
 
     q, out [B, H, D] bf16 or fp16. mass: optional float32 [B, Hk, M], to which each token's
@@ -693,19 +686,16 @@ def paged_attention_decode_int4(out, q, key_cache, value_cache, kv_params, block
         mass_len = _mass(mass, "mass", B, hk, dev)
         mass_ptr = mass.data_ptr()
     sp = _stream_ptr(stream, dev)
-    need = decode_int4_workspace_bytes(B, H, hk, D, max_context_len or mb * bs, partition_size, mass is not None)
-    ws_ptr, ws_bytes = None, 0
-    if need:
+    with _on(dev):
+        need = decode_int4_workspace_bytes(B, H, hk, D, max_context_len or mb * bs, mass is not None)
         if workspace is None:
             workspace = _workspace(dev, sp, need)
         _cuda(workspace, "workspace", torch.uint8, dev)
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
-    with _on(dev):
         rc = _lib.pa_paged_attention_decode_int4(out.data_ptr(), q.data_ptr(), key_cache.data_ptr(),
                                                  value_cache.data_ptr(), kv_params.data_ptr(), mass_ptr, mass_len,
                                                  block_tables.data_ptr(), mb, context_lens.data_ptr(), B, H, hk, D, bs,
-                                                 nb, float(scale), int(max_context_len), int(partition_size), ws_ptr,
-                                                 ws_bytes, _dtype_code(q), sp)
+                                                 nb, float(scale), int(max_context_len), workspace.data_ptr(),
+                                                 workspace.numel(), _dtype_code(q), sp)
     _check(rc, "pa_paged_attention_decode_int4")
 
 

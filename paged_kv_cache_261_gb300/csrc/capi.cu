@@ -286,6 +286,14 @@ int scored_workspace(pa::DecodeParams &p, int64_t P, int64_t max_ctx, void *work
     return PA_OK;
 }
 
+// Workspace of a 4-bit decode: the partials, then (with_mass) every row's (max, sum) pair
+// and the scores.
+size_t int4_workspace_bytes(int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_ctx, bool with_mass) {
+    const pa::Int4WorkSizes z = pa::decode_int4_work_sizes(B, H, Hk, D, max_ctx, device_sm_count());
+    return align256(z.rows) + align256(z.part_ml) + align256(z.part_o) +
+           (with_mass ? align256((size_t)(B * H * 8)) + (size_t)(B * H * max_ctx * 4) : 0);
+}
+
 int64_t call_max_context(int max_blocks_per_seq, int block_size, int max_context_len) {
     return max_context_len == 0 ? (int64_t)max_blocks_per_seq * block_size : max_context_len;
 }
@@ -833,41 +841,28 @@ int pa_copy_blocks_int4(void *key_cache, void *value_cache, void *kv_params, con
     return PA_OK;
 }
 
-int pa_decode_int4_partition_size(int num_seqs, int num_kv_heads, int max_context_len, int partition_size) {
-    if (num_seqs < 0 || num_kv_heads <= 0 || max_context_len < 0 || partition_size < 0) return 0;
-    return resolve_partition(partition_size, num_seqs, max_context_len);
-}
-
 size_t pa_decode_int4_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
-                                      int max_context_len, int partition_size, int with_mass) {
-    if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || max_context_len < 0 ||
-        partition_size < 0)
+                                      int max_context_len, int with_mass) {
+    if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 || head_dim <= 0 ||
+        max_context_len < 0)
         return 0;
-    const int part = pa_decode_int4_partition_size(num_seqs, num_kv_heads, max_context_len, partition_size);
-    const int64_t P = num_partitions(max_context_len, part);
-    return with_mass ? scored_workspace_bytes(num_seqs, num_heads, head_dim, P, max_context_len)
-                     : workspace_bytes_for(num_seqs, num_heads, head_dim, P);
+    return int4_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len, with_mass != 0);
 }
 
 int pa_paged_attention_decode_int4(void *out, const void *q, const void *key_cache, const void *value_cache,
                                    const void *kv_params, float *mass, int64_t mass_len, const int32_t *block_tables,
                                    int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_heads,
                                    int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale,
-                                   int max_context_len, int partition_size, void *workspace, size_t workspace_bytes,
-                                   int dtype, void *stream) {
+                                   int max_context_len, void *workspace, size_t workspace_bytes, int dtype,
+                                   void *stream) {
     const pa::CallRange range(__func__);
     if (dtype != PA_DTYPE_BF16 && dtype != PA_DTYPE_F16) return elem_size(dtype) ? PA_ERR_UNSUPPORTED
                                                                                   : PA_ERR_INVALID_ARG;
     pa::DecodeParams p{};
     int64_t P = 0;
-    if (partition_size == 0 && num_seqs > 0 && num_kv_heads > 0 && max_blocks_per_seq > 0 && block_size > 0 &&
-        max_context_len >= 0) {
-        const int64_t m = call_max_context(max_blocks_per_seq, block_size, max_context_len);
-        if (m <= INT32_MAX) partition_size = pa_decode_int4_partition_size(num_seqs, num_kv_heads, (int)m, 0);
-    }
     int rc = decode_setup(p, P, out, q, key_cache, value_cache, block_tables, max_blocks_per_seq, context_lens,
                           num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
-                          max_context_len, partition_size);
+                          max_context_len, 0);
     if (rc == kNothingToDo) return PA_OK;
     if (rc != PA_OK) return rc;
     if (!kv_params || !aligned16(kv_params)) return PA_ERR_INVALID_ARG;
@@ -877,13 +872,35 @@ int pa_paged_attention_decode_int4(void *out, const void *q, const void *key_cac
     if (!pa::decode_int4_supported(p, dtype)) return PA_ERR_UNSUPPORTED;
     if ((rc = error_word(&p.err)) != PA_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    void *owned = nullptr;
-    const int64_t max_ctx = call_max_context(max_blocks_per_seq, block_size, max_context_len);
-    rc = mass ? scored_workspace(p, P, max_ctx, workspace, workspace_bytes, s, &owned)
-              : decode_workspace(p, P, workspace, workspace_bytes, s, &owned);
-    if (rc != PA_OK) return rc;
-    int krc = pa::launch_decode_int4(p, dtype, s);
-    if (krc == 0 && P > 1) krc = pa::launch_decode_reduce(p, dtype, s);
+    const int64_t max_ctx = max_context_len == 0 ? (int64_t)max_blocks_per_seq * block_size : max_context_len;
+    const size_t need = int4_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_ctx, mass != nullptr);
+    void *ws = workspace, *owned = nullptr;
+    if (ws) {
+        if (workspace_bytes < need) return PA_ERR_WORKSPACE;
+        if (!aligned16(ws)) return PA_ERR_INVALID_ARG;
+    } else {
+        if (cudaMallocAsync(&ws, need, s) != cudaSuccess) return PA_ERR_CUDA;
+        owned = ws;
+    }
+    const pa::Int4WorkSizes z =
+        pa::decode_int4_work_sizes(num_seqs, num_heads, num_kv_heads, head_dim, max_ctx, device_sm_count());
+    char *at = static_cast<char *>(ws);
+    pa::Int4Work w;
+    w.rows = reinterpret_cast<int2 *>(at);
+    at += align256(z.rows);
+    w.part_ml = reinterpret_cast<float2 *>(at);
+    at += align256(z.part_ml);
+    w.part_o = reinterpret_cast<float *>(at);
+    at += align256(z.part_o);
+    if (mass) {
+        p.ws_score_ml = reinterpret_cast<float *>(at);
+        at += align256((size_t)num_seqs * num_heads * 8);
+        p.ws_logits = reinterpret_cast<float *>(at);
+        p.logits_len = (int)max_ctx;
+    }
+    p.max_partitions = 1;                     // as the accumulation of the weights sees it
+    p.partition_size = INT32_MAX;
+    int krc = pa::launch_decode_int4(p, w, max_ctx, device_sm_count(), dtype, s);
     if (krc == 0 && mass) krc = pa::launch_decode_mass(p, mass, mass_len, s);
     if (owned) cudaFreeAsync(owned, s);
     if (krc == -2) return PA_ERR_UNSUPPORTED;

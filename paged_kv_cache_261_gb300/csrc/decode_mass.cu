@@ -32,7 +32,7 @@ __global__ __launch_bounds__(kThreads) void decode_mass_kernel(const DecodeParam
     ctx = ctx < 0 ? 0 : min(ctx, p.context_limit);
     const int64_t c0 = (int64_t)blockIdx.x * kChunk;
     if (c0 >= ctx) return;
-    const int nparts = (ctx + p.partition_size - 1) / p.partition_size;
+    const int nparts = (ctx - 1) / p.partition_size + 1;
     for (int g = warp; g < G; g += kThreads / 32) {
         const float2 *ml = reinterpret_cast<const float2 *>(p.ws_score_ml) +
                            ((int64_t)b * p.num_heads + (int64_t)kvh * G + g) * p.max_partitions;

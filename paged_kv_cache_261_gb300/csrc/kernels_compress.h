@@ -29,11 +29,29 @@ int launch_kv_read_int4(void *k, void *v, int dst_dtype, const int32_t *slot_map
 int launch_copy_params_int4(void *params, const int32_t *pairs, int64_t num_pairs, int64_t num_blocks,
                             int64_t block_bytes, unsigned int *err, cudaStream_t stream);
 
-// Decode attention over a 4-bit cache (p.key_cache, p.value_cache, p.kv_params);
-// partials for multi-partition sequences go to p.ws_ml / p.ws_o. With p.ws_logits set
-// it also stores every score and every partition's (max, sum) pair.
+// Tokens per stage and CTAs per SM of the 4-bit decode, by the padded group (8 or 16).
+__host__ __device__ constexpr int kInt4StageTokens(int gt) { return gt == 8 ? 32 : 64; }
+__host__ __device__ constexpr int kInt4Ctas(int gt) { return gt == 8 ? 2 : 1; }
+
+// Workspace of the 4-bit decode's partials.
+struct Int4Work {
+    int2 *rows;                // [sequence][kv head] of a launch: first partial, how many
+    float2 *part_ml;           // [partial][head of the group]: reference (log2 units), sum
+    float *part_o;             // [partial][head of the group][head_dim]
+};
+struct Int4WorkSizes {
+    size_t rows, part_ml, part_o;
+};
+Int4WorkSizes decode_int4_work_sizes(int64_t num_seqs, int64_t num_heads, int64_t num_kv_heads, int64_t head_dim,
+                                     int64_t max_ctx, int sms);
+
+// Decode attention over a 4-bit cache (p.key_cache, p.value_cache, p.kv_params) of contexts
+// up to max_ctx tokens, on `sms` multiprocessors; p's split-K fields are not used. With
+// p.ws_logits set it also stores every score, and every row's (max, sum) pair in
+// p.ws_score_ml as of one partition.
 bool decode_int4_supported(const DecodeParams &p, int dtype);
-int launch_decode_int4(const DecodeParams &p, int dtype, cudaStream_t stream);
+int launch_decode_int4(const DecodeParams &p, const Int4Work &ws, int64_t max_ctx, int sms, int dtype,
+                       cudaStream_t stream);
 
 // Adds each token's softmax weights, summed over the query heads of its kv head, to
 // mass [num_seqs, num_kv_heads, mass_len], from the scores and (max, sum) pairs that a

@@ -49,17 +49,16 @@ def test_copy_blocks_int4_refusals(pa):
 
 def _decode(pa, **kw):
     a = dict(out=16, q=16, kc=16, vc=16, par=16, mass=None, ml=0, bt=16, mb=4, cl=16, B=2, H=8, Hk=2, D=128, bs=16,
-             nb=64, scale=0.1, mc=0, part=0, ws=None, wsb=0, dt=2)
+             nb=64, scale=0.1, mc=0, ws=None, wsb=0, dt=2)
     a.update(kw)
     order = ("out", "q", "kc", "vc", "par", "mass", "ml", "bt", "mb", "cl", "B", "H", "Hk", "D", "bs", "nb", "scale",
-             "mc", "part", "ws", "wsb", "dt")
+             "mc", "ws", "wsb", "dt")
     return pa.lib().pa_paged_attention_decode_int4(*[a[x] for x in order], None)
 
 
 @pytest.mark.parametrize("bad,code", [
     (dict(H=6, Hk=4), INVALID), (dict(D=96), UNSUPPORTED), (dict(bs=12), UNSUPPORTED), (dict(bs=4), UNSUPPORTED),
-    (dict(bs=512), UNSUPPORTED), (dict(H=64, Hk=2), UNSUPPORTED), (dict(part=100), INVALID), (dict(part=-1), INVALID),
-    (dict(dt=0), UNSUPPORTED), (dict(dt=3), INVALID), (dict(dt=9), INVALID), (dict(out=None), INVALID),
+    (dict(bs=512), UNSUPPORTED), (dict(H=64, Hk=2), UNSUPPORTED), (dict(dt=0), UNSUPPORTED), (dict(dt=3), INVALID), (dict(dt=9), INVALID), (dict(out=None), INVALID),
     (dict(par=None), INVALID), (dict(par=8), INVALID), (dict(q=8), INVALID), (dict(nb=0), INVALID),
     (dict(B=-1), INVALID), (dict(mb=0), INVALID), (dict(mc=-1), INVALID), (dict(scale=float("nan")), INVALID),
     (dict(mass=16, ml=0), INVALID), (dict(mass=18, ml=9), INVALID), (dict(B=0), 0)])
@@ -120,19 +119,21 @@ def test_python_checks_refuse_host_tensors_and_wrong_shapes(pa):
 
 
 def test_workspace_sizes(pa):
-    for B, H, Hk, D, ctx, part in ((1, 8, 8, 128, 700, 0), (64, 32, 8, 128, 4096, 0), (8, 64, 8, 64, 131072, 512)):
-        P = -(-ctx // pa.decode_int4_partition_size(B, Hk, ctx, part))
-        split = B * H * P * (2 + D) * 4 if P > 1 else 0
-        n = pa.decode_int4_workspace_bytes(B, H, Hk, D, ctx, part)
-        assert split <= n < split + 256 or n == split == 0
-        n = pa.decode_int4_workspace_bytes(B, H, Hk, D, ctx, part, True)
-        assert 0 <= n - (split + B * H * P * 8 + B * H * ctx * 4) < 3 * 256
+    for B, H, Hk, D, ctx, part in ((1, 8, 8, 128, 700, 0), (64, 32, 8, 128, 4096, 0), (8, 64, 8, 64, 131072, 512),
+                                   (4000, 12, 1, 64, 50, 0)):
+        # a partial of a group for every warp of the grid and every row, with and without the scores
+        n, with_mass = (pa.decode_int4_workspace_bytes(B, H, Hk, D, ctx, w) for w in (False, True))
+        assert n >= min(B, 1536) * Hk * (8 + H // Hk * (8 + 4 * D))
+        assert 0 <= with_mass - n - B * H * (8 + 4 * ctx) < 256
         P = -(-ctx // pa.decode_partition_size(B, ctx, part))
         split = B * H * P * (2 + D) * 4 if P > 1 else 0
         n = pa.decode_scored_workspace_bytes(B, H, D, ctx, part)
         assert 0 <= n - (split + B * H * P * 8 + B * H * ctx * 4) < 3 * 256
-    assert pa.decode_int4_partition_size(3, 2, 5000, 256) == 256
+    # a larger batch never needs less
+    sizes = [pa.decode_int4_workspace_bytes(B, 32, 8, 128, 2048) for B in (1, 2, 64, 512, 5000)]
+    assert sizes == sorted(sizes)
     assert pa.decode_int4_workspace_bytes(0, 8, 2, 128, 100) == 0
+    assert pa.decode_int4_workspace_bytes(2, 9, 2, 128, 100) == 0
 
 
 def test_plain_quantisation_pins():

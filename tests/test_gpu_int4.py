@@ -252,11 +252,14 @@ def test_decode_ragged(pa, dtype, H, Hk, D, bs):
     assert torch.equal(out, plain)                       # accumulating weights does not change the output
 
 
-@pytest.mark.parametrize("part", [128, 256, 512, 1024])
-def test_decode_partitions(pa, part):
-    case = Case(np.random.default_rng(3), [2000, 1, 128, 700, 0, 1537], 16, 4, 128, 16, "f16")
-    mass = torch.full((6, 4, 2000), 0.25, device=dev())
-    out = case.run(pa, mass, partition_size=part)
+@pytest.mark.parametrize("lens", [[2000, 1, 128, 700, 0, 1537], [31] * 700, [0, 0, 33], [0], [9000], [70, 5000] * 40])
+@pytest.mark.parametrize("H,Hk", [(16, 4), (12, 1)])
+def test_decode_cuts(pa, lens, H, Hk):
+    """Rows that one run covers, rows cut into many, runs over many rows; non-zero mass."""
+    case = Case(np.random.default_rng(3), lens, H, Hk, 128, 16, "f16")
+    n = max(1, max(lens))
+    mass = torch.full((len(lens), Hk, n), 0.25, device=dev())
+    out = case.run(pa, mass, max_context_len=n)
     case.check(out, mass, before=0.25)
     assert pa.get_device_error() == 0
 
@@ -299,11 +302,11 @@ def test_decode_long_context(pa):
 
 
 def test_decode_many_sequences(pa):
-    """More sequences than one launch's item order holds."""
+    """More sequences than one launch takes."""
     rng = np.random.default_rng(41)
-    lens = rng.integers(0, 40, 1100)
+    lens = rng.integers(0, 40, 3500)
     case = Case(rng, lens, 4, 2, 64, 8, "bf16")
-    mass = torch.zeros((1100, 2, 40), device=dev())
+    mass = torch.zeros((3500, 2, 40), device=dev())
     case.check(case.run(pa, mass, max_context_len=40), mass)
     assert pa.get_device_error() == 0
 
@@ -362,23 +365,23 @@ def test_decode_workspaces_and_streams(pa):
     """A caller's workspace, too small a one, none through the C ABI; another stream."""
     case = Case(np.random.default_rng(81), [1500, 1400], 8, 2, 128, 16, "f16")
     want_mass = torch.zeros((2, 2, 1500), device=dev())
-    want = case.run(pa, want_mass, partition_size=256)
-    need = pa.decode_int4_workspace_bytes(2, 8, 2, 128, case.bt.shape[1] * 16, 256, True)
+    want = case.run(pa, want_mass)
+    need = pa.decode_int4_workspace_bytes(2, 8, 2, 128, case.bt.shape[1] * 16, True)
     ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=dev())
     mass = torch.zeros_like(want_mass)
-    assert torch.equal(case.run(pa, mass, partition_size=256, workspace=ws), want) and torch.equal(mass, want_mass)
+    assert torch.equal(case.run(pa, mass, workspace=ws), want) and torch.equal(mass, want_mass)
     with pytest.raises(pa.PagedAttnError) as e:
-        case.run(pa, mass, partition_size=256, workspace=ws[:need - 16])
+        case.run(pa, mass, workspace=ws[:need - 16])
     assert e.value.status == pa.PA_ERR_WORKSPACE
     t, out, mass = case.t, torch.empty_like(want), torch.zeros_like(want_mass)
     rc = pa.lib().pa_paged_attention_decode_int4(
         out.data_ptr(), t["q"].data_ptr(), t["kc"].data_ptr(), t["vc"].data_ptr(), t["par"].data_ptr(),
         mass.data_ptr(), 1500, t["bt"].data_ptr(), case.bt.shape[1], t["lens"].data_ptr(), 2, 8, 2, 128, 16, case.NB,
-        case.scale, 0, 256, None, 0, pa.PA_DTYPE_F16, torch.cuda.current_stream().cuda_stream)
+        case.scale, 0, None, 0, pa.PA_DTYPE_F16, torch.cuda.current_stream().cuda_stream)
     assert rc == 0 and torch.equal(out, want) and torch.equal(mass, want_mass)
     side = torch.cuda.Stream()
     mass = torch.zeros_like(want_mass)
     torch.cuda.synchronize()
-    out = case.run(pa, mass, partition_size=256, stream=side)
+    out = case.run(pa, mass, stream=side)
     side.synchronize()
     assert torch.equal(out, want) and torch.equal(mass, want_mass)
