@@ -589,82 +589,102 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
 }
 
 // Joins the partials of the rows that several runs share: M = max m_i, L = sum l_i
-// 2^(m_i - M), out = sum o_i 2^(m_i - M) / L. One CTA per (query head, sequence): its
-// warps take the partials in turn, eight of a warp's in flight, and are joined through
-// shared memory.
-constexpr int kJoinWarps = 4;
+// 2^(m_i - M), out = sum o_i 2^(m_i - M) / L. Warps per (query head, sequence): one where a
+// row has few partials, four (joined through shared memory) where it has many. A warp reads
+// 32 partials' pairs at once, one a lane, and then their outputs, kJoinBatch in flight.
+constexpr int kJoinThreads = 128;
 constexpr int kJoinBatch = 8;
 
-template <typename T, int D, bool kScore>
-__global__ __launch_bounds__(kJoinWarps * 32) void decode_int4_join_kernel(const DecodeParams p, const Int4Work ws) {
+template <typename T, int D, bool kScore, int WPR>
+__global__ __launch_bounds__(kJoinThreads) void decode_int4_join_kernel(const DecodeParams p, const Int4Work ws) {
     constexpr int N = D / 32;                          // channels of a lane
-    __shared__ float2 ml_s[kJoinWarps];
-    __shared__ float o_s[kJoinWarps][D];
-    const int h = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G = p.group;
+    __shared__ float2 ml_s[4];
+    __shared__ float o_s[4][D];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int sub = warp % WPR;
+    const int64_t head = (int64_t)blockIdx.x * (4 / WPR) + warp / WPR;   // (sequence, query head)
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int2 info = ws.rows[(int64_t)b * p.num_kv_heads + h / G];
-    if (info.y == 0) return;
-    const float2 *ml = ws.part_ml + (int64_t)info.x * G + h % G;
-    const float *o = ws.part_o + ((int64_t)info.x * G + h % G) * D + lane * N;
+    if (head >= (int64_t)p.num_seqs * p.num_heads) return;   // with WPR 4, the whole CTA
+    const int G = p.group;
+    const int64_t row = head / G;
+    const int g = (int)(head - row * G);
+    const int2 info = ws.rows[row];
+    if (info.y == 0) return;                           // likewise
+    const float2 *ml = ws.part_ml + (int64_t)info.x * G + g;
+    const float *o = ws.part_o + ((int64_t)info.x * G + g) * D + lane * N;
     float m = -INFINITY, l = 0.f, acc[N];
 #pragma unroll
     for (int u = 0; u < N; ++u) acc[u] = 0.f;
-    for (int i0 = warp; i0 < info.y; i0 += kJoinWarps * kJoinBatch) {
-        float2 mi[kJoinBatch];
-        float x[kJoinBatch][N];
+    for (int i0 = sub; i0 < info.y; i0 += 32 * WPR) {
+        const int i = i0 + lane * WPR;
+        const float2 mine = i < info.y ? ml[(int64_t)i * G] : make_float2(-INFINITY, 0.f);
+        float mb = mine.x;
 #pragma unroll
-        for (int k = 0; k < kJoinBatch; ++k) {
-            const int i = i0 + k * kJoinWarps;
-            mi[k] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-            for (int u = 0; u < N; ++u) x[k][u] = 0.f;
-            if (i < info.y) {
-                mi[k] = ml[(int64_t)i * G];
-                const float *src = o + (int64_t)i * G * D;
-                if constexpr (N == 4) *reinterpret_cast<float4 *>(x[k]) = *reinterpret_cast<const float4 *>(src);
-                else *reinterpret_cast<float2 *>(x[k]) = *reinterpret_cast<const float2 *>(src);
-            }
-        }
-        float mb = m;
-#pragma unroll
-        for (int k = 0; k < kJoinBatch; ++k) mb = fmaxf(mb, mi[k].x);
+        for (int k = 16; k > 0; k >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, k));
+        mb = fmaxf(mb, m);
         const float a = m == -INFINITY ? 0.f : fast_exp2(m - mb);
         l *= a;
 #pragma unroll
         for (int u = 0; u < N; ++u) acc[u] *= a;
-#pragma unroll
-        for (int k = 0; k < kJoinBatch; ++k) {
-            // a partial whose scores are all NaN has no reference and a NaN sum: keep the NaN
-            const float c = mi[k].x == -INFINITY ? (mi[k].y == mi[k].y ? 0.f : mi[k].y) : fast_exp2(mi[k].x - mb);
-            l = fmaf(mi[k].y, c, l);
-#pragma unroll
-            for (int u = 0; u < N; ++u) acc[u] = fmaf(x[k][u], c, acc[u]);
-        }
         m = mb;
+        // a partial whose scores are all NaN has no reference and a NaN sum: keep the NaN
+        const float c = mine.x == -INFINITY ? (mine.y == mine.y ? 0.f : mine.y) : fast_exp2(mine.x - mb);
+        float lc = mine.y * c;
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) lc += __shfl_xor_sync(0xffffffffu, lc, k);
+        l += lc;
+        const int n = min(32, (info.y - i0 + WPR - 1) / WPR);
+        for (int k0 = 0; k0 < n; k0 += kJoinBatch) {
+            float x[kJoinBatch][N];
+#pragma unroll
+            for (int k = 0; k < kJoinBatch; ++k) {
+                if (k0 + k < n) {
+                    const float *src = o + (int64_t)(i0 + (k0 + k) * WPR) * G * D;
+                    if constexpr (N == 4) *reinterpret_cast<float4 *>(x[k]) = *reinterpret_cast<const float4 *>(src);
+                    else *reinterpret_cast<float2 *>(x[k]) = *reinterpret_cast<const float2 *>(src);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kJoinBatch; ++k) {
+                if (k0 + k < n) {
+                    const float ck = __shfl_sync(0xffffffffu, c, k0 + k);
+#pragma unroll
+                    for (int u = 0; u < N; ++u) acc[u] = fmaf(x[k][u], ck, acc[u]);
+                }
+            }
+        }
     }
-    if (lane == 0) ml_s[warp] = make_float2(m, l);
+    if constexpr (WPR > 1) {
+        if (lane == 0) ml_s[warp] = make_float2(m, l);
 #pragma unroll
-    for (int u = 0; u < N; ++u) o_s[warp][lane * N + u] = acc[u];
-    __syncthreads();
-    float M = -INFINITY, L = 0.f;
+        for (int u = 0; u < N; ++u) o_s[warp][lane * N + u] = acc[u];
+        __syncthreads();
+        if (warp != 0) return;
+        float M = -INFINITY;
+        l = 0.f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, ml_s[w].x);
-    float f[kJoinWarps];
+        for (int u = 0; u < N; ++u) acc[u] = 0.f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-        f[w] = ml_s[w].x == -INFINITY ? (ml_s[w].y == ml_s[w].y ? 0.f : ml_s[w].y) : fast_exp2(ml_s[w].x - M);
-        L = fmaf(ml_s[w].y, f[w], L);
+        for (int w = 0; w < 4; ++w) M = fmaxf(M, ml_s[w].x);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float2 v = ml_s[w];
+            const float f = v.x == -INFINITY ? (v.y == v.y ? 0.f : v.y) : fast_exp2(v.x - M);
+            l = fmaf(v.y, f, l);
+#pragma unroll
+            for (int u = 0; u < N; ++u) acc[u] = fmaf(o_s[w][lane * N + u], f, acc[u]);
+        }
+        m = M;
     }
-    const int64_t head = (int64_t)b * p.num_heads + h;
-    if (threadIdx.x < D) {
-        float A = 0.f;
+    const float inv = 1.f / l;
+    alignas(8) T h[N];
 #pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) A = fmaf(o_s[w][threadIdx.x], f[w], A);
-        reinterpret_cast<T *>(p.out)[head * D + threadIdx.x] = Elem<T>::from_f(A / L);
-    }
-    if (kScore && threadIdx.x == 0) reinterpret_cast<float2 *>(p.ws_score_ml)[head] = make_float2(M, L);
+    for (int u = 0; u < N; ++u) h[u] = Elem<T>::from_f(acc[u] * inv);
+    T *dst = reinterpret_cast<T *>(p.out) + head * D + lane * N;
+    if constexpr (N == 4) *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<uint2 *>(h);
+    else *reinterpret_cast<uint32_t *>(dst) = *reinterpret_cast<uint32_t *>(h);
+    if (kScore && lane == 0) reinterpret_cast<float2 *>(p.ws_score_ml)[head] = make_float2(m, l);
 }
 
 template <typename T, int D, int GT, bool kScore>
@@ -680,8 +700,13 @@ int launch_t(const DecodeParams &p, const Int4Work &ws, int grid, cudaStream_t s
     }
     const int rc = launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), C::kSmem, stream, p, ws);
     if (rc != 0) return rc;
-    return launch_pdl(decode_int4_join_kernel<T, D, kScore>, dim3((unsigned)p.num_heads, (unsigned)p.num_seqs),
-                      dim3(kJoinWarps * 32), 0, stream, p, ws);
+    // partials a row, about: (runs + rows) / rows
+    const int64_t heads = (int64_t)p.num_seqs * p.num_heads, rows = (int64_t)p.num_seqs * p.num_kv_heads;
+    if ((int64_t)grid * kWarps <= 8 * rows)
+        return launch_pdl(decode_int4_join_kernel<T, D, kScore, 1>, dim3((unsigned)((heads + 3) / 4)),
+                          dim3(kJoinThreads), 0, stream, p, ws);
+    return launch_pdl(decode_int4_join_kernel<T, D, kScore, 4>, dim3((unsigned)heads), dim3(kJoinThreads), 0, stream, p,
+                      ws);
 }
 
 template <typename T, int D> int launch_g(const DecodeParams &p, const Int4Work &ws, int grid, cudaStream_t stream) {
