@@ -106,6 +106,32 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 __device__ __forceinline__ float2 unpack_half2(uint32_t u) { return __half22float2(*reinterpret_cast<__half2 *>(&u)); }
+// Two fp32 lanes in one instruction: a * b + c, a * b, a + b.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};"
+        "\n\tfma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};"
+        "\n\tmul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};"
+        "\n\tadd.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 // Largest value over the lanes of the same lane & 3 (the rows of a fragment's column).
 __device__ __forceinline__ float rows_max(float v) {
 #pragma unroll
@@ -253,6 +279,8 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
         kind == 2 ? p.kv_params : (kind == 1 ? p.value_cache : p.key_cache));
     const uint32_t dst_off = (kind == 2 ? C::kOffPar : (kind == 1 ? C::kOffV : 0)) + piece_off * piece_row;
     const uint32_t piece_bytes = piece_tok * piece_row;
+    const uint32_t run_bytes = (uint32_t)piece_row << p.log2_block_size;   // a block's rows of one kv head
+    const uint32_t block_bytes = run_bytes * (uint32_t)Hk;                 // at most 2^16 * 2^8 * 64
 
     Cursor nx = at;                                    // the stage to fetch next
     int to_fetch = todo;
@@ -276,9 +304,9 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
         if (lane == 0) mbar_arrive_expect_tx(bar, blocks * piece_tok * (2 * C::kRow + 8));
         __syncwarp();
         if (good) {
-            const int64_t row = (((int64_t)entry * Hk + nx.kvh) << p.log2_block_size) +
-                                ((nx.s * C::kTok + piece_off) & (p.block_size - 1));
-            bulk_load(dst, src_base + row * piece_row, piece_bytes, bar);
+            const uint32_t off = (uint32_t)nx.kvh * run_bytes +
+                                 (uint32_t)((nx.s * C::kTok + piece_off) & (p.block_size - 1)) * piece_row;
+            bulk_load(dst, src_base + ((uint64_t)(uint32_t)entry * block_bytes + off), piece_bytes, bar);
         } else if (live) {
             // a bad block id: zeros, so its tokens have score and value 0
             if (kind == 0) raise_error(p.err, PA_DEVERR_BLOCK_ID);
@@ -307,7 +335,7 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
         // the group's query as B fragments, and the factors of x = S * (k_scale * sa) + k_zero * sb
         // of the heads of S^T's columns
         uint32_t qb[NT][kSteps][2];
-        float sa[NT][2], sb[NT][2];
+        float2 sa[NT], sb[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             constexpr int N = D / 4;                   // channels of a lane
@@ -342,14 +370,12 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
                 }
             }
             const float a = p.scale_log2 * pow2f(-e2) * 16777216.f, c = p.scale_log2 * sum;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                sa[nt][u] = __shfl_sync(0xffffffffu, a, 8 * lj + 4 * u);
-                sb[nt][u] = __shfl_sync(0xffffffffu, c, 8 * lj + 4 * u);
-            }
+            sa[nt] = make_float2(__shfl_sync(0xffffffffu, a, 8 * lj), __shfl_sync(0xffffffffu, a, 8 * lj + 4));
+            sb[nt] = make_float2(__shfl_sync(0xffffffffu, c, 8 * lj), __shfl_sync(0xffffffffu, c, 8 * lj + 4));
         }
         float O[NT][kSteps][4];
-        float m[NT][2], l[NT][2], z[NT][2];
+        float m[NT][2];
+        float2 l[NT], z[NT];
         int r_exp = -40;                               // 2^r_exp = r_top > every v_scale seen
         float r_top = 0.f, cr = 0.f;                   // cr: v_scale * cr < 2^kWeightExp
         bool first = true;
@@ -360,10 +386,8 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
 #pragma unroll
                 for (int c = 0; c < 4; ++c) O[nt][u][c] = 0.f;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                m[nt][c] = -INFINITY;
-                l[nt][c] = z[nt][c] = 0.f;
-            }
+            for (int c = 0; c < 2; ++c) m[nt][c] = -INFINITY;
+            l[nt] = z[nt] = both(0.f);
         }
         // one stage; kTail: only its first n tokens belong to the row
         auto stage = [&](auto tail, const unsigned char *slot, int ts, int n) {
@@ -374,10 +398,11 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
             float rmax = 0.f;
 #pragma unroll
             for (int sub = 0; sub < kSub; ++sub) {
+                float S2[NT][4];                       // a second chain of sums
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) S[sub][nt][c] = 0.f;
+                    for (int c = 0; c < 4; ++c) S[sub][nt][c] = S2[nt][c] = 0.f;
                 uint32_t ka[D / 32], kb[D / 32];   // this lane's words of the two rows
                 const unsigned char *kr = slot + (sub * 16 + li) * C::kRow + lj * (D / 8);
                 if constexpr (D == 128) {
@@ -394,7 +419,7 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
                         const uint32_t a = ka[w] >> (8 * hh), b = kb[w] >> (8 * hh);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            mma16816(S[sub][nt], a & 0x000F000Fu, b & 0x000F000Fu, a & 0x00F000F0u,
+                            mma16816(hh ? S2[nt] : S[sub][nt], a & 0x000F000Fu, b & 0x000F000Fu, a & 0x00F000F0u,
                                      b & 0x00F000F0u, qb[nt][2 * w + hh][0], qb[nt][2 * w + hh][1]);
                     }
                 }
@@ -409,12 +434,11 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
                     rmax = fmaxf(rmax, fabsf(vs[sub][r]));
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float &x = S[sub][nt][2 * r + c];
-                            x = fmaf(x, kp.x * sa[nt][c], kp.y * sb[nt][c]);
-                            if (!valid) x = -INFINITY;
-                        }
+                        const float2 dot = add2(make_float2(S[sub][nt][2 * r], S[sub][nt][2 * r + 1]),
+                                                make_float2(S2[nt][2 * r], S2[nt][2 * r + 1]));
+                        const float2 x = fma2(dot, mul2(both(kp.x), sa[nt]), mul2(both(kp.y), sb[nt]));
+                        S[sub][nt][2 * r] = valid ? x.x : -INFINITY;
+                        S[sub][nt][2 * r + 1] = valid ? x.y : -INFINITY;
                         if constexpr (kScore) {
                             const int g = nt * 8 + 2 * lj;
                             float *lg = p.ws_logits +
@@ -448,25 +472,27 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
                 r_top = pow2f(r_new);
                 cr = pow2f(kWeightExp - r_new);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
+                    float a[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         float v = m[nt][c];
 #pragma unroll
                         for (int sub = 0; sub < kSub; ++sub) v = fmaxf(v, fmaxf(S[sub][nt][c], S[sub][nt][2 + c]));
                         v = rows_max(v);
-                        if (!first) {
-                            const float a = fast_exp2(m[nt][c] - v);
-                            l[nt][c] *= a;
-                            z[nt][c] *= a;
-#pragma unroll
-                            for (int u = 0; u < kSteps; ++u) {
-                                O[nt][u][c] *= a * rs;
-                                O[nt][u][2 + c] *= a * rs;
-                            }
-                        }
+                        a[c] = first ? 0.f : fast_exp2(m[nt][c] - v);
                         m[nt][c] = v;
                     }
+                    if (!first) {
+                        const float2 a2 = make_float2(a[0], a[1]);
+                        l[nt] = mul2(l[nt], a2);
+                        z[nt] = mul2(z[nt], a2);
+#pragma unroll
+                        for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) O[nt][u][c] *= a[c & 1] * rs;
+                    }
+                }
                 first = false;
             }
             // ---- weights and O^T
@@ -477,14 +503,13 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const float p0 = fast_exp2(S[sub][nt][2 * r] - m[nt][0]);
-                        const float p1 = fast_exp2(S[sub][nt][2 * r + 1] - m[nt][1]);
-                        l[nt][0] += p0;
-                        l[nt][1] += p1;
-                        z[nt][0] = fmaf(p0, vz[sub][r], z[nt][0]);
-                        z[nt][1] = fmaf(p1, vz[sub][r], z[nt][1]);
-                        const float v = vs[sub][r] * cr;
-                        wb[nt][r] = transpose8x8(pack_half2(p0 * v, p1 * v));
+                        const float2 d = add2(make_float2(S[sub][nt][2 * r], S[sub][nt][2 * r + 1]),
+                                              make_float2(-m[nt][0], -m[nt][1]));
+                        const float2 w = make_float2(fast_exp2(d.x), fast_exp2(d.y));
+                        l[nt] = add2(l[nt], w);
+                        z[nt] = fma2(w, both(vz[sub][r]), z[nt]);
+                        const float2 wv = mul2(w, both(vs[sub][r] * cr));
+                        wb[nt][r] = transpose8x8(pack_half2(wv.x, wv.y));
                     }
                 // this lane's bytes of tokens 2 lj, 2 lj + 1, 2 lj + 8, 2 lj + 9
                 const unsigned char *vr = slot + C::kOffV + (sub * 16 + 2 * lj) * C::kRow + li * (D / 16);
@@ -528,7 +553,9 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
         };
         for (; at.s < s_end; ++at.s, ++used) {
             const unsigned char *slot = ring + (used % kStages) * C::kSlot;
-            if (__any_sync(0xffffffffu, *abort_flag != 0) || !warp_wait(&full[used % kStages], (used / kStages) & 1)) {
+            const uint32_t ph = (used / kStages) & 1;
+            if (!__all_sync(0xffffffffu, mbar_try_wait(&full[used % kStages], ph)) &&
+                (__any_sync(0xffffffffu, *abort_flag != 0) || !warp_wait(&full[used % kStages], ph))) {
                 ok = false;
                 break;
             }
@@ -548,7 +575,7 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const float ls = rows_sum(l[nt][c]), zs = rows_sum(z[nt][c]);
+                const float ls = rows_sum(c ? l[nt].y : l[nt].x), zs = rows_sum(c ? z[nt].y : z[nt].x);
                 const int g = nt * 8 + 2 * lj + c;
                 if (g >= G) continue;
                 const float inv = whole ? 1.f / ls : 1.f;
