@@ -55,7 +55,6 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;
 constexpr int kMaxSeqs = 1536;                    // sequences per launch (the host splits larger batches)
-constexpr int kMinRun = 2;                        // stages a warp takes at least
 
 // The softmax reference of a head is not raised before a score exceeds it by this many
 // powers of two: the weights (f16, up to 2^kWeightExp times 2^kSlack) have the room.
@@ -131,7 +130,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 // Largest value over the lanes of the same lane & 3 (the rows of a fragment's column).
 __device__ __forceinline__ float rows_max(float v) {
 #pragma unroll
@@ -145,13 +143,17 @@ __device__ __forceinline__ float rows_sum(float v) {
 }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126..127
 
-// The cut of `total` stages into runs: warp w takes [first(w), first(w + 1)).
+// The cut of `total` stages into `warps` runs: the first `longer` of them have `len` + 1
+// stages, the others `len`; run w starts at stage first(w).
 struct Runs {
-    int64_t total;
-    int warps;
-    __device__ __forceinline__ int64_t first(int w) const { return (int64_t)w * total / warps; }
-    // the warp whose run holds stage s
-    __device__ __forceinline__ int owner(int64_t s) const { return (int)(((s + 1) * warps - 1) / total); }
+    uint32_t len, longer;
+    __device__ __forceinline__ Runs(uint32_t total, uint32_t warps) : len(total / warps), longer(total - len * warps) {}
+    __device__ __forceinline__ uint32_t first(uint32_t w) const { return w * len + min(w, longer); }
+    // the run that holds stage s
+    __device__ __forceinline__ uint32_t owner(uint32_t s) const {
+        const uint32_t head = longer * (len + 1);
+        return s < head ? s / (len + 1) : longer + (s - head) / len;
+    }
 };
 
 // A place in the order of stages: stage s of row (b, kvh), which has ns of them.
@@ -212,48 +214,26 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
         if (b1 == B && (b0 < B || tid == 0)) pre[B] = at;
     }
     __syncthreads();
-    Runs runs;
-    runs.total = (int64_t)pre[B] * Hk;
-    runs.warps = (int)max((int64_t)1, min((int64_t)gridDim.x * kWarps, (runs.total + kMinRun - 1) / kMinRun));
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-
-    // what the joining kernel needs of every row: its first partial and how many there are
-    // (0: the row is written here). A run's partial of a row is number run + row: both rise
-    // along the order, so the numbers are distinct and a row's are consecutive.
-    for (int64_t r = (int64_t)blockIdx.x * kThreads + tid; r < (int64_t)B * Hk; r += (int64_t)gridDim.x * kThreads) {
-        const int b = (int)(r / Hk), h = (int)(r - (int64_t)b * Hk), ns = pre[b + 1] - pre[b];
-        int2 info = make_int2(0, 0);
-        if (ns > 0) {
-            const int64_t s0 = (int64_t)pre[b] * Hk + (int64_t)h * ns;
-            const int w0 = runs.owner(s0), w1 = runs.owner(s0 + ns - 1);
-            if (w1 > w0) info = make_int2((int)(w0 + r), w1 - w0 + 1);
-        }
-        ws.rows[r] = info;
-    }
-    T *out = reinterpret_cast<T *>(p.out);
-    for (int b = blockIdx.x; b < B; b += gridDim.x)    // rows of empty contexts
-        if (pre[b + 1] == pre[b])
-            for (int i = tid; i < p.num_heads * D; i += kThreads)
-                out[(int64_t)b * p.num_heads * D + i] = Elem<T>::from_f(0.f);
-
+    const uint32_t total = (uint32_t)pre[B] * Hk;      // below 2^31: the host sees to it
+    const uint32_t num_runs = max(1u, min(gridDim.x * kWarps, total));
+    const Runs runs(total, num_runs);
     // runs go to the SMs in turn, so few of them still use all
-    const int run = warp * gridDim.x + blockIdx.x;
-    if (run >= runs.warps || runs.total == 0) return;
-    const int64_t run0 = runs.first(run);
-    const int todo = (int)(runs.first(run + 1) - run0);
-
-    Cursor at;
-    {
+    const uint32_t run = warp * gridDim.x + blockIdx.x;
+    int todo = 0;
+    Cursor at = {};
+    if (run < num_runs && total > 0) {
+        const uint32_t run0 = runs.first(run);
+        todo = (int)(runs.len + (run < runs.longer ? 1 : 0));
         int lo = 0, hi = B - 1;                        // the first b whose stages end after run0
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
-            if ((int64_t)pre[mid + 1] * Hk > run0) hi = mid; else lo = mid + 1;
+            if ((uint32_t)pre[mid + 1] * Hk > run0) hi = mid; else lo = mid + 1;
         }
         at.b = lo;
         at.ns = pre[lo + 1] - pre[lo];
-        const int64_t rest = run0 - (int64_t)pre[lo] * Hk;
-        at.kvh = (int)(rest / at.ns);
-        at.s = (int)(rest - (int64_t)at.kvh * at.ns);
+        const uint32_t rest = run0 - (uint32_t)pre[lo] * Hk;
+        at.kvh = (int)(rest / (uint32_t)at.ns);
+        at.s = (int)(rest - (uint32_t)at.kvh * at.ns);
         at.ctx = context(lo);
     }
     // the next row that has stages (there is one)
@@ -282,24 +262,20 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
     const uint32_t run_bytes = (uint32_t)piece_row << p.log2_block_size;   // a block's rows of one kv head
     const uint32_t block_bytes = run_bytes * (uint32_t)Hk;                 // at most 2^16 * 2^8 * 64
 
-    Cursor nx = at;                                    // the stage to fetch next
-    int to_fetch = todo;
-    uint32_t fetched = 0;
-    int entry = -1;                                    // its table entry of this lane's piece
-    bool live = false;
-    auto look_up = [&]() {
-        const int t = nx.s * C::kTok + piece_off;
-        live = fetches && t < nx.ctx;
-        if (live) entry = p.block_tables[(int64_t)nx.b * p.max_blocks_per_seq + (t >> p.log2_block_size)];
+    // whether this lane has a piece of the stage to fetch, and its table entry
+    auto has_piece = [&](const Cursor &c) { return fetches && c.s * C::kTok + piece_off < c.ctx; };
+    auto look_up = [&](const Cursor &c) {
+        const int t = c.s * C::kTok + piece_off;
+        return has_piece(c) ? p.block_tables[(int64_t)c.b * p.max_blocks_per_seq + (t >> p.log2_block_size)] : -1;
     };
-    // fetch that stage into the next slot of the ring (which no lane reads any more), and
-    // look up the one after it, whose entry is on its way until the next call
-    auto fetch_one = [&]() {
-        if (to_fetch == 0) return;
-        const uint32_t sl = fetched % kStages;
+    auto step = [&](Cursor &c) {
+        if (++c.s == c.ns) next_row(c);
+    };
+    // fetch a stage into a slot of the ring (which no lane reads any more)
+    auto fetch = [&](const Cursor &nx, int entry, int sl) {
         unsigned char *dst = ring + sl * C::kSlot + dst_off;
         uint64_t *bar = &full[sl];
-        const bool good = live && entry >= 0 && entry < p.num_blocks;
+        const bool live = has_piece(nx), good = live && entry >= 0 && entry < p.num_blocks;
         const uint32_t blocks = __popc(__ballot_sync(0xffffffffu, good) & 0xFFu);
         if (lane == 0) mbar_arrive_expect_tx(bar, blocks * piece_tok * (2 * C::kRow + 8));
         __syncwarp();
@@ -314,21 +290,57 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
             fence_proxy_async_smem();
         }
         __syncwarp();
-        ++fetched;
-        if (--to_fetch == 0) return;
-        if (++nx.s == nx.ns) next_row(nx);
-        look_up();
     };
-    look_up();
-    for (int i = 0; i < kStages; ++i) fetch_one();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the first stages, their look-ups in flight together; then one look-up ahead
+    Cursor nx = at;
+    int entry = -1;
+    if (todo > 0) {
+        Cursor c[kStages];
+        int e[kStages];
+#pragma unroll
+        for (int i = 0; i < kStages; ++i)
+            if (i < todo) {
+                c[i] = nx;
+                e[i] = look_up(nx);
+                if (i + 1 < todo) step(nx);
+            }
+#pragma unroll
+        for (int i = 0; i < kStages; ++i)
+            if (i < todo) fetch(c[i], e[i], i);
+        entry = look_up(nx);
+    }
+    // what the joining kernel needs of every row: its first partial and how many there are
+    // (0: the row is written here). A run's partial of a row is number run + row: both rise
+    // along the order, so the numbers are distinct and a row's are consecutive.
+    for (int r = blockIdx.x * kThreads + tid; r < B * Hk; r += gridDim.x * kThreads) {
+        const int b = r / Hk, h = r - b * Hk, ns = pre[b + 1] - pre[b];
+        int2 info = make_int2(0, 0);
+        if (ns > 0) {
+            const uint32_t s0 = (uint32_t)pre[b] * Hk + (uint32_t)h * ns;
+            const int w0 = (int)runs.owner(s0), w1 = (int)runs.owner(s0 + ns - 1);
+            if (w1 > w0) info = make_int2(w0 + r, w1 - w0 + 1);
+        }
+        ws.rows[r] = info;
+    }
+    T *out = reinterpret_cast<T *>(p.out);
+    for (int b = blockIdx.x; b < B; b += gridDim.x)    // rows of empty contexts
+        if (pre[b + 1] == pre[b])
+            for (int i = tid; i < p.num_heads * D; i += kThreads)
+                out[(int64_t)b * p.num_heads * D + i] = Elem<T>::from_f(0.f);
+
+    if (todo == 0) return;
+    int left = todo;                                   // stages to consume
+    int unfetched = todo - min(todo, kStages);         // and to fetch
+    int sl = 0;                                        // the slot of the next stage
+    uint32_t phase = 0;                                // and its barrier's phase
+    bool ok = true;
 
     const T *q = reinterpret_cast<const T *>(p.q);
-    uint32_t used = 0;                                 // stages consumed
-    bool ok = true;
-    while ((int)used < todo) {
+    while (left > 0) {
         // ---- the part of row (b, kvh) that lies in this run
         const int I_b = at.b, I_kvh = at.kvh;
-        const int s_end = (int)min((int64_t)at.ns, (int64_t)at.s + (todo - (int)used));
+        const int s_end = min(at.ns, at.s + left);
         const bool whole = at.s == 0 && s_end == at.ns;
         const int64_t head0 = (int64_t)I_b * p.num_heads + (int64_t)I_kvh * G;
 
@@ -374,8 +386,7 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
             sb[nt] = make_float2(__shfl_sync(0xffffffffu, c, 8 * lj), __shfl_sync(0xffffffffu, c, 8 * lj + 4));
         }
         float O[NT][kSteps][4];
-        float m[NT][2];
-        float2 l[NT], z[NT];
+        float2 nm[NT], l[NT], z[NT];                   // nm: the negated references
         int r_exp = -40;                               // 2^r_exp = r_top > every v_scale seen
         float r_top = 0.f, cr = 0.f;                   // cr: v_scale * cr < 2^kWeightExp
         bool first = true;
@@ -385,9 +396,8 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
             for (int u = 0; u < kSteps; ++u)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) O[nt][u][c] = 0.f;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) m[nt][c] = -INFINITY;
-            l[nt] = z[nt] = both(0.f);
+            nm[nt] = make_float2(INFINITY, INFINITY);
+            l[nt] = z[nt] = make_float2(0.f, 0.f);
         }
         // one stage; kTail: only its first n tokens belong to the row
         auto stage = [&](auto tail, const unsigned char *slot, int ts, int n) {
@@ -436,7 +446,8 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
                     for (int nt = 0; nt < NT; ++nt) {
                         const float2 dot = add2(make_float2(S[sub][nt][2 * r], S[sub][nt][2 * r + 1]),
                                                 make_float2(S2[nt][2 * r], S2[nt][2 * r + 1]));
-                        const float2 x = fma2(dot, mul2(both(kp.x), sa[nt]), mul2(both(kp.y), sb[nt]));
+                        const float2 x = fma2(dot, make_float2(kp.x * sa[nt].x, kp.x * sa[nt].y),
+                                              make_float2(kp.y * sb[nt].x, kp.y * sb[nt].y));
                         S[sub][nt][2 * r] = valid ? x.x : -INFINITY;
                         S[sub][nt][2 * r + 1] = valid ? x.y : -INFINITY;
                         if constexpr (kScore) {
@@ -463,7 +474,7 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
                     float v = S[0][nt][c];
 #pragma unroll
                     for (int sub = 0; sub < kSub; ++sub) v = fmaxf(v, fmaxf(S[sub][nt][c], S[sub][nt][2 + c]));
-                    over = fmaxf(over, v - m[nt][c]);
+                    over = fmaxf(over, v + (c ? nm[nt].y : nm[nt].x));
                 }
             if (__any_sync(0xffffffffu, first || over > kSlack || rmax >= r_top)) {
                 const int r_new = max(r_exp, min(17, (int)((__float_as_uint(rows_max(rmax)) >> 23) & 0xFF) - 126));
@@ -476,12 +487,13 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
                     float a[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float v = m[nt][c];
+                        float &neg = c ? nm[nt].y : nm[nt].x;
+                        float v = -neg;
 #pragma unroll
                         for (int sub = 0; sub < kSub; ++sub) v = fmaxf(v, fmaxf(S[sub][nt][c], S[sub][nt][2 + c]));
                         v = rows_max(v);
-                        a[c] = first ? 0.f : fast_exp2(m[nt][c] - v);
-                        m[nt][c] = v;
+                        a[c] = first ? 0.f : fast_exp2(-neg - v);
+                        neg = -v;
                     }
                     if (!first) {
                         const float2 a2 = make_float2(a[0], a[1]);
@@ -504,12 +516,13 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const float2 d = add2(make_float2(S[sub][nt][2 * r], S[sub][nt][2 * r + 1]),
-                                              make_float2(-m[nt][0], -m[nt][1]));
+                                              nm[nt]);
                         const float2 w = make_float2(fast_exp2(d.x), fast_exp2(d.y));
                         l[nt] = add2(l[nt], w);
-                        z[nt] = fma2(w, both(vz[sub][r]), z[nt]);
-                        const float2 wv = mul2(w, both(vs[sub][r] * cr));
-                        wb[nt][r] = transpose8x8(pack_half2(wv.x, wv.y));
+                        z[nt].x = fmaf(w.x, vz[sub][r], z[nt].x);
+                        z[nt].y = fmaf(w.y, vz[sub][r], z[nt].y);
+                        const float v = vs[sub][r] * cr;
+                        wb[nt][r] = transpose8x8(pack_half2(w.x * v, w.y * v));
                     }
                 // this lane's bytes of tokens 2 lj, 2 lj + 1, 2 lj + 8, 2 lj + 9
                 const unsigned char *vr = slot + C::kOffV + (sub * 16 + 2 * lj) * C::kRow + li * (D / 16);
@@ -551,11 +564,10 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
                     }
             }
         };
-        for (; at.s < s_end; ++at.s, ++used) {
-            const unsigned char *slot = ring + (used % kStages) * C::kSlot;
-            const uint32_t ph = (used / kStages) & 1;
-            if (!__all_sync(0xffffffffu, mbar_try_wait(&full[used % kStages], ph)) &&
-                (__any_sync(0xffffffffu, *abort_flag != 0) || !warp_wait(&full[used % kStages], ph))) {
+        for (; at.s < s_end; ++at.s) {
+            const unsigned char *slot = ring + sl * C::kSlot;
+            if (!__all_sync(0xffffffffu, mbar_try_wait(&full[sl], phase)) &&
+                (__any_sync(0xffffffffu, *abort_flag != 0) || !warp_wait(&full[sl], phase))) {
                 ok = false;
                 break;
             }
@@ -563,13 +575,24 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
             if (n >= C::kTok) stage(std::false_type{}, slot, ts, n);
             else stage(std::true_type{}, slot, ts, n);
             __syncwarp();                              // every lane has read the slot
-            fetch_one();
+            --left;
+            if (unfetched > 0) {
+                fetch(nx, entry, sl);
+                if (--unfetched > 0) {
+                    step(nx);
+                    entry = look_up(nx);               // on its way until the next fetch
+                }
+            }
+            if (++sl == kStages) {
+                sl = 0;
+                phase ^= 1;
+            }
         }
         if (!ok) break;
 
         // ---- the row, or this run's partial of it (unnormalised, with its reference and sum).
         // A lane has channels li D / 8 + r D / 16 + u of heads 2 lj and 2 lj + 1.
-        const int64_t r = (int64_t)I_b * Hk + I_kvh;
+        const int r = I_b * Hk + I_kvh;
         const float even = pow2f(r_exp + 24 - kWeightExp), odd = pow2f(r_exp + 20 - kWeightExp);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -594,24 +617,30 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
                         if constexpr (kSteps == 8) *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<uint4 *>(h);
                         else *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<uint2 *>(h);
                     } else {
-                        float *dst = ws.part_o + ((run + r) * G + g) * D + d0;
+                        float *dst = ws.part_o + ((int64_t)(run + r) * G + g) * D + d0;
 #pragma unroll
                         for (int u = 0; u < kSteps; u += 4)
                             *reinterpret_cast<float4 *>(dst + u) = make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
                     }
                 }
                 if (li == 0) {
-                    if (!whole) ws.part_ml[(run + r) * G + g] = make_float2(m[nt][c], ls);
-                    else if (kScore) reinterpret_cast<float2 *>(p.ws_score_ml)[head0 + g] = make_float2(m[nt][c], ls);
+                    if (!whole) ws.part_ml[(int64_t)(run + r) * G + g] = make_float2(-(c ? nm[nt].y : nm[nt].x), ls);
+                    else if (kScore) reinterpret_cast<float2 *>(p.ws_score_ml)[head0 + g] = make_float2(-(c ? nm[nt].y : nm[nt].x), ls);
                 }
             }
-        if ((int)used < todo) next_row(at);
+        if (left > 0) next_row(at);
     }
     if (!ok) {
         *abort_flag = 1;
         raise_error(p.err, PA_DEVERR_WAIT);
         // copies still in flight land before the CTA's shared memory goes away
-        for (uint32_t j = used; j != fetched; ++j) mbar_wait(&full[j % kStages], (j / kStages) & 1);
+        for (; left > unfetched; --left) {
+            mbar_wait(&full[sl], phase);
+            if (++sl == kStages) {
+                sl = 0;
+                phase ^= 1;
+            }
+        }
     }
 }
 
@@ -751,9 +780,9 @@ int64_t row_stages(int64_t max_ctx, int group) {
     return (max_ctx + kInt4StageTokens(gt) - 1) / kInt4StageTokens(gt);
 }
 
-// Sequences per launch: what the kernel's prefix holds, and its sums in 31 bits.
-int64_t seqs_per_launch(int64_t max_ctx, int group) {
-    const int64_t ns = row_stages(max_ctx, group);
+// Sequences per launch: what the kernel's prefix holds, and a launch's stages in 31 bits.
+int64_t seqs_per_launch(int64_t max_ctx, int64_t kv_heads, int group) {
+    const int64_t ns = row_stages(max_ctx, group) * kv_heads;
     return std::max<int64_t>(1, std::min<int64_t>(kMaxSeqs, INT32_MAX / std::max<int64_t>(ns, 1)));
 }
 
@@ -775,7 +804,7 @@ bool decode_int4_supported(const DecodeParams &p, int dtype) {
 Int4WorkSizes decode_int4_work_sizes(int64_t num_seqs, int64_t num_heads, int64_t num_kv_heads, int64_t head_dim,
                                      int64_t max_ctx, int sms) {
     const int group = (int)(num_heads / num_kv_heads);
-    const int64_t seqs = std::min(num_seqs, seqs_per_launch(max_ctx, group));
+    const int64_t seqs = std::min(num_seqs, seqs_per_launch(max_ctx, num_kv_heads, group));
     const int64_t rows = seqs * num_kv_heads;
     const int64_t parts = (int64_t)launch_grid(seqs, num_kv_heads, max_ctx, group, sms) * kWarps + rows;
     Int4WorkSizes s;
@@ -787,8 +816,8 @@ Int4WorkSizes decode_int4_work_sizes(int64_t num_seqs, int64_t num_heads, int64_
 
 int launch_decode_int4(const DecodeParams &p, const Int4Work &ws, int64_t max_ctx, int sms, int dtype,
                        cudaStream_t stream) {
-    if (!decode_int4_supported(p, dtype)) return -2;
-    const int chunk = (int)std::min<int64_t>(p.num_seqs, seqs_per_launch(max_ctx, p.group));
+    if (!decode_int4_supported(p, dtype) || row_stages(max_ctx, p.group) * p.num_kv_heads > INT32_MAX) return -2;
+    const int chunk = (int)std::min<int64_t>(p.num_seqs, seqs_per_launch(max_ctx, p.num_kv_heads, p.group));
     for (int b0 = 0; b0 < p.num_seqs; b0 += chunk) {
         DecodeParams c = p;
         const int64_t rows = (int64_t)b0 * p.num_heads;
