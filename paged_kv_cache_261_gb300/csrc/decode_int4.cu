@@ -27,16 +27,21 @@
 // it below, whatever the scale of V. The query enters as f16 times a power of two per
 // head: exact for bf16 and f16 at every channel within 2^-22 of the row's largest.
 //
-// Work: the stages (32 or 64 tokens of one sequence and kv head) of the whole call, in
-// order, are cut into equal runs, one for each warp of the persistent grid; a run that
-// covers a row (sequence, kv head) writes its result, the others leave partials that a
-// second kernel joins. Warps share nothing, so nothing synchronises them: items of a CTA
-// whose 8 warps joined their states through shared memory took 65 us on the 8B-shaped
-// batch, twice the instructions a token of this form (27.7 against 14), and left the last
-// CTAs alone. Each warp fetches its own stages, two ahead and across rows, into its own
-// ring: a block of one kv head is one contiguous run for K, V and the parameters each, so
-// a stage is a few untiled bulk copies on one mbarrier.
+// Work: the stages (64 tokens of one sequence and kv head) of the whole call, in order,
+// are cut into equal runs, one for each warp of the persistent grid; a run that covers a
+// row (sequence, kv head) writes its result, the others leave partials that a second
+// kernel joins. Warps share nothing, so nothing synchronises them. (Items of a CTA whose
+// warps joined their states through shared memory took 65 us on the 8B-shaped batch, with
+// 27.7 instructions a token against 18 in this form.) Each warp fetches its own stages, one ahead
+// and across rows, into its own ring: a block of one kv head is one contiguous run for K,
+// V and the parameters each, so a stage is a few untiled bulk copies on one mbarrier.
 //
+// What bounds it (one GB300): the 8B-shaped batch, 162 MB, takes 38.0 us, of which about 8
+// are the two kernels' start and the join; long contexts, 711 MB, take 123 us, 5.8 TB/s.
+// The copies alone take 33.7 and 115 us, the arithmetic alone 30.0 and 99.
+// Stages of 32 tokens and 16 warps per SM: 39.9 and 135 us (a stage's fixed work, about 60
+// instructions, comes twice as often, and 128 registers leave less in flight).
+
 // Every wait is bounded; on a timeout the kernel sets PA_DEVERR_WAIT, waits (bounded)
 // for its copies in flight and returns.
 #include "common.cuh"
@@ -51,9 +56,10 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
+// Two stages a warp: 209 KB per SM. (With stages of 32 tokens, where a third fitted, it
+// measured slower: 41.7 against 39.9 us on the 8B-shaped batch, 137.8 against 135.4 us on
+// long contexts.)
+constexpr int kStages = 2;
 constexpr int kMaxSeqs = 1536;                    // sequences per launch (the host splits larger batches)
 
 // The softmax reference of a head is not raised before a score exceeds it by this many
@@ -63,7 +69,9 @@ constexpr int kWeightExp = 8;
 
 // GT: query heads padded to 8 or 16.
 template <int D, int GT> struct Cfg {
-    static constexpr int kTok = kInt4StageTokens(GT);         // tokens per stage
+    static constexpr int kWarps = kInt4Warps(GT);
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kTok = kInt4StageTokens;             // tokens per stage
     static constexpr int kRow = D / 2;                        // bytes of a token's codes
     static constexpr int kOffV = kTok * kRow;
     static constexpr int kOffPar = 2 * kTok * kRow;
@@ -72,10 +80,9 @@ template <int D, int GT> struct Cfg {
     // after the ring
     static constexpr int kOffBar = kRing;                             // [kWarps][kStages]
     static constexpr int kOffMisc = kOffBar + kWarps * kStages * 8;   // abort flag; warp sums of the prefix
-    static constexpr int kOffPre = kOffMisc + 64;                     // int [kMaxSeqs + 1]
+    static constexpr int kOffPre = kOffMisc + 16 + kWarps * 4;        // int [kMaxSeqs + 1]
     static constexpr int kSmem = kOffPre + (kMaxSeqs + 1) * 4;
-    static constexpr int kCtas = kInt4Ctas(GT);               // per SM: registers and shared memory
-    static_assert(kSmem <= (kCtas == 2 ? 115712 : 232448), "shared memory budget");
+    static_assert(kSmem <= 232448, "shared memory budget");
     static_assert(kSlot % 16 == 0 && kOffV % 16 == 0 && kOffPar % 16 == 0, "bulk copies start on 16 bytes");
 };
 
@@ -162,9 +169,9 @@ struct Cursor {
 };
 
 template <typename T, int D, int GT, bool kScore>
-__global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_kernel(const DecodeParams p,
-                                                                                    const Int4Work ws) {
+__global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_int4_kernel(const DecodeParams p, const Int4Work ws) {
     using C = Cfg<D, GT>;
+    constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
     constexpr int NT = GT / 8;                         // tiles of 8 heads
     constexpr int kSteps = D / 16;                     // instructions per 16 tokens, S and O alike
     constexpr int kSub = C::kTok / 16;
@@ -465,6 +472,19 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
                     }
                 }
             }
+            // ---- this lane's V words of every 16 tokens (2 lj, 2 lj + 1, 2 lj + 8, 2 lj + 9), read
+            // before the references are looked at (long contexts 127.9 -> 122.7 us)
+            uint32_t vw[kSub][4][D / 64];
+#pragma unroll
+            for (int sub = 0; sub < kSub; ++sub) {
+                const unsigned char *vr = slot + C::kOffV + (sub * 16 + 2 * lj) * C::kRow + li * (D / 16);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const unsigned char *src = vr + ((k & 1) + (k & 2) * 4) * C::kRow;
+                    if constexpr (D == 128) *reinterpret_cast<uint2 *>(vw[sub][k]) = *reinterpret_cast<const uint2 *>(src);
+                    else vw[sub][k][0] = *reinterpret_cast<const uint32_t *>(src);
+                }
+            }
             // ---- the references, raised where a score or a V scale outgrew them
             float over = -INFINITY;
 #pragma unroll
@@ -515,8 +535,7 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const float2 d = add2(make_float2(S[sub][nt][2 * r], S[sub][nt][2 * r + 1]),
-                                              nm[nt]);
+                        const float2 d = add2(make_float2(S[sub][nt][2 * r], S[sub][nt][2 * r + 1]), nm[nt]);
                         const float2 w = make_float2(fast_exp2(d.x), fast_exp2(d.y));
                         l[nt] = add2(l[nt], w);
                         z[nt].x = fmaf(w.x, vz[sub][r], z[nt].x);
@@ -524,23 +543,9 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
                         const float v = vs[sub][r] * cr;
                         wb[nt][r] = transpose8x8(pack_half2(w.x * v, w.y * v));
                     }
-                // this lane's bytes of tokens 2 lj, 2 lj + 1, 2 lj + 8, 2 lj + 9
-                const unsigned char *vr = slot + C::kOffV + (sub * 16 + 2 * lj) * C::kRow + li * (D / 16);
-                uint32_t v0[D / 64], v1[D / 64], v2[D / 64], v3[D / 64];
-                if constexpr (D == 128) {
-                    *reinterpret_cast<uint2 *>(v0) = *reinterpret_cast<const uint2 *>(vr);
-                    *reinterpret_cast<uint2 *>(v1) = *reinterpret_cast<const uint2 *>(vr + C::kRow);
-                    *reinterpret_cast<uint2 *>(v2) = *reinterpret_cast<const uint2 *>(vr + 8 * C::kRow);
-                    *reinterpret_cast<uint2 *>(v3) = *reinterpret_cast<const uint2 *>(vr + 9 * C::kRow);
-                } else {
-                    v0[0] = *reinterpret_cast<const uint32_t *>(vr);
-                    v1[0] = *reinterpret_cast<const uint32_t *>(vr + C::kRow);
-                    v2[0] = *reinterpret_cast<const uint32_t *>(vr + 8 * C::kRow);
-                    v3[0] = *reinterpret_cast<const uint32_t *>(vr + 9 * C::kRow);
-                }
                 // 16 bits (4 channels) of two tokens' bytes side by side: byte b of both in
                 // the low bytes of the halves, for the pairs of nibbles that byte holds
-                constexpr int H = D / 32;          // 16-bit pieces of a lane's bytes
+                constexpr int H = D / 32;              // 16-bit pieces of a lane's bytes
 #pragma unroll
                 for (int h = 0; h < H / 2; ++h)
 #pragma unroll
@@ -549,10 +554,10 @@ __global__ __launch_bounds__(kThreads, (Cfg<D, GT>::kCtas)) void decode_int4_ker
                         const int h2 = h + H / 2;
                         const uint32_t sel = (h & 1 ? 0x6622u : 0x4400u) + (eb ? 0x1111u : 0u);
                         const uint32_t sel2 = (h2 & 1 ? 0x6622u : 0x4400u) + (eb ? 0x1111u : 0u);
-                        const uint32_t x0 = __byte_perm(v0[h / 2], v1[h / 2], sel);
-                        const uint32_t x1 = __byte_perm(v0[h2 / 2], v1[h2 / 2], sel2);
-                        const uint32_t x2 = __byte_perm(v2[h / 2], v3[h / 2], sel);
-                        const uint32_t x3 = __byte_perm(v2[h2 / 2], v3[h2 / 2], sel2);
+                        const uint32_t x0 = __byte_perm(vw[sub][0][h / 2], vw[sub][1][h / 2], sel);
+                        const uint32_t x1 = __byte_perm(vw[sub][0][h2 / 2], vw[sub][1][h2 / 2], sel2);
+                        const uint32_t x2 = __byte_perm(vw[sub][2][h / 2], vw[sub][3][h / 2], sel);
+                        const uint32_t x3 = __byte_perm(vw[sub][2][h2 / 2], vw[sub][3][h2 / 2], sel2);
 #pragma unroll
                         for (int en = 0; en < 2; ++en) {
                             const uint32_t mask = en ? 0x00F000F0u : 0x000F000Fu;
@@ -673,8 +678,21 @@ __global__ __launch_bounds__(kJoinThreads) void decode_int4_join_kernel(const De
 #pragma unroll
     for (int u = 0; u < N; ++u) acc[u] = 0.f;
     for (int i0 = sub; i0 < info.y; i0 += 32 * WPR) {
+        const int n = min(32, (info.y - i0 + WPR - 1) / WPR);   // this warp's partials of the round
+        float x[kJoinBatch][N];
+        auto load = [&](int k0) {
+#pragma unroll
+            for (int k = 0; k < kJoinBatch; ++k) {
+                if (k0 + k < n) {
+                    const float *src = o + (int64_t)(i0 + (k0 + k) * WPR) * G * D;
+                    if constexpr (N == 4) *reinterpret_cast<float4 *>(x[k]) = *reinterpret_cast<const float4 *>(src);
+                    else *reinterpret_cast<float2 *>(x[k]) = *reinterpret_cast<const float2 *>(src);
+                }
+            }
+        };
         const int i = i0 + lane * WPR;
         const float2 mine = i < info.y ? ml[(int64_t)i * G] : make_float2(-INFINITY, 0.f);
+        load(0);                                       // in flight with the pairs
         float mb = mine.x;
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, k));
@@ -690,17 +708,8 @@ __global__ __launch_bounds__(kJoinThreads) void decode_int4_join_kernel(const De
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) lc += __shfl_xor_sync(0xffffffffu, lc, k);
         l += lc;
-        const int n = min(32, (info.y - i0 + WPR - 1) / WPR);
         for (int k0 = 0; k0 < n; k0 += kJoinBatch) {
-            float x[kJoinBatch][N];
-#pragma unroll
-            for (int k = 0; k < kJoinBatch; ++k) {
-                if (k0 + k < n) {
-                    const float *src = o + (int64_t)(i0 + (k0 + k) * WPR) * G * D;
-                    if constexpr (N == 4) *reinterpret_cast<float4 *>(x[k]) = *reinterpret_cast<const float4 *>(src);
-                    else *reinterpret_cast<float2 *>(x[k]) = *reinterpret_cast<const float2 *>(src);
-                }
-            }
+            if (k0 > 0) load(k0);
 #pragma unroll
             for (int k = 0; k < kJoinBatch; ++k) {
                 if (k0 + k < n) {
@@ -754,11 +763,11 @@ int launch_t(const DecodeParams &p, const Int4Work &ws, int grid, cudaStream_t s
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return -1;
         attr_set[dev] = true;
     }
-    const int rc = launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), C::kSmem, stream, p, ws);
+    const int rc = launch_pdl(kern, dim3((unsigned)grid), dim3(C::kThreads), C::kSmem, stream, p, ws);
     if (rc != 0) return rc;
     // partials a row, about: (runs + rows) / rows
     const int64_t heads = (int64_t)p.num_seqs * p.num_heads, rows = (int64_t)p.num_seqs * p.num_kv_heads;
-    if ((int64_t)grid * kWarps <= 8 * rows)
+    if ((int64_t)grid * C::kWarps <= 8 * rows)
         return launch_pdl(decode_int4_join_kernel<T, D, kScore, 1>, dim3((unsigned)((heads + 3) / 4)),
                           dim3(kJoinThreads), 0, stream, p, ws);
     return launch_pdl(decode_int4_join_kernel<T, D, kScore, 4>, dim3((unsigned)heads), dim3(kJoinThreads), 0, stream, p,
@@ -775,21 +784,17 @@ template <typename T> int launch_d(const DecodeParams &p, const Int4Work &ws, in
     return p.head_dim == 128 ? launch_g<T, 128>(p, ws, grid, stream) : launch_g<T, 64>(p, ws, grid, stream);
 }
 
-int64_t row_stages(int64_t max_ctx, int group) {
-    const int gt = group <= 8 ? 8 : 16;
-    return (max_ctx + kInt4StageTokens(gt) - 1) / kInt4StageTokens(gt);
-}
+int64_t row_stages(int64_t max_ctx) { return (max_ctx + kInt4StageTokens - 1) / kInt4StageTokens; }
 
 // Sequences per launch: what the kernel's prefix holds, and a launch's stages in 31 bits.
-int64_t seqs_per_launch(int64_t max_ctx, int64_t kv_heads, int group) {
-    const int64_t ns = row_stages(max_ctx, group) * kv_heads;
+int64_t seqs_per_launch(int64_t max_ctx, int64_t kv_heads) {
+    const int64_t ns = row_stages(max_ctx) * kv_heads;
     return std::max<int64_t>(1, std::min<int64_t>(kMaxSeqs, INT32_MAX / std::max<int64_t>(ns, 1)));
 }
 
-int launch_grid(int64_t seqs, int64_t kv_heads, int64_t max_ctx, int group, int sms) {
-    const int64_t slots = (int64_t)kInt4Ctas(group <= 8 ? 8 : 16) * sms;
-    const int64_t most = seqs * kv_heads * row_stages(max_ctx, group);
-    return (int)std::max<int64_t>(1, std::min(slots, most));
+// One CTA per SM, and no more than there can be stages.
+int launch_grid(int64_t seqs, int64_t kv_heads, int64_t max_ctx, int sms) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>(sms, seqs * kv_heads * row_stages(max_ctx)));
 }
 
 }  // namespace
@@ -804,9 +809,9 @@ bool decode_int4_supported(const DecodeParams &p, int dtype) {
 Int4WorkSizes decode_int4_work_sizes(int64_t num_seqs, int64_t num_heads, int64_t num_kv_heads, int64_t head_dim,
                                      int64_t max_ctx, int sms) {
     const int group = (int)(num_heads / num_kv_heads);
-    const int64_t seqs = std::min(num_seqs, seqs_per_launch(max_ctx, num_kv_heads, group));
+    const int64_t seqs = std::min(num_seqs, seqs_per_launch(max_ctx, num_kv_heads));
     const int64_t rows = seqs * num_kv_heads;
-    const int64_t parts = (int64_t)launch_grid(seqs, num_kv_heads, max_ctx, group, sms) * kWarps + rows;
+    const int64_t parts = (int64_t)launch_grid(seqs, num_kv_heads, max_ctx, sms) * kInt4Warps(group <= 8 ? 8 : 16) + rows;
     Int4WorkSizes s;
     s.rows = (size_t)(rows * 8);
     s.part_ml = (size_t)(parts * group * 8);
@@ -816,8 +821,8 @@ Int4WorkSizes decode_int4_work_sizes(int64_t num_seqs, int64_t num_heads, int64_
 
 int launch_decode_int4(const DecodeParams &p, const Int4Work &ws, int64_t max_ctx, int sms, int dtype,
                        cudaStream_t stream) {
-    if (!decode_int4_supported(p, dtype) || row_stages(max_ctx, p.group) * p.num_kv_heads > INT32_MAX) return -2;
-    const int chunk = (int)std::min<int64_t>(p.num_seqs, seqs_per_launch(max_ctx, p.num_kv_heads, p.group));
+    if (!decode_int4_supported(p, dtype) || row_stages(max_ctx) * p.num_kv_heads > INT32_MAX) return -2;
+    const int chunk = (int)std::min<int64_t>(p.num_seqs, seqs_per_launch(max_ctx, p.num_kv_heads));
     for (int b0 = 0; b0 < p.num_seqs; b0 += chunk) {
         DecodeParams c = p;
         const int64_t rows = (int64_t)b0 * p.num_heads;
@@ -830,7 +835,7 @@ int launch_decode_int4(const DecodeParams &p, const Int4Work &ws, int64_t max_ct
             c.ws_logits = p.ws_logits + rows * p.logits_len;
             c.ws_score_ml = p.ws_score_ml + rows * 2;
         }
-        const int grid = launch_grid(c.num_seqs, c.num_kv_heads, max_ctx, c.group, sms);
+        const int grid = launch_grid(c.num_seqs, c.num_kv_heads, max_ctx, sms);
         const int rc = dtype == PA_DTYPE_BF16 ? launch_d<__nv_bfloat16>(c, ws, grid, stream)
                                               : launch_d<__half>(c, ws, grid, stream);
         if (rc != 0) return rc;

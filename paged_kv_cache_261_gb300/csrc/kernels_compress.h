@@ -29,9 +29,10 @@ int launch_kv_read_int4(void *k, void *v, int dst_dtype, const int32_t *slot_map
 int launch_copy_params_int4(void *params, const int32_t *pairs, int64_t num_pairs, int64_t num_blocks,
                             int64_t block_bytes, unsigned int *err, cudaStream_t stream);
 
-// Tokens per stage and CTAs per SM of the 4-bit decode, by the padded group (8 or 16).
-__host__ __device__ constexpr int kInt4StageTokens(int gt) { return gt == 8 ? 32 : 64; }
-__host__ __device__ constexpr int kInt4Ctas(int gt) { return gt == 8 ? 2 : 1; }
+// Tokens per stage of the 4-bit decode, and warps of its CTAs (one per SM) by the padded
+// group, 8 or 16: as many as the registers allow.
+constexpr int kInt4StageTokens = 64;
+__host__ __device__ constexpr int kInt4Warps(int gt) { return gt == 8 ? 12 : 8; }
 
 // Workspace of the 4-bit decode's partials.
 struct Int4Work {
