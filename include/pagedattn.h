@@ -535,7 +535,8 @@ int pa_paged_attention_decode_scored(void *out, const void *q, float *mass, int6
  * block that moved rows land in must not be read by another sequence (copy-on-write, or
  * other out blocks, guarantee it). kept: int32 [num_seqs, num_kv_heads, kept_len].
  * dtype: PA_DTYPE_F32, _F16, _BF16 or _E4M3 (caches [num_blocks, block_size,
- * num_kv_heads, head_dim], kv_params unused; rows a multiple of 16 bytes) or PA_DTYPE_INT4.
+ * num_kv_heads, head_dim], kv_params unused; rows a multiple of 16 bytes, at most 16 KiB) or
+ * PA_DTYPE_INT4.
  * A length outside its range sets PA_DEVERR_CONTEXT and is cut; a bad block id sets
  * PA_DEVERR_BLOCK_ID and its row is not moved.
  */

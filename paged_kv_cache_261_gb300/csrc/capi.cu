@@ -923,7 +923,7 @@ int pa_paged_kv_evict(int32_t *kept, int64_t kept_len, const float *mass, int64_
     if (!pow2(block_size) || block_size > 256 || num_seqs > 65535 || num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
     if (int4 && ((head_dim != 64 && head_dim != 128) || block_size < 8)) return PA_ERR_UNSUPPORTED;
     const int64_t row = int4 ? head_dim / 2 : (int64_t)head_dim * es;
-    if (row % 16 != 0 || row > 1 << 20) return PA_ERR_UNSUPPORTED;
+    if (row % 16 != 0 || row > 1 << 14) return PA_ERR_UNSUPPORTED;     // one CTA moves 16 KiB at a time
     if (num_seqs == 0) return PA_OK;
     if (!kept || !mass || !mass_out || !key_cache || !value_cache || !block_tables || !out_block_tables ||
         !context_lens || !keep_lens || (int4 && !kv_params))
@@ -967,7 +967,7 @@ int pa_paged_kv_evict(int32_t *kept, int64_t kept_len, const float *mass, int64_
         pl.token_stride = int4 ? bytes : bytes * num_kv_heads;
         pl.head_stride = int4 ? bytes * block_size : bytes;
     }
-    return pa::launch_evict(p, static_cast<cudaStream_t>(stream)) == 0 ? PA_OK : PA_ERR_CUDA;
+    return pa::launch_evict(p, device_sm_count(), static_cast<cudaStream_t>(stream)) == 0 ? PA_OK : PA_ERR_CUDA;
 }
 
 int pa_check_bounded_wait(int64_t limit_ns, int64_t *report, void *stream) {

@@ -5,24 +5,33 @@
 // the largest mass (equal masses: the lower index first; a NaN counts below every
 // number). The staying tokens keep their order; token kept[i] becomes token i.
 //
-// Selection (evict_select_kernel, one CTA per (sequence, kv head)): masses become
-// unsigned keys of the same order, a radix descent over the key's digits finds the
-// (n - r)-th largest key and how many of the tokens equal to it stay, and one ordered
-// pass writes the indices and the masses. Counts and prefix sums are whole numbers, so
-// the result does not depend on timing.
+// Selection (evict_select_kernel, a cluster of CTAs per (sequence, kv head)): the row's
+// masses are read once, each CTA keeping a slice in shared memory. As unsigned keys of the
+// same order, a radix descent over three digits finds the (n - r)-th largest key and how
+// many of the tokens equal to it stay: each CTA counts its slice's digits, and every CTA
+// adds the counts of the cluster. Then each warp writes the indices and masses that stay
+// of its part of the slice, behind those that the parts before it keep. Counts are whole
+// numbers, so the result does not depend on timing, and every mass has been read before
+// the first is written, so mass_out may be mass.
 //
-// Movement (evict_move_kernel): a CTA moves one slice of one plane's rows of one
-// (sequence, kv head), tile after tile in increasing order, each tile read into
-// registers by the whole CTA before any of it is written. Since kept[i] >= i and both
-// rise, a tile's writes land on rows that no later tile reads, also when the
-// out table names the sequence's own blocks (eviction in place).
+// Rows too long for the shared memory of a cluster take evict_select_long_kernel: one CTA,
+// the masses read again for every digit, written in one ordered pass.
+//
+// Movement (evict_move_kernel, a cluster of CTAs per (sequence, kv head, plane)): the rows
+// move in waves, each read into registers by the whole cluster before any of it is
+// written. Since kept[i] >= i and both rise, a wave's writes land on rows that no later
+// wave reads, also when the out table names the sequence's own blocks (eviction in place).
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "kernels_compress.h"
 
 namespace pa {
 namespace {
 
-constexpr int kSelThreads = 1024;
+namespace cg = cooperative_groups;
+
+constexpr int kSelThreads = 1024;       // of the kernel for long rows
 constexpr int kDigitBits = 11;
 constexpr int kBins = 1 << kDigitBits;
 
@@ -34,7 +43,7 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
 }
 
 // Exclusive prefix of v over the CTA's threads, in thread order; *total: the sum.
-__device__ __forceinline__ int block_prefix(int v, int *warp_sums, int *total) {
+template <int kThreads> __device__ __forceinline__ int block_prefix(int v, int *warp_sums, int *total) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int inc = v;
 #pragma unroll
@@ -44,7 +53,7 @@ __device__ __forceinline__ int block_prefix(int v, int *warp_sums, int *total) {
     }
     if (lane == 31) warp_sums[warp] = inc;
     __syncthreads();
-    int w = lane < kSelThreads / 32 ? warp_sums[lane] : 0;
+    int w = lane < kThreads / 32 ? warp_sums[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, w, o);
@@ -75,7 +84,7 @@ __device__ __forceinline__ EvictSplit evict_split(const EvictParams &p, int b, b
     return s;
 }
 
-__global__ __launch_bounds__(kSelThreads) void evict_select_kernel(const EvictParams p) {
+__global__ __launch_bounds__(kSelThreads) void evict_select_long_kernel(const EvictParams p) {
     __shared__ int hist[kBins];
     __shared__ int warp_sums[32];
     __shared__ uint32_t found[2];       // the digit of the threshold, and how many keys lie above it
@@ -104,7 +113,7 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(const EvictPa
             const int top = (1 << bits) - 1, i0 = top - 2 * tid;
             const int h0 = i0 >= 0 ? hist[i0] : 0, h1 = i0 >= 1 ? hist[i0 - 1] : 0;
             int total;
-            const int above = block_prefix(h0 + h1, warp_sums, &total);
+            const int above = block_prefix<kSelThreads>(h0 + h1, warp_sums, &total);
             if (above < want && above + h0 >= want) {
                 found[0] = (uint32_t)i0;
                 found[1] = (uint32_t)above;
@@ -130,10 +139,10 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(const EvictPa
             const uint32_t k = mass_key(x);
             const int eq = t < cand && !all && k == key;
             int total;
-            const int eq_before = block_prefix(eq, warp_sums, &total) + ties;
+            const int eq_before = block_prefix<kSelThreads>(eq, warp_sums, &total) + ties;
             ties += total;
             const int stay = t < cand && (all || k > key || (eq && eq_before < want));
-            const int at = base + block_prefix(stay, warp_sums, &total);
+            const int at = base + block_prefix<kSelThreads>(stay, warp_sums, &total);
             base += total;
             if (stay) {
                 kept[at] = t;
@@ -155,28 +164,185 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(const EvictPa
     for (int64_t i = s.n + tid; i < p.mass_out_len; i += kSelThreads) mass_out[i] = 0.f;
 }
 
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxSlice = 48 * 1024;    // masses per CTA: 192 KB of shared memory
+
+__global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictParams p) {
+    extern __shared__ float slice[];    // this CTA's masses
+    __shared__ int hist[kBins];
+    __shared__ int warp_sums[32];
+    __shared__ int found[2];            // the digit of the threshold, and how many keys lie above it
+    __shared__ int counts[2];           // of this CTA's slice: keys above the threshold, keys equal to it
+    __shared__ int seg_gt[kWarps], seg_eq[kWarps];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.x / nc, b = blockIdx.y;
+    const EvictSplit s = evict_split(p, b, tid == 0 && blockIdx.x == 0);
+    const int64_t row = (int64_t)b * p.num_kv_heads + h;
+    const float *mass = p.mass + row * p.mass_len;
+    float *mass_out = p.mass_out + row * p.mass_out_len;
+    int32_t *kept = p.kept + row * p.kept_len;
+    const int cand = s.c - s.r;         // tokens that compete
+    int want = s.n - s.r;               // how many of them stay
+    const bool all = want >= cand, none = want <= 0;
+
+    // this CTA's tokens [t0, t0 + len), and this warp's part of them
+    const int per = (((s.c + nc - 1) / nc) + 3) & ~3;
+    const int t0 = min(s.c, rank * per), len = min(s.c, t0 + per) - t0;
+    {
+        constexpr int kUnroll = 8;
+        for (int i0 = 0; i0 < len; i0 += kThreads * kUnroll) {
+            float v[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int i = i0 + u * kThreads + tid;
+                v[u] = i < len ? mass[t0 + i] : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int i = i0 + u * kThreads + tid;
+                if (i < len) slice[i] = v[u];
+            }
+        }
+    }
+    uint32_t key = 0, mask = 0;         // the digits found so far
+    if (!all && !none) {
+        const int n_cand = max(0, min(len, cand - t0));
+        for (int shift = 32 - kDigitBits;; shift = shift > kDigitBits ? shift - kDigitBits : 0) {
+            const int bits = mask == 0 ? kDigitBits : min(kDigitBits, 32 - __popc(mask));
+            const uint32_t dmask = ((1u << bits) - 1u) << shift;
+            for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+            __syncthreads();
+            for (int i = tid; i < n_cand; i += kThreads) {
+                const uint32_t k = mass_key(slice[i]);
+                if ((k & mask) == key) atomicAdd(&hist[(k & dmask) >> shift], 1);
+            }
+            cluster.sync();
+            // thread i takes the bins counted from the top, 4 i to 4 i + 3, of the whole cluster
+            static_assert(kBins == 4 * kThreads, "four bins a thread");
+            const int top = (1 << bits) - 1, i0 = top - 4 * tid;
+            int hb[4] = {0, 0, 0, 0};
+            if (i0 >= 3) {
+                for (int c = 0; c < nc; ++c) {
+                    const int4 v = *reinterpret_cast<const int4 *>(cluster.map_shared_rank(hist, c) + i0 - 3);
+                    hb[0] += v.w;
+                    hb[1] += v.z;
+                    hb[2] += v.y;
+                    hb[3] += v.x;
+                }
+            }
+            int total;
+            int above = block_prefix<kThreads>(hb[0] + hb[1] + hb[2] + hb[3], warp_sums, &total);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (above < want && above + hb[j] >= want) {
+                    found[0] = i0 - j;
+                    found[1] = above;
+                }
+                above += hb[j];
+            }
+            cluster.sync();             // the counts have been read, `found` is there
+            key |= (uint32_t)found[0] << shift;
+            mask |= dmask;
+            want -= found[1];
+            if (shift == 0) break;
+        }
+    }
+    __syncthreads();
+    // ---- what stays: the recent tokens, keys above `key`, and the first `want` equal to it.
+    // Warp w has the tokens [w0, w1) of the slice.
+    const int wlen = (((len + kWarps - 1) / kWarps) + 31) & ~31;
+    const int w0 = min(len, warp * wlen), w1 = min(len, w0 + wlen);
+    int gt = 0, eq = 0;                 // of this warp's tokens: stay anyway; equal to the threshold
+    for (int i = w0 + lane; i < w1; i += 32) {
+        const uint32_t k = mass_key(slice[i]);
+        const bool sure = t0 + i >= cand || all || (!none && k > key);
+        gt += sure;
+        eq += !sure && !none && k == key;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        gt += __shfl_xor_sync(0xffffffffu, gt, o);
+        eq += __shfl_xor_sync(0xffffffffu, eq, o);
+    }
+    if (lane == 0) {
+        seg_gt[warp] = gt;
+        seg_eq[warp] = eq;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        int g = 0, e = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            g += seg_gt[w];
+            e += seg_eq[w];
+        }
+        counts[0] = g;
+        counts[1] = e;
+    }
+    cluster.sync();                     // every mass of the row has been read, too
+    int before_gt = 0, before_eq = 0;   // in the tokens before this warp's
+    for (int c = 0; c < rank; ++c) {
+        const int *o = cluster.map_shared_rank(counts, c);
+        before_gt += o[0];
+        before_eq += o[1];
+    }
+    for (int w = 0; w < warp; ++w) {
+        before_gt += seg_gt[w];
+        before_eq += seg_eq[w];
+    }
+    const uint32_t below = (1u << lane) - 1u;
+    for (int i0 = w0; i0 < w1; i0 += 32) {
+        const int i = i0 + lane;
+        const float x = i < w1 ? slice[i] : 0.f;
+        const uint32_t k = mass_key(x);
+        const bool sure = i < w1 && (t0 + i >= cand || all || (!none && k > key));
+        const bool tie = i < w1 && !sure && !none && k == key;
+        const uint32_t ms = __ballot_sync(0xffffffffu, sure), mt = __ballot_sync(0xffffffffu, tie);
+        const int eq_rank = before_eq + __popc(mt & below);
+        const bool stays = sure || (tie && eq_rank < want);
+        // position: the sure ones before, and the ties before, of which at most `want` stay
+        if (stays) {
+            const int at = before_gt + __popc(ms & below) + min(eq_rank, want);
+            kept[at] = t0 + i;
+            mass_out[at] = x;
+        }
+        before_gt += __popc(ms);
+        before_eq += __popc(mt);
+    }
+    for (int64_t i = s.n + rank * kThreads + tid; i < p.kept_len; i += nc * kThreads) kept[i] = -1;
+    for (int64_t i = s.n + rank * kThreads + tid; i < p.mass_out_len; i += nc * kThreads) mass_out[i] = 0.f;
+    cluster.sync();                     // the counts are read by other CTAs until here
+}
+
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;
 
 // VecT: 16 bytes (code and channel rows) or 8 (parameter rows).
 template <typename VecT>
 __device__ __forceinline__ void move_rows(const EvictParams &p, const EvictPlane &pl, const EvictSplit &s, int b,
-                                          int h, const int32_t *kept) {
-    const int vecs = pl.row_bytes / (int)sizeof(VecT);           // vectors per row
+                                          int h, const int32_t *kept, int rank, int nc) {
+    cg::cluster_group cluster = cg::this_cluster();
+    const uint32_t vecs = pl.row_bytes / (int)sizeof(VecT);      // vectors per row
     const int32_t *src_table = p.block_tables + (int64_t)b * p.max_blocks;
     const int32_t *dst_table = p.out_block_tables + (int64_t)b * p.out_max_blocks;
     const int bs_mask = (1 << p.log2_block_size) - 1;
     char *base = pl.base + h * pl.head_stride;
-    const int64_t total = (int64_t)s.n * vecs;
-    for (int64_t i0 = 0; i0 < total; i0 += kMoveThreads * kMoveUnroll) {
+    // a wave: every thread of the cluster moves kMoveUnroll vectors
+    const uint32_t rows_cta = kMoveThreads * kMoveUnroll / vecs; // whole rows per CTA and wave
+    const uint32_t used = rows_cta * vecs;                       // vectors of them
+    for (int64_t r0 = 0; r0 < s.n; r0 += (int64_t)rows_cta * nc) {
         VecT v[kMoveUnroll];
         VecT *dst[kMoveUnroll];
 #pragma unroll
         for (int u = 0; u < kMoveUnroll; ++u) {
-            const int64_t i = i0 + u * kMoveThreads + threadIdx.x;
+            const uint32_t i = u * kMoveThreads + threadIdx.x;
+            const uint32_t r = i / vecs, c = i - r * vecs;
+            const int64_t to = r0 + (int64_t)rank * rows_cta + r;
             dst[u] = nullptr;
-            if (i >= total) continue;
-            const int to = (int)(i / vecs), c = (int)(i - (int64_t)to * vecs);
+            if (i >= used || to >= s.n) continue;
             const int from = kept[to];
             const int32_t sb = src_table[from >> p.log2_block_size], db = dst_table[to >> p.log2_block_size];
             if (sb < 0 || sb >= p.num_blocks || db < 0 || db >= p.num_blocks) {
@@ -189,7 +355,8 @@ __device__ __forceinline__ void move_rows(const EvictParams &p, const EvictPlane
             if (dst[u] == src) dst[u] = nullptr;                 // stays where it is
             else v[u] = *src;
         }
-        __syncthreads();                                         // the whole tile has been read
+        if (nc > 1) cluster.sync();                              // the whole wave has been read
+        else __syncthreads();
 #pragma unroll
         for (int u = 0; u < kMoveUnroll; ++u)
             if (dst[u]) *dst[u] = v[u];
@@ -197,22 +364,69 @@ __device__ __forceinline__ void move_rows(const EvictParams &p, const EvictPlane
 }
 
 __global__ __launch_bounds__(kMoveThreads) void evict_move_kernel(const EvictParams p) {
-    const int h = blockIdx.x, b = blockIdx.y;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int h = blockIdx.x / nc, b = blockIdx.y;
     const EvictPlane &pl = p.planes[blockIdx.z];
     const EvictSplit s = evict_split(p, b, false);
     const int32_t *kept = p.kept + ((int64_t)b * p.num_kv_heads + h) * p.kept_len;
-    if (pl.row_bytes % 16 == 0) move_rows<uint4>(p, pl, s, b, h, kept);
-    else move_rows<uint2>(p, pl, s, b, h, kept);
+    if (pl.row_bytes % 16 == 0) move_rows<uint4>(p, pl, s, b, h, kept, rank, nc);
+    else move_rows<uint2>(p, pl, s, b, h, kept, rank, nc);
+}
+
+template <typename Kern>
+int launch_cluster(Kern kern, int heads, int seqs, int z, int cluster, int threads, size_t smem, cudaStream_t stream,
+                   const EvictParams &p) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(heads * cluster), (unsigned)seqs, (unsigned)z);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? 0 : -1;
+}
+
+// CTAs per cluster: enough that the launch fills the SMs twice, at most 8.
+int cluster_for(int64_t units, int sms) {
+    int c = 1;
+    while (c < kMaxCluster && units * c < 2 * (int64_t)sms) c *= 2;
+    return c;
 }
 
 }  // namespace
 
-int launch_evict(const EvictParams &p, cudaStream_t stream) {
-    evict_select_kernel<<<dim3((unsigned)p.num_kv_heads, (unsigned)p.num_seqs), kSelThreads, 0, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return -1;
-    evict_move_kernel<<<dim3((unsigned)p.num_kv_heads, (unsigned)p.num_seqs, (unsigned)p.num_planes), kMoveThreads, 0,
-                        stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+int launch_evict(const EvictParams &p, int sms, cudaStream_t stream) {
+    static bool attr_set[kMaxDevices] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
+    if (!attr_set[dev]) {
+        if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSlice * 4) !=
+            cudaSuccess)
+            return -1;
+        attr_set[dev] = true;
+    }
+    const int64_t rows = (int64_t)p.num_seqs * p.num_kv_heads;
+    // the selection's clusters also grow with the row: at most 8192 masses a CTA where that is possible
+    int c = cluster_for(rows, sms);
+    while (c < kMaxCluster && (int64_t)c * 8192 < p.context_limit) c *= 2;
+    const int64_t slice = ((p.context_limit + c - 1) / c + 3) & ~int64_t(3);
+    int rc = 0;
+    if (slice <= kMaxSlice) {
+        rc = launch_cluster(evict_select_kernel, p.num_kv_heads, p.num_seqs, 1, c, kThreads, (size_t)slice * 4, stream,
+                            p);
+    } else {
+        evict_select_long_kernel<<<dim3((unsigned)p.num_kv_heads, (unsigned)p.num_seqs), kSelThreads, 0, stream>>>(p);
+        rc = cudaGetLastError() == cudaSuccess ? 0 : -1;
+    }
+    if (rc != 0) return rc;
+    return launch_cluster(evict_move_kernel, p.num_kv_heads, p.num_seqs, p.num_planes,
+                          cluster_for(rows * p.num_planes, 2 * sms), kMoveThreads, 0, stream, p);
 }
 
 }  // namespace pa

@@ -86,6 +86,6 @@ struct EvictParams {
     int num_planes;
     EvictPlane planes[3];
 };
-int launch_evict(const EvictParams &p, cudaStream_t stream);
+int launch_evict(const EvictParams &p, int sms, cudaStream_t stream);
 
 }  // namespace pa

@@ -95,7 +95,7 @@ def _evict(pa, **kw):
 @pytest.mark.parametrize("bad,code", [
     (dict(recent=-1), INVALID), (dict(kl=0), INVALID), (dict(ml=0), INVALID), (dict(mol=0), INVALID),
     (dict(mb=0), INVALID), (dict(omb=0), INVALID), (dict(dt=5), INVALID), (dict(dt=-1), INVALID),
-    (dict(D=100), UNSUPPORTED), (dict(bs=12), UNSUPPORTED), (dict(bs=512), UNSUPPORTED), (dict(B=70000), UNSUPPORTED),
+    (dict(D=100), UNSUPPORTED), (dict(D=8200), UNSUPPORTED), (dict(bs=12), UNSUPPORTED), (dict(bs=512), UNSUPPORTED), (dict(B=70000), UNSUPPORTED),
     (dict(kept=None), INVALID), (dict(mass=None), INVALID), (dict(mo=None), INVALID), (dict(obt=None), INVALID),
     (dict(kp=None), INVALID), (dict(kc=8), INVALID), (dict(mass=2), INVALID), (dict(kept=2), INVALID),
     (dict(dt=4), INVALID), (dict(dt=4, par=8), INVALID), (dict(dt=4, par=16, D=96), UNSUPPORTED),

@@ -156,6 +156,21 @@ def test_evict_long(pa, keep, recent):
     run_case(pa, 30, [40000, 12345], [keep, keep], recent, 2, 64, 64, "bf16", kind="ties", in_place=True)
 
 
+def test_evict_rows_beyond_a_cluster(pa):
+    """A row too long for the selection's shared memory, next to a short one."""
+    run_case(pa, 37, [430000, 700], [300, 400], 50, 1, 64, 256, "int4", extra=0)
+    run_case(pa, 38, [430000, 700], [429000, 400], 50, 1, 64, 256, "int4", kind="ties", in_place=True, extra=0)
+
+
+@pytest.mark.parametrize("B", [1, 20, 90])
+def test_evict_batch_sizes(pa, B):
+    """From whole clusters for a row to one CTA."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(1, 700, B)
+    keep = np.minimum(rng.integers(0, 600, B), lens)
+    run_case(pa, 39 + B, lens, keep, 11, 2, 128, 16, "bf16", kind="special", in_place=B == 20)
+
+
 def test_evict_own_blocks_named_by_a_shorter_table(pa):
     """Eviction in place through another tensor that names the first blocks of each sequence."""
     rng = np.random.default_rng(33)
