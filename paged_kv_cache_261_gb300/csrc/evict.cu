@@ -168,10 +168,14 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSlice = 48 * 1024;    // masses per CTA: 192 KB of shared memory
+// Accumulated weights crowd into a few exponents, so a digit's counts are kept 16 times over,
+// one a lane and the lane 16 further: no two lanes of a half-warp add to the same word.
+constexpr int kDigits = 256, kCopies = 16;
 
 __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictParams p) {
     extern __shared__ float slice[];    // this CTA's masses
-    __shared__ int hist[kBins];
+    __shared__ __align__(16) int hist[kDigits * kCopies];
+    __shared__ int totals[2][kDigits];  // of this CTA, by digit parity
     __shared__ int warp_sums[32];
     __shared__ int found[2];            // the digit of the threshold, and how many keys lie above it
     __shared__ int counts[2];           // of this CTA's slice: keys above the threshold, keys equal to it
@@ -211,44 +215,43 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictParam
     uint32_t key = 0, mask = 0;         // the digits found so far
     if (!all && !none) {
         const int n_cand = max(0, min(len, cand - t0));
-        for (int shift = 32 - kDigitBits;; shift = shift > kDigitBits ? shift - kDigitBits : 0) {
-            const int bits = mask == 0 ? kDigitBits : min(kDigitBits, 32 - __popc(mask));
-            const uint32_t dmask = ((1u << bits) - 1u) << shift;
-            for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
-            __syncthreads();
+        for (int i = tid; i < kDigits * kCopies / 4; i += kThreads)
+            reinterpret_cast<int4 *>(hist)[i] = make_int4(0, 0, 0, 0);
+        __syncthreads();
+        for (int shift = 24; shift >= 0; shift -= 8) {
             for (int i = tid; i < n_cand; i += kThreads) {
                 const uint32_t k = mass_key(slice[i]);
-                if ((k & mask) == key) atomicAdd(&hist[(k & dmask) >> shift], 1);
+                if ((k & mask) == key) atomicAdd(&hist[((k >> shift) & 255u) * kCopies + (lane & (kCopies - 1))], 1);
+            }
+            __syncthreads();
+            int *sum = totals[(shift >> 3) & 1];
+            {                           // two threads a digit add its copies, and clear them
+                static_assert(kThreads == 2 * kDigits && kCopies == 16, "half a digit's copies a thread");
+                int4 *mine = reinterpret_cast<int4 *>(hist) + 2 * tid;
+                const int4 x = mine[0], y = mine[1];
+                mine[0] = mine[1] = make_int4(0, 0, 0, 0);
+                int t = x.x + x.y + x.z + x.w + y.x + y.y + y.z + y.w;
+                t += __shfl_xor_sync(0xffffffffu, t, 1);
+                if ((tid & 1) == 0) sum[tid >> 1] = t;
             }
             cluster.sync();
-            // thread i takes the bins counted from the top, 4 i to 4 i + 3, of the whole cluster
-            static_assert(kBins == 4 * kThreads, "four bins a thread");
-            const int top = (1 << bits) - 1, i0 = top - 4 * tid;
-            int hb[4] = {0, 0, 0, 0};
-            if (i0 >= 3) {
-                for (int c = 0; c < nc; ++c) {
-                    const int4 v = *reinterpret_cast<const int4 *>(cluster.map_shared_rank(hist, c) + i0 - 3);
-                    hb[0] += v.w;
-                    hb[1] += v.z;
-                    hb[2] += v.y;
-                    hb[3] += v.x;
-                }
+            // thread i < 256: digit 255 - i of the whole cluster, so counted from the top
+            int n = 0;
+            if (tid < kDigits) {
+#pragma unroll
+                for (int c = 0; c < kMaxCluster; ++c)
+                    if (c < nc) n += cluster.map_shared_rank(sum, c)[kDigits - 1 - tid];
             }
             int total;
-            int above = block_prefix<kThreads>(hb[0] + hb[1] + hb[2] + hb[3], warp_sums, &total);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (above < want && above + hb[j] >= want) {
-                    found[0] = i0 - j;
-                    found[1] = above;
-                }
-                above += hb[j];
+            const int above = block_prefix<kThreads>(n, warp_sums, &total);
+            if (above < want && above + n >= want) {
+                found[0] = kDigits - 1 - tid;
+                found[1] = above;
             }
-            cluster.sync();             // the counts have been read, `found` is there
+            __syncthreads();
             key |= (uint32_t)found[0] << shift;
-            mask |= dmask;
+            mask |= 255u << shift;
             want -= found[1];
-            if (shift == 0) break;
         }
     }
     __syncthreads();
@@ -330,31 +333,52 @@ __device__ __forceinline__ void move_rows(const EvictParams &p, const EvictPlane
     const int32_t *dst_table = p.out_block_tables + (int64_t)b * p.out_max_blocks;
     const int bs_mask = (1 << p.log2_block_size) - 1;
     char *base = pl.base + h * pl.head_stride;
-    // a wave: every thread of the cluster moves kMoveUnroll vectors
-    const uint32_t rows_cta = kMoveThreads * kMoveUnroll / vecs; // whole rows per CTA and wave
-    const uint32_t used = rows_cta * vecs;                       // vectors of them
-    for (int64_t r0 = 0; r0 < s.n; r0 += (int64_t)rows_cta * nc) {
+    // A wave: up to 256 whole rows a CTA, kMoveUnroll vectors a thread. While a wave's rows are
+    // read, the next one's places are looked up, one row a thread, into shared memory.
+    const uint32_t rows_cta = min((uint32_t)kMoveThreads, kMoveThreads * kMoveUnroll / vecs);
+    const uint32_t used = rows_cta * vecs;
+    const int64_t step = (int64_t)rows_cta * nc;
+    __shared__ longlong2 place[2][kMoveThreads];                 // source and destination in bytes, or -1
+    auto index = [&](int64_t r0) -> int {                        // this thread's row of the wave: its source token
+        const int64_t to = r0 + (int64_t)rank * rows_cta + threadIdx.x;
+        return threadIdx.x < rows_cta && to < s.n ? kept[to] : -1;
+    };
+    auto look_up = [&](int64_t r0, int from, int buf) {
+        longlong2 at = make_longlong2(-1, -1);
+        if (from >= 0) {
+            const int to = (int)(r0 + (int64_t)rank * rows_cta + threadIdx.x);
+            const int32_t sb = src_table[from >> p.log2_block_size], db = dst_table[to >> p.log2_block_size];
+            if (sb < 0 || sb >= p.num_blocks || db < 0 || db >= p.num_blocks) {
+                raise_error(p.err, PA_DEVERR_BLOCK_ID);
+            } else {
+                at.x = sb * pl.block_stride + (from & bs_mask) * pl.token_stride;
+                at.y = db * pl.block_stride + (to & bs_mask) * pl.token_stride;
+                if (at.x == at.y) at.y = -1;                     // stays where it is
+            }
+        }
+        place[buf][threadIdx.x] = at;
+    };
+    int from = index(0);
+    look_up(0, from, 0);
+    from = index(step);
+    __syncthreads();
+    int buf = 0;
+    for (int64_t r0 = 0; r0 < s.n; r0 += step, buf ^= 1) {
         VecT v[kMoveUnroll];
         VecT *dst[kMoveUnroll];
 #pragma unroll
         for (int u = 0; u < kMoveUnroll; ++u) {
             const uint32_t i = u * kMoveThreads + threadIdx.x;
             const uint32_t r = i / vecs, c = i - r * vecs;
-            const int64_t to = r0 + (int64_t)rank * rows_cta + r;
             dst[u] = nullptr;
-            if (i >= used || to >= s.n) continue;
-            const int from = kept[to];
-            const int32_t sb = src_table[from >> p.log2_block_size], db = dst_table[to >> p.log2_block_size];
-            if (sb < 0 || sb >= p.num_blocks || db < 0 || db >= p.num_blocks) {
-                raise_error(p.err, PA_DEVERR_BLOCK_ID);
-                continue;
-            }
-            const VecT *src = reinterpret_cast<const VecT *>(base + sb * pl.block_stride +
-                                                             (from & bs_mask) * pl.token_stride) + c;
-            dst[u] = reinterpret_cast<VecT *>(base + db * pl.block_stride + (to & bs_mask) * pl.token_stride) + c;
-            if (dst[u] == src) dst[u] = nullptr;                 // stays where it is
-            else v[u] = *src;
+            if (i >= used) continue;
+            const longlong2 at = place[buf][r];
+            if (at.y < 0) continue;
+            v[u] = reinterpret_cast<const VecT *>(base + at.x)[c];
+            dst[u] = reinterpret_cast<VecT *>(base + at.y) + c;
         }
+        look_up(r0 + step, from, buf ^ 1);
+        from = index(r0 + 2 * step);
         if (nc > 1) cluster.sync();                              // the whole wave has been read
         else __syncthreads();
 #pragma unroll
