@@ -37,9 +37,8 @@ constexpr int kBins = 1 << kDigitBits;
 
 // Masses as keys of the same order: NaN lowest, -0 equal to +0.
 __device__ __forceinline__ uint32_t mass_key(float x) {
-    if (x != x) return 0u;
     const uint32_t u = __float_as_uint(x + 0.f);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return x == x ? u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u) : 0u;
 }
 
 // Exclusive prefix of v over the CTA's threads, in thread order; *total: the sum.
@@ -168,18 +167,12 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSlice = 48 * 1024;    // masses per CTA: 192 KB of shared memory
-// Accumulated weights crowd into a few exponents, so a digit's counts are kept 16 times over,
-// one a lane and the lane 16 further: no two lanes of a half-warp add to the same word.
-constexpr int kDigits = 256, kCopies = 16;
-
 __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictParams p) {
-    extern __shared__ float slice[];    // this CTA's masses
-    __shared__ __align__(16) int hist[kDigits * kCopies];
-    __shared__ int totals[2][kDigits];  // of this CTA, by digit parity
-    __shared__ int warp_sums[32];
+    extern __shared__ __align__(16) float slice[];      // this CTA's masses
+    __shared__ __align__(16) int hist[kBins];
+    __shared__ uint32_t seg[kWarps];    // sums of each warp
     __shared__ int found[2];            // the digit of the threshold, and how many keys lie above it
-    __shared__ int counts[2];           // of this CTA's slice: keys above the threshold, keys equal to it
-    __shared__ int seg_gt[kWarps], seg_eq[kWarps];
+    __shared__ uint32_t counts;         // of this CTA's slice: tokens that stay anyway, ties << 16
     cg::cluster_group cluster = cg::this_cluster();
     const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -212,112 +205,145 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictParam
             }
         }
     }
+    auto sync = [&]() {
+        if (nc > 1) cluster.sync();
+        else __syncthreads();
+    };
     uint32_t key = 0, mask = 0;         // the digits found so far
     if (!all && !none) {
         const int n_cand = max(0, min(len, cand - t0));
-        for (int i = tid; i < kDigits * kCopies / 4; i += kThreads)
-            reinterpret_cast<int4 *>(hist)[i] = make_int4(0, 0, 0, 0);
-        __syncthreads();
-        for (int shift = 24; shift >= 0; shift -= 8) {
+        static_assert(kBins == 4 * kThreads, "four bins a thread");
+        for (int shift = 32 - kDigitBits;; shift = shift > kDigitBits ? shift - kDigitBits : 0) {
+            const int bits = shift > 0 ? kDigitBits : 32 - 2 * kDigitBits;
+            reinterpret_cast<int4 *>(hist)[tid] = make_int4(0, 0, 0, 0);
+            __syncthreads();
             for (int i = tid; i < n_cand; i += kThreads) {
                 const uint32_t k = mass_key(slice[i]);
-                if ((k & mask) == key) atomicAdd(&hist[((k >> shift) & 255u) * kCopies + (lane & (kCopies - 1))], 1);
+                if ((k & mask) == key) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1);
             }
+            sync();
+            // thread i: the bins counted from the top, 4 i to 4 i + 3, of the whole cluster
+            const int i0 = (1 << bits) - 1 - 4 * tid;
+            int n[4] = {0, 0, 0, 0};
+            if (i0 >= 3) {
+                for (int c = 0; c < nc; ++c) {
+                    const int4 v = *reinterpret_cast<const int4 *>((nc > 1 ? cluster.map_shared_rank(hist, c) : hist) +
+                                                                   i0 - 3);
+                    n[0] += v.w;
+                    n[1] += v.z;
+                    n[2] += v.y;
+                    n[3] += v.x;
+                }
+            }
+            const int mine = n[0] + n[1] + n[2] + n[3];
+            const int of_warp = __reduce_add_sync(0xffffffffu, mine);
+            if (lane == 0) seg[warp] = (uint32_t)of_warp;
             __syncthreads();
-            int *sum = totals[(shift >> 3) & 1];
-            {                           // two threads a digit add its copies, and clear them
-                static_assert(kThreads == 2 * kDigits && kCopies == 16, "half a digit's copies a thread");
-                int4 *mine = reinterpret_cast<int4 *>(hist) + 2 * tid;
-                const int4 x = mine[0], y = mine[1];
-                mine[0] = mine[1] = make_int4(0, 0, 0, 0);
-                int t = x.x + x.y + x.z + x.w + y.x + y.y + y.z + y.w;
-                t += __shfl_xor_sync(0xffffffffu, t, 1);
-                if ((tid & 1) == 0) sum[tid >> 1] = t;
-            }
-            cluster.sync();
-            // thread i < 256: digit 255 - i of the whole cluster, so counted from the top
-            int n = 0;
-            if (tid < kDigits) {
+            // the warp that holds the threshold looks for it among its bins
+            const int v = lane < kWarps ? (int)seg[lane] : 0;
+            int up_to = v;
 #pragma unroll
-                for (int c = 0; c < kMaxCluster; ++c)
-                    if (c < nc) n += cluster.map_shared_rank(sum, c)[kDigits - 1 - tid];
+            for (int o = 1; o < kWarps; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, up_to, o);
+                if (lane >= o) up_to += x;
             }
-            int total;
-            const int above = block_prefix<kThreads>(n, warp_sums, &total);
-            if (above < want && above + n >= want) {
-                found[0] = kDigits - 1 - tid;
-                found[1] = above;
+            const int target = __ffs(__ballot_sync(0xffffffffu, up_to >= want)) - 1;
+            if (warp == target) {
+                int above = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, above, o);
+                    if (lane >= o) above += x;
+                }
+                above += __shfl_sync(0xffffffffu, up_to - v, target) - mine;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (above < want && above + n[j] >= want) {
+                        found[0] = i0 - j;
+                        found[1] = above;
+                    }
+                    above += n[j];
+                }
             }
-            __syncthreads();
+            sync();                     // every CTA has read the counts
             key |= (uint32_t)found[0] << shift;
-            mask |= 255u << shift;
+            mask |= ((1u << bits) - 1u) << shift;
             want -= found[1];
+            if (shift == 0) break;
         }
     }
     __syncthreads();
     // ---- what stays: the recent tokens, keys above `key`, and the first `want` equal to it.
-    // Warp w has the tokens [w0, w1) of the slice.
-    const int wlen = (((len + kWarps - 1) / kWarps) + 31) & ~31;
+    // Warp w has the tokens [w0, w1) of the slice, a lane four neighbours at a time.
+    static_assert(kMaxSlice < 65536, "counts of a slice in 16 bits");
+    const int wlen = (((len + kWarps - 1) / kWarps) + 127) & ~127;
     const int w0 = min(len, warp * wlen), w1 = min(len, w0 + wlen);
-    int gt = 0, eq = 0;                 // of this warp's tokens: stay anyway; equal to the threshold
-    for (int i = w0 + lane; i < w1; i += 32) {
-        const uint32_t k = mass_key(slice[i]);
-        const bool sure = t0 + i >= cand || all || (!none && k > key);
-        gt += sure;
-        eq += !sure && !none && k == key;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        gt += __shfl_xor_sync(0xffffffffu, gt, o);
-        eq += __shfl_xor_sync(0xffffffffu, eq, o);
-    }
-    if (lane == 0) {
-        seg_gt[warp] = gt;
-        seg_eq[warp] = eq;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        int g = 0, e = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            g += seg_gt[w];
-            e += seg_eq[w];
-        }
-        counts[0] = g;
-        counts[1] = e;
-    }
-    cluster.sync();                     // every mass of the row has been read, too
-    int before_gt = 0, before_eq = 0;   // in the tokens before this warp's
-    for (int c = 0; c < rank; ++c) {
-        const int *o = cluster.map_shared_rank(counts, c);
-        before_gt += o[0];
-        before_eq += o[1];
-    }
-    for (int w = 0; w < warp; ++w) {
-        before_gt += seg_gt[w];
-        before_eq += seg_eq[w];
-    }
-    const uint32_t below = (1u << lane) - 1u;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + lane;
-        const float x = i < w1 ? slice[i] : 0.f;
+    // token i of the slice: 1 = stays anyway, 1 << 16 = equal to the threshold
+    auto verdict = [&](float x, int i) -> uint32_t {
         const uint32_t k = mass_key(x);
-        const bool sure = i < w1 && (t0 + i >= cand || all || (!none && k > key));
-        const bool tie = i < w1 && !sure && !none && k == key;
-        const uint32_t ms = __ballot_sync(0xffffffffu, sure), mt = __ballot_sync(0xffffffffu, tie);
-        const int eq_rank = before_eq + __popc(mt & below);
-        const bool stays = sure || (tie && eq_rank < want);
-        // position: the sure ones before, and the ties before, of which at most `want` stay
-        if (stays) {
-            const int at = before_gt + __popc(ms & below) + min(eq_rank, want);
-            kept[at] = t0 + i;
-            mass_out[at] = x;
+        const bool sure = t0 + i >= cand || all || (!none && k > key);
+        return i >= w1 ? 0u : (sure ? 1u : (!none && k == key ? 0x10000u : 0u));
+    };
+    uint32_t sum = 0;
+    for (int i = w0 + 4 * lane; i < w1; i += 128) {
+        const float4 x = *reinterpret_cast<const float4 *>(slice + i);
+        sum += verdict(x.x, i) + verdict(x.y, i + 1) + verdict(x.z, i + 2) + verdict(x.w, i + 3);
+    }
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (lane == 0) seg[warp] = sum;
+    __syncthreads();
+    uint32_t up_to = lane < kWarps ? seg[lane] : 0u;    // of the warps 0 .. lane
+#pragma unroll
+    for (int o = 1; o < kWarps; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, up_to, o);
+        if (lane >= o) up_to += v;
+    }
+    const uint32_t whole = __shfl_sync(0xffffffffu, up_to, kWarps - 1);
+    const uint32_t ahead = warp == 0 ? 0u : __shfl_sync(0xffffffffu, up_to, warp - 1);
+    int sure_before = (int)(ahead & 0xFFFFu), ties_before = (int)(ahead >> 16);   // this warp's tokens
+    if (nc > 1) {
+        if (tid == 0) counts = whole;
+        cluster.sync();                 // every mass of the row has been read, too
+        for (int c = 0; c < rank; ++c) {
+            const uint32_t o = *cluster.map_shared_rank(&counts, c);
+            sure_before += (int)(o & 0xFFFFu);
+            ties_before += (int)(o >> 16);
         }
-        before_gt += __popc(ms);
-        before_eq += __popc(mt);
+    }
+    for (int i0 = w0; i0 < w1; i0 += 128) {
+        const int i = i0 + 4 * lane;
+        const float4 x4 = i < w1 ? *reinterpret_cast<const float4 *>(slice + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+        uint32_t d[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = verdict(x[j], i + j);
+        const uint32_t mine = d[0] + d[1] + d[2] + d[3];
+        uint32_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const uint32_t tile = __shfl_sync(0xffffffffu, upto, 31);
+        int sure = sure_before + (int)((upto - mine) & 0xFFFFu), ties = ties_before + (int)((upto - mine) >> 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool tie = d[j] >> 16;
+            // position: the sure ones before, and the ties before, of which `want` stay
+            if (d[j] == 1u || (tie && ties < want)) {
+                const int at = sure + min(ties, want);
+                kept[at] = t0 + i + j;
+                mass_out[at] = x[j];
+            }
+            sure += (int)(d[j] & 1u);
+            ties += tie;
+        }
+        sure_before += (int)(tile & 0xFFFFu);
+        ties_before += (int)(tile >> 16);
     }
     for (int64_t i = s.n + rank * kThreads + tid; i < p.kept_len; i += nc * kThreads) kept[i] = -1;
     for (int64_t i = s.n + rank * kThreads + tid; i < p.mass_out_len; i += nc * kThreads) mass_out[i] = 0.f;
-    cluster.sync();                     // the counts are read by other CTAs until here
+    if (nc > 1) cluster.sync();         // the counts are read by other CTAs until here
 }
 
 constexpr int kMoveThreads = 256;
