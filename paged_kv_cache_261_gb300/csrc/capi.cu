@@ -312,6 +312,7 @@ int int4_setup(pa::Int4Cache &c, const void *k, const void *v, const int32_t *sl
     if (!aligned16(k) || !aligned16(v) || !aligned16(key_cache) || !aligned16(value_cache) || !aligned16(kv_params))
         return PA_ERR_INVALID_ARG;
     if (num_blocks > INT64_MAX / ((int64_t)block_size * num_kv_heads * head_dim)) return PA_ERR_INVALID_ARG;
+    if (num_tokens > (INT32_MAX - 65536) / num_kv_heads) return PA_ERR_UNSUPPORTED;   // rows are counted in 31 bits
     c.key = key_cache;
     c.value = value_cache;
     c.params = kv_params;

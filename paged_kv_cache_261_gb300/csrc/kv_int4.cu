@@ -21,18 +21,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename T> __device__ __forceinline__ void load8(const T *src, float *x);
-template <> __device__ __forceinline__ void load8<float>(const float *src, float *x) {
-    Vec16<float>::unpack(__ldcs(reinterpret_cast<const uint4 *>(src)), x);
-    Vec16<float>::unpack(__ldcs(reinterpret_cast<const uint4 *>(src) + 1), x + 4);
-}
-template <> __device__ __forceinline__ void load8<__half>(const __half *src, float *x) {
-    Vec16<__half>::unpack(__ldcs(reinterpret_cast<const uint4 *>(src)), x);
-}
-template <> __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *src, float *x) {
-    Vec16<__nv_bfloat16>::unpack(__ldcs(reinterpret_cast<const uint4 *>(src)), x);
-}
-
 template <typename T> __device__ __forceinline__ void store8(T *dst, const float *x) {
     alignas(16) T v[8];
 #pragma unroll
@@ -53,6 +41,62 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
+// Eight channels of a row as loaded, their values, and their smallest and largest: packed as
+// (min, -max), so that one packed min takes both on to the row's other lanes.
+template <typename T> struct Run8;
+template <> struct Run8<float> {
+    uint4 raw[2];
+    __device__ __forceinline__ void load(const float *src) {
+        raw[0] = __ldcs(reinterpret_cast<const uint4 *>(src));
+        raw[1] = __ldcs(reinterpret_cast<const uint4 *>(src) + 1);
+    }
+    __device__ __forceinline__ void clear() { raw[0] = raw[1] = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void values(float *x) const {
+        Vec16<float>::unpack(raw[0], x);
+        Vec16<float>::unpack(raw[1], x + 4);
+    }
+    template <int kLanes> __device__ __forceinline__ void extrema(float &lo, float &hi) const {
+        float x[8];
+        values(x);
+        lo = hi = x[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) {
+            lo = min_nan(lo, x[i]);
+            hi = max_nan(hi, x[i]);
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) {
+            lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        }
+    }
+};
+template <typename T2> __device__ __forceinline__ T2 as2(uint32_t u) { return *reinterpret_cast<T2 *>(&u); }
+template <typename T2> __device__ __forceinline__ uint32_t bits2(T2 v) { return *reinterpret_cast<uint32_t *>(&v); }
+template <typename T, typename T2> struct Run8Packed {
+    uint4 raw;
+    __device__ __forceinline__ void load(const T *src) { raw = __ldcs(reinterpret_cast<const uint4 *>(src)); }
+    __device__ __forceinline__ void clear() { raw = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void values(float *x) const { Vec16<T>::unpack(raw, x); }
+    template <int kLanes> __device__ __forceinline__ void extrema(float &lo, float &hi) const {
+        const T2 a = as2<T2>(raw.x), b = as2<T2>(raw.y), c = as2<T2>(raw.z), d = as2<T2>(raw.w);
+        const uint32_t mn = bits2(__hmin2_nan(__hmin2_nan(a, b), __hmin2_nan(c, d)));
+        const uint32_t mx = bits2(__hmax2_nan(__hmax2_nan(a, b), __hmax2_nan(c, d)));
+        // (mn.lo, -mx.lo) and (mn.hi, -mx.hi)
+        const uint32_t l = __byte_perm(mn, mx, 0x5410) ^ 0x80000000u, h = __byte_perm(mn, mx, 0x7632) ^ 0x80000000u;
+        T2 both = __hmin2_nan(as2<T2>(l), as2<T2>(h));
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1)
+            both = __hmin2_nan(both, as2<T2>(__shfl_xor_sync(0xffffffffu, bits2(both), o)));
+        float f[8];
+        Vec16<T>::unpack(make_uint4(bits2(both), 0, 0, 0), f);
+        lo = f[0];
+        hi = -f[1];
+    }
+};
+template <> struct Run8<__half> : Run8Packed<__half, __half2> {};
+template <> struct Run8<__nv_bfloat16> : Run8Packed<__nv_bfloat16, __nv_bfloat162> {};
+
 // Row of the cache (in rows of one kv head's token) of a slot, or -1: skip the token.
 __device__ __forceinline__ int64_t cache_row(const Int4Cache &c, int64_t slot, int h, bool first, unsigned int *err) {
     if (slot == -1) return -1;
@@ -64,80 +108,136 @@ __device__ __forceinline__ int64_t cache_row(const Int4Cache &c, int64_t slot, i
     return (((slot >> c.log2_block_size) * c.num_kv_heads + h) << c.log2_block_size) + (slot & (bs - 1));
 }
 
-template <typename T, int D>
-__global__ __launch_bounds__(kThreads) void kv_write_int4_kernel(const T *__restrict__ k, const T *__restrict__ v,
-                                                                 const int32_t *__restrict__ slots,
-                                                                 int64_t num_tokens, const Int4Cache c,
-                                                                 unsigned int *err) {
-    constexpr int kLanes = D / 8;                       // lanes per row
-    // a decode launched after this kernel may start its set-up now; it waits for this
-    // grid to finish before reading the cache
-    asm volatile("griddepcontrol.launch_dependents;");
-    const int64_t idx = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int part = (int)(idx % kLanes);               // which 8 channels
-    const int64_t row = idx / kLanes;                   // ((token, kv head), K or V)
-    const bool is_v = row & 1;
-    const int64_t th = row >> 1;
-    const int64_t t = th / c.num_kv_heads;
-    const int h = (int)(th - t * c.num_kv_heads);
-    const bool live = t < num_tokens;
-    float x[8] = {};
-    if (live) load8((is_v ? v : k) + th * D + part * 8, x);
-    const int64_t dst = live ? cache_row(c, slots[t], h, part == 0 && h == 0 && !is_v, err) : -1;
-    float lo = x[0], hi = x[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) {
-        lo = min_nan(lo, x[i]);
-        hi = max_nan(hi, x[i]);
-    }
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) {
-        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
-    lo = max_nan(min_nan(lo, 65504.f), -65504.f);
-    hi = max_nan(min_nan(hi, 65504.f), -65504.f);
-    const __half zero_h = __float2half_rn(lo);
-    const __half scale_h = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
-    const float zero = __half2float(zero_h), scale = __half2float(scale_h);
+// Eight codes of (x - zero) / scale, `inv` the reciprocal of scale. The product decides unless
+// it is so near a tie that the IEEE quotient has to (below 16 they differ by less than 2^-19).
+__device__ __forceinline__ uint32_t encode8(const float *x, float zero, float scale, float inv) {
+    constexpr float kMagic = 12582912.f;                 // 1.5 * 2^23: adding it rounds to an integer
     uint32_t codes = 0;
-    if (scale > 0.f) {
+    bool tie = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], zero), inv), 0.f), 15.f);
+        const float n = __fadd_rn(q, kMagic);
+        tie |= fabsf(__fsub_rn(q, __fsub_rn(n, kMagic))) > 0.5f - 4e-6f;
+        codes += (__float_as_uint(n) - 0x4B400000u) << (4 * i);
+    }
+    if (tie) {
+        codes = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float n = rintf(__fdiv_rn(__fsub_rn(x[i], zero), scale));
             codes |= (uint32_t)fminf(fmaxf(n, 0.f), 15.f) << (4 * i);
         }
     }
-    const uint32_t mine = (uint32_t)__half_as_ushort(scale_h) | ((uint32_t)__half_as_ushort(zero_h) << 16);
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, kLanes);   // the V row's, for the K row's lanes
-    if (dst < 0) return;
-    reinterpret_cast<uint32_t *>(is_v ? c.value : c.key)[dst * kLanes + part] = codes;
-    if (part == 0 && !is_v) reinterpret_cast<uint2 *>(c.params)[dst] = make_uint2(mine, other);
+    return codes;
 }
 
-template <typename T, int D>
+// The (token, kv head) pairs of a thread: kU of them, `pairs` (those a CTA has side by side)
+// apart, so that their loads are in flight together. step_t and step_h: pairs / kv heads and
+// the rest.
+struct Walk {
+    uint32_t t;
+    int h;
+    __device__ __forceinline__ Walk(uint32_t th, int kv_heads) : t(th / (uint32_t)kv_heads), h((int)(th - t * kv_heads)) {}
+    __device__ __forceinline__ void next(int kv_heads, int step_t, int step_h) {
+        t += step_t;
+        h += step_h;
+        if (h >= kv_heads) {
+            h -= kv_heads;
+            ++t;
+        }
+    }
+};
+
+template <typename T, int D, int kU>
+__global__ __launch_bounds__(kThreads) void kv_write_int4_kernel(const T *__restrict__ k, const T *__restrict__ v,
+                                                                 const int32_t *__restrict__ slots,
+                                                                 uint32_t num_tokens, const Int4Cache c,
+                                                                 int step_t, int step_h, unsigned int *err) {
+    constexpr int kLanes = D / 8;                       // lanes per row
+    constexpr int kPairs = kThreads / kLanes / 2;
+    // a decode launched after this kernel may start its set-up now; it waits for this
+    // grid to finish before reading the cache
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int part = threadIdx.x % kLanes;              // which 8 channels
+    const bool is_v = (threadIdx.x / kLanes) & 1;
+    const uint32_t th0 = blockIdx.x * (kPairs * kU) + threadIdx.x / (2 * kLanes);
+    const T *src = (is_v ? v : k) + (int64_t)th0 * D + part * 8;
+    Walk at(th0, c.num_kv_heads);
+    Run8<T> x[kU];
+    int64_t dst[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        dst[u] = -1;
+        x[u].clear();
+        if (at.t < num_tokens) {
+            x[u].load(src + (int64_t)u * kPairs * D);
+            dst[u] = cache_row(c, slots[at.t], at.h, part == 0 && at.h == 0 && !is_v, err);
+        }
+        at.next(c.num_kv_heads, step_t, step_h);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        float lo, hi, y[8];
+        x[u].template extrema<kLanes>(lo, hi);
+        x[u].values(y);
+        lo = max_nan(min_nan(lo, 65504.f), -65504.f);
+        hi = max_nan(min_nan(hi, 65504.f), -65504.f);
+        const __half zero_h = __float2half_rn(lo);
+        const __half scale_h = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+        const float zero = __half2float(zero_h), scale = __half2float(scale_h);
+        const uint32_t codes = scale > 0.f ? encode8(y, zero, scale, __frcp_rn(scale)) : 0u;
+        const uint32_t mine = (uint32_t)__half_as_ushort(scale_h) | ((uint32_t)__half_as_ushort(zero_h) << 16);
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, kLanes);   // the V row's, for the K row's lanes
+        if (dst[u] >= 0) {
+            reinterpret_cast<uint32_t *>(is_v ? c.value : c.key)[dst[u] * kLanes + part] = codes;
+            if (part == 0 && !is_v) reinterpret_cast<uint2 *>(c.params)[dst[u]] = make_uint2(mine, other);
+        }
+    }
+}
+
+template <typename T, int D, int kU>
 __global__ __launch_bounds__(kThreads) void kv_read_int4_kernel(T *__restrict__ k, T *__restrict__ v,
                                                                 const int32_t *__restrict__ slots,
-                                                                int64_t num_tokens, const Int4Cache c,
-                                                                unsigned int *err) {
-    constexpr int kLanes = D / 8;
-    const int64_t idx = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int part = (int)(idx % kLanes);
-    const int64_t row = idx / kLanes;
-    const bool is_v = row & 1;
-    const int64_t th = row >> 1;
-    const int64_t t = th / c.num_kv_heads;
-    const int h = (int)(th - t * c.num_kv_heads);
-    if (t >= num_tokens) return;
-    const int64_t src = cache_row(c, slots[t], h, part == 0 && h == 0 && !is_v, err);
-    if (src < 0) return;
-    const uint32_t codes = reinterpret_cast<const uint32_t *>(is_v ? c.value : c.key)[src * kLanes + part];
-    const float2 sz = __half22float2(reinterpret_cast<const __half2 *>(c.params)[src * 2 + is_v]);
-    float x[8] = {};
-    // code * scale is exact in float32 (4 + 11 bits), so the fused form rounds once
+                                                                uint32_t num_tokens, const Int4Cache c, int step_t,
+                                                                int step_h, unsigned int *err) {
+    constexpr int kLanes = D / 8, kPairs = kThreads / kLanes / 2;
+    const int part = threadIdx.x % kLanes;
+    const bool is_v = (threadIdx.x / kLanes) & 1;
+    const uint32_t th0 = blockIdx.x * (kPairs * kU) + threadIdx.x / (2 * kLanes);
+    const uint32_t *cache = reinterpret_cast<const uint32_t *>(is_v ? c.value : c.key);
+    T *dst = (is_v ? v : k) + (int64_t)th0 * D + part * 8;
+    Walk at(th0, c.num_kv_heads);
+    int64_t src[kU];
+    uint32_t codes[kU];
+    __half2 sz[kU];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = fmaf((float)((codes >> (4 * i)) & 15u), sz.x, sz.y);
-    store8((is_v ? v : k) + th * D + part * 8, x);
+    for (int u = 0; u < kU; ++u) {
+        src[u] = at.t < num_tokens ? cache_row(c, slots[at.t], at.h, part == 0 && at.h == 0 && !is_v, err) : -1;
+        at.next(c.num_kv_heads, step_t, step_h);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        if (src[u] < 0) continue;
+        codes[u] = __ldcs(cache + src[u] * kLanes + part);
+        sz[u] = reinterpret_cast<const __half2 *>(c.params)[src[u] * 2 + is_v];
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        if (src[u] < 0) continue;
+        const float2 f = __half22float2(sz[u]);
+        const float scale = f.x * 16777216.f;
+        float x[8];
+        // a code in an f16's low bits is code * 2^-24, so no integer is converted; its product
+        // with the scale is exact in float32 (4 + 11 bits), so the fused form rounds once
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 n = __half22float2(as2<__half2>((codes[u] >> (4 * i)) & 0x000F000Fu));
+            x[i] = fmaf(n.x, scale, f.y);
+            x[i + 4] = fmaf(n.y, scale, f.y);
+        }
+        store8(dst + (int64_t)u * kPairs * D, x);
+    }
 }
 
 // params[dst] = params[src] for each pair, in 16-byte vectors.
@@ -153,33 +253,55 @@ __global__ __launch_bounds__(kThreads) void copy_params_kernel(uint4 *params, co
         params[dst * block_vecs + i] = params[src * block_vecs + i];
 }
 
-int64_t row_grid(const Int4Cache &c, int64_t num_tokens) {
-    const int64_t rows = num_tokens * 2 * c.num_kv_heads;
-    return (rows * (c.head_dim / 8) + kThreads - 1) / kThreads;
+// Rows per thread: several where there are enough rows to fill the SMs all the same.
+constexpr int kWriteUnroll = 2, kReadUnroll = 4;
+constexpr int64_t kManyRows = 16384;             // (token, kv head) pairs
+
+unsigned row_grid(const Int4Cache &c, int64_t num_tokens, int per_thread) {
+    const int64_t pairs = (int64_t)kThreads / (c.head_dim / 8) / 2 * per_thread;
+    return (unsigned)((num_tokens * c.num_kv_heads + pairs - 1) / pairs);
 }
 
-template <typename T>
+template <typename T, int D>
 int write_t(const void *k, const void *v, const int32_t *slots, int64_t n, const Int4Cache &c, unsigned int *err,
             cudaStream_t s) {
-    const int64_t grid = row_grid(c, n);
-    if (grid > 0x7FFFFFFF) return -2;
-    if (c.head_dim == 128)
-        kv_write_int4_kernel<T, 128><<<(unsigned)grid, kThreads, 0, s>>>((const T *)k, (const T *)v, slots, n, c, err);
+    constexpr int pairs = kThreads / (D / 8) / 2;
+    const int st = pairs / c.num_kv_heads, sh = pairs % c.num_kv_heads;
+    const bool many = n * c.num_kv_heads >= kManyRows;
+    const unsigned grid = row_grid(c, n, many ? kWriteUnroll : 1);
+    if (many)
+        kv_write_int4_kernel<T, D, kWriteUnroll><<<grid, kThreads, 0, s>>>((const T *)k, (const T *)v, slots,
+                                                                           (uint32_t)n, c, st, sh, err);
     else
-        kv_write_int4_kernel<T, 64><<<(unsigned)grid, kThreads, 0, s>>>((const T *)k, (const T *)v, slots, n, c, err);
+        kv_write_int4_kernel<T, D, 1><<<grid, kThreads, 0, s>>>((const T *)k, (const T *)v, slots, (uint32_t)n, c, st,
+                                                                sh, err);
+    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+template <typename T, int D>
+int read_t(void *k, void *v, const int32_t *slots, int64_t n, const Int4Cache &c, unsigned int *err,
+           cudaStream_t s) {
+    constexpr int pairs = kThreads / (D / 8) / 2;
+    const int st = pairs / c.num_kv_heads, sh = pairs % c.num_kv_heads;
+    const bool many = n * c.num_kv_heads >= kManyRows;
+    const unsigned grid = row_grid(c, n, many ? kReadUnroll : 1);
+    if (many)
+        kv_read_int4_kernel<T, D, kReadUnroll><<<grid, kThreads, 0, s>>>((T *)k, (T *)v, slots, (uint32_t)n, c, st, sh,
+                                                                         err);
+    else
+        kv_read_int4_kernel<T, D, 1><<<grid, kThreads, 0, s>>>((T *)k, (T *)v, slots, (uint32_t)n, c, st, sh, err);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
 template <typename T>
-int read_t(void *k, void *v, const int32_t *slots, int64_t n, const Int4Cache &c, unsigned int *err,
+int write_d(const void *k, const void *v, const int32_t *slots, int64_t n, const Int4Cache &c, unsigned int *err,
+            cudaStream_t s) {
+    return c.head_dim == 128 ? write_t<T, 128>(k, v, slots, n, c, err, s) : write_t<T, 64>(k, v, slots, n, c, err, s);
+}
+template <typename T>
+int read_d(void *k, void *v, const int32_t *slots, int64_t n, const Int4Cache &c, unsigned int *err,
            cudaStream_t s) {
-    const int64_t grid = row_grid(c, n);
-    if (grid > 0x7FFFFFFF) return -2;
-    if (c.head_dim == 128)
-        kv_read_int4_kernel<T, 128><<<(unsigned)grid, kThreads, 0, s>>>((T *)k, (T *)v, slots, n, c, err);
-    else
-        kv_read_int4_kernel<T, 64><<<(unsigned)grid, kThreads, 0, s>>>((T *)k, (T *)v, slots, n, c, err);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    return c.head_dim == 128 ? read_t<T, 128>(k, v, slots, n, c, err, s) : read_t<T, 64>(k, v, slots, n, c, err, s);
 }
 
 }  // namespace
@@ -187,9 +309,9 @@ int read_t(void *k, void *v, const int32_t *slots, int64_t n, const Int4Cache &c
 int launch_kv_write_int4(const void *k, const void *v, int src_dtype, const int32_t *slot_mapping,
                          int64_t num_tokens, const Int4Cache &c, unsigned int *err, cudaStream_t stream) {
     switch (src_dtype) {
-    case PA_DTYPE_F32: return write_t<float>(k, v, slot_mapping, num_tokens, c, err, stream);
-    case PA_DTYPE_F16: return write_t<__half>(k, v, slot_mapping, num_tokens, c, err, stream);
-    case PA_DTYPE_BF16: return write_t<__nv_bfloat16>(k, v, slot_mapping, num_tokens, c, err, stream);
+    case PA_DTYPE_F32: return write_d<float>(k, v, slot_mapping, num_tokens, c, err, stream);
+    case PA_DTYPE_F16: return write_d<__half>(k, v, slot_mapping, num_tokens, c, err, stream);
+    case PA_DTYPE_BF16: return write_d<__nv_bfloat16>(k, v, slot_mapping, num_tokens, c, err, stream);
     default: return -2;
     }
 }
@@ -197,9 +319,9 @@ int launch_kv_write_int4(const void *k, const void *v, int src_dtype, const int3
 int launch_kv_read_int4(void *k, void *v, int dst_dtype, const int32_t *slot_mapping, int64_t num_tokens,
                         const Int4Cache &c, unsigned int *err, cudaStream_t stream) {
     switch (dst_dtype) {
-    case PA_DTYPE_F32: return read_t<float>(k, v, slot_mapping, num_tokens, c, err, stream);
-    case PA_DTYPE_F16: return read_t<__half>(k, v, slot_mapping, num_tokens, c, err, stream);
-    case PA_DTYPE_BF16: return read_t<__nv_bfloat16>(k, v, slot_mapping, num_tokens, c, err, stream);
+    case PA_DTYPE_F32: return read_d<float>(k, v, slot_mapping, num_tokens, c, err, stream);
+    case PA_DTYPE_F16: return read_d<__half>(k, v, slot_mapping, num_tokens, c, err, stream);
+    case PA_DTYPE_BF16: return read_d<__nv_bfloat16>(k, v, slot_mapping, num_tokens, c, err, stream);
     default: return -2;
     }
 }

@@ -33,9 +33,6 @@ def _rw(pa, name, **kw):
     (dict(k=8), INVALID), (dict(kc=8), INVALID), (dict(par=8), INVALID), (dict(nb=1 << 62), INVALID),
     (dict(T=0), 0), (dict(T=1 << 60), UNSUPPORTED)])
 def test_int4_rows_refusals(pa, name, bad, code):
-    if bad.get("T") == 1 << 60:
-        assert _rw(pa, name, **bad) in (UNSUPPORTED, -4)      # the size check comes after the device's error word
-        return
     assert _rw(pa, name, **bad) == code
 
 
