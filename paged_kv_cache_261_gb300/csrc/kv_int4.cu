@@ -156,8 +156,9 @@ __global__ __launch_bounds__(kThreads) void kv_write_int4_kernel(const T *__rest
                                                                  int step_t, int step_h, unsigned int *err) {
     constexpr int kLanes = D / 8;                       // lanes per row
     constexpr int kPairs = kThreads / kLanes / 2;
-    // a decode launched after this kernel may start its set-up now; it waits for this
-    // grid to finish before reading the cache
+    // launched as a dependent of the kernel before; a kernel launched after this one may start
+    // its set-up once everything before this one has finished
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int part = threadIdx.x % kLanes;              // which 8 channels
     const bool is_v = (threadIdx.x / kLanes) & 1;
@@ -202,6 +203,8 @@ __global__ __launch_bounds__(kThreads) void kv_read_int4_kernel(T *__restrict__ 
                                                                 uint32_t num_tokens, const Int4Cache c, int step_t,
                                                                 int step_h, unsigned int *err) {
     constexpr int kLanes = D / 8, kPairs = kThreads / kLanes / 2;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     const int part = threadIdx.x % kLanes;
     const bool is_v = (threadIdx.x / kLanes) & 1;
     const uint32_t th0 = blockIdx.x * (kPairs * kU) + threadIdx.x / (2 * kLanes);
@@ -269,13 +272,9 @@ int write_t(const void *k, const void *v, const int32_t *slots, int64_t n, const
     const int st = pairs / c.num_kv_heads, sh = pairs % c.num_kv_heads;
     const bool many = n * c.num_kv_heads >= kManyRows;
     const unsigned grid = row_grid(c, n, many ? kWriteUnroll : 1);
-    if (many)
-        kv_write_int4_kernel<T, D, kWriteUnroll><<<grid, kThreads, 0, s>>>((const T *)k, (const T *)v, slots,
-                                                                           (uint32_t)n, c, st, sh, err);
-    else
-        kv_write_int4_kernel<T, D, 1><<<grid, kThreads, 0, s>>>((const T *)k, (const T *)v, slots, (uint32_t)n, c, st,
-                                                                sh, err);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    auto kern = many ? kv_write_int4_kernel<T, D, kWriteUnroll> : kv_write_int4_kernel<T, D, 1>;
+    return launch_pdl(kern, dim3(grid), dim3(kThreads), 0, s, (const T *)k, (const T *)v, slots, (uint32_t)n, c, st, sh,
+                      err);
 }
 
 template <typename T, int D>
@@ -285,12 +284,8 @@ int read_t(void *k, void *v, const int32_t *slots, int64_t n, const Int4Cache &c
     const int st = pairs / c.num_kv_heads, sh = pairs % c.num_kv_heads;
     const bool many = n * c.num_kv_heads >= kManyRows;
     const unsigned grid = row_grid(c, n, many ? kReadUnroll : 1);
-    if (many)
-        kv_read_int4_kernel<T, D, kReadUnroll><<<grid, kThreads, 0, s>>>((T *)k, (T *)v, slots, (uint32_t)n, c, st, sh,
-                                                                         err);
-    else
-        kv_read_int4_kernel<T, D, 1><<<grid, kThreads, 0, s>>>((T *)k, (T *)v, slots, (uint32_t)n, c, st, sh, err);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    auto kern = many ? kv_read_int4_kernel<T, D, kReadUnroll> : kv_read_int4_kernel<T, D, 1>;
+    return launch_pdl(kern, dim3(grid), dim3(kThreads), 0, s, (T *)k, (T *)v, slots, (uint32_t)n, c, st, sh, err);
 }
 
 template <typename T>
