@@ -177,18 +177,20 @@ _SAME_DEVICE = contextlib.nullcontext()
 def _on(device):
     """The tensors' device made current for a library call: the library launches on,
     and sizes its grids for, the current device (no switch when it already is)."""
-    torch = _torch()
     idx = device.index
-    if idx is None or idx == torch.cuda.current_device():
+    if idx is None or idx == _torch().cuda.current_device():
         return _SAME_DEVICE
-    return torch.cuda.device(idx)
+    return _torch().cuda.device(idx)
 
 
 def _stream_ptr(stream, device) -> int:
     torch = _torch()
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return int(stream.cuda_stream)
+    if stream is not None:
+        return int(stream.cuda_stream)
+    if device.index is not None:
+        # the pointer alone, without a Stream object around it (0.1 against 1.9 us)
+        return int(torch._C._cuda_getCurrentRawStream(device.index))
+    return int(torch.cuda.current_stream(device).cuda_stream)
 
 
 def _cuda(t, name: str, dtype=None, device=None):
@@ -201,6 +203,13 @@ def _cuda(t, name: str, dtype=None, device=None):
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     return t
+
+
+def _all_cuda(dev, *tensors) -> None:
+    """_cuda for (tensor, name, dtype) triples, in one pass where nothing is wrong."""
+    for t, name, dtype in tensors:
+        if t.device != dev or t.dtype != dtype or not t.is_contiguous():
+            _cuda(t, name, dtype, dev)
 
 
 def paged_kv_write(k, v, slot_mapping, key_cache, value_cache, stream=None) -> None:
@@ -596,25 +605,21 @@ def _int4_caches(key_cache, value_cache, kv_params, dev):
     """Checks the tensors of a 4-bit cache; (num_blocks, num_kv_heads, block_size, head_dim)."""
     torch = _torch()
     _cuda(key_cache, "key_cache", torch.uint8)
-    _cuda(value_cache, "value_cache", torch.uint8, dev)
-    _cuda(kv_params, "kv_params", torch.float16, dev)
+    _all_cuda(dev, (value_cache, "value_cache", torch.uint8), (kv_params, "kv_params", torch.float16))
     if key_cache.dim() != 4 or value_cache.shape != key_cache.shape:
         raise ValueError("key_cache and value_cache must be [num_blocks, num_kv_heads, block_size, head_dim / 2]")
     nb, hk, bs, half = key_cache.shape
-    if tuple(kv_params.shape) != (nb, hk, bs, 4):
+    if kv_params.shape != (nb, hk, bs, 4):
         raise ValueError(f"kv_params must be [{nb}, {hk}, {bs}, 4]")
     return nb, hk, bs, 2 * half
 
 
 def _int4_rows(k, v, slot_mapping, hk, d, dev):
-    torch = _torch()
-    _cuda(k, "k", None, dev)
-    _cuda(v, "v", k.dtype, dev)
-    _cuda(slot_mapping, "slot_mapping", torch.int32, dev)
+    _all_cuda(dev, (k, "k", k.dtype), (v, "v", k.dtype), (slot_mapping, "slot_mapping", _torch().int32))
     if slot_mapping.dim() != 1:
         raise ValueError("slot_mapping must be [T]")
     T = slot_mapping.shape[0]
-    if tuple(k.shape) != (T, hk, d) or tuple(v.shape) != (T, hk, d):
+    if k.shape != (T, hk, d) or v.shape != (T, hk, d):
         raise ValueError(f"k/v must be [{T}, {hk}, {d}]")
     return T
 
@@ -647,16 +652,32 @@ def paged_kv_read_int4(k, v, slot_mapping, key_cache, value_cache, kv_params, st
 
 
 def _mass(mass, name, B, hk, dev):
-    torch = _torch()
-    _cuda(mass, name, torch.float32, dev)
-    if mass.dim() != 3 or tuple(mass.shape[:2]) != (B, hk):
+    _all_cuda(dev, (mass, name, _torch().float32))
+    if mass.dim() != 3 or mass.shape[0] != B or mass.shape[1] != hk:
         raise ValueError(f"{name} must be [{B}, {hk}, length]")
     return mass.shape[2]
 
 
+_sizes: dict = {}
+
+
+def _memo(fn, *args) -> int:
+    """A workspace size function's value, which depends on its arguments alone."""
+    key = (fn, args)
+    n = _sizes.get(key)
+    if n is None:
+        if len(_sizes) >= 4096:
+            _sizes.clear()
+        n = _sizes[key] = fn(*args)
+    return n
+
+
 def decode_int4_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
-                                max_context_len: int, with_mass: bool = False) -> int:
-    """Workspace bytes of a 4-bit decode call on the current device."""
+                                max_context_len: int, with_mass: bool = False, device=None) -> int:
+    """Workspace bytes of a 4-bit decode call on `device` (default: the current one)."""
+    if device is not None:
+        with _torch().cuda.device(device):
+            return decode_int4_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len, with_mass)
     return int(_lib.pa_decode_int4_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len,
                                                    int(with_mass)))
 
@@ -671,14 +692,14 @@ def paged_attention_decode_int4(out, q, key_cache, value_cache, kv_params, block
     torch = _torch()
     dev = key_cache.device
     nb, hk, bs, d = _int4_caches(key_cache, value_cache, kv_params, dev)
-    _cuda(q, "q", None, dev)
-    _cuda(out, "out", q.dtype, dev)
-    _cuda(block_tables, "block_tables", torch.int32, dev)
-    _cuda(context_lens, "context_lens", torch.int32, dev)
-    B, H, D = q.shape
-    if D != d or tuple(out.shape) != (B, H, D):
+    _all_cuda(dev, (q, "q", q.dtype), (out, "out", q.dtype), (block_tables, "block_tables", torch.int32),
+              (context_lens, "context_lens", torch.int32))
+    if q.dim() != 3:
         raise ValueError("q/out must be [B, H, head_dim]")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(context_lens.shape) != (B,):
+    B, H, D = q.shape
+    if D != d or out.shape != q.shape:
+        raise ValueError("q/out must be [B, H, head_dim]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
         raise ValueError("block_tables must be [B, MB] and context_lens [B]")
     mb = block_tables.shape[1]
     mass_ptr, mass_len = None, 0
@@ -687,10 +708,11 @@ def paged_attention_decode_int4(out, q, key_cache, value_cache, kv_params, block
         mass_ptr = mass.data_ptr()
     sp = _stream_ptr(stream, dev)
     with _on(dev):
-        need = decode_int4_workspace_bytes(B, H, hk, D, max_context_len or mb * bs, mass is not None)
+        need = _memo(decode_int4_workspace_bytes, B, H, hk, D, max_context_len or mb * bs, mass is not None, dev.index)
         if workspace is None:
             workspace = _workspace(dev, sp, need)
-        _cuda(workspace, "workspace", torch.uint8, dev)
+        else:
+            _cuda(workspace, "workspace", torch.uint8, dev)
         rc = _lib.pa_paged_attention_decode_int4(out.data_ptr(), q.data_ptr(), key_cache.data_ptr(),
                                                  value_cache.data_ptr(), kv_params.data_ptr(), mass_ptr, mass_len,
                                                  block_tables.data_ptr(), mb, context_lens.data_ptr(), B, H, hk, D, bs,
@@ -712,27 +734,28 @@ def paged_attention_decode_scored(out, q, mass, key_cache, value_cache, block_ta
     query heads of its kv head, to mass float32 [B, Hk, M]. Entries past a context stay."""
     torch = _torch()
     dev = key_cache.device
+    dt = key_cache.dtype
     _cuda(key_cache, "key_cache")
-    _cuda(value_cache, "value_cache", key_cache.dtype, dev)
-    _cuda(q, "q", key_cache.dtype, dev)
-    _cuda(out, "out", key_cache.dtype, dev)
-    _cuda(block_tables, "block_tables", torch.int32, dev)
-    _cuda(context_lens, "context_lens", torch.int32, dev)
+    _all_cuda(dev, (value_cache, "value_cache", dt), (q, "q", dt), (out, "out", dt),
+              (block_tables, "block_tables", torch.int32), (context_lens, "context_lens", torch.int32))
+    if key_cache.dim() != 4 or q.dim() != 3:
+        raise ValueError("caches must be [NB, bs, Hk, D] and q/out [B, H, D]")
     nb, bs, hk, d = key_cache.shape
     if value_cache.shape != key_cache.shape:
         raise ValueError("value_cache shape differs from key_cache")
     B, H, D = q.shape
-    if D != d or tuple(out.shape) != (B, H, D):
+    if D != d or out.shape != q.shape:
         raise ValueError("q/out must be [B, H, head_dim]")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(context_lens.shape) != (B,):
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
         raise ValueError("block_tables must be [B, MB] and context_lens [B]")
     mass_len = _mass(mass, "mass", B, hk, dev)
     mb = block_tables.shape[1]
     sp = _stream_ptr(stream, dev)
-    need = decode_scored_workspace_bytes(B, H, D, max_context_len or mb * bs, partition_size)
+    need = _memo(decode_scored_workspace_bytes, B, H, D, max_context_len or mb * bs, partition_size)
     if workspace is None:
         workspace = _workspace(dev, sp, need)
-    _cuda(workspace, "workspace", torch.uint8, dev)
+    else:
+        _cuda(workspace, "workspace", torch.uint8, dev)
     with _on(dev):
         rc = _lib.pa_paged_attention_decode_scored(out.data_ptr(), q.data_ptr(), mass.data_ptr(), mass_len,
                                                    key_cache.data_ptr(), value_cache.data_ptr(),
@@ -764,16 +787,17 @@ def paged_kv_evict(kept, mass, mass_out, key_cache, value_cache, block_tables, o
             raise ValueError("key_cache and value_cache must be [num_blocks, block_size, num_kv_heads, head_dim]")
         nb, bs, hk, d = key_cache.shape
         dt, par = _storage_code(key_cache), None
-    for t, n in ((kept, "kept"), (block_tables, "block_tables"), (out_block_tables, "out_block_tables"),
-                 (context_lens, "context_lens"), (keep_lens, "keep_lens")):
-        _cuda(t, n, torch.int32, dev)
+    i32 = torch.int32
+    _all_cuda(dev, (kept, "kept", i32), (block_tables, "block_tables", i32),
+              (out_block_tables, "out_block_tables", i32), (context_lens, "context_lens", i32),
+              (keep_lens, "keep_lens", i32))
     if context_lens.dim() != 1:
         raise ValueError("context_lens must be [B]")
     B = context_lens.shape[0]
-    if tuple(keep_lens.shape) != (B,) or block_tables.dim() != 2 or out_block_tables.dim() != 2 or \
+    if keep_lens.shape != (B,) or block_tables.dim() != 2 or out_block_tables.dim() != 2 or \
             block_tables.shape[0] != B or out_block_tables.shape[0] != B:
         raise ValueError("block_tables and out_block_tables must be [B, MB], context_lens and keep_lens [B]")
-    if kept.dim() != 3 or tuple(kept.shape[:2]) != (B, hk):
+    if kept.dim() != 3 or kept.shape[0] != B or kept.shape[1] != hk:
         raise ValueError(f"kept must be [{B}, {hk}, length]")
     mass_len, out_len = _mass(mass, "mass", B, hk, dev), _mass(mass_out, "mass_out", B, hk, dev)
     with _on(dev):

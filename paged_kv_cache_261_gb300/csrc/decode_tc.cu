@@ -651,7 +651,13 @@ __global__ __launch_bounds__(kThreads, 1) void decode_tc_kernel(const __grid_con
                 if constexpr (kScore) {
                     // [sequence][kv head][token][head]: a thread stores its token's heads
                     float *lg = p.ws_logits + (((int64_t)I.b * p.num_kv_heads + I.kvh) * p.logits_len + tok) * G + c0;
-                    if (valid) {
+                    if (valid && G == GT) {             // whole vectors, aligned: G is a multiple of kC
+                        if constexpr (kC == 2) *reinterpret_cast<float2 *>(lg) = make_float2(s[0], s[1]);
+                        else
+#pragma unroll
+                            for (int u = 0; u < kC; u += 4)
+                                *reinterpret_cast<float4 *>(lg + u) = make_float4(s[u], s[u + 1], s[u + 2], s[u + 3]);
+                    } else if (valid) {
 #pragma unroll
                         for (int u = 0; u < kC; ++u)
                             if (c0 + u < G) lg[u] = s[u];

@@ -177,8 +177,8 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictParam
     const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x / nc, b = blockIdx.y;
+    // (no early trigger: the moving CTAs, resident early, slowed the second wave of long rows)
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
     const EvictSplit s = evict_split(p, b, tid == 0 && blockIdx.x == 0);
     const int64_t row = (int64_t)b * p.num_kv_heads + h;
     const float *mass = p.mass + row * p.mass_len;
@@ -421,7 +421,6 @@ __global__ __launch_bounds__(kMoveThreads) void evict_move_kernel(const EvictPar
     const int h = blockIdx.x / nc, b = blockIdx.y;
     const EvictPlane &pl = p.planes[blockIdx.z];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
     const EvictSplit s = evict_split(p, b, false);
     const int32_t *kept = p.kept + ((int64_t)b * p.num_kv_heads + h) * p.kept_len;
     if (pl.row_bytes % 16 == 0) move_rows<uint4>(p, pl, s, b, h, kept, rank, nc);
