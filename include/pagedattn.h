@@ -492,8 +492,8 @@ int pa_paged_attention_decode_int4(void *out, const void *q, const void *key_cac
  */
 
 /* Bytes of workspace pa_paged_attention_decode_scored needs for these sizes. */
-size_t pa_decode_scored_workspace_bytes(int num_seqs, int num_heads, int head_dim, int max_context_len,
-                                        int partition_size);
+size_t pa_decode_scored_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                        int max_context_len, int partition_size);
 
 /*
  * pa_paged_attention_decode that also accumulates each token's attention weight:
@@ -506,7 +506,8 @@ size_t pa_decode_scored_workspace_bytes(int num_seqs, int num_heads, int head_di
  * A context longer than mass_len sets PA_DEVERR_CONTEXT and is cut to it. out is that of
  * pa_paged_attention_decode, bit for bit, with the same arguments (caches of float32,
  * f16 or bf16). The workspace (size from pa_decode_scored_workspace_bytes; NULL =
- * cudaMallocAsync on the stream) holds the scores: 4 bytes per query head and token.
+ * cudaMallocAsync on the stream) holds the scores: 4 bytes per query head and token, the
+ * heads of a group rounded up to 2, 4, 8 or 16.
  */
 int pa_paged_attention_decode_scored(void *out, const void *q, float *mass, int64_t mass_len, const void *key_cache,
                                      const void *value_cache, const int32_t *block_tables, int max_blocks_per_seq,

@@ -113,7 +113,7 @@ _decl("pa_copy_blocks_int4", [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _i32, 
 _decl("pa_decode_int4_workspace_bytes", [_i32, _i32, _i32, _i32, _i32, _i32], _sz)
 _decl("pa_paged_attention_decode_int4", [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i32, _vp, _i32, _i32, _i32, _i32,
                                          _i32, _i64, _f, _i32, _vp, _sz, _i32, _vp])
-_decl("pa_decode_scored_workspace_bytes", [_i32, _i32, _i32, _i32, _i32], _sz)
+_decl("pa_decode_scored_workspace_bytes", [_i32, _i32, _i32, _i32, _i32, _i32], _sz)
 _decl("pa_paged_attention_decode_scored", [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32,
                                            _i32, _i64, _f, _i32, _i32, _vp, _sz, _i32, _vp])
 _decl("pa_paged_kv_evict", [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _i32,
@@ -721,9 +721,10 @@ def paged_attention_decode_int4(out, q, key_cache, value_cache, kv_params, block
     _check(rc, "pa_paged_attention_decode_int4")
 
 
-def decode_scored_workspace_bytes(num_seqs: int, num_heads: int, head_dim: int, max_context_len: int,
-                                  partition_size: int = 0) -> int:
-    return int(_lib.pa_decode_scored_workspace_bytes(num_seqs, num_heads, head_dim, max_context_len,
+def decode_scored_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                  max_context_len: int, partition_size: int = 0) -> int:
+    """Workspace bytes of a paged_attention_decode_scored call."""
+    return int(_lib.pa_decode_scored_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len,
                                                      partition_size))
 
 
@@ -751,7 +752,7 @@ def paged_attention_decode_scored(out, q, mass, key_cache, value_cache, block_ta
     mass_len = _mass(mass, "mass", B, hk, dev)
     mb = block_tables.shape[1]
     sp = _stream_ptr(stream, dev)
-    need = _memo(decode_scored_workspace_bytes, B, H, D, max_context_len or mb * bs, partition_size)
+    need = _memo(decode_scored_workspace_bytes, B, H, hk, D, max_context_len or mb * bs, partition_size)
     if workspace is None:
         workspace = _workspace(dev, sp, need)
     else:

@@ -253,11 +253,22 @@ int decode_fp8_call(void *out, const void *q, const void *k_new, const void *v_n
     return krc == 0 ? PA_OK : PA_ERR_CUDA;
 }
 
+// Scores of a decode: rows of a multiple of four tokens, so that every plane is aligned.
+int64_t logits_len(int64_t max_ctx) { return (max_ctx + 3) & ~int64_t(3); }
+size_t logits_bytes(int64_t B, int64_t H, int64_t Hk, int64_t max_ctx) {
+    return (size_t)(B * Hk * pa::padded_group((int)(H / Hk)) * logits_len(max_ctx) * 4);
+}
+
 // Workspace of a scored decode: the split-K partials, then every partition's (max, sum)
 // pair, then the scores.
-size_t scored_workspace_bytes(int64_t B, int64_t H, int64_t D, int64_t P, int64_t max_ctx) {
+size_t scored_workspace_bytes(int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t P, int64_t max_ctx) {
     return align256(workspace_bytes_for(B, H, D, P)) + align256((size_t)(B * H * P * 2 * 4)) +
-           (size_t)(B * H * max_ctx * 4);
+           logits_bytes(B, H, Hk, max_ctx);
+}
+
+void set_logits(pa::DecodeParams &p, int64_t max_ctx) {
+    p.logits_len = (int)logits_len(max_ctx);
+    p.logits_row = (int64_t)pa::padded_group(p.group) * p.logits_len;
 }
 
 // Workspace of a decode that may be scored (max_ctx > 0: the scores of so many tokens a
@@ -266,7 +277,7 @@ int scored_workspace(pa::DecodeParams &p, int64_t P, int64_t max_ctx, void *work
                      cudaStream_t s, void **owned) {
     *owned = nullptr;
     const int64_t B = p.num_seqs, H = p.num_heads;
-    const size_t need = scored_workspace_bytes(B, H, p.head_dim, P, max_ctx);
+    const size_t need = scored_workspace_bytes(B, H, p.num_kv_heads, p.head_dim, P, max_ctx);
     void *ws = workspace;
     if (ws) {
         if (workspace_bytes < need) return PA_ERR_WORKSPACE;
@@ -282,7 +293,7 @@ int scored_workspace(pa::DecodeParams &p, int64_t P, int64_t max_ctx, void *work
     p.ws_score_ml = reinterpret_cast<float *>(at);
     at += align256((size_t)(B * H * P * 2 * 4));
     p.ws_logits = reinterpret_cast<float *>(at);
-    p.logits_len = (int)max_ctx;
+    set_logits(p, max_ctx);
     return PA_OK;
 }
 
@@ -291,7 +302,7 @@ int scored_workspace(pa::DecodeParams &p, int64_t P, int64_t max_ctx, void *work
 size_t int4_workspace_bytes(int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_ctx, bool with_mass) {
     const pa::Int4WorkSizes z = pa::decode_int4_work_sizes(B, H, Hk, D, max_ctx, device_sm_count());
     return align256(z.rows) + align256(z.part_ml) + align256(z.part_o) +
-           (with_mass ? align256((size_t)(B * H * 8)) + (size_t)(B * H * max_ctx * 4) : 0);
+           (with_mass ? align256((size_t)(B * H * 8)) + logits_bytes(B, H, Hk, max_ctx) : 0);
 }
 
 int64_t call_max_context(int max_blocks_per_seq, int block_size, int max_context_len) {
@@ -741,11 +752,13 @@ int pa_copy_blocks(void *key_cache, void *value_cache, const int32_t *src_dst_pa
     return PA_OK;
 }
 
-size_t pa_decode_scored_workspace_bytes(int num_seqs, int num_heads, int head_dim, int max_context_len,
-                                        int partition_size) {
-    if (num_seqs <= 0 || num_heads <= 0 || head_dim <= 0 || max_context_len < 0 || partition_size < 0) return 0;
+size_t pa_decode_scored_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                        int max_context_len, int partition_size) {
+    if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 || head_dim <= 0 ||
+        max_context_len < 0 || partition_size < 0 || num_heads / num_kv_heads > 16)
+        return 0;
     const int part = resolve_partition(partition_size, num_seqs, max_context_len);
-    return scored_workspace_bytes(num_seqs, num_heads, head_dim, num_partitions(max_context_len, part),
+    return scored_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, num_partitions(max_context_len, part),
                                   max_context_len);
 }
 
@@ -772,13 +785,10 @@ int pa_paged_attention_decode_scored(void *out, const void *q, float *mass, int6
     const int64_t max_ctx = call_max_context(max_blocks_per_seq, block_size, max_context_len);
     if ((rc = scored_workspace(p, P, max_ctx, workspace, workspace_bytes, s, &owned)) != PA_OK) return rc;
     const DecodeKernel choice = decode_kernel_choice();
-    int krc;
-    if (choice == DecodeKernel::Tc || (choice == DecodeKernel::Auto && pa::decode_tc_supported(p, dtype)))
-        krc = pa::launch_decode_tc(p, dtype, s);
-    else
-        krc = pa::launch_decode_simt(p, dtype, s);
+    const bool tc = choice == DecodeKernel::Tc || (choice == DecodeKernel::Auto && pa::decode_tc_supported(p, dtype));
+    int krc = tc ? pa::launch_decode_tc(p, dtype, s) : pa::launch_decode_simt(p, dtype, s);
     if (krc == 0 && P > 1) krc = pa::launch_decode_reduce(p, dtype, s);
-    if (krc == 0) krc = pa::launch_decode_mass(p, mass, mass_len, s);
+    if (krc == 0) krc = pa::launch_decode_mass(p, tc ? pa::score_plane_tc(p.group) : 1, mass, mass_len, s);
     if (owned) cudaFreeAsync(owned, s);
     if (krc == -2) return PA_ERR_UNSUPPORTED;
     return krc == 0 ? PA_OK : PA_ERR_CUDA;
@@ -845,7 +855,7 @@ int pa_copy_blocks_int4(void *key_cache, void *value_cache, void *kv_params, con
 size_t pa_decode_int4_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                                       int max_context_len, int with_mass) {
     if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 || head_dim <= 0 ||
-        max_context_len < 0)
+        max_context_len < 0 || num_heads / num_kv_heads > 16)
         return 0;
     return int4_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len, with_mass != 0);
 }
@@ -897,12 +907,12 @@ int pa_paged_attention_decode_int4(void *out, const void *q, const void *key_cac
         p.ws_score_ml = reinterpret_cast<float *>(at);
         at += align256((size_t)num_seqs * num_heads * 8);
         p.ws_logits = reinterpret_cast<float *>(at);
-        p.logits_len = (int)max_ctx;
+        set_logits(p, max_ctx);
     }
     p.max_partitions = 1;                     // as the accumulation of the weights sees it
     p.partition_size = INT32_MAX;
     int krc = pa::launch_decode_int4(p, w, max_ctx, device_sm_count(), dtype, s);
-    if (krc == 0 && mass) krc = pa::launch_decode_mass(p, mass, mass_len, s);
+    if (krc == 0 && mass) krc = pa::launch_decode_mass(p, 2, mass, mass_len, s);
     if (owned) cudaFreeAsync(owned, s);
     if (krc == -2) return PA_ERR_UNSUPPORTED;
     return krc == 0 ? PA_OK : PA_ERR_CUDA;

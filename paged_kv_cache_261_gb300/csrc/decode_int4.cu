@@ -458,16 +458,12 @@ __global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_int4_kernel(
                         S[sub][nt][2 * r] = valid ? x.x : -INFINITY;
                         S[sub][nt][2 * r + 1] = valid ? x.y : -INFINITY;
                         if constexpr (kScore) {
-                            const int g = nt * 8 + 2 * lj;
-                            float *lg = p.ws_logits +
-                                        (((int64_t)I_b * p.num_kv_heads + I_kvh) * p.logits_len + ts + t) * G + g;
-                            const float x0 = S[sub][nt][2 * r], x1 = S[sub][nt][2 * r + 1];
-                            if (valid && g + 1 < G && (G & 1) == 0) {
-                                *reinterpret_cast<float2 *>(lg) = make_float2(x0, x1);
-                            } else {
-                                if (valid && g < G) lg[0] = x0;
-                                if (valid && g + 1 < G) lg[1] = x1;
-                            }
+                            const int pl = nt * 4 + lj;    // planes of two heads
+                            if (valid && 2 * pl < G)
+                                *reinterpret_cast<float2 *>(
+                                    p.ws_logits + ((int64_t)I_b * Hk + I_kvh) * p.logits_row +
+                                    ((int64_t)pl * p.logits_len + ts + t) * 2) =
+                                    make_float2(S[sub][nt][2 * r], S[sub][nt][2 * r + 1]);
                         }
                     }
                 }
@@ -832,7 +828,7 @@ int launch_decode_int4(const DecodeParams &p, const Int4Work &ws, int64_t max_ct
         c.block_tables = p.block_tables + (int64_t)b0 * p.max_blocks_per_seq;
         c.context_lens = p.context_lens + b0;
         if (p.ws_logits) {
-            c.ws_logits = p.ws_logits + rows * p.logits_len;
+            c.ws_logits = p.ws_logits + (int64_t)b0 * p.num_kv_heads * p.logits_row;
             c.ws_score_ml = p.ws_score_ml + rows * 2;
         }
         const int grid = launch_grid(c.num_seqs, c.num_kv_heads, max_ctx, sms);

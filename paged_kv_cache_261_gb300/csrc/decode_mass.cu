@@ -6,9 +6,9 @@
 //   mass[b, kvh, t] += sum over the heads of kv head kvh of that weight,
 // added in head order, so the result does not depend on timing.
 //
-// The decode kernels leave the scores as [sequence, kv head, token, head] and the pairs
-// of every partition in the workspace; this kernel reads each score once (4 G bytes per
-// token and kv head, next to the 8 of mass itself) and is bound by that traffic.
+// The decode kernels leave the scores (planes of V heads, see kernels.h) and the pairs of
+// every partition in the workspace; this kernel reads each score once (4 G bytes per token
+// and kv head, next to the 8 of mass itself) and is bound by that traffic.
 #include "common.cuh"
 #include "kernels_compress.h"
 
@@ -18,56 +18,69 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxG = 16;
 
-// Tokens per thread, kThreads apart: their scores (kTok * G floats), and the weights they are
-// added to, are read before the heads' (M, L) are joined, which takes two round trips itself.
-// (A loop of one token a thread after the join took 22 us on the 8B-shaped batch, against XX.)
-template <int G> struct MassCfg {
-    static constexpr int kTok = G <= 4 ? 8 : (G <= 8 ? 4 : 2);
-};
+// Tokens per thread, kThreads apart: their scores (kTok * V * NP floats), and the weights they
+// are added to, are read before the heads' (M, L) are joined, which takes two round trips
+// itself. (A loop of one token a thread after the join took 22 us on the 8B-shaped batch,
+// against 6.)
+constexpr int tokens_per_thread(int heads) { return heads <= 2 ? 8 : (heads <= 4 ? 4 : (heads <= 8 ? 2 : 1)); }
 
-// G: heads of the group, or 0: any number, read one score at a time.
-template <int G>
+// V floats as one load.
+template <int V> __device__ __forceinline__ void load_vec(const float *src, float *v) {
+    if constexpr (V == 1) {
+        v[0] = __ldcs(src);
+    } else if constexpr (V == 2) {
+        const float2 f = __ldcs(reinterpret_cast<const float2 *>(src));
+        v[0] = f.x;
+        v[1] = f.y;
+    } else {
+#pragma unroll
+        for (int u = 0; u < V; u += 4) {
+            const float4 f = __ldcs(reinterpret_cast<const float4 *>(src + u));
+            v[u] = f.x;
+            v[u + 1] = f.y;
+            v[u + 2] = f.z;
+            v[u + 3] = f.w;
+        }
+    }
+}
+
+// NP planes of V heads, of which the first `group` exist.
+template <int V, int NP>
 __global__ __launch_bounds__(kThreads) void decode_mass_kernel(const DecodeParams p, float *__restrict__ mass,
-                                                               int64_t mass_len) {
-    constexpr int kTok = MassCfg<G>::kTok;
+                                                               int64_t mass_len, int rounds) {
+    constexpr int kHeads = V * NP, kTok = tokens_per_thread(kHeads);
     constexpr int kChunk = kThreads * kTok;
     __shared__ float M_s[kMaxG], inv_s[kMaxG];
     const int kvh = blockIdx.y, b = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g_n = G ? G : p.group;
+    const int G = p.group;
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int ctx = p.context_lens[b];
     ctx = ctx < 0 ? 0 : min(ctx, p.context_limit);
-    const int64_t c0 = (int64_t)blockIdx.x * kChunk;
+    const int64_t c0 = (int64_t)blockIdx.x * rounds * kChunk;
     if (c0 >= ctx) return;
-    const float *x = p.ws_logits + ((int64_t)b * p.num_kv_heads + kvh) * p.logits_len * g_n;
+    const float *x = p.ws_logits + ((int64_t)b * p.num_kv_heads + kvh) * p.logits_row;
     float *dst = mass + ((int64_t)b * p.num_kv_heads + kvh) * mass_len;
-    const int t0 = (int)c0 + threadIdx.x;
-    float v[kTok][G ? G : 1], old[kTok];
+    int t0 = (int)c0 + threadIdx.x;
+    const int end = (int)min((int64_t)ctx, c0 + (int64_t)rounds * kChunk);
+    float v[kTok][kHeads], old[kTok];
+    auto load = [&]() {
 #pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-        const int t = t0 + i * kThreads;
-        if (t >= ctx) continue;
-        old[i] = dst[t];
-        if constexpr (G % 4 == 0 && G > 0) {
+        for (int i = 0; i < kTok; ++i) {
+            const int t = t0 + i * kThreads;
+            if (t >= end) continue;
+            old[i] = dst[t];
 #pragma unroll
-            for (int g = 0; g < G; g += 4) {
-                const float4 f = __ldcs(reinterpret_cast<const float4 *>(x + (int64_t)t * G + g));
-                v[i][g] = f.x;
-                v[i][g + 1] = f.y;
-                v[i][g + 2] = f.z;
-                v[i][g + 3] = f.w;
-            }
-        } else if constexpr (G > 0) {
-#pragma unroll
-            for (int g = 0; g < G; ++g) v[i][g] = __ldcs(x + (int64_t)t * G + g);
+            for (int pl = 0; pl < NP; ++pl)
+                if (pl * V < G) load_vec<V>(x + ((int64_t)pl * p.logits_len + t) * V, v[i] + pl * V);
         }
-    }
+    };
+    load();
     const int nparts = (ctx - 1) / p.partition_size + 1;
-    for (int g = warp; g < g_n; g += kThreads / 32) {
+    for (int g = warp; g < G; g += kThreads / 32) {
         const float2 *ml = reinterpret_cast<const float2 *>(p.ws_score_ml) +
-                           ((int64_t)b * p.num_heads + (int64_t)kvh * g_n + g) * p.max_partitions;
+                           ((int64_t)b * p.num_heads + (int64_t)kvh * G + g) * p.max_partitions;
         float M = -INFINITY, L = 0.f;
         for (int i = lane; i < nparts; i += 32) {       // the lane's own pairs, one pass
             const float2 a = ml[i];
@@ -88,38 +101,56 @@ __global__ __launch_bounds__(kThreads) void decode_mass_kernel(const DecodeParam
         }
     }
     __syncthreads();
+    for (;;) {
 #pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-        const int t = t0 + i * kThreads;
-        if (t >= ctx) continue;
-        float w = 0.f;
-        if constexpr (G > 0) {
+        for (int i = 0; i < kTok; ++i) {
+            const int t = t0 + i * kThreads;
+            if (t >= end) continue;
+            float w = 0.f;
 #pragma unroll
-            for (int g = 0; g < G; ++g) w = fmaf(fast_exp2(v[i][g] - M_s[g]), inv_s[g], w);
-        } else {
-            for (int g = 0; g < g_n; ++g) w = fmaf(fast_exp2(__ldcs(x + (int64_t)t * g_n + g) - M_s[g]), inv_s[g], w);
+            for (int g = 0; g < kHeads; ++g)
+                if (g < G) w = fmaf(fast_exp2(v[i][g] - M_s[g]), inv_s[g], w);
+            dst[t] = old[i] + w;
         }
-        dst[t] = old[i] + w;
+        t0 += kChunk;
+        if (t0 >= end) break;
+        load();
     }
 }
 
-template <int G> int launch_g(const DecodeParams &p, float *mass, int64_t mass_len, cudaStream_t stream) {
-    constexpr int chunk = kThreads * MassCfg<G>::kTok;
-    const dim3 grid((unsigned)((p.context_limit + chunk - 1) / chunk), (unsigned)p.num_kv_heads, (unsigned)p.num_seqs);
-    return launch_pdl(decode_mass_kernel<G>, grid, dim3(kThreads), 0, stream, p, mass, mass_len);
+template <int V, int NP>
+int launch_t(const DecodeParams &p, float *mass, int64_t mass_len, cudaStream_t stream) {
+    constexpr int chunk = kThreads * tokens_per_thread(V * NP);
+    const int64_t chunks = (p.context_limit + chunk - 1) / chunk;
+    // a CTA takes several chunks where there are many of them, so that the joining of its heads'
+    // pairs is paid less often
+    const int64_t all = chunks * p.num_kv_heads * p.num_seqs;
+    const int rounds = (int)(all < 2048 ? 1 : (all / 1024 < 8 ? all / 1024 : 8));
+    const dim3 grid((unsigned)((chunks + rounds - 1) / rounds), (unsigned)p.num_kv_heads, (unsigned)p.num_seqs);
+    return launch_pdl(decode_mass_kernel<V, NP>, grid, dim3(kThreads), 0, stream, p, mass, mass_len, rounds);
 }
 
 }  // namespace
 
-int launch_decode_mass(const DecodeParams &p, float *mass, int64_t mass_len, cudaStream_t stream) {
+int launch_decode_mass(const DecodeParams &p, int heads_per_plane, float *mass, int64_t mass_len,
+                       cudaStream_t stream) {
     if (p.context_limit <= 0) return 0;
-    switch (p.group) {
-    case 1: return launch_g<1>(p, mass, mass_len, stream);
-    case 2: return launch_g<2>(p, mass, mass_len, stream);
-    case 4: return launch_g<4>(p, mass, mass_len, stream);
-    case 8: return launch_g<8>(p, mass, mass_len, stream);
-    case 16: return launch_g<16>(p, mass, mass_len, stream);
-    default: return launch_g<0>(p, mass, mass_len, stream);
+    const int planes = (p.group + heads_per_plane - 1) / heads_per_plane;
+    switch (heads_per_plane) {
+    case 1:
+        if (planes <= 1) return launch_t<1, 1>(p, mass, mass_len, stream);
+        if (planes <= 2) return launch_t<1, 2>(p, mass, mass_len, stream);
+        if (planes <= 4) return launch_t<1, 4>(p, mass, mass_len, stream);
+        if (planes <= 8) return launch_t<1, 8>(p, mass, mass_len, stream);
+        return launch_t<1, 16>(p, mass, mass_len, stream);
+    case 2:
+        if (planes <= 1) return launch_t<2, 1>(p, mass, mass_len, stream);
+        if (planes <= 2) return launch_t<2, 2>(p, mass, mass_len, stream);
+        if (planes <= 4) return launch_t<2, 4>(p, mass, mass_len, stream);
+        return launch_t<2, 8>(p, mass, mass_len, stream);
+    case 4: return launch_t<4, 2>(p, mass, mass_len, stream);
+    case 8: return launch_t<8, 2>(p, mass, mass_len, stream);
+    default: return -2;
     }
 }
 

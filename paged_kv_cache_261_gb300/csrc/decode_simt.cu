@@ -184,9 +184,9 @@ __global__ __launch_bounds__(kThreads) void decode_simt_kernel(const DecodeParam
                 if (g < GT) {
                     const float s = r < nvalid ? acc[hh] : -INFINITY;
                     if constexpr (kScore) {
-                        if (r < nvalid && g < G)
-                            p.ws_logits[(((int64_t)b * p.num_kv_heads + kvh) * p.logits_len + tile_start + r) * G + g] =
-                                s;
+                        if (r < nvalid && g < G)         // planes of one head: a warp's tokens side by side
+                            p.ws_logits[((int64_t)b * p.num_kv_heads + kvh) * p.logits_row +
+                                        (int64_t)g * p.logits_len + tile_start + r] = s;
                     }
                     float mx = s;
 #pragma unroll

@@ -648,21 +648,6 @@ __global__ __launch_bounds__(kThreads, 1) void decode_tc_kernel(const __grid_con
                     ok = false;
                     break;
                 }
-                if constexpr (kScore) {
-                    // [sequence][kv head][token][head]: a thread stores its token's heads
-                    float *lg = p.ws_logits + (((int64_t)I.b * p.num_kv_heads + I.kvh) * p.logits_len + tok) * G + c0;
-                    if (valid && G == GT) {             // whole vectors, aligned: G is a multiple of kC
-                        if constexpr (kC == 2) *reinterpret_cast<float2 *>(lg) = make_float2(s[0], s[1]);
-                        else
-#pragma unroll
-                            for (int u = 0; u < kC; u += 4)
-                                *reinterpret_cast<float4 *>(lg + u) = make_float4(s[u], s[u + 1], s[u + 2], s[u + 3]);
-                    } else if (valid) {
-#pragma unroll
-                        for (int u = 0; u < kC; ++u)
-                            if (c0 + u < G) lg[u] = s[u];
-                    }
-                }
                 float alpha[kC];
                 unsigned char *pb = sP + buf * kPBytes + (row >> 6) * (kN * 128);
                 const int colb = (row & 63) * 2;
@@ -701,6 +686,19 @@ __global__ __launch_bounds__(kThreads, 1) void decode_tc_kernel(const __grid_con
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.p_full[buf]);
+                if constexpr (kScore) {
+                    // this warpgroup's plane of the scores, whole vectors (columns past the group's
+                    // heads have room there), once the tile's P.V can start
+                    if (valid && c0 < G) {
+                        float *lg = p.ws_logits + ((int64_t)I.b * p.num_kv_heads + I.kvh) * p.logits_row +
+                                    ((int64_t)wg * p.logits_len + tok) * kC;
+                        if constexpr (kC == 2) *reinterpret_cast<float2 *>(lg) = make_float2(s[0], s[1]);
+                        else
+#pragma unroll
+                            for (int u = 0; u < kC; u += 4)
+                                *reinterpret_cast<float4 *>(lg + u) = make_float4(s[u], s[u + 1], s[u + 2], s[u + 3]);
+                    }
+                }
                 // the previous tile's O: this item's, or the last tile of the item before
                 if (tile > 0 ? !accumulate(it - 1, o_acc, alpha_prev) : !finish_pending()) {
                     ok = false;
@@ -861,7 +859,7 @@ int launch_decode_tc(const DecodeParams &p, int dtype, cudaStream_t stream) {
             c.ws_o = p.ws_o + rows * p.max_partitions * kD;
         }
         if (p.ws_logits) {
-            c.ws_logits = p.ws_logits + (int64_t)b0 * p.num_kv_heads * p.logits_len * p.group;
+            c.ws_logits = p.ws_logits + (int64_t)b0 * p.num_kv_heads * p.logits_row;
             c.ws_score_ml = p.ws_score_ml + rows * p.max_partitions * 2;
         }
         const int rc = dtype == PA_DTYPE_BF16

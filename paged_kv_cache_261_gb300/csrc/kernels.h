@@ -8,6 +8,9 @@
 
 namespace pa {
 
+// Heads of a group that a scored decode's workspace has room for.
+inline int padded_group(int group) { return group <= 2 ? 2 : (group <= 4 ? 4 : (group <= 8 ? 8 : 16)); }
+
 // Everything a decode kernel needs; built and validated by the C-ABI layer.
 struct DecodeParams {
     void *out;
@@ -50,13 +53,16 @@ struct DecodeParams {
     // while it runs. Not with the 8-bit kernel, whose two CTAs per SM, resident
     // early, slow that merge down more than their set-up gains.
     int chain_next;
-    // Scored decode: every score in log2 units, [num_seqs][num_kv_heads][logits_len][group],
-    // and every partition's (max, sum) pair, [B][H][P][2], those of whole rows included.
+    // Scored decode: every score in log2 units, [num_seqs][num_kv_heads][plane][logits_len][V]
+    // with V consecutive heads of the group to a plane (1, 2, 4 or 8: those that a thread of
+    // the kernel has of a token, so that its stores fill whole sectors), room for
+    // padded_group(group) heads; and every partition's (max, sum) pair, [B][H][P][2], those of whole rows included.
     // The sum is of the fp32 weights; ws_ml's is of the weights as the P.V product has
     // them (16 bits in the tensor-core kernel).
     float *ws_logits;
     float *ws_score_ml;
     int logits_len;
+    int64_t logits_row;        // floats per (sequence, kv head): padded_group * logits_len
     // 4-bit cache: (K scale, K zero, V scale, V zero) float16,
     // [num_blocks][num_kv_heads][block_size][4]
     const void *kv_params;

@@ -55,9 +55,12 @@ int launch_decode_int4(const DecodeParams &p, const Int4Work &ws, int64_t max_ct
                        cudaStream_t stream);
 
 // Adds each token's softmax weights, summed over the query heads of its kv head, to
-// mass [num_seqs, num_kv_heads, mass_len], from the scores and (max, sum) pairs that a
-// decode with p.ws_logits left in the workspace.
-int launch_decode_mass(const DecodeParams &p, float *mass, int64_t mass_len, cudaStream_t stream);
+// mass [num_seqs, num_kv_heads, mass_len], from the scores (planes of heads_per_plane) and
+// (max, sum) pairs that a decode with p.ws_logits left in the workspace.
+int launch_decode_mass(const DecodeParams &p, int heads_per_plane, float *mass, int64_t mass_len,
+                       cudaStream_t stream);
+// Heads per plane of the kernels: SIMT 1, 4-bit 2, and half the padded group here.
+inline int score_plane_tc(int group) { return group <= 4 ? 2 : (group <= 8 ? 4 : 8); }
 
 // One array of rows that an eviction moves: row of (block, offset, kv head) at
 // base + block * block_stride + offset * token_stride + head * head_stride.

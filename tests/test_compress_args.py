@@ -121,11 +121,14 @@ def test_workspace_sizes(pa):
         # a partial of a group for every warp of the grid and every row, with and without the scores
         n, with_mass = (pa.decode_int4_workspace_bytes(B, H, Hk, D, ctx, w) for w in (False, True))
         assert n >= min(B, 1536) * Hk * (8 + H // Hk * (8 + 4 * D))
-        assert 0 <= with_mass - n - B * H * (8 + 4 * ctx) < 256
+        # the scores: the heads of a group rounded up to 2, 4, 8 or 16, the tokens to a multiple of 4
+        G = H // Hk
+        scores = B * Hk * (2 if G <= 2 else 4 if G <= 4 else 8 if G <= 8 else 16) * -(-ctx // 4) * 16
+        assert 0 <= with_mass - n - B * H * 8 - scores < 256
         P = -(-ctx // pa.decode_partition_size(B, ctx, part))
         split = B * H * P * (2 + D) * 4 if P > 1 else 0
-        n = pa.decode_scored_workspace_bytes(B, H, D, ctx, part)
-        assert 0 <= n - (split + B * H * P * 8 + B * H * ctx * 4) < 3 * 256
+        n = pa.decode_scored_workspace_bytes(B, H, Hk, D, ctx, part)
+        assert 0 <= n - (split + B * H * P * 8 + scores) < 3 * 256
     # a larger batch never needs less
     sizes = [pa.decode_int4_workspace_bytes(B, 32, 8, 128, 2048) for B in (1, 2, 64, 512, 5000)]
     assert sizes == sorted(sizes)

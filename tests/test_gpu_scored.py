@@ -127,7 +127,7 @@ def test_scored_errors(pa):
     case.lens = np.array([64, 60], np.int32)
     case.k[0], case.v[0] = case.k[0][:64], case.v[0][:64]
     case.check(mass, np.zeros((2, 2, 64)))
-    need = pa.decode_scored_workspace_bytes(2, 8, 128, case.bt.shape[1] * 16, 0)
+    need = pa.decode_scored_workspace_bytes(2, 8, 2, 128, case.bt.shape[1] * 16, 0)
     with pytest.raises(pa.PagedAttnError) as e:
         case.run(pa, mass, workspace=torch.empty(need - 16, dtype=torch.uint8, device=dev()))
     assert e.value.status == pa.PA_ERR_WORKSPACE
