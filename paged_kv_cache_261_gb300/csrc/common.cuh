@@ -82,6 +82,23 @@ __device__ __forceinline__ float fast_exp2(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Stores that should stay in L2 until they are read (scratch between two kernels), against
+// the streams that pass by. policy: from l2_keep().
+__device__ __forceinline__ uint64_t l2_keep() {
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(policy));
+    return policy;
+}
+__device__ __forceinline__ void store_keep(float *dst, float2 v, uint64_t policy) {
+    asm volatile("st.global.L2::cache_hint.v2.f32 [%0], {%1, %2}, %3;" ::"l"(dst), "f"(v.x), "f"(v.y), "l"(policy)
+                 : "memory");
+}
+__device__ __forceinline__ void store_keep(float *dst, float4 v, uint64_t policy) {
+    asm volatile("st.global.L2::cache_hint.v4.f32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(dst), "f"(v.x), "f"(v.y), "f"(v.z),
+                 "f"(v.w), "l"(policy)
+                 : "memory");
+}
+
 // Launch with programmatic stream serialization: the kernel may start while the
 // previous kernel in the stream is still finishing, so it must execute
 // griddepcontrol.wait before reading anything that kernel (or any earlier work)

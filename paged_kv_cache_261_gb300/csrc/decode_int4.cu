@@ -343,6 +343,7 @@ __global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_int4_kernel(
     uint32_t phase = 0;                                // and its barrier's phase
     bool ok = true;
 
+    [[maybe_unused]] const uint64_t keep = kScore ? l2_keep() : 0;
     const T *q = reinterpret_cast<const T *>(p.q);
     while (left > 0) {
         // ---- the part of row (b, kvh) that lies in this run
@@ -460,10 +461,9 @@ __global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_int4_kernel(
                         if constexpr (kScore) {
                             const int pl = nt * 4 + lj;    // planes of two heads
                             if (valid && 2 * pl < G)
-                                *reinterpret_cast<float2 *>(
-                                    p.ws_logits + ((int64_t)I_b * Hk + I_kvh) * p.logits_row +
-                                    ((int64_t)pl * p.logits_len + ts + t) * 2) =
-                                    make_float2(S[sub][nt][2 * r], S[sub][nt][2 * r + 1]);
+                                store_keep(p.ws_logits + ((int64_t)I_b * Hk + I_kvh) * p.logits_row +
+                                               ((int64_t)pl * p.logits_len + ts + t) * 2,
+                                           make_float2(S[sub][nt][2 * r], S[sub][nt][2 * r + 1]), keep);
                         }
                     }
                 }
