@@ -148,17 +148,26 @@ def _check(rc: int, what: str) -> None:
 # torch glue
 # ---------------------------------------------------------------------------
 
+_torch_module = None
+_dtype_codes: dict = {}
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _dtype_codes.update({torch.float32: PA_DTYPE_F32, torch.float16: PA_DTYPE_F16,
+                             torch.bfloat16: PA_DTYPE_BF16})
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
-    torch = _torch()
-    m = {torch.float32: PA_DTYPE_F32, torch.float16: PA_DTYPE_F16, torch.bfloat16: PA_DTYPE_BF16}
-    if t.dtype not in m:
+    _torch()
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    return m[t.dtype]
+    return code
 
 
 def _is_fp8_cache(t) -> bool:
@@ -181,6 +190,11 @@ def _on(device):
     if idx is None or idx == _torch().cuda.current_device():
         return _SAME_DEVICE
     return _torch().cuda.device(idx)
+
+
+def _elsewhere(device) -> bool:
+    """Whether a call has to go through _on (the tensors are on another device than the current one)."""
+    return device.index != _torch_module._C._cuda_getDevice()
 
 
 def _stream_ptr(stream, device) -> int:
@@ -604,55 +618,71 @@ def paged_attention_decode_fp8_append(out, q, k_new, v_new, slot_mapping, key_ca
 def _int4_caches(key_cache, value_cache, kv_params, dev):
     """Checks the tensors of a 4-bit cache; (num_blocks, num_kv_heads, block_size, head_dim)."""
     torch = _torch()
-    _cuda(key_cache, "key_cache", torch.uint8)
-    _all_cuda(dev, (value_cache, "value_cache", torch.uint8), (kv_params, "kv_params", torch.float16))
-    if key_cache.dim() != 4 or value_cache.shape != key_cache.shape:
+    u8, f16 = torch.uint8, torch.float16
+    if not (key_cache.is_cuda and key_cache.dtype == u8 and key_cache.is_contiguous() and
+            value_cache.device == dev and value_cache.dtype == u8 and value_cache.is_contiguous() and
+            kv_params.device == dev and kv_params.dtype == f16 and kv_params.is_contiguous()):
+        _cuda(key_cache, "key_cache", u8)
+        _cuda(value_cache, "value_cache", u8, dev)
+        _cuda(kv_params, "kv_params", f16, dev)
+    shape = key_cache.shape
+    if len(shape) != 4 or value_cache.shape != shape:
         raise ValueError("key_cache and value_cache must be [num_blocks, num_kv_heads, block_size, head_dim / 2]")
-    nb, hk, bs, half = key_cache.shape
+    nb, hk, bs, half = shape
     if kv_params.shape != (nb, hk, bs, 4):
         raise ValueError(f"kv_params must be [{nb}, {hk}, {bs}, 4]")
     return nb, hk, bs, 2 * half
 
 
 def _int4_rows(k, v, slot_mapping, hk, d, dev):
-    _all_cuda(dev, (k, "k", k.dtype), (v, "v", k.dtype), (slot_mapping, "slot_mapping", _torch().int32))
-    if slot_mapping.dim() != 1:
+    i32 = _torch_module.int32
+    if not (k.device == dev and k.is_contiguous() and v.device == dev and v.dtype == k.dtype and v.is_contiguous() and
+            slot_mapping.device == dev and slot_mapping.dtype == i32 and slot_mapping.is_contiguous()):
+        _cuda(k, "k", None, dev)
+        _cuda(v, "v", k.dtype, dev)
+        _cuda(slot_mapping, "slot_mapping", i32, dev)
+    shape = slot_mapping.shape
+    if len(shape) != 1:
         raise ValueError("slot_mapping must be [T]")
-    T = slot_mapping.shape[0]
+    T = shape[0]
     if k.shape != (T, hk, d) or v.shape != (T, hk, d):
         raise ValueError(f"k/v must be [{T}, {hk}, {d}]")
     return T
+
+
+def _int4_move(fn, what, k, v, slot_mapping, key_cache, value_cache, kv_params, stream):
+    dev = key_cache.device
+    nb, hk, bs, d = _int4_caches(key_cache, value_cache, kv_params, dev)
+    T = _int4_rows(k, v, slot_mapping, hk, d, dev)
+    if _elsewhere(dev):
+        with _on(dev):
+            return _int4_move(fn, what, k, v, slot_mapping, key_cache, value_cache, kv_params,
+                              stream or _torch().cuda.current_stream(dev))
+    rc = fn(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), T, key_cache.data_ptr(), value_cache.data_ptr(),
+            kv_params.data_ptr(), nb, bs, hk, d, _dtype_code(k), _stream_ptr(stream, dev))
+    if rc:
+        _check(rc, what)
 
 
 def paged_kv_write_int4(k, v, slot_mapping, key_cache, value_cache, kv_params, stream=None) -> None:
     """Scatter k/v [T, Hk, D] (fp32/fp16/bf16) into 4-bit caches [NB, Hk, bs, D / 2] with
     kv_params [NB, Hk, bs, 4] at slot_mapping[T]: per row, zero = f16(min), scale =
     f16((max - min) / 15), code = the nearest of (x - zero) / scale in 0..15."""
-    dev = key_cache.device
-    nb, hk, bs, d = _int4_caches(key_cache, value_cache, kv_params, dev)
-    T = _int4_rows(k, v, slot_mapping, hk, d, dev)
-    with _on(dev):
-        rc = _lib.pa_paged_kv_write_int4(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), T, key_cache.data_ptr(),
-                                         value_cache.data_ptr(), kv_params.data_ptr(), nb, bs, hk, d, _dtype_code(k),
-                                         _stream_ptr(stream, dev))
-    _check(rc, "pa_paged_kv_write_int4")
+    _int4_move(_lib.pa_paged_kv_write_int4, "pa_paged_kv_write_int4", k, v, slot_mapping, key_cache, value_cache,
+               kv_params, stream)
 
 
 def paged_kv_read_int4(k, v, slot_mapping, key_cache, value_cache, kv_params, stream=None) -> None:
     """The inverse: k[t], v[t] [T, Hk, D] (fp32/fp16/bf16) = the values held at
     slot_mapping[t]; rows of slot -1 stay as they are."""
-    dev = key_cache.device
-    nb, hk, bs, d = _int4_caches(key_cache, value_cache, kv_params, dev)
-    T = _int4_rows(k, v, slot_mapping, hk, d, dev)
-    with _on(dev):
-        rc = _lib.pa_paged_kv_read_int4(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), T, key_cache.data_ptr(),
-                                        value_cache.data_ptr(), kv_params.data_ptr(), nb, bs, hk, d, _dtype_code(k),
-                                        _stream_ptr(stream, dev))
-    _check(rc, "pa_paged_kv_read_int4")
+    _int4_move(_lib.pa_paged_kv_read_int4, "pa_paged_kv_read_int4", k, v, slot_mapping, key_cache, value_cache,
+               kv_params, stream)
 
 
 def _mass(mass, name, B, hk, dev):
-    _all_cuda(dev, (mass, name, _torch().float32))
+    f32 = _torch().float32
+    if not (mass.device == dev and mass.dtype == f32 and mass.is_contiguous()):
+        _cuda(mass, name, f32, dev)
     if mass.dim() != 3 or mass.shape[0] != B or mass.shape[1] != hk:
         raise ValueError(f"{name} must be [{B}, {hk}, length]")
     return mass.shape[2]
@@ -682,6 +712,26 @@ def decode_int4_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int
                                                    int(with_mass)))
 
 
+def _decode_args(out, q, block_tables, context_lens, d, dev, dtype):
+    """Checks what every decode call takes besides its caches; (B, H, MB)."""
+    i32 = _torch_module.int32
+    if not (q.device == dev and q.dtype == dtype and q.is_contiguous() and out.device == dev and out.dtype == dtype and
+            out.is_contiguous() and block_tables.device == dev and block_tables.dtype == i32 and
+            block_tables.is_contiguous() and context_lens.device == dev and context_lens.dtype == i32 and
+            context_lens.is_contiguous()):
+        _cuda(q, "q", dtype, dev)
+        _cuda(out, "out", dtype, dev)
+        _cuda(block_tables, "block_tables", i32, dev)
+        _cuda(context_lens, "context_lens", i32, dev)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != d or out.shape != shape:
+        raise ValueError("q/out must be [B, H, head_dim]")
+    B, table = shape[0], block_tables.shape
+    if len(table) != 2 or table[0] != B or context_lens.shape != (B,):
+        raise ValueError("block_tables must be [B, MB] and context_lens [B]")
+    return B, shape[1], table[1]
+
+
 def paged_attention_decode_int4(out, q, key_cache, value_cache, kv_params, block_tables, context_lens, scale: float,
                                 max_context_len: int = 0, workspace=None, mass=None, stream=None) -> None:
     """Decode attention over 4-bit caches [NB, Hk, bs, D / 2] with kv_params [NB, Hk, bs, 4].
@@ -689,36 +739,31 @@ def paged_attention_decode_int4(out, q, key_cache, value_cache, kv_params, block
     q, out [B, H, D] bf16 or fp16. mass: optional float32 [B, Hk, M], to which each token's
     weight is added (see paged_attention_decode_scored). Other arguments as
     paged_attention_decode."""
-    torch = _torch()
     dev = key_cache.device
     nb, hk, bs, d = _int4_caches(key_cache, value_cache, kv_params, dev)
-    _all_cuda(dev, (q, "q", q.dtype), (out, "out", q.dtype), (block_tables, "block_tables", torch.int32),
-              (context_lens, "context_lens", torch.int32))
-    if q.dim() != 3:
-        raise ValueError("q/out must be [B, H, head_dim]")
-    B, H, D = q.shape
-    if D != d or out.shape != q.shape:
-        raise ValueError("q/out must be [B, H, head_dim]")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
-        raise ValueError("block_tables must be [B, MB] and context_lens [B]")
-    mb = block_tables.shape[1]
+    B, H, mb = _decode_args(out, q, block_tables, context_lens, d, dev, q.dtype)
     mass_ptr, mass_len = None, 0
     if mass is not None:
         mass_len = _mass(mass, "mass", B, hk, dev)
         mass_ptr = mass.data_ptr()
+    if _elsewhere(dev):
+        with _on(dev):
+            return paged_attention_decode_int4(out, q, key_cache, value_cache, kv_params, block_tables, context_lens,
+                                               scale, max_context_len, workspace, mass,
+                                               stream or _torch().cuda.current_stream(dev))
     sp = _stream_ptr(stream, dev)
-    with _on(dev):
-        need = _memo(decode_int4_workspace_bytes, B, H, hk, D, max_context_len or mb * bs, mass is not None, dev.index)
-        if workspace is None:
-            workspace = _workspace(dev, sp, need)
-        else:
-            _cuda(workspace, "workspace", torch.uint8, dev)
-        rc = _lib.pa_paged_attention_decode_int4(out.data_ptr(), q.data_ptr(), key_cache.data_ptr(),
-                                                 value_cache.data_ptr(), kv_params.data_ptr(), mass_ptr, mass_len,
-                                                 block_tables.data_ptr(), mb, context_lens.data_ptr(), B, H, hk, D, bs,
-                                                 nb, float(scale), int(max_context_len), workspace.data_ptr(),
-                                                 workspace.numel(), _dtype_code(q), sp)
-    _check(rc, "pa_paged_attention_decode_int4")
+    if workspace is None:
+        workspace = _workspace(dev, sp, _memo(decode_int4_workspace_bytes, B, H, hk, d, max_context_len or mb * bs,
+                                              mass is not None, dev.index))
+    else:
+        _cuda(workspace, "workspace", _torch_module.uint8, dev)
+    rc = _lib.pa_paged_attention_decode_int4(out.data_ptr(), q.data_ptr(), key_cache.data_ptr(),
+                                             value_cache.data_ptr(), kv_params.data_ptr(), mass_ptr, mass_len,
+                                             block_tables.data_ptr(), mb, context_lens.data_ptr(), B, H, hk, d, bs, nb,
+                                             float(scale), int(max_context_len), workspace.data_ptr(),
+                                             workspace.numel(), _dtype_code(q), sp)
+    if rc:
+        _check(rc, "pa_paged_attention_decode_int4")
 
 
 def decode_scored_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
@@ -733,38 +778,36 @@ def paged_attention_decode_scored(out, q, mass, key_cache, value_cache, block_ta
                                   stream=None) -> None:
     """paged_attention_decode that also adds each token's attention weight, summed over the
     query heads of its kv head, to mass float32 [B, Hk, M]. Entries past a context stay."""
-    torch = _torch()
-    dev = key_cache.device
-    dt = key_cache.dtype
-    _cuda(key_cache, "key_cache")
-    _all_cuda(dev, (value_cache, "value_cache", dt), (q, "q", dt), (out, "out", dt),
-              (block_tables, "block_tables", torch.int32), (context_lens, "context_lens", torch.int32))
-    if key_cache.dim() != 4 or q.dim() != 3:
-        raise ValueError("caches must be [NB, bs, Hk, D] and q/out [B, H, D]")
-    nb, bs, hk, d = key_cache.shape
-    if value_cache.shape != key_cache.shape:
-        raise ValueError("value_cache shape differs from key_cache")
-    B, H, D = q.shape
-    if D != d or out.shape != q.shape:
-        raise ValueError("q/out must be [B, H, head_dim]")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
-        raise ValueError("block_tables must be [B, MB] and context_lens [B]")
+    _torch()
+    dev, dt = key_cache.device, key_cache.dtype
+    if not (key_cache.is_cuda and key_cache.is_contiguous() and value_cache.device == dev and
+            value_cache.dtype == dt and value_cache.is_contiguous()):
+        _cuda(key_cache, "key_cache")
+        _cuda(value_cache, "value_cache", dt, dev)
+    shape = key_cache.shape
+    if len(shape) != 4 or value_cache.shape != shape:
+        raise ValueError("key_cache and value_cache must be [num_blocks, block_size, num_kv_heads, head_dim]")
+    nb, bs, hk, d = shape
+    B, H, mb = _decode_args(out, q, block_tables, context_lens, d, dev, dt)
     mass_len = _mass(mass, "mass", B, hk, dev)
-    mb = block_tables.shape[1]
+    if _elsewhere(dev):
+        with _on(dev):
+            return paged_attention_decode_scored(out, q, mass, key_cache, value_cache, block_tables, context_lens, scale,
+                                                 max_context_len, partition_size, workspace,
+                                                 stream or _torch().cuda.current_stream(dev))
     sp = _stream_ptr(stream, dev)
-    need = _memo(decode_scored_workspace_bytes, B, H, hk, D, max_context_len or mb * bs, partition_size)
     if workspace is None:
-        workspace = _workspace(dev, sp, need)
+        workspace = _workspace(dev, sp, _memo(decode_scored_workspace_bytes, B, H, hk, d, max_context_len or mb * bs,
+                                              partition_size))
     else:
-        _cuda(workspace, "workspace", torch.uint8, dev)
-    with _on(dev):
-        rc = _lib.pa_paged_attention_decode_scored(out.data_ptr(), q.data_ptr(), mass.data_ptr(), mass_len,
-                                                   key_cache.data_ptr(), value_cache.data_ptr(),
-                                                   block_tables.data_ptr(), mb, context_lens.data_ptr(), B, H, hk, D,
-                                                   bs, nb, float(scale), int(max_context_len), int(partition_size),
-                                                   workspace.data_ptr(), workspace.numel(), _dtype_code(key_cache),
-                                                   sp)
-    _check(rc, "pa_paged_attention_decode_scored")
+        _cuda(workspace, "workspace", _torch_module.uint8, dev)
+    rc = _lib.pa_paged_attention_decode_scored(out.data_ptr(), q.data_ptr(), mass.data_ptr(), mass_len,
+                                               key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(),
+                                               mb, context_lens.data_ptr(), B, H, hk, d, bs, nb, float(scale),
+                                               int(max_context_len), int(partition_size), workspace.data_ptr(),
+                                               workspace.numel(), _dtype_code(key_cache), sp)
+    if rc:
+        _check(rc, "pa_paged_attention_decode_scored")
 
 
 def paged_kv_evict(kept, mass, mass_out, key_cache, value_cache, block_tables, out_block_tables, context_lens,
