@@ -167,11 +167,16 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSlice = 48 * 1024;    // masses per CTA: 192 KB of shared memory
+constexpr int kList = 2048;
 __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictParams p) {
     extern __shared__ __align__(16) float slice[];      // this CTA's masses
     __shared__ __align__(16) int hist[kBins];
     __shared__ uint32_t seg[kWarps];    // sums of each warp
     __shared__ int found[2];            // the digit of the threshold, and how many keys lie above it
+    __shared__ uint32_t list[kList];    // keys of the candidates that share the threshold's first digit,
+    __shared__ unsigned char list_warp[kList];   // whose warp's tokens they are,
+    __shared__ int listed;                       // how many,
+    __shared__ uint32_t extra[kWarps];           // and how many of a warp's stay, ties << 16
     __shared__ uint32_t counts;         // of this CTA's slice: tokens that stay anyway, ties << 16
     cg::cluster_group cluster = cg::this_cluster();
     const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -188,9 +193,24 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictParam
     int want = s.n - s.r;               // how many of them stay
     const bool all = want >= cand, none = want <= 0;
 
-    // this CTA's tokens [t0, t0 + len), and this warp's part of them
+    // this CTA's tokens [t0, t0 + len), and this warp's part [w0, w1) of them
     const int per = (((s.c + nc - 1) / nc) + 3) & ~3;
     const int t0 = min(s.c, rank * per), len = min(s.c, t0 + per) - t0;
+    const int n_cand = max(0, min(len, cand - t0));
+    const int wlen = (((len + kWarps - 1) / kWarps) + 127) & ~127;
+    const int w0 = min(len, warp * wlen), w1 = min(len, w0 + wlen);
+    const bool search = !all && !none;
+    auto sync = [&]() {
+        if (nc > 1) cluster.sync();
+        else __syncthreads();
+    };
+    static_assert(kBins == 4 * kThreads, "four bins a thread");
+    reinterpret_cast<int4 *>(hist)[tid] = make_int4(0, 0, 0, 0);
+    if (tid < kWarps) extra[tid] = 0;
+    if (tid == 0) listed = 0;
+    __syncthreads();
+    // the masses come in, and the first digit of their keys is counted
+    constexpr int kFirst = 32 - kDigitBits;
     {
         constexpr int kUnroll = 8;
         for (int i0 = 0; i0 < len; i0 += kThreads * kUnroll) {
@@ -204,28 +224,28 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictParam
             for (int u = 0; u < kUnroll; ++u) {
                 const int i = i0 + u * kThreads + tid;
                 if (i < len) slice[i] = v[u];
+                if (search && i < n_cand) atomicAdd(&hist[mass_key(v[u]) >> kFirst], 1);
             }
         }
     }
-    auto sync = [&]() {
-        if (nc > 1) cluster.sync();
-        else __syncthreads();
-    };
-    uint32_t key = 0, mask = 0;         // the digits found so far
-    if (!all && !none) {
-        const int n_cand = max(0, min(len, cand - t0));
-        static_assert(kBins == 4 * kThreads, "four bins a thread");
-        for (int shift = 32 - kDigitBits;; shift = shift > kDigitBits ? shift - kDigitBits : 0) {
+    uint32_t key = 0, mask = 0, sum = 0;   // the digits found; this warp's tokens that stay anyway, ties << 16
+    bool short_list = false;
+    if (search) {
+        for (int shift = kFirst;; shift = shift > kDigitBits ? shift - kDigitBits : 0) {
             const int bits = shift > 0 ? kDigitBits : 32 - 2 * kDigitBits;
-            reinterpret_cast<int4 *>(hist)[tid] = make_int4(0, 0, 0, 0);
-            __syncthreads();
-            for (int i = tid; i < n_cand; i += kThreads) {
-                const uint32_t k = mass_key(slice[i]);
-                if ((k & mask) == key) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1);
+            const uint32_t digits = (1u << bits) - 1u;
+            if (shift != kFirst) {
+                reinterpret_cast<int4 *>(hist)[tid] = make_int4(0, 0, 0, 0);
+                __syncthreads();
+                const int n = short_list ? listed : n_cand;
+                for (int i = tid; i < n; i += kThreads) {
+                    const uint32_t k = short_list ? list[i] : mass_key(slice[i]);
+                    if ((k & mask) == key) atomicAdd(&hist[(k >> shift) & digits], 1);
+                }
             }
             sync();
             // thread i: the bins counted from the top, 4 i to 4 i + 3, of the whole cluster
-            const int i0 = (1 << bits) - 1 - 4 * tid;
+            const int i0 = (int)digits - 4 * tid;
             int n[4] = {0, 0, 0, 0};
             if (i0 >= 3) {
                 for (int c = 0; c < nc; ++c) {
@@ -269,29 +289,54 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictParam
             }
             sync();                     // every CTA has read the counts
             key |= (uint32_t)found[0] << shift;
-            mask |= ((1u << bits) - 1u) << shift;
+            mask |= digits << shift;
             want -= found[1];
             if (shift == 0) break;
+            if (shift == kFirst && hist[found[0]] <= kList) {
+                // few candidates share the threshold's first digit: the other digits, and the
+                // verdict on the rest, need no further pass over the slice
+                short_list = true;
+                for (int i = w0 + 4 * lane; i < w1; i += 128) {
+                    const float4 x4 = *reinterpret_cast<const float4 *>(slice + i);
+                    const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t k = mass_key(x[j]), d = k >> kFirst;
+                        const bool in = i + j < n_cand;
+                        sum += i + j < w1 && (!in || d > (key >> kFirst));
+                        if (in && i + j < w1 && d == key >> kFirst) {
+                            const int at = atomicAdd(&listed, 1);
+                            list[at] = k;
+                            list_warp[at] = (unsigned char)warp;
+                        }
+                    }
+                }
+                __syncthreads();
+            }
         }
     }
     __syncthreads();
-    // ---- what stays: the recent tokens, keys above `key`, and the first `want` equal to it.
-    // Warp w has the tokens [w0, w1) of the slice, a lane four neighbours at a time.
+    // ---- what stays: the recent tokens, keys above `key`, and the first `want` equal to it
     static_assert(kMaxSlice < 65536, "counts of a slice in 16 bits");
-    const int wlen = (((len + kWarps - 1) / kWarps) + 127) & ~127;
-    const int w0 = min(len, warp * wlen), w1 = min(len, w0 + wlen);
     // token i of the slice: 1 = stays anyway, 1 << 16 = equal to the threshold
     auto verdict = [&](float x, int i) -> uint32_t {
         const uint32_t k = mass_key(x);
         const bool sure = t0 + i >= cand || all || (!none && k > key);
         return i >= w1 ? 0u : (sure ? 1u : (!none && k == key ? 0x10000u : 0u));
     };
-    uint32_t sum = 0;
-    for (int i = w0 + 4 * lane; i < w1; i += 128) {
-        const float4 x = *reinterpret_cast<const float4 *>(slice + i);
-        sum += verdict(x.x, i) + verdict(x.y, i + 1) + verdict(x.z, i + 2) + verdict(x.w, i + 3);
+    if (short_list) {
+        for (int i = tid; i < listed; i += kThreads) {
+            const uint32_t k = list[i];
+            if (k >= key) atomicAdd(&extra[list_warp[i]], k > key ? 1u : 0x10000u);
+        }
+        __syncthreads();
+    } else {
+        for (int i = w0 + 4 * lane; i < w1; i += 128) {
+            const float4 x = *reinterpret_cast<const float4 *>(slice + i);
+            sum += verdict(x.x, i) + verdict(x.y, i + 1) + verdict(x.z, i + 2) + verdict(x.w, i + 3);
+        }
     }
-    sum = __reduce_add_sync(0xffffffffu, sum);
+    sum = __reduce_add_sync(0xffffffffu, sum) + extra[warp];
     if (lane == 0) seg[warp] = sum;
     __syncthreads();
     uint32_t up_to = lane < kWarps ? seg[lane] : 0u;    // of the warps 0 .. lane

@@ -27,6 +27,8 @@ def masses(rng, shape, kind):
         return rng.integers(0, 4, shape).astype(np.float32) * np.float32(0.25)
     if kind == "equal":
         return np.full(shape, 0.125, np.float32)
+    if kind == "crowd":                      # one exponent and two mantissa bits for all but a few
+        return (1.0 + 0.2 * rng.random(shape)).astype(np.float32)
     m = rng.random(shape).astype(np.float32) ** 8
     if kind == "special":
         flat = m.reshape(-1)
@@ -143,7 +145,7 @@ def test_evict_is_bit_exact(pa, dtype, Hk, D, bs, in_place):
     run_case(pa, 3 + D + bs, LENS, KEEP, 7, Hk, D, bs, dtype, in_place=in_place)
 
 
-@pytest.mark.parametrize("kind", ["ties", "equal", "special"])
+@pytest.mark.parametrize("kind", ["ties", "equal", "special", "crowd"])
 @pytest.mark.parametrize("recent", [0, 1, 33, 100000])
 def test_evict_ties_and_special_masses(pa, kind, recent):
     for in_place in (False, True):
@@ -154,6 +156,7 @@ def test_evict_ties_and_special_masses(pa, kind, recent):
 def test_evict_long(pa, keep, recent):
     run_case(pa, 29, [40000, 12345], [keep, keep], recent, 1, 128, 16, "int4")
     run_case(pa, 30, [40000, 12345], [keep, keep], recent, 2, 64, 64, "bf16", kind="ties", in_place=True)
+    run_case(pa, 31, [40000, 12345], [keep, keep], recent, 1, 64, 64, "f16", kind="crowd", in_place=True)
 
 
 def test_evict_rows_beyond_a_cluster(pa):
