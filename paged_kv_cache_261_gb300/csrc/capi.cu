@@ -788,7 +788,7 @@ int pa_paged_attention_decode_scored(void *out, const void *q, float *mass, int6
     const bool tc = choice == DecodeKernel::Tc || (choice == DecodeKernel::Auto && pa::decode_tc_supported(p, dtype));
     int krc = tc ? pa::launch_decode_tc(p, dtype, s) : pa::launch_decode_simt(p, dtype, s);
     if (krc == 0 && P > 1) krc = pa::launch_decode_reduce(p, dtype, s);
-    if (krc == 0) krc = pa::launch_decode_mass(p, tc ? pa::score_plane_tc(p.group) : 1, mass, mass_len, s);
+    if (krc == 0) krc = pa::launch_decode_mass(p, tc ? pa::score_plane_tc(p.group) : 1, mass, mass_len, nullptr, s);
     if (owned) cudaFreeAsync(owned, s);
     if (krc == -2) return PA_ERR_UNSUPPORTED;
     return krc == 0 ? PA_OK : PA_ERR_CUDA;
@@ -911,8 +911,7 @@ int pa_paged_attention_decode_int4(void *out, const void *q, const void *key_cac
     }
     p.max_partitions = 1;                     // as the accumulation of the weights sees it
     p.partition_size = INT32_MAX;
-    int krc = pa::launch_decode_int4(p, w, max_ctx, device_sm_count(), dtype, s);
-    if (krc == 0 && mass) krc = pa::launch_decode_mass(p, 2, mass, mass_len, s);
+    const int krc = pa::launch_decode_int4(p, w, max_ctx, device_sm_count(), mass, mass_len, dtype, s);
     if (owned) cudaFreeAsync(owned, s);
     if (krc == -2) return PA_ERR_UNSUPPORTED;
     return krc == 0 ? PA_OK : PA_ERR_CUDA;

@@ -652,7 +652,7 @@ __global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_int4_kernel(
 constexpr int kJoinThreads = 128;
 constexpr int kJoinBatch = 8;
 
-template <typename T, int D, bool kScore, int WPR>
+template <typename T, int D, int WPR>
 __global__ __launch_bounds__(kJoinThreads) void decode_int4_join_kernel(const DecodeParams p, const Int4Work ws) {
     constexpr int N = D / 32;                          // channels of a lane
     __shared__ float2 ml_s[4];
@@ -660,8 +660,9 @@ __global__ __launch_bounds__(kJoinThreads) void decode_int4_join_kernel(const De
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = warp % WPR;
     const int64_t head = (int64_t)blockIdx.x * (4 / WPR) + warp / WPR;   // (sequence, query head)
-    asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // after the wait: the accumulation of the weights relies on the decode having finished
+    asm volatile("griddepcontrol.launch_dependents;");
     if (head >= (int64_t)p.num_seqs * p.num_heads) return;   // with WPR 4, the whole CTA
     const int G = p.group;
     const int64_t row = head / G;
@@ -736,7 +737,6 @@ __global__ __launch_bounds__(kJoinThreads) void decode_int4_join_kernel(const De
 #pragma unroll
             for (int u = 0; u < N; ++u) acc[u] = fmaf(o_s[w][lane * N + u], f, acc[u]);
         }
-        m = M;
     }
     const float inv = 1.f / l;
     alignas(8) T h[N];
@@ -745,7 +745,6 @@ __global__ __launch_bounds__(kJoinThreads) void decode_int4_join_kernel(const De
     T *dst = reinterpret_cast<T *>(p.out) + head * D + lane * N;
     if constexpr (N == 4) *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<uint2 *>(h);
     else *reinterpret_cast<uint32_t *>(dst) = *reinterpret_cast<uint32_t *>(h);
-    if (kScore && lane == 0) reinterpret_cast<float2 *>(p.ws_score_ml)[head] = make_float2(m, l);
 }
 
 template <typename T, int D, int GT, bool kScore>
@@ -764,9 +763,9 @@ int launch_t(const DecodeParams &p, const Int4Work &ws, int grid, cudaStream_t s
     // partials a row, about: (runs + rows) / rows
     const int64_t heads = (int64_t)p.num_seqs * p.num_heads, rows = (int64_t)p.num_seqs * p.num_kv_heads;
     if ((int64_t)grid * C::kWarps <= 8 * rows)
-        return launch_pdl(decode_int4_join_kernel<T, D, kScore, 1>, dim3((unsigned)((heads + 3) / 4)),
+        return launch_pdl(decode_int4_join_kernel<T, D, 1>, dim3((unsigned)((heads + 3) / 4)),
                           dim3(kJoinThreads), 0, stream, p, ws);
-    return launch_pdl(decode_int4_join_kernel<T, D, kScore, 4>, dim3((unsigned)heads), dim3(kJoinThreads), 0, stream, p,
+    return launch_pdl(decode_int4_join_kernel<T, D, 4>, dim3((unsigned)heads), dim3(kJoinThreads), 0, stream, p,
                       ws);
 }
 
@@ -815,8 +814,8 @@ Int4WorkSizes decode_int4_work_sizes(int64_t num_seqs, int64_t num_heads, int64_
     return s;
 }
 
-int launch_decode_int4(const DecodeParams &p, const Int4Work &ws, int64_t max_ctx, int sms, int dtype,
-                       cudaStream_t stream) {
+int launch_decode_int4(const DecodeParams &p, const Int4Work &ws, int64_t max_ctx, int sms, float *mass,
+                       int64_t mass_len, int dtype, cudaStream_t stream) {
     if (!decode_int4_supported(p, dtype) || row_stages(max_ctx) * p.num_kv_heads > INT32_MAX) return -2;
     const int chunk = (int)std::min<int64_t>(p.num_seqs, seqs_per_launch(max_ctx, p.num_kv_heads));
     for (int b0 = 0; b0 < p.num_seqs; b0 += chunk) {
@@ -832,8 +831,10 @@ int launch_decode_int4(const DecodeParams &p, const Int4Work &ws, int64_t max_ct
             c.ws_score_ml = p.ws_score_ml + rows * 2;
         }
         const int grid = launch_grid(c.num_seqs, c.num_kv_heads, max_ctx, sms);
-        const int rc = dtype == PA_DTYPE_BF16 ? launch_d<__nv_bfloat16>(c, ws, grid, stream)
-                                              : launch_d<__half>(c, ws, grid, stream);
+        int rc = dtype == PA_DTYPE_BF16 ? launch_d<__nv_bfloat16>(c, ws, grid, stream)
+                                        : launch_d<__half>(c, ws, grid, stream);
+        if (rc == 0 && mass)
+            rc = launch_decode_mass(c, 2, mass + (int64_t)b0 * p.num_kv_heads * mass_len, mass_len, &ws, stream);
         if (rc != 0) return rc;
     }
     return 0;

@@ -24,18 +24,19 @@ constexpr int kMaxG = 16;
 // against 6.)
 constexpr int tokens_per_thread(int heads) { return heads <= 2 ? 8 : (heads <= 4 ? 4 : (heads <= 8 ? 2 : 1)); }
 
-// V floats as one load.
+// V floats as one load. (All loads here are of L2: beside the joining kernel, nothing has
+// made this SM's L1 forget what earlier kernels read.)
 template <int V> __device__ __forceinline__ void load_vec(const float *src, float *v) {
     if constexpr (V == 1) {
-        v[0] = __ldcs(src);
+        v[0] = __ldcg(src);
     } else if constexpr (V == 2) {
-        const float2 f = __ldcs(reinterpret_cast<const float2 *>(src));
+        const float2 f = __ldcg(reinterpret_cast<const float2 *>(src));
         v[0] = f.x;
         v[1] = f.y;
     } else {
 #pragma unroll
         for (int u = 0; u < V; u += 4) {
-            const float4 f = __ldcs(reinterpret_cast<const float4 *>(src + u));
+            const float4 f = __ldcg(reinterpret_cast<const float4 *>(src + u));
             v[u] = f.x;
             v[u + 1] = f.y;
             v[u + 2] = f.z;
@@ -47,19 +48,26 @@ template <int V> __device__ __forceinline__ void load_vec(const float *src, floa
 // NP planes of V heads, of which the first `group` exist.
 template <int V, int NP>
 __global__ __launch_bounds__(kThreads) void decode_mass_kernel(const DecodeParams p, float *__restrict__ mass,
-                                                               int64_t mass_len, int rounds) {
+                                                               int64_t mass_len, int rounds, const Int4Work ws) {
     constexpr int kHeads = V * NP, kTok = tokens_per_thread(kHeads);
     constexpr int kChunk = kThreads * kTok;
     __shared__ float M_s[kMaxG], inv_s[kMaxG];
     const int kvh = blockIdx.y, b = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.group;
+    // Over a 4-bit cache the kernel before is the one that joins the partials. Nothing here needs
+    // its results, and it starts dependents only once the decode has finished, so the two run side
+    // by side; this one waits for it at its end, so that whatever follows comes after both.
+    const bool beside = ws.rows != nullptr;
+    if (!beside) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     int ctx = p.context_lens[b];
     ctx = ctx < 0 ? 0 : min(ctx, p.context_limit);
     const int64_t c0 = (int64_t)blockIdx.x * rounds * kChunk;
-    if (c0 >= ctx) return;
+    if (c0 >= ctx) {
+        if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     const float *x = p.ws_logits + ((int64_t)b * p.num_kv_heads + kvh) * p.logits_row;
     float *dst = mass + ((int64_t)b * p.num_kv_heads + kvh) * mass_len;
     int t0 = (int)c0 + threadIdx.x;
@@ -70,20 +78,25 @@ __global__ __launch_bounds__(kThreads) void decode_mass_kernel(const DecodeParam
         for (int i = 0; i < kTok; ++i) {
             const int t = t0 + i * kThreads;
             if (t >= end) continue;
-            old[i] = dst[t];
+            old[i] = __ldcg(dst + t);
 #pragma unroll
             for (int pl = 0; pl < NP; ++pl)
                 if (pl * V < G) load_vec<V>(x + ((int64_t)pl * p.logits_len + t) * V, v[i] + pl * V);
         }
     };
     load();
-    const int nparts = (ctx - 1) / p.partition_size + 1;
+    // the pairs of a head: of its partitions, or (4-bit) of the runs that share the row, or the
+    // one of a row that a run covers
+    const int64_t row = (int64_t)b * p.num_kv_heads + kvh;
+    const int2 info = beside ? __ldcg(ws.rows + row) : make_int2(0, 0);
+    const int nparts = beside ? max(1, info.y) : (ctx - 1) / p.partition_size + 1;
     for (int g = warp; g < G; g += kThreads / 32) {
-        const float2 *ml = reinterpret_cast<const float2 *>(p.ws_score_ml) +
-                           ((int64_t)b * p.num_heads + (int64_t)kvh * G + g) * p.max_partitions;
+        const float2 *ml = info.y > 0 ? ws.part_ml + (int64_t)info.x * G + g
+                                      : reinterpret_cast<const float2 *>(p.ws_score_ml) + (row * G + g) * p.max_partitions;
+        const int64_t step = info.y > 0 ? G : 1;
         float M = -INFINITY, L = 0.f;
         for (int i = lane; i < nparts; i += 32) {       // the lane's own pairs, one pass
-            const float2 a = ml[i];
+            const float2 a = __ldcg(ml + i * step);
             const float m = fmaxf(M, a.x);
             L = L * (M == -INFINITY ? 0.f : fast_exp2(M - m));
             L = fmaf(a.y, a.x == -INFINITY ? (a.y == a.y ? 0.f : a.y) : fast_exp2(a.x - m), L);
@@ -116,10 +129,11 @@ __global__ __launch_bounds__(kThreads) void decode_mass_kernel(const DecodeParam
         if (t0 >= end) break;
         load();
     }
+    if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int V, int NP>
-int launch_t(const DecodeParams &p, float *mass, int64_t mass_len, cudaStream_t stream) {
+int launch_t(const DecodeParams &p, float *mass, int64_t mass_len, const Int4Work &ws, cudaStream_t stream) {
     constexpr int chunk = kThreads * tokens_per_thread(V * NP);
     const int64_t chunks = (p.context_limit + chunk - 1) / chunk;
     // a CTA takes several chunks where there are many of them, so that the joining of its heads'
@@ -127,29 +141,30 @@ int launch_t(const DecodeParams &p, float *mass, int64_t mass_len, cudaStream_t 
     const int64_t all = chunks * p.num_kv_heads * p.num_seqs;
     const int rounds = (int)(all < 2048 ? 1 : (all / 1024 < 8 ? all / 1024 : 8));
     const dim3 grid((unsigned)((chunks + rounds - 1) / rounds), (unsigned)p.num_kv_heads, (unsigned)p.num_seqs);
-    return launch_pdl(decode_mass_kernel<V, NP>, grid, dim3(kThreads), 0, stream, p, mass, mass_len, rounds);
+    return launch_pdl(decode_mass_kernel<V, NP>, grid, dim3(kThreads), 0, stream, p, mass, mass_len, rounds, ws);
 }
 
 }  // namespace
 
-int launch_decode_mass(const DecodeParams &p, int heads_per_plane, float *mass, int64_t mass_len,
+int launch_decode_mass(const DecodeParams &p, int heads_per_plane, float *mass, int64_t mass_len, const Int4Work *work,
                        cudaStream_t stream) {
+    const Int4Work ws = work ? *work : Int4Work{};
     if (p.context_limit <= 0) return 0;
     const int planes = (p.group + heads_per_plane - 1) / heads_per_plane;
     switch (heads_per_plane) {
     case 1:
-        if (planes <= 1) return launch_t<1, 1>(p, mass, mass_len, stream);
-        if (planes <= 2) return launch_t<1, 2>(p, mass, mass_len, stream);
-        if (planes <= 4) return launch_t<1, 4>(p, mass, mass_len, stream);
-        if (planes <= 8) return launch_t<1, 8>(p, mass, mass_len, stream);
-        return launch_t<1, 16>(p, mass, mass_len, stream);
+        if (planes <= 1) return launch_t<1, 1>(p, mass, mass_len, ws, stream);
+        if (planes <= 2) return launch_t<1, 2>(p, mass, mass_len, ws, stream);
+        if (planes <= 4) return launch_t<1, 4>(p, mass, mass_len, ws, stream);
+        if (planes <= 8) return launch_t<1, 8>(p, mass, mass_len, ws, stream);
+        return launch_t<1, 16>(p, mass, mass_len, ws, stream);
     case 2:
-        if (planes <= 1) return launch_t<2, 1>(p, mass, mass_len, stream);
-        if (planes <= 2) return launch_t<2, 2>(p, mass, mass_len, stream);
-        if (planes <= 4) return launch_t<2, 4>(p, mass, mass_len, stream);
-        return launch_t<2, 8>(p, mass, mass_len, stream);
-    case 4: return launch_t<4, 2>(p, mass, mass_len, stream);
-    case 8: return launch_t<8, 2>(p, mass, mass_len, stream);
+        if (planes <= 1) return launch_t<2, 1>(p, mass, mass_len, ws, stream);
+        if (planes <= 2) return launch_t<2, 2>(p, mass, mass_len, ws, stream);
+        if (planes <= 4) return launch_t<2, 4>(p, mass, mass_len, ws, stream);
+        return launch_t<2, 8>(p, mass, mass_len, ws, stream);
+    case 4: return launch_t<4, 2>(p, mass, mass_len, ws, stream);
+    case 8: return launch_t<8, 2>(p, mass, mass_len, ws, stream);
     default: return -2;
     }
 }

@@ -47,17 +47,18 @@ Int4WorkSizes decode_int4_work_sizes(int64_t num_seqs, int64_t num_heads, int64_
                                      int64_t max_ctx, int sms);
 
 // Decode attention over a 4-bit cache (p.key_cache, p.value_cache, p.kv_params) of contexts
-// up to max_ctx tokens, on `sms` multiprocessors; p's split-K fields are not used. With
-// p.ws_logits set it also stores every score, and every row's (max, sum) pair in
-// p.ws_score_ml as of one partition.
+// up to max_ctx tokens, on `sms` multiprocessors; p's split-K fields are not used. With mass
+// set, p.ws_logits and p.ws_score_ml hold the scores and the pairs of rows that one run
+// covers, and the weights are added to mass as by launch_decode_mass.
 bool decode_int4_supported(const DecodeParams &p, int dtype);
-int launch_decode_int4(const DecodeParams &p, const Int4Work &ws, int64_t max_ctx, int sms, int dtype,
-                       cudaStream_t stream);
+int launch_decode_int4(const DecodeParams &p, const Int4Work &ws, int64_t max_ctx, int sms, float *mass,
+                       int64_t mass_len, int dtype, cudaStream_t stream);
 
 // Adds each token's softmax weights, summed over the query heads of its kv head, to
 // mass [num_seqs, num_kv_heads, mass_len], from the scores (planes of heads_per_plane) and
-// (max, sum) pairs that a decode with p.ws_logits left in the workspace.
-int launch_decode_mass(const DecodeParams &p, int heads_per_plane, float *mass, int64_t mass_len,
+// (max, sum) pairs that a decode with p.ws_logits left in the workspace. ws: of a 4-bit decode,
+// whose joining kernel is the one before on the stream.
+int launch_decode_mass(const DecodeParams &p, int heads_per_plane, float *mass, int64_t mass_len, const Int4Work *ws,
                        cudaStream_t stream);
 // Heads per plane of the kernels: SIMT 1, 4-bit 2, and half the padded group here.
 inline int score_plane_tc(int group) { return group <= 4 ? 2 : (group <= 8 ? 4 : 8); }
