@@ -10,9 +10,8 @@
 // byte (channel 2i low, 2i + 1 high); a block of one kv head is one contiguous run of
 // block_size rows, and so are its (K scale, K zero, V scale, V zero) float16 quadruples.
 //
-// Both kernels: a row is head_dim / 8 lanes of 8 channels, so a lane moves 16 bytes of a
-// 16-bit row and 4 bytes of codes; a K row and its V row sit side by side in a warp, and
-// the extrema are butterfly shuffles inside a row's lanes.
+// In both kernels a row is shared by a few lanes, and a K row and its V row sit side by
+// side in a warp; the extrema are butterfly shuffles inside a row's lanes.
 #include "common.cuh"
 #include "kernels_compress.h"
 
@@ -41,61 +40,88 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// Eight channels of a row as loaded, their values, and their smallest and largest: packed as
-// (min, -max), so that one packed min takes both on to the row's other lanes.
-template <typename T> struct Run8;
+// The smallest and largest of some channels. In 16 bits packed as (min, -max), so that one
+// packed min takes both further.
+template <typename T> struct Extrema;
+template <> struct Extrema<float> {
+    float lo, hi;
+    __device__ __forceinline__ void merge(const Extrema &o) {
+        lo = min_nan(lo, o.lo);
+        hi = max_nan(hi, o.hi);
+    }
+    __device__ __forceinline__ Extrema of_lane(int mask) const {
+        return {__shfl_xor_sync(0xffffffffu, lo, mask), __shfl_xor_sync(0xffffffffu, hi, mask)};
+    }
+    __device__ __forceinline__ float2 values() const { return make_float2(lo, hi); }
+};
+template <typename T2> __device__ __forceinline__ T2 as2(uint32_t u) { return *reinterpret_cast<T2 *>(&u); }
+template <typename T2> __device__ __forceinline__ uint32_t bits2(T2 v) { return *reinterpret_cast<uint32_t *>(&v); }
+template <typename T, typename T2> struct PackedExtrema {
+    uint32_t both;
+    __device__ __forceinline__ void merge_bits(uint32_t o) { both = bits2(__hmin2_nan(as2<T2>(both), as2<T2>(o))); }
+    __device__ __forceinline__ float2 values() const {
+        float f[8];
+        Vec16<T>::unpack(make_uint4(both, 0, 0, 0), f);
+        return make_float2(f[0], -f[1]);
+    }
+};
+template <> struct Extrema<__half> : PackedExtrema<__half, __half2> {
+    using T2 = __half2;
+    __device__ __forceinline__ void merge(const Extrema &o) { merge_bits(o.both); }
+    __device__ __forceinline__ Extrema of_lane(int mask) const {
+        Extrema e;
+        e.both = __shfl_xor_sync(0xffffffffu, both, mask);
+        return e;
+    }
+};
+template <> struct Extrema<__nv_bfloat16> : PackedExtrema<__nv_bfloat16, __nv_bfloat162> {
+    using T2 = __nv_bfloat162;
+    __device__ __forceinline__ void merge(const Extrema &o) { merge_bits(o.both); }
+    __device__ __forceinline__ Extrema of_lane(int mask) const {
+        Extrema e;
+        e.both = __shfl_xor_sync(0xffffffffu, both, mask);
+        return e;
+    }
+};
+
+// Eight channels of a row as loaded.
+template <typename T> struct Run8 {
+    uint4 raw;
+    __device__ __forceinline__ void load(const T *src) { raw = *reinterpret_cast<const uint4 *>(src); }
+    __device__ __forceinline__ void clear() { raw = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void values(float *x) const { Vec16<T>::unpack(raw, x); }
+    __device__ __forceinline__ Extrema<T> extrema() const {
+        using T2 = typename Extrema<T>::T2;
+        const T2 a = as2<T2>(raw.x), b = as2<T2>(raw.y), c = as2<T2>(raw.z), d = as2<T2>(raw.w);
+        const uint32_t mn = bits2(__hmin2_nan(__hmin2_nan(a, b), __hmin2_nan(c, d)));
+        const uint32_t mx = bits2(__hmax2_nan(__hmax2_nan(a, b), __hmax2_nan(c, d)));
+        // (mn.lo, -mx.lo) and (mn.hi, -mx.hi)
+        Extrema<T> e;
+        e.both = __byte_perm(mn, mx, 0x5410) ^ 0x80000000u;
+        e.merge_bits(__byte_perm(mn, mx, 0x7632) ^ 0x80000000u);
+        return e;
+    }
+};
 template <> struct Run8<float> {
     uint4 raw[2];
     __device__ __forceinline__ void load(const float *src) {
-        raw[0] = __ldcs(reinterpret_cast<const uint4 *>(src));
-        raw[1] = __ldcs(reinterpret_cast<const uint4 *>(src) + 1);
+        raw[0] = reinterpret_cast<const uint4 *>(src)[0];
+        raw[1] = reinterpret_cast<const uint4 *>(src)[1];
     }
     __device__ __forceinline__ void clear() { raw[0] = raw[1] = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void values(float *x) const {
         Vec16<float>::unpack(raw[0], x);
         Vec16<float>::unpack(raw[1], x + 4);
     }
-    template <int kLanes> __device__ __forceinline__ void extrema(float &lo, float &hi) const {
+    __device__ __forceinline__ Extrema<float> extrema() const {
         float x[8];
         values(x);
-        lo = hi = x[0];
+        Extrema<float> e{x[0], x[0]};
 #pragma unroll
-        for (int i = 1; i < 8; ++i) {
-            lo = min_nan(lo, x[i]);
-            hi = max_nan(hi, x[i]);
-        }
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) {
-            lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        }
+        for (int i = 1; i < 8; ++i) e.merge({x[i], x[i]});
+        return e;
     }
 };
-template <typename T2> __device__ __forceinline__ T2 as2(uint32_t u) { return *reinterpret_cast<T2 *>(&u); }
-template <typename T2> __device__ __forceinline__ uint32_t bits2(T2 v) { return *reinterpret_cast<uint32_t *>(&v); }
-template <typename T, typename T2> struct Run8Packed {
-    uint4 raw;
-    __device__ __forceinline__ void load(const T *src) { raw = __ldcs(reinterpret_cast<const uint4 *>(src)); }
-    __device__ __forceinline__ void clear() { raw = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void values(float *x) const { Vec16<T>::unpack(raw, x); }
-    template <int kLanes> __device__ __forceinline__ void extrema(float &lo, float &hi) const {
-        const T2 a = as2<T2>(raw.x), b = as2<T2>(raw.y), c = as2<T2>(raw.z), d = as2<T2>(raw.w);
-        const uint32_t mn = bits2(__hmin2_nan(__hmin2_nan(a, b), __hmin2_nan(c, d)));
-        const uint32_t mx = bits2(__hmax2_nan(__hmax2_nan(a, b), __hmax2_nan(c, d)));
-        // (mn.lo, -mx.lo) and (mn.hi, -mx.hi)
-        const uint32_t l = __byte_perm(mn, mx, 0x5410) ^ 0x80000000u, h = __byte_perm(mn, mx, 0x7632) ^ 0x80000000u;
-        T2 both = __hmin2_nan(as2<T2>(l), as2<T2>(h));
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1)
-            both = __hmin2_nan(both, as2<T2>(__shfl_xor_sync(0xffffffffu, bits2(both), o)));
-        float f[8];
-        Vec16<T>::unpack(make_uint4(bits2(both), 0, 0, 0), f);
-        lo = f[0];
-        hi = -f[1];
-    }
-};
-template <> struct Run8<__half> : Run8Packed<__half, __half2> {};
-template <> struct Run8<__nv_bfloat16> : Run8Packed<__nv_bfloat16, __nv_bfloat162> {};
 
 // Row of the cache (in rows of one kv head's token) of a slot, or -1: skip the token.
 __device__ __forceinline__ int64_t cache_row(const Int4Cache &c, int64_t slot, int h, bool first, unsigned int *err) {
@@ -132,9 +158,69 @@ __device__ __forceinline__ uint32_t encode8(const float *x, float zero, float sc
     return codes;
 }
 
-// The (token, kv head) pairs of a thread: kU of them, `pairs` (those a CTA has side by side)
-// apart, so that their loads are in flight together. step_t and step_h: pairs / kv heads and
-// the rest.
+// Writing: a lane has kCh channels of a row. What is done once a row -- the shuffles, the
+// parameters, the slot's address -- is most of a lane's instructions at 8 channels, and the
+// kernel is bound by instructions (8192 tokens of 8 kv heads, written and read back: 26.8 us
+// at 8, 23.3 at 16, 21.3 at 32; two rows a lane were slower at each).
+template <typename T, int D, int kCh>
+__global__ __launch_bounds__(kThreads) void kv_write_int4_kernel(const T *__restrict__ k, const T *__restrict__ v,
+                                                                 const int32_t *__restrict__ slots,
+                                                                 uint32_t num_tokens, const Int4Cache c,
+                                                                 unsigned int *err) {
+    constexpr int kLanes = D / kCh, kWords = kCh / 8;   // lanes per row; 8 channels, a word of codes, each
+    constexpr int kPairs = kThreads / kLanes / 2;
+    // launched as a dependent of the kernel before; a kernel launched after this one may start
+    // its set-up once everything before this one has finished
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int part = threadIdx.x % kLanes;
+    const bool is_v = (threadIdx.x / kLanes) & 1;
+    const uint32_t th = blockIdx.x * kPairs + threadIdx.x / (2 * kLanes);   // (token, kv head) pair
+    const uint32_t t = th / (uint32_t)c.num_kv_heads;
+    const int h = (int)(th - t * c.num_kv_heads);
+    Run8<T> x[kWords];
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) x[w].clear();
+    int64_t dst = -1;
+    if (t < num_tokens) {
+        const T *src = (is_v ? v : k) + (int64_t)th * D + part * kCh;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) x[w].load(src + 8 * w);
+        dst = cache_row(c, slots[t], h, part == 0 && h == 0 && !is_v, err);
+    }
+    Extrema<T> e = x[0].extrema();
+#pragma unroll
+    for (int w = 1; w < kWords; ++w) e.merge(x[w].extrema());
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) e.merge(e.of_lane(o));
+    const float2 range = e.values();
+    const float lo = max_nan(min_nan(range.x, 65504.f), -65504.f);
+    const float hi = max_nan(min_nan(range.y, 65504.f), -65504.f);
+    const __half zero_h = __float2half_rn(lo);
+    const __half scale_h = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+    const float zero = __half2float(zero_h), scale = __half2float(scale_h);
+    const float inv = scale > 0.f ? __frcp_rn(scale) : 0.f;
+    alignas(16) uint32_t codes[kWords];
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+        float y[8];
+        x[w].values(y);
+        codes[w] = scale > 0.f ? encode8(y, zero, scale, inv) : 0u;
+    }
+    const uint32_t mine = (uint32_t)__half_as_ushort(scale_h) | ((uint32_t)__half_as_ushort(zero_h) << 16);
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, kLanes);   // the V row's, for the K row's lanes
+    if (dst < 0) return;
+    uint32_t *out = reinterpret_cast<uint32_t *>(is_v ? c.value : c.key) + dst * (D / 8) + part * kWords;
+    if constexpr (kWords == 4) *reinterpret_cast<uint4 *>(out) = *reinterpret_cast<uint4 *>(codes);
+    else if constexpr (kWords == 2) *reinterpret_cast<uint2 *>(out) = *reinterpret_cast<uint2 *>(codes);
+    else out[0] = codes[0];
+    if (part == 0 && !is_v) reinterpret_cast<uint2 *>(c.params)[dst] = make_uint2(mine, other);
+}
+
+// The (token, kv head) pairs of a thread that reads: kU of them, `pairs` (those a CTA has side
+// by side) apart, so that their loads are in flight together (one: 206 us for 131,071 tokens of
+// 8 kv heads, four: 135; with the codes widened as below 109.5, 5.6 TB/s). step_t and step_h:
+// pairs / kv heads and the rest.
 struct Walk {
     uint32_t t;
     int h;
@@ -148,54 +234,6 @@ struct Walk {
         }
     }
 };
-
-template <typename T, int D, int kU>
-__global__ __launch_bounds__(kThreads) void kv_write_int4_kernel(const T *__restrict__ k, const T *__restrict__ v,
-                                                                 const int32_t *__restrict__ slots,
-                                                                 uint32_t num_tokens, const Int4Cache c,
-                                                                 int step_t, int step_h, unsigned int *err) {
-    constexpr int kLanes = D / 8;                       // lanes per row
-    constexpr int kPairs = kThreads / kLanes / 2;
-    // launched as a dependent of the kernel before; a kernel launched after this one may start
-    // its set-up once everything before this one has finished
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
-    const int part = threadIdx.x % kLanes;              // which 8 channels
-    const bool is_v = (threadIdx.x / kLanes) & 1;
-    const uint32_t th0 = blockIdx.x * (kPairs * kU) + threadIdx.x / (2 * kLanes);
-    const T *src = (is_v ? v : k) + (int64_t)th0 * D + part * 8;
-    Walk at(th0, c.num_kv_heads);
-    Run8<T> x[kU];
-    int64_t dst[kU];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-        dst[u] = -1;
-        x[u].clear();
-        if (at.t < num_tokens) {
-            x[u].load(src + (int64_t)u * kPairs * D);
-            dst[u] = cache_row(c, slots[at.t], at.h, part == 0 && at.h == 0 && !is_v, err);
-        }
-        at.next(c.num_kv_heads, step_t, step_h);
-    }
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-        float lo, hi, y[8];
-        x[u].template extrema<kLanes>(lo, hi);
-        x[u].values(y);
-        lo = max_nan(min_nan(lo, 65504.f), -65504.f);
-        hi = max_nan(min_nan(hi, 65504.f), -65504.f);
-        const __half zero_h = __float2half_rn(lo);
-        const __half scale_h = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
-        const float zero = __half2float(zero_h), scale = __half2float(scale_h);
-        const uint32_t codes = scale > 0.f ? encode8(y, zero, scale, __frcp_rn(scale)) : 0u;
-        const uint32_t mine = (uint32_t)__half_as_ushort(scale_h) | ((uint32_t)__half_as_ushort(zero_h) << 16);
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, kLanes);   // the V row's, for the K row's lanes
-        if (dst[u] >= 0) {
-            reinterpret_cast<uint32_t *>(is_v ? c.value : c.key)[dst[u] * kLanes + part] = codes;
-            if (part == 0 && !is_v) reinterpret_cast<uint2 *>(c.params)[dst[u]] = make_uint2(mine, other);
-        }
-    }
-}
 
 template <typename T, int D, int kU>
 __global__ __launch_bounds__(kThreads) void kv_read_int4_kernel(T *__restrict__ k, T *__restrict__ v,
@@ -256,25 +294,22 @@ __global__ __launch_bounds__(kThreads) void copy_params_kernel(uint4 *params, co
         params[dst * block_vecs + i] = params[src * block_vecs + i];
 }
 
-// Rows per thread: several where there are enough rows to fill the SMs all the same.
-constexpr int kWriteUnroll = 2, kReadUnroll = 4;
+// Channels per lane in writing, rows per thread in reading: more where there are enough rows to
+// fill the SMs all the same.
+constexpr int kWriteChannels = 32, kReadUnroll = 4;
 constexpr int64_t kManyRows = 16384;             // (token, kv head) pairs
 
-unsigned row_grid(const Int4Cache &c, int64_t num_tokens, int per_thread) {
-    const int64_t pairs = (int64_t)kThreads / (c.head_dim / 8) / 2 * per_thread;
+unsigned row_grid(const Int4Cache &c, int64_t num_tokens, int pairs) {     // pairs of a CTA
     return (unsigned)((num_tokens * c.num_kv_heads + pairs - 1) / pairs);
 }
 
 template <typename T, int D>
 int write_t(const void *k, const void *v, const int32_t *slots, int64_t n, const Int4Cache &c, unsigned int *err,
             cudaStream_t s) {
-    constexpr int pairs = kThreads / (D / 8) / 2;
-    const int st = pairs / c.num_kv_heads, sh = pairs % c.num_kv_heads;
     const bool many = n * c.num_kv_heads >= kManyRows;
-    const unsigned grid = row_grid(c, n, many ? kWriteUnroll : 1);
-    auto kern = many ? kv_write_int4_kernel<T, D, kWriteUnroll> : kv_write_int4_kernel<T, D, 1>;
-    return launch_pdl(kern, dim3(grid), dim3(kThreads), 0, s, (const T *)k, (const T *)v, slots, (uint32_t)n, c, st, sh,
-                      err);
+    const unsigned grid = row_grid(c, n, kThreads / (D / (many ? kWriteChannels : 8)) / 2);
+    auto kern = many ? kv_write_int4_kernel<T, D, kWriteChannels> : kv_write_int4_kernel<T, D, 8>;
+    return launch_pdl(kern, dim3(grid), dim3(kThreads), 0, s, (const T *)k, (const T *)v, slots, (uint32_t)n, c, err);
 }
 
 template <typename T, int D>
@@ -283,7 +318,7 @@ int read_t(void *k, void *v, const int32_t *slots, int64_t n, const Int4Cache &c
     constexpr int pairs = kThreads / (D / 8) / 2;
     const int st = pairs / c.num_kv_heads, sh = pairs % c.num_kv_heads;
     const bool many = n * c.num_kv_heads >= kManyRows;
-    const unsigned grid = row_grid(c, n, many ? kReadUnroll : 1);
+    const unsigned grid = row_grid(c, n, pairs * (many ? kReadUnroll : 1));
     auto kern = many ? kv_read_int4_kernel<T, D, kReadUnroll> : kv_read_int4_kernel<T, D, 1>;
     return launch_pdl(kern, dim3(grid), dim3(kThreads), 0, s, (T *)k, (T *)v, slots, (uint32_t)n, c, st, sh, err);
 }
