@@ -270,12 +270,19 @@ def decode_shared_partition_size(num_seqs: int, num_groups: int, num_kv_heads: i
 
 
 def _workspace(device, stream_ptr: int, nbytes: int):
-    """Cached per (device, stream) workspace buffer, grown on demand."""
+    """Cached per (device, stream) workspace buffer, grown on demand. While a graph is
+    captured, a buffer of the call's own, from the graph's memory: a cached one would be
+    shared with other graphs, or go with the graph that it was first made for."""
     torch = _torch()
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
     key = (device, stream_ptr)
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+        if stream_ptr != torch._C._cuda_getCurrentRawStream(device.index):
+            # used on a stream it was not allocated on: not handed out again before that is done
+            buf.record_stream(torch.cuda.ExternalStream(stream_ptr, device=device))
         _ws_cache[key] = buf
     return buf
 

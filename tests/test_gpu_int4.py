@@ -239,7 +239,8 @@ RAGGED = [1, 7, 0, 15, 16, 17, 31, 33, 64, 127, 128, 129, 300, 513, 1000, 1025]
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("H,Hk,D,bs", [(8, 8, 128, 16), (32, 8, 128, 16), (6, 2, 64, 8), (7, 1, 128, 32), (16, 2, 64, 64),
-                                       (12, 1, 128, 256), (32, 2, 128, 8), (10, 2, 64, 16)])
+                                       (12, 1, 128, 256), (32, 2, 128, 8), (10, 2, 64, 16),
+                                       (16, 1, 64, 8), (3, 3, 64, 128)])
 def test_decode_ragged(pa, dtype, H, Hk, D, bs):
     """Contexts of nothing, one token, tiles and their neighbours, several partitions; group
     sizes 1 to 16; from zero mass."""
