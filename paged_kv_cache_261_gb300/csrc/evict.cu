@@ -173,7 +173,8 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictParam
     __shared__ __align__(16) int hist[kBins];
     __shared__ __align__(16) int sums[kBins / 2];      // this CTA's part of the cluster's counts
     __shared__ uint32_t seg[kWarps];    // sums of each warp
-    __shared__ int found[2];            // the digit of the threshold, and how many keys lie above it
+    __shared__ int found[3];            // the digit of the threshold, how many keys lie above it, and how many
+                                        // of this CTA's have it (the counts themselves are cleared soon)
     __shared__ uint32_t list[kList];    // keys of the candidates that share the threshold's first digit,
     __shared__ unsigned char list_warp[kList];   // whose warp's tokens they are,
     __shared__ int listed;                       // how many,
@@ -296,6 +297,7 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictParam
                     if (above < want && above + n[j] >= want) {
                         found[0] = i0 - j;
                         found[1] = above;
+                        found[2] = hist[i0 - j];
                     }
                     above += n[j];
                 }
@@ -305,7 +307,7 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictParam
             mask |= digits << shift;
             want -= found[1];
             if (shift == 0) break;
-            if (shift == kFirst && hist[found[0]] <= kList) {
+            if (shift == kFirst && found[2] <= kList) {
                 // few candidates share the threshold's first digit: the other digits, and the
                 // verdict on the rest, need no further pass over the slice
                 short_list = true;

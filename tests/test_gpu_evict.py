@@ -165,6 +165,12 @@ def test_evict_rows_beyond_a_cluster(pa):
     run_case(pa, 38, [430000, 700], [429000, 400], 50, 1, 64, 256, "int4", kind="ties", in_place=True, extra=0)
 
 
+@pytest.mark.parametrize("kind", ["equal", "crowd"])
+def test_evict_long_list_in_one_cta(pa, kind):
+    """As many rows as give each one CTA, with more masses of the threshold's first digit than its list holds."""
+    run_case(pa, 41, [2900] * 160, [1500] * 160, 9, 2, 64, 64, "int4", kind=kind, in_place=True)
+
+
 @pytest.mark.parametrize("B", [1, 20, 90])
 def test_evict_batch_sizes(pa, B):
     """From whole clusters for a row to one CTA."""
