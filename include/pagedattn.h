@@ -37,10 +37,10 @@
  * pa_get_device_error(). No kernel traps or asserts.
  *
  * Launch chaining: the decode and merge kernels are launched as programmatic
- * dependents of the kernel before them on the stream, and the decode kernels read
- * context_lens (and prefix_lens) before they wait for it. A kernel the caller
- * launches just before a decode call therefore must not write those two arrays
- * after it signals its dependents early (griddepcontrol.launch_dependents); a
+ * dependents of the kernel before them on the stream, and the decode kernels (over
+ * 4-bit caches too) read context_lens (and prefix_lens) before they wait for it. A
+ * kernel the caller launches just before a decode call therefore must not write those
+ * two arrays after it signals its dependents early (griddepcontrol.launch_dependents); a
  * kernel that never signals is waited for in full, as usual.
  */
 #ifndef PAGEDATTN_H
@@ -444,8 +444,9 @@ int pa_paged_kv_write_int4(const void *k, const void *v, const int32_t *slot_map
 
 /*
  * Read-back: k[t], v[t] = the values held at slot_mapping[t], computed in float32 (one
- * rounding) and rounded to dst_dtype (PA_DTYPE_F32, _F16 or _BF16). A token of slot -1, or of a slot out of range (which
- * sets PA_DEVERR_SLOT), keeps its row of k and v as it was. Slots may repeat. Read into
+ * rounding) and rounded to dst_dtype (PA_DTYPE_F32, _F16 or _BF16). A token of slot -1,
+ * or of a slot out of range (which sets PA_DEVERR_SLOT), keeps its row of k and v as it
+ * was. Slots may repeat. Read into
  * a [num_blocks', block_size', num_kv_heads, head_dim] buffer, a cached context can be
  * attended by pa_paged_attention_prefill.
  */
@@ -473,6 +474,7 @@ size_t pa_decode_int4_workspace_bytes(int num_seqs, int num_heads, int num_kv_he
  * [num_seqs, num_heads, head_dim], PA_DTYPE_BF16 or PA_DTYPE_F16; head_dim 64 or 128,
  * num_heads / num_kv_heads <= 16. mass (NULL: none): float32 [num_seqs, num_kv_heads,
  * mass_len], accumulated as by pa_paged_attention_decode_scored, out staying the same.
+ * Queries are below 2^118 in magnitude (times |scale|; beyond, a head's output may be NaN).
  * Parameters of the slots past a context's end are never used, whatever they hold; a
  * NaN parameter inside a context makes the outputs of its heads NaN. The work is cut
  * into equal runs of tokens over the device, whatever the lengths (there is no partition
@@ -532,7 +534,8 @@ int pa_paged_attention_decode_scored(void *out, const void *q, float *mass, int6
  *
  * out_block_tables [num_seqs, out_max_blocks_per_seq] names blocks of the same caches:
  * either blocks that no sequence of the call reads, or, for eviction in place, the
- * sequence's own blocks in their order (then mass_out may be mass itself). In place, a
+ * sequence's own blocks in their order. mass_out is mass itself (of the same length) or
+ * does not overlap it. In place, a
  * block that moved rows land in must not be read by another sequence (copy-on-write, or
  * other out blocks, guarantee it). kept: int32 [num_seqs, num_kv_heads, kept_len].
  * dtype: PA_DTYPE_F32, _F16, _BF16 or _E4M3 (caches [num_blocks, block_size,

@@ -719,9 +719,11 @@ def decode_int4_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int
                                                    int(with_mass)))
 
 
-def _decode_args(out, q, block_tables, context_lens, d, dev, dtype):
+def _decode_args(out, q, block_tables, context_lens, d, dev, dtype, max_context_len):
     """Checks what every decode call takes besides its caches; (B, H, MB)."""
     i32 = _torch_module.int32
+    if not 0 <= max_context_len <= 0x7FFFFFFF:
+        raise ValueError("max_context_len must be in [0, 2^31)")
     if not (q.device == dev and q.dtype == dtype and q.is_contiguous() and out.device == dev and out.dtype == dtype and
             out.is_contiguous() and block_tables.device == dev and block_tables.dtype == i32 and
             block_tables.is_contiguous() and context_lens.device == dev and context_lens.dtype == i32 and
@@ -748,7 +750,7 @@ def paged_attention_decode_int4(out, q, key_cache, value_cache, kv_params, block
     paged_attention_decode."""
     dev = key_cache.device
     nb, hk, bs, d = _int4_caches(key_cache, value_cache, kv_params, dev)
-    B, H, mb = _decode_args(out, q, block_tables, context_lens, d, dev, q.dtype)
+    B, H, mb = _decode_args(out, q, block_tables, context_lens, d, dev, q.dtype, max_context_len)
     mass_ptr, mass_len = None, 0
     if mass is not None:
         mass_len = _mass(mass, "mass", B, hk, dev)
@@ -795,7 +797,7 @@ def paged_attention_decode_scored(out, q, mass, key_cache, value_cache, block_ta
     if len(shape) != 4 or value_cache.shape != shape:
         raise ValueError("key_cache and value_cache must be [num_blocks, block_size, num_kv_heads, head_dim]")
     nb, bs, hk, d = shape
-    B, H, mb = _decode_args(out, q, block_tables, context_lens, d, dev, dt)
+    B, H, mb = _decode_args(out, q, block_tables, context_lens, d, dev, dt, max_context_len)
     mass_len = _mass(mass, "mass", B, hk, dev)
     if _elsewhere(dev):
         with _on(dev):
@@ -851,12 +853,15 @@ def paged_kv_evict(kept, mass, mass_out, key_cache, value_cache, block_tables, o
     if kept.dim() != 3 or kept.shape[0] != B or kept.shape[1] != hk:
         raise ValueError(f"kept must be [{B}, {hk}, length]")
     mass_len, out_len = _mass(mass, "mass", B, hk, dev), _mass(mass_out, "mass_out", B, hk, dev)
+    recent = min(int(recent), 0x7FFFFFFF)
+    if recent < 0:
+        raise ValueError("recent must not be negative")
     with _on(dev):
         rc = _lib.pa_paged_kv_evict(kept.data_ptr(), kept.shape[2], mass.data_ptr(), mass_len, mass_out.data_ptr(),
                                     out_len, key_cache.data_ptr(), value_cache.data_ptr(), par,
                                     block_tables.data_ptr(), block_tables.shape[1], out_block_tables.data_ptr(),
                                     out_block_tables.shape[1], context_lens.data_ptr(), keep_lens.data_ptr(),
-                                    int(recent), B, hk, d, bs, nb, dt, _stream_ptr(stream, dev))
+                                    recent, B, hk, d, bs, nb, dt, _stream_ptr(stream, dev))
     _check(rc, "pa_paged_kv_evict")
 
 

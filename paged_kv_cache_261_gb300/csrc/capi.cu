@@ -305,6 +305,9 @@ size_t int4_workspace_bytes(int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t
            (with_mass ? align256((size_t)(B * H * 8)) + logits_bytes(B, H, Hk, max_ctx) : 0);
 }
 
+// Tokens of a context that the kernels of this part count in 31 bits, a tile past its end.
+constexpr int64_t kMaxTokens = INT32_MAX - 65536;
+
 int64_t call_max_context(int max_blocks_per_seq, int block_size, int max_context_len) {
     return max_context_len == 0 ? (int64_t)max_blocks_per_seq * block_size : max_context_len;
 }
@@ -778,11 +781,12 @@ int pa_paged_attention_decode_scored(void *out, const void *q, float *mass, int6
     if (rc == kNothingToDo) return PA_OK;
     if (rc != PA_OK) return rc;
     if (!mass || mass_len <= 0 || (reinterpret_cast<uintptr_t>(mass) & 3u) != 0) return PA_ERR_INVALID_ARG;
+    const int64_t max_ctx = call_max_context(max_blocks_per_seq, block_size, max_context_len);
+    if (max_ctx > kMaxTokens) return PA_ERR_UNSUPPORTED;
     if (p.context_limit > mass_len) p.context_limit = (int)mass_len;
     if ((rc = error_word(&p.err)) != PA_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void *owned = nullptr;
-    const int64_t max_ctx = call_max_context(max_blocks_per_seq, block_size, max_context_len);
     if ((rc = scored_workspace(p, P, max_ctx, workspace, workspace_bytes, s, &owned)) != PA_OK) return rc;
     const DecodeKernel choice = decode_kernel_choice();
     const bool tc = choice == DecodeKernel::Tc || (choice == DecodeKernel::Auto && pa::decode_tc_supported(p, dtype));
@@ -880,10 +884,10 @@ int pa_paged_attention_decode_int4(void *out, const void *q, const void *key_cac
     if (mass && (mass_len <= 0 || (reinterpret_cast<uintptr_t>(mass) & 3u) != 0)) return PA_ERR_INVALID_ARG;
     p.kv_params = kv_params;
     if (mass && p.context_limit > mass_len) p.context_limit = (int)mass_len;
-    if (!pa::decode_int4_supported(p, dtype)) return PA_ERR_UNSUPPORTED;
+    const int64_t max_ctx = call_max_context(max_blocks_per_seq, block_size, max_context_len);
+    if (!pa::decode_int4_supported(p, dtype) || max_ctx > kMaxTokens) return PA_ERR_UNSUPPORTED;
     if ((rc = error_word(&p.err)) != PA_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int64_t max_ctx = max_context_len == 0 ? (int64_t)max_blocks_per_seq * block_size : max_context_len;
     const size_t need = int4_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_ctx, mass != nullptr);
     void *ws = workspace, *owned = nullptr;
     if (ws) {
@@ -943,6 +947,14 @@ int pa_paged_kv_evict(int32_t *kept, int64_t kept_len, const float *mass, int64_
         (reinterpret_cast<uintptr_t>(kept) & 3u) != 0)
         return PA_ERR_INVALID_ARG;
     if (num_blocks > INT64_MAX / ((int64_t)block_size * num_kv_heads * row)) return PA_ERR_INVALID_ARG;
+    // mass_out: mass itself, row for row, or elsewhere
+    if (mass_out != mass || mass_out_len != mass_len) {
+        const int64_t rows = (int64_t)num_seqs * num_kv_heads;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(mass), b = reinterpret_cast<uintptr_t>(mass_out);
+        if (mass_len > INT64_MAX / 4 / rows || mass_out_len > INT64_MAX / 4 / rows) return PA_ERR_INVALID_ARG;
+        if (a < b + (uintptr_t)(rows * mass_out_len * 4) && b < a + (uintptr_t)(rows * mass_len * 4))
+            return PA_ERR_INVALID_ARG;
+    }
     pa::EvictParams p{};
     int rc = error_word(&p.err);
     if (rc != PA_OK) return rc;
@@ -959,7 +971,7 @@ int pa_paged_kv_evict(int32_t *kept, int64_t kept_len, const float *mass, int64_
     p.num_blocks = num_blocks;
     p.max_blocks = max_blocks_per_seq;
     p.out_max_blocks = out_max_blocks_per_seq;
-    const int64_t top = INT32_MAX;
+    const int64_t top = kMaxTokens;
     p.context_limit = (int)std::min(top, std::min((int64_t)max_blocks_per_seq * block_size, mass_len));
     p.keep_limit = (int)std::min({top, (int64_t)out_max_blocks_per_seq * block_size, mass_out_len, kept_len});
     p.num_seqs = num_seqs;

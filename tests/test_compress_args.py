@@ -101,6 +101,19 @@ def test_evict_refusals(pa, bad, code):
     assert _evict(pa, **bad) == code
 
 
+def test_evict_refuses_overlapping_masses(pa):
+    # rows of 64 masses, 2 sequences of 2 kv heads: 1024 bytes from 4096 on; 8 a row out: 128 bytes
+    for mo, mol in ((4096, 8), (4100, 64), (3972, 8), (5116, 8), (4096, 65)):
+        assert _evict(pa, mass=4096, mo=mo, mol=mol) == INVALID
+    assert _evict(pa, mass=4096, ml=1 << 62, mo=1 << 20) == INVALID
+
+
+def test_contexts_past_the_token_count_are_refused(pa):
+    top = 2 ** 31 - 1
+    assert _decode(pa, mc=top) == UNSUPPORTED and _decode(pa, mb=2 ** 31 // 16, mc=0) == UNSUPPORTED
+    assert _scored(pa, mc=top) == UNSUPPORTED
+
+
 def test_python_checks_refuse_host_tensors_and_wrong_shapes(pa):
     torch = pytest.importorskip("torch")
     x = torch.zeros(2, 2, 128)
