@@ -32,16 +32,16 @@
 // row (sequence, kv head) writes its result, the others leave partials that a second
 // kernel joins. Warps share nothing, so nothing synchronises them. (Items of a CTA whose
 // warps joined their states through shared memory took 65 us on the 8B-shaped batch, with
-// 27.7 instructions a token against 18 in this form.) Each warp fetches its own stages, one ahead
-// and across rows, into its own ring: a block of one kv head is one contiguous run for K,
-// V and the parameters each, so a stage is a few untiled bulk copies on one mbarrier.
+// 27.7 instructions a token against 18 in this form.) Each warp fetches its own stages, one
+// ahead and across rows, into its own ring: a block of one kv head is one contiguous run for
+// K, V and the parameters each, so a stage is a few untiled bulk copies on one mbarrier.
 //
-// What bounds it (one GB300): the 8B-shaped batch, 162 MB, takes 38.0 us, of which about 8
-// are the two kernels' start and the join; long contexts, 711 MB, take 123 us, 5.8 TB/s.
+// What bounds it (one GB300): the 8B-shaped batch, 162 MB, takes 37.2 us, of which about 8
+// are the two kernels' start and the join; long contexts, 711 MB, take 122.3 us, 5.8 TB/s.
 // The copies alone take 33.7 and 115 us, the arithmetic alone 30.0 and 99.
 // Stages of 32 tokens and 16 warps per SM: 39.9 and 135 us (a stage's fixed work, about 60
 // instructions, comes twice as often, and 128 registers leave less in flight).
-
+//
 // Every wait is bounded; on a timeout the kernel sets PA_DEVERR_WAIT, waits (bounded)
 // for its copies in flight and returns.
 #include "common.cuh"

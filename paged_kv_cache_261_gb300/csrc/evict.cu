@@ -21,6 +21,11 @@
 // move in waves, each read into registers by the whole cluster before any of it is
 // written. Since kept[i] >= i and both rise, a wave's writes land on rows that no later
 // wave reads, also when the out table names the sequence's own blocks (eviction in place).
+//
+// What bounds it (one GB300): 64 sequences of 512 to 4096 tokens, 8 kv heads, cut to 1024 in
+// bf16 take 102 us: the movement 84, at 6.4 TB/s of rows read and written, and the selection
+// 16.5, its barriers and counts. For 8 sequences of 32k to 128k cut to 8192 the selection takes
+// 54 us (two waves of CTAs, with 21 MB of masses beside their counts in shared memory).
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -167,7 +172,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSlice = 48 * 1024;    // masses per CTA: 192 KB of shared memory
-constexpr int kList = 2048;
+constexpr int kList = 2048;             // long 4-bit contexts 189 -> 179 us, with their read-back
 __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictParams p) {
     extern __shared__ __align__(16) float slice[];      // this CTA's masses
     __shared__ __align__(16) int hist[kBins];
