@@ -27,6 +27,16 @@
 // it below, whatever the scale of V. The query enters as f16 times a power of two per
 // head: exact for bf16 and f16 at every channel within 2^-22 of the row's largest.
 //
+// The codes enter about their middle, 7.5, or the rounding of W would come out multiplied by
+// codes that are all of one sign, and the sums over a long context, which cancel against
+// those of the zeros, would drown it. Odd tokens have their codes complemented (by the mask's
+// instruction) and their W negated, so the products sum up around zero; with
+// v_mid = v_zero + 7.5 v_scale and s = +-1,
+//   sum_t p_t V_t[c] = sum_t (s_t W_t) n'_t[c] - 7.5 sum_t (s_t W_t) + sum_t p_t v_mid_t,
+// n' = n or 15 - n, and every W the rounded one. Error of f16 outputs over contexts of 60,000
+// flat weights: 2.9e-4, 2.0e-4 of it their own rounding (6.1e-4 with plain codes, at 3 % less
+// time; codes made signed by an f16 addition cost 7 %).
+//
 // Work: the stages (64 tokens of one sequence and kv head) of the whole call, in order,
 // are cut into equal runs, one for each warp of the persistent grid; a run that covers a
 // row (sequence, kv head) writes its result, the others leave partials that a second
@@ -36,9 +46,9 @@
 // ahead and across rows, into its own ring: a block of one kv head is one contiguous run for
 // K, V and the parameters each, so a stage is a few untiled bulk copies on one mbarrier.
 //
-// What bounds it (one GB300): the 8B-shaped batch, 162 MB, takes 37.2 us, of which about 8
-// are the two kernels' start and the join; long contexts, 711 MB, take 122.3 us, 5.8 TB/s.
-// The copies alone take 33.7 and 115 us, the arithmetic alone 30.0 and 99.
+// What bounds it (one GB300): the 8B-shaped batch, 162 MB, takes 38.0 us, of which about 8
+// are the two kernels' start and the join; long contexts, 711 MB, take 126.8 us, 5.6 TB/s.
+// The copies alone take 33.7 and 115 us.
 // Stages of 32 tokens and 16 warps per SM: 39.9 and 135 us (a stage's fixed work, about 60
 // instructions, comes twice as often, and 128 registers leave less in flight).
 //
@@ -136,6 +146,18 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "=f"(d.x), "=f"(d.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
+}
+// a += the two halves of b, in f32.
+__device__ __forceinline__ void add_halves(float2 &a, uint32_t b) {
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tadd.rn.f32.f16 %0, lo, %0;\n\tadd.rn.f32.f16 %1, hi, %1;\n\t}"
+        : "+f"(a.x), "+f"(a.y)
+        : "r"(b));
+}
+// (x ^ flip) & mask in one instruction.
+__device__ __forceinline__ uint32_t codes(uint32_t x, uint32_t mask, uint32_t flip) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x48;" : "=r"(r) : "r"(x), "r"(mask), "r"(flip));
+    return r;
 }
 // Largest value over the lanes of the same lane & 3 (the rows of a fragment's column).
 __device__ __forceinline__ float rows_max(float v) {
@@ -343,6 +365,8 @@ __global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_int4_kernel(
     uint32_t phase = 0;                                // and its barrier's phase
     bool ok = true;
 
+    uint32_t flip;                                     // odd tokens' codes, complemented; a register, so that
+    asm volatile("mov.b32 %0, 0xFFFF0000;" : "=r"(flip));   // complement and mask are one instruction
     [[maybe_unused]] const uint64_t keep = kScore ? l2_keep() : 0;
     const T *q = reinterpret_cast<const T *>(p.q);
     while (left > 0) {
@@ -394,9 +418,9 @@ __global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_int4_kernel(
             sb[nt] = make_float2(__shfl_sync(0xffffffffu, c, 8 * lj), __shfl_sync(0xffffffffu, c, 8 * lj + 4));
         }
         float O[NT][kSteps][4];
-        float2 nm[NT], l[NT], z[NT];                   // nm: the negated references
+        float2 nm[NT], l[NT], z[NT], sw[NT];           // nm: the negated references; sw: sums of W
         int r_exp = -40;                               // 2^r_exp = r_top > every v_scale seen
-        float r_top = 0.f, cr = 0.f;                   // cr: v_scale * cr < 2^kWeightExp
+        float r_top = 0.f, cr = 0.f;                   // |v_scale * cr| < 2^kWeightExp, negative in odd rows
         bool first = true;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -405,7 +429,7 @@ __global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_int4_kernel(
 #pragma unroll
                 for (int c = 0; c < 4; ++c) O[nt][u][c] = 0.f;
             nm[nt] = make_float2(INFINITY, INFINITY);
-            l[nt] = z[nt] = make_float2(0.f, 0.f);
+            l[nt] = z[nt] = sw[nt] = make_float2(0.f, 0.f);
         }
         // one stage; kTail: only its first n tokens belong to the row
         auto stage = [&](auto tail, const unsigned char *slot, int ts, int n) {
@@ -448,7 +472,7 @@ __global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_int4_kernel(
                     const float2 kp = unpack_half2(par.x), vp = unpack_half2(par.y);
                     const bool valid = !kTail || t < n;
                     vs[sub][r] = valid ? vp.x : 0.f;
-                    vz[sub][r] = valid ? vp.y : 0.f;
+                    vz[sub][r] = valid ? fmaf(7.5f, vp.x, vp.y) : 0.f;    // the value of code 7.5
                     rmax = fmaxf(rmax, fabsf(vs[sub][r]));
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
@@ -497,7 +521,7 @@ __global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_int4_kernel(
                 const float rs = pow2f(r_exp - r_new);
                 r_exp = r_new;
                 r_top = pow2f(r_new);
-                cr = pow2f(kWeightExp - r_new);
+                cr = pow2f(kWeightExp - r_new) * (li & 1 ? -1.f : 1.f);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float a[2];
@@ -515,6 +539,7 @@ __global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_int4_kernel(
                         const float2 a2 = make_float2(a[0], a[1]);
                         l[nt] = mul2(l[nt], a2);
                         z[nt] = mul2(z[nt], a2);
+                        sw[nt] = mul2(sw[nt], make_float2(a[0] * rs, a[1] * rs));
 #pragma unroll
                         for (int u = 0; u < kSteps; ++u)
 #pragma unroll
@@ -537,7 +562,9 @@ __global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_int4_kernel(
                         z[nt].x = fmaf(w.x, vz[sub][r], z[nt].x);
                         z[nt].y = fmaf(w.y, vz[sub][r], z[nt].y);
                         const float v = vs[sub][r] * cr;
-                        wb[nt][r] = transpose8x8(pack_half2(w.x * v, w.y * v));
+                        const uint32_t wh = pack_half2(w.x * v, w.y * v);
+                        add_halves(sw[nt], wh);
+                        wb[nt][r] = transpose8x8(wh);
                     }
                 // 16 bits (4 channels) of two tokens' bytes side by side: byte b of both in
                 // the low bytes of the halves, for the pairs of nibbles that byte holds
@@ -559,8 +586,8 @@ __global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_int4_kernel(
                             const uint32_t mask = en ? 0x00F000F0u : 0x000F000Fu;
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma16816(O[nt][4 * h + 2 * eb + en], x0 & mask, x1 & mask, x2 & mask, x3 & mask,
-                                         wb[nt][0], wb[nt][1]);
+                                mma16816(O[nt][4 * h + 2 * eb + en], codes(x0, mask, flip), codes(x1, mask, flip),
+                                         codes(x2, mask, flip), codes(x3, mask, flip), wb[nt][0], wb[nt][1]);
                         }
                     }
             }
@@ -594,12 +621,14 @@ __global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_int4_kernel(
         // ---- the row, or this run's partial of it (unnormalised, with its reference and sum).
         // A lane has channels li D / 8 + r D / 16 + u of heads 2 lj and 2 lj + 1.
         const int r = I_b * Hk + I_kvh;
-        const float even = pow2f(r_exp + 24 - kWeightExp), odd = pow2f(r_exp + 20 - kWeightExp);
+        const float unit = pow2f(r_exp - kWeightExp), even = pow2f(r_exp + 24 - kWeightExp),
+                    odd = pow2f(r_exp + 20 - kWeightExp);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const float ls = rows_sum(c ? l[nt].y : l[nt].x), zs = rows_sum(c ? z[nt].y : z[nt].x);
+                const float ls = rows_sum(c ? l[nt].y : l[nt].x);
+                const float zs = rows_sum(fmaf(c ? sw[nt].y : sw[nt].x, -7.5f * unit, c ? z[nt].y : z[nt].x));
                 const int g = nt * 8 + 2 * lj + c;
                 if (g >= G) continue;
                 const float inv = whole ? 1.f / ls : 1.f;

@@ -386,3 +386,33 @@ def test_decode_workspaces_and_streams(pa):
     out = case.run(pa, mass, stream=side)
     side.synchronize()
     assert torch.equal(out, want) and torch.equal(mass, want_mass)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [500, 20000])
+def test_decode_error_of_flat_contexts(pa, n, D):
+    """The rounding of the weights must not be amplified by what cancels between codes and zeros.
+
+    f16 weights are off by at most half a step, 2^-11 of their power of two: 2^-11 / sqrt(3) = 2.8e-4 in
+    the root mean square at most, independently of each other. Each is multiplied by a value about the
+    row's middle, so the output's relative error is 2.8e-4 times that value's size against the values'
+    own (1 for rows that are symmetric; 1.05 allowed), and the output's own rounding adds as much:
+    sqrt(2.8e-4^2 * 1.05^2 + 2.8e-4^2) = 4.1e-4. (The products of plain codes with the weights are off
+    by 1.9 times as much: 6.1e-4.) The norms are over 2048 outputs or more: 5 % of scatter at most."""
+    rng = np.random.default_rng(n + D)
+    case = Case(rng, [n, n], 8, 2, D, 16, "f16")
+    t = case.t
+    k, v = (torch.from_numpy(rng.standard_normal((2 * n, 2, D)).astype(np.float32)).to(dev()) for _ in range(2))
+    slots = torch.from_numpy(np.concatenate([case.bt[b][np.arange(n) // 16] * 16 + np.arange(n) % 16
+                                             for b in range(2)]).astype(np.int32)).to(dev())
+    pa.paged_kv_write_int4(k, v, slots, t["kc"], t["vc"], t["par"])
+    hk, hv = torch.empty_like(k), torch.empty_like(v)
+    pa.paged_kv_read_int4(hk, hv, slots, t["kc"], t["vc"], t["par"])
+    q = torch.from_numpy(rng.standard_normal((2, 8, D)).astype(np.float32)).to(dev()).half()
+    out = torch.empty_like(q)
+    pa.paged_attention_decode_int4(out, q, t["kc"], t["vc"], t["par"], t["bt"], t["lens"], D ** -0.5)
+    hk, hv = (x.double().view(2, n, 2, D) for x in (hk, hv))
+    w = torch.softmax(torch.einsum("bhgd,bthd->bhgt", q.double().view(2, 2, 4, D), hk) * D ** -0.5, -1)
+    ref = torch.einsum("bhgt,bthd->bhgd", w, hv).reshape(2, 8, D)
+    err = float((out.double() - ref).norm() / ref.norm())
+    assert err <= 4.1e-4 * 1.05, err
