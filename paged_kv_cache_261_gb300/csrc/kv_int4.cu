@@ -134,28 +134,30 @@ __device__ __forceinline__ int64_t cache_row(const Int4Cache &c, int64_t slot, i
     return (((slot >> c.log2_block_size) * c.num_kv_heads + h) << c.log2_block_size) + (slot & (bs - 1));
 }
 
-// Eight codes of (x - zero) / scale, `inv` the reciprocal of scale. The product decides unless
-// it is so near a tie that the IEEE quotient has to (below 16 they differ by less than 2^-19).
-__device__ __forceinline__ uint32_t encode8(const float *x, float zero, float scale, float inv) {
+// Eight codes of (x - zero) / scale; inv15 is the reciprocal of scale, over 15. The product,
+// clamped as a number in [0, 1], decides unless it is so near a tie that the IEEE quotient has to
+// (they differ by less than 2^-18).
+__device__ __forceinline__ uint32_t encode8(const float *x, float zero, float scale, float inv15) {
     constexpr float kMagic = 12582912.f;                 // 1.5 * 2^23: adding it rounds to an integer
-    uint32_t codes = 0;
-    bool tie = false;
+    float n[8], off = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], zero), inv), 0.f), 15.f);
-        const float n = __fadd_rn(q, kMagic);
-        tie |= fabsf(__fsub_rn(q, __fsub_rn(n, kMagic))) > 0.5f - 4e-6f;
-        codes += (__float_as_uint(n) - 0x4B400000u) << (4 * i);
+        const float t = __saturatef(__fmul_rn(__fsub_rn(x[i], zero), inv15));
+        n[i] = __fsub_rn(__fmaf_rn(t, 15.f, kMagic), kMagic);
+        off = fmaxf(off, fabsf(__fmaf_rn(t, 15.f, -n[i])));
     }
-    if (tie) {
-        codes = 0;
+    if (off > 0.5f - 6e-6f) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float n = rintf(__fdiv_rn(__fsub_rn(x[i], zero), scale));
-            codes |= (uint32_t)fminf(fmaxf(n, 0.f), 15.f) << (4 * i);
-        }
+        for (int i = 0; i < 8; ++i)
+            n[i] = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[i], zero), scale)), 0.f), 15.f);
     }
-    return codes;
+    // four codes make a whole number below 2^16
+    float four[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        four[h] = __fmaf_rn(__fmaf_rn(n[4 * h + 3], 16.f, n[4 * h + 2]), 256.f, __fmaf_rn(n[4 * h + 1], 16.f, n[4 * h]));
+    return __byte_perm(__float_as_uint(__fadd_rn(four[0], 8388608.f)), __float_as_uint(__fadd_rn(four[1], 8388608.f)),
+                       0x5410);
 }
 
 // Writing: a lane has kCh channels of a row. What is done once a row -- the shuffles, the
@@ -199,13 +201,13 @@ __global__ __launch_bounds__(kThreads) void kv_write_int4_kernel(const T *__rest
     const __half zero_h = __float2half_rn(lo);
     const __half scale_h = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
     const float zero = __half2float(zero_h), scale = __half2float(scale_h);
-    const float inv = scale > 0.f ? __frcp_rn(scale) : 0.f;
+    const float inv15 = scale > 0.f ? __fdiv_rn(__frcp_rn(scale), 15.f) : 0.f;
     alignas(16) uint32_t codes[kWords];
 #pragma unroll
     for (int w = 0; w < kWords; ++w) {
         float y[8];
         x[w].values(y);
-        codes[w] = scale > 0.f ? encode8(y, zero, scale, inv) : 0u;
+        codes[w] = scale > 0.f ? encode8(y, zero, scale, inv15) : 0u;
     }
     const uint32_t mine = (uint32_t)__half_as_ushort(scale_h) | ((uint32_t)__half_as_ushort(zero_h) << 16);
     const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, kLanes);   // the V row's, for the K row's lanes
@@ -217,67 +219,46 @@ __global__ __launch_bounds__(kThreads) void kv_write_int4_kernel(const T *__rest
     if (part == 0 && !is_v) reinterpret_cast<uint2 *>(c.params)[dst] = make_uint2(mine, other);
 }
 
-// The (token, kv head) pairs of a thread that reads: kU of them, `pairs` (those a CTA has side
-// by side) apart, so that their loads are in flight together (one: 206 us for 131,071 tokens of
-// 8 kv heads, four: 135; with the codes widened as below 109.5, 5.6 TB/s). step_t and step_h:
-// pairs / kv heads and the rest.
-struct Walk {
-    uint32_t t;
-    int h;
-    __device__ __forceinline__ Walk(uint32_t th, int kv_heads) : t(th / (uint32_t)kv_heads), h((int)(th - t * kv_heads)) {}
-    __device__ __forceinline__ void next(int kv_heads, int step_t, int step_h) {
-        t += step_t;
-        h += step_h;
-        if (h >= kv_heads) {
-            h -= kv_heads;
-            ++t;
-        }
-    }
-};
-
-template <typename T, int D, int kU>
+// Reading: a lane has kCh channels of a row, in words of 8 a row's lanes apart, so that loads and
+// stores of a warp are contiguous; again most instructions come once a row (131,071 tokens of 8
+// kv heads: 8 channels 206 us, four such rows a lane 109.7, 16 channels of two rows 103.8, 32 of
+// one 103.2, 6.6 TB/s).
+template <typename T, int D, int kCh>
 __global__ __launch_bounds__(kThreads) void kv_read_int4_kernel(T *__restrict__ k, T *__restrict__ v,
                                                                 const int32_t *__restrict__ slots,
-                                                                uint32_t num_tokens, const Int4Cache c, int step_t,
-                                                                int step_h, unsigned int *err) {
-    constexpr int kLanes = D / 8, kPairs = kThreads / kLanes / 2;
+                                                                uint32_t num_tokens, const Int4Cache c,
+                                                                unsigned int *err) {
+    constexpr int kLanes = D / kCh, kWords = kCh / 8;
+    constexpr int kPairs = kThreads / kLanes / 2;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int part = threadIdx.x % kLanes;
     const bool is_v = (threadIdx.x / kLanes) & 1;
-    const uint32_t th0 = blockIdx.x * (kPairs * kU) + threadIdx.x / (2 * kLanes);
-    const uint32_t *cache = reinterpret_cast<const uint32_t *>(is_v ? c.value : c.key);
-    T *dst = (is_v ? v : k) + (int64_t)th0 * D + part * 8;
-    Walk at(th0, c.num_kv_heads);
-    int64_t src[kU];
-    uint32_t codes[kU];
-    __half2 sz[kU];
+    const uint32_t th = blockIdx.x * kPairs + threadIdx.x / (2 * kLanes);   // (token, kv head) pair
+    const uint32_t t = th / (uint32_t)c.num_kv_heads;
+    const int h = (int)(th - t * c.num_kv_heads);
+    if (t >= num_tokens) return;
+    const int64_t src = cache_row(c, slots[t], h, part == 0 && h == 0 && !is_v, err);
+    if (src < 0) return;
+    const uint32_t *row = reinterpret_cast<const uint32_t *>(is_v ? c.value : c.key) + src * (D / 8) + part;
+    uint32_t codes[kWords];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-        src[u] = at.t < num_tokens ? cache_row(c, slots[at.t], at.h, part == 0 && at.h == 0 && !is_v, err) : -1;
-        at.next(c.num_kv_heads, step_t, step_h);
-    }
+    for (int w = 0; w < kWords; ++w) codes[w] = __ldcs(row + w * kLanes);
+    const float2 f = __half22float2(reinterpret_cast<const __half2 *>(c.params)[src * 2 + is_v]);
+    const float scale = f.x * 16777216.f;
+    T *dst = (is_v ? v : k) + (int64_t)th * D + part * 8;
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-        if (src[u] < 0) continue;
-        codes[u] = __ldcs(cache + src[u] * kLanes + part);
-        sz[u] = reinterpret_cast<const __half2 *>(c.params)[src[u] * 2 + is_v];
-    }
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-        if (src[u] < 0) continue;
-        const float2 f = __half22float2(sz[u]);
-        const float scale = f.x * 16777216.f;
-        float x[8];
+    for (int w = 0; w < kWords; ++w) {
         // a code in an f16's low bits is code * 2^-24, so no integer is converted; its product
         // with the scale is exact in float32 (4 + 11 bits), so the fused form rounds once
+        float x[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 n = __half22float2(as2<__half2>((codes[u] >> (4 * i)) & 0x000F000Fu));
+            const float2 n = __half22float2(as2<__half2>((codes[w] >> (4 * i)) & 0x000F000Fu));
             x[i] = fmaf(n.x, scale, f.y);
             x[i + 4] = fmaf(n.y, scale, f.y);
         }
-        store8(dst + (int64_t)u * kPairs * D, x);
+        store8(dst + w * kLanes * 8, x);
     }
 }
 
@@ -294,12 +275,12 @@ __global__ __launch_bounds__(kThreads) void copy_params_kernel(uint4 *params, co
         params[dst * block_vecs + i] = params[src * block_vecs + i];
 }
 
-// Channels per lane in writing, rows per thread in reading: more where there are enough rows to
-// fill the SMs all the same.
-constexpr int kWriteChannels = 32, kReadUnroll = 4;
+// Channels per lane: more where there are enough rows to fill the SMs all the same.
+constexpr int kFewChannels = 8, kManyChannels = 32;
 constexpr int64_t kManyRows = 16384;             // (token, kv head) pairs
 
-unsigned row_grid(const Int4Cache &c, int64_t num_tokens, int pairs) {     // pairs of a CTA
+template <int D> unsigned row_grid(const Int4Cache &c, int64_t num_tokens, int channels) {
+    const int pairs = kThreads / (D / channels) / 2;     // of a CTA
     return (unsigned)((num_tokens * c.num_kv_heads + pairs - 1) / pairs);
 }
 
@@ -307,20 +288,18 @@ template <typename T, int D>
 int write_t(const void *k, const void *v, const int32_t *slots, int64_t n, const Int4Cache &c, unsigned int *err,
             cudaStream_t s) {
     const bool many = n * c.num_kv_heads >= kManyRows;
-    const unsigned grid = row_grid(c, n, kThreads / (D / (many ? kWriteChannels : 8)) / 2);
-    auto kern = many ? kv_write_int4_kernel<T, D, kWriteChannels> : kv_write_int4_kernel<T, D, 8>;
-    return launch_pdl(kern, dim3(grid), dim3(kThreads), 0, s, (const T *)k, (const T *)v, slots, (uint32_t)n, c, err);
+    auto kern = many ? kv_write_int4_kernel<T, D, kManyChannels> : kv_write_int4_kernel<T, D, kFewChannels>;
+    return launch_pdl(kern, dim3(row_grid<D>(c, n, many ? kManyChannels : kFewChannels)), dim3(kThreads), 0, s,
+                      (const T *)k, (const T *)v, slots, (uint32_t)n, c, err);
 }
 
 template <typename T, int D>
 int read_t(void *k, void *v, const int32_t *slots, int64_t n, const Int4Cache &c, unsigned int *err,
            cudaStream_t s) {
-    constexpr int pairs = kThreads / (D / 8) / 2;
-    const int st = pairs / c.num_kv_heads, sh = pairs % c.num_kv_heads;
     const bool many = n * c.num_kv_heads >= kManyRows;
-    const unsigned grid = row_grid(c, n, pairs * (many ? kReadUnroll : 1));
-    auto kern = many ? kv_read_int4_kernel<T, D, kReadUnroll> : kv_read_int4_kernel<T, D, 1>;
-    return launch_pdl(kern, dim3(grid), dim3(kThreads), 0, s, (T *)k, (T *)v, slots, (uint32_t)n, c, st, sh, err);
+    auto kern = many ? kv_read_int4_kernel<T, D, kManyChannels> : kv_read_int4_kernel<T, D, kFewChannels>;
+    return launch_pdl(kern, dim3(row_grid<D>(c, n, many ? kManyChannels : kFewChannels)), dim3(kThreads), 0, s, (T *)k,
+                      (T *)v, slots, (uint32_t)n, c, err);
 }
 
 template <typename T>
