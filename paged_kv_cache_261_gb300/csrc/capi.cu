@@ -978,16 +978,16 @@ int pa_paged_kv_evict(int32_t *kept, int64_t kept_len, const float *mass, int64_
     p.num_kv_heads = num_kv_heads;
     p.log2_block_size = ilog2(block_size);
     p.recent = recent;
-    p.num_planes = int4 ? 3 : 2;
-    void *bases[3] = {key_cache, value_cache, kv_params};
-    for (int i = 0; i < p.num_planes; ++i) {
-        const int64_t bytes = i == 2 ? 8 : row;
+    void *bases[2] = {key_cache, value_cache};
+    for (int i = 0; i < 2; ++i) {
         pa::EvictPlane &pl = p.planes[i];
         pl.base = static_cast<char *>(bases[i]);
-        pl.row_bytes = (int)bytes;
-        pl.block_stride = bytes * block_size * num_kv_heads;
-        pl.token_stride = int4 ? bytes : bytes * num_kv_heads;
-        pl.head_stride = int4 ? bytes * block_size : bytes;
+        pl.row_bytes = (int)row;
+        pl.block_stride = row * block_size * num_kv_heads;
+        pl.token_stride = int4 ? row : row * num_kv_heads;
+        pl.head_stride = int4 ? row * block_size : row;
+        pl.side = int4 ? static_cast<char *>(kv_params) + 4 * i : nullptr;
+        pl.side_shift = int4 ? ilog2((int)row / 8) : 0;
     }
     return pa::launch_evict(p, device_sm_count(), static_cast<cudaStream_t>(stream)) == 0 ? PA_OK : PA_ERR_CUDA;
 }

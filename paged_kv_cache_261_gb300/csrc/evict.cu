@@ -416,16 +416,19 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictParam
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;
 
-// VecT: 16 bytes (code and channel rows) or 8 (parameter rows).
-template <typename VecT>
+// kSide: the rows have parameters (4-bit caches). A plane's CTAs move its half of them, a row a
+// thread. (CTAs of their own, a third of the launch for a ninth of the bytes, took as long as the
+// others: long 4-bit contexts 159.5 us, with their read-back, against 152.)
+template <bool kSide>
 __device__ __forceinline__ void move_rows(const EvictParams &p, const EvictPlane &pl, const EvictSplit &s, int b,
                                           int h, const int32_t *kept, int rank, int nc) {
     cg::cluster_group cluster = cg::this_cluster();
-    const uint32_t vecs = pl.row_bytes / (int)sizeof(VecT);      // vectors per row
+    const uint32_t vecs = pl.row_bytes / 16;                     // vectors per row
     const int32_t *src_table = p.block_tables + (int64_t)b * p.max_blocks;
     const int32_t *dst_table = p.out_block_tables + (int64_t)b * p.out_max_blocks;
     const int bs_mask = (1 << p.log2_block_size) - 1;
     char *base = pl.base + h * pl.head_stride;
+    [[maybe_unused]] char *side = kSide ? pl.side + ((h * pl.head_stride) >> pl.side_shift) : nullptr;
     // A wave: up to 256 whole rows a CTA, kMoveUnroll vectors a thread. While a wave's rows are
     // read, the next one's places are looked up, one row a thread, into shared memory.
     const uint32_t rows_cta = min((uint32_t)kMoveThreads, kMoveThreads * kMoveUnroll / vecs);
@@ -457,8 +460,15 @@ __device__ __forceinline__ void move_rows(const EvictParams &p, const EvictPlane
     __syncthreads();
     int buf = 0;
     for (int64_t r0 = 0; r0 < s.n; r0 += step, buf ^= 1) {
-        VecT v[kMoveUnroll];
-        VecT *dst[kMoveUnroll];
+        uint4 v[kMoveUnroll], *dst[kMoveUnroll];
+        [[maybe_unused]] uint32_t sv = 0, *sdst = nullptr;       // the parameters of row threadIdx.x
+        if (kSide && threadIdx.x < rows_cta) {
+            const longlong2 at = place[buf][threadIdx.x];
+            if (at.y >= 0) {
+                sv = *reinterpret_cast<const uint32_t *>(side + (at.x >> pl.side_shift));
+                sdst = reinterpret_cast<uint32_t *>(side + (at.y >> pl.side_shift));
+            }
+        }
 #pragma unroll
         for (int u = 0; u < kMoveUnroll; ++u) {
             const uint32_t i = u * kMoveThreads + threadIdx.x;
@@ -467,8 +477,8 @@ __device__ __forceinline__ void move_rows(const EvictParams &p, const EvictPlane
             if (i >= used) continue;
             const longlong2 at = place[buf][r];
             if (at.y < 0) continue;
-            v[u] = reinterpret_cast<const VecT *>(base + at.x)[c];
-            dst[u] = reinterpret_cast<VecT *>(base + at.y) + c;
+            v[u] = reinterpret_cast<const uint4 *>(base + at.x)[c];
+            dst[u] = reinterpret_cast<uint4 *>(base + at.y) + c;
         }
         look_up(r0 + step, from, buf ^ 1);
         from = index(r0 + 2 * step);
@@ -477,10 +487,11 @@ __device__ __forceinline__ void move_rows(const EvictParams &p, const EvictPlane
 #pragma unroll
         for (int u = 0; u < kMoveUnroll; ++u)
             if (dst[u]) *dst[u] = v[u];
+        if (kSide && sdst) *sdst = sv;
     }
 }
 
-__global__ __launch_bounds__(kMoveThreads) void evict_move_kernel(const EvictParams p) {
+template <bool kSide> __global__ __launch_bounds__(kMoveThreads) void evict_move_kernel(const EvictParams p) {
     cg::cluster_group cluster = cg::this_cluster();
     const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int h = blockIdx.x / nc, b = blockIdx.y;
@@ -488,8 +499,7 @@ __global__ __launch_bounds__(kMoveThreads) void evict_move_kernel(const EvictPar
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const EvictSplit s = evict_split(p, b, false);
     const int32_t *kept = p.kept + ((int64_t)b * p.num_kv_heads + h) * p.kept_len;
-    if (pl.row_bytes % 16 == 0) move_rows<uint4>(p, pl, s, b, h, kept, rank, nc);
-    else move_rows<uint2>(p, pl, s, b, h, kept, rank, nc);
+    move_rows<kSide>(p, pl, s, b, h, kept, rank, nc);
 }
 
 template <typename Kern>
@@ -545,8 +555,8 @@ int launch_evict(const EvictParams &p, int sms, cudaStream_t stream) {
         rc = cudaGetLastError() == cudaSuccess ? 0 : -1;
     }
     if (rc != 0) return rc;
-    return launch_cluster(evict_move_kernel, p.num_kv_heads, p.num_seqs, p.num_planes,
-                          cluster_for(rows * p.num_planes, 2 * sms), kMoveThreads, 0, stream, p);
+    return launch_cluster(p.planes[0].side ? evict_move_kernel<true> : evict_move_kernel<false>, p.num_kv_heads,
+                          p.num_seqs, 2, cluster_for(rows * 2, sms), kMoveThreads, 0, stream, p);
 }
 
 }  // namespace pa

@@ -68,7 +68,11 @@ inline int score_plane_tc(int group) { return group <= 4 ? 2 : (group <= 8 ? 4 :
 struct EvictPlane {
     char *base;
     int64_t block_stride, token_stride, head_stride;
-    int row_bytes;             // a multiple of 8
+    int row_bytes;             // a multiple of 16
+    // 4-bit caches: where this array's halves (scale and zero, 4 of 8 bytes) of the parameters
+    // are, which lie as the rows do, 1 / 2^side_shift as far apart
+    char *side;
+    int side_shift;
 };
 
 struct EvictParams {
@@ -87,8 +91,7 @@ struct EvictParams {
     int num_seqs, num_kv_heads;
     int log2_block_size;
     int recent;
-    int num_planes;
-    EvictPlane planes[3];
+    EvictPlane planes[2];      // K and V
 };
 int launch_evict(const EvictParams &p, int sms, cudaStream_t stream);
 

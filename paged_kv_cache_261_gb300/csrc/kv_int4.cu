@@ -18,7 +18,7 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 template <typename T> __device__ __forceinline__ void store8(T *dst, const float *x) {
     alignas(16) T v[8];
