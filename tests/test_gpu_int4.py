@@ -120,6 +120,46 @@ def test_read_back(pa, dst, T, Hk, D, bs):
         assert torch.equal(out.cpu(), torch.from_numpy(ref).to(cc.TORCH[dst]))
 
 
+@pytest.mark.parametrize("src", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D,bs", [(64, 8), (128, 32)])
+def test_write_and_read_many_rows(pa, src, D, bs):
+    """Enough rows for the wide form of both kernels: ties between codes, constant rows, infinities and
+    NaN among them, slots of -1 and out of range, a last CTA that is not full."""
+    rng = np.random.default_rng(D)
+    T, Hk, d = 5501, 3, dev()
+    x = np.stack([rows(rng, (T, Hk, D), "k"), rows(rng, (T, Hk, D))])
+    x[:, 10:400] = rng.integers(-8, 24, (2, 390, Hk, D)) * np.float32(0.5)     # ties, halves of a step
+    x[:, 10:400, :, 0], x[:, 10:400, :, 1] = 0.0, 7.5
+    x[0, 500], x[1, 501], x[0, 502, 1, 7], x[1, 503, 2, 5], x[0, 504, 0, 9] = 1.25, 0.0, np.nan, np.inf, -np.inf
+    x[:, 600:700] *= np.float32(1e-6)
+    x[:, 700:800] *= np.float32(1e4)
+    NB = -(-T // bs) + 1
+    slots = rng.choice(NB * bs, T, replace=False).astype(np.int32)
+    slots[[0, 77, T - 1]] = -1, NB * bs, -5
+    kc = torch.full((NB, Hk, bs, D // 2), 0xA5, dtype=torch.uint8, device=d)
+    vc, par = torch.full_like(kc, 0x5A), torch.full((NB, Hk, bs, 4), 7.0, dtype=torch.float16, device=d)
+    src_t = [torch.from_numpy(a).to(d).to(cc.TORCH[src]) for a in x]
+    pa.paged_kv_write_int4(*src_t, torch.from_numpy(slots).to(d), kc, vc, par)
+    want = [t.cpu().numpy() for t in (torch.full_like(kc, 0xA5), torch.full_like(vc, 0x5A), torch.full_like(par, 7.0))]
+    live = np.flatnonzero((slots >= 0) & (slots < NB * bs))
+    b, o = slots[live] // bs, slots[live] % bs
+    back = []
+    for i, a in enumerate(x):
+        codes, sc, ze = cc.cache_rows(cc.stored(a[live], src).astype(np.float32))
+        want[i][b, :, o] = codes
+        want[2][b, :, o, 2 * i], want[2][b, :, o, 2 * i + 1] = sc, ze
+        back.append(cc.values(codes, sc, ze).astype(np.float32))
+    assert_cache((kc, vc, par), want)
+    out = [torch.full((T, Hk, D), 5.0 + i, dtype=cc.TORCH[src], device=d) for i in range(2)]
+    pa.paged_kv_read_int4(*out, torch.from_numpy(slots).to(d), kc, vc, par)
+    for i, (got, v) in enumerate(zip(out, back)):
+        ref = np.full((T, Hk, D), 5.0 + i, np.float32)
+        ref[live] = v
+        assert np.array_equal(got.float().cpu().numpy(), torch.from_numpy(ref).to(cc.TORCH[src]).float().numpy(),
+                              equal_nan=True)
+    assert pa.get_device_error() == pa.PA_DEVERR_SLOT
+
+
 def test_copy_blocks_moves_codes_and_parameters(pa):
     rng = np.random.default_rng(5)
     d = dev()
