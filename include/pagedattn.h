@@ -479,7 +479,8 @@ size_t pa_decode_int4_workspace_bytes(int num_seqs, int num_heads, int num_kv_he
  * NaN parameter inside a context makes the outputs of its heads NaN. The work is cut
  * into equal runs of tokens over the device, whatever the lengths (there is no partition
  * size). max_context_len, the workspace (size from pa_decode_int4_workspace_bytes; NULL =
- * cudaMallocAsync on the stream) and the device error bits are those of
+ * cudaMallocAsync on the stream; it serves one call at a time, so calls that may run at the
+ * same time need one each) and the device error bits are those of
  * pa_paged_attention_decode.
  */
 int pa_paged_attention_decode_int4(void *out, const void *q, const void *key_cache, const void *value_cache,
@@ -490,7 +491,7 @@ int pa_paged_attention_decode_int4(void *out, const void *q, const void *key_cac
                                    void *stream);
 
 /* ---- accumulated attention weights, and eviction by them --------------------
- * Not on the pages [P1-P3]; an extension that keeps long caches within a budget.
+ * Not on the pages [P1-P3]; an extension that keeps long caches to a size.
  */
 
 /* Bytes of workspace pa_paged_attention_decode_scored needs for these sizes. */
@@ -509,7 +510,7 @@ size_t pa_decode_scored_workspace_bytes(int num_seqs, int num_heads, int num_kv_
  * pa_paged_attention_decode, bit for bit, with the same arguments (caches of float32,
  * f16 or bf16). The workspace (size from pa_decode_scored_workspace_bytes; NULL =
  * cudaMallocAsync on the stream) holds the scores: 4 bytes per query head and token, the
- * heads of a group rounded up to 2, 4, 8 or 16.
+ * heads of a group rounded up to 2, 4, 8 or 16; it serves one call at a time.
  */
 int pa_paged_attention_decode_scored(void *out, const void *q, float *mass, int64_t mass_len, const void *key_cache,
                                      const void *value_cache, const int32_t *block_tables, int max_blocks_per_seq,

@@ -30,11 +30,12 @@ def decode(pa, case, t, out, mass, **kw):
 
 # ---------------------------------------------------------------------------- graphs
 
-@pytest.mark.parametrize("own_workspace", [False, True])
-def test_two_graphs_replayed_in_turn(pa, own_workspace):
+@pytest.mark.parametrize("workspace", ["none", "each", "shared"])
+def test_two_graphs_replayed_in_turn(pa, workspace):
     """A step (write, decode with weights, eviction into other blocks, read-back) captured twice, for two
     batches of unlike sizes; the graphs are replayed in turn, with new inputs written in place, and the
-    first is destroyed before the second runs on."""
+    first is destroyed before the second runs on. workspace: the binding's, one of each batch's own,
+    or one that both graphs hold."""
     rng = np.random.default_rng(3)
     d = dev()
 
@@ -59,7 +60,7 @@ def test_two_graphs_replayed_in_turn(pa, own_workspace):
         t["vo"] = torch.zeros_like(t["ko"])
         t["oslots"] = torch.arange(extra * 16, dtype=torch.int32, device=d) + case.NB * 16
         n = pa.decode_int4_workspace_bytes(B, H, Hk, 128, max(lens), True)
-        t["ws"] = torch.empty(n, dtype=torch.uint8, device=d) if own_workspace else None
+        t["ws"] = None if workspace == "none" else torch.empty(n, dtype=torch.uint8, device=d)
         return case, t
 
     def step(case, t):
@@ -71,6 +72,10 @@ def test_two_graphs_replayed_in_turn(pa, own_workspace):
         return [t[k].clone() for k in ("out", "mass", "kept", "mass_out", "ko", "vo")]
 
     sets = [make(1, [300, 41, 77], 8, 2), make(2, [90, 2000, 40, 64, 700], 16, 4)]
+    if workspace == "shared":
+        sizes = [t["ws"].numel() for _, t in sets]
+        for _, t in sets:
+            t["ws"] = sets[sizes.index(max(sizes))][1]["ws"]
     want = []
     for case, t in sets:
         step(case, t)
