@@ -856,13 +856,17 @@ def paged_kv_evict(kept, mass, mass_out, key_cache, value_cache, block_tables, o
     recent = min(int(recent), 0x7FFFFFFF)
     if recent < 0:
         raise ValueError("recent must not be negative")
-    with _on(dev):
-        rc = _lib.pa_paged_kv_evict(kept.data_ptr(), kept.shape[2], mass.data_ptr(), mass_len, mass_out.data_ptr(),
-                                    out_len, key_cache.data_ptr(), value_cache.data_ptr(), par,
-                                    block_tables.data_ptr(), block_tables.shape[1], out_block_tables.data_ptr(),
-                                    out_block_tables.shape[1], context_lens.data_ptr(), keep_lens.data_ptr(),
-                                    recent, B, hk, d, bs, nb, dt, _stream_ptr(stream, dev))
-    _check(rc, "pa_paged_kv_evict")
+    if _elsewhere(dev):
+        with _on(dev):
+            return paged_kv_evict(kept, mass, mass_out, key_cache, value_cache, block_tables, out_block_tables,
+                                  context_lens, keep_lens, recent, kv_params, stream or torch.cuda.current_stream(dev))
+    rc = _lib.pa_paged_kv_evict(kept.data_ptr(), kept.shape[2], mass.data_ptr(), mass_len, mass_out.data_ptr(),
+                                out_len, key_cache.data_ptr(), value_cache.data_ptr(), par, block_tables.data_ptr(),
+                                block_tables.shape[1], out_block_tables.data_ptr(), out_block_tables.shape[1],
+                                context_lens.data_ptr(), keep_lens.data_ptr(), recent, B, hk, d, bs, nb, dt,
+                                _stream_ptr(stream, dev))
+    if rc:
+        _check(rc, "pa_paged_kv_evict")
 
 
 def get_device_error(stream=None, device=None) -> int:

@@ -28,6 +28,8 @@
 // 54 us (two waves of CTAs, with 21 MB of masses beside their counts in shared memory).
 #include <cooperative_groups.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels_compress.h"
 
@@ -542,9 +544,12 @@ int launch_evict(const EvictParams &p, int sms, cudaStream_t stream) {
         attr_set[dev] = true;
     }
     const int64_t rows = (int64_t)p.num_seqs * p.num_kv_heads;
-    // the selection's clusters also grow with the row: at most 8192 masses a CTA where that is possible
-    int c = cluster_for(rows, sms);
-    while (c < kMaxCluster && (int64_t)c * 8192 < p.context_limit) c *= 2;
+    // The selection's clusters grow with the row alone, to 16384 masses a CTA: what a cluster's
+    // barriers cost is more than its other CTAs save (8 kv heads, whole call, us, against clusters
+    // that fill the SMs: one sequence of 300 tokens 8.5 and 14.7, 16 of 2000 14.7 and 33.6, 16 of
+    // 16000 23.9 and 37.7, 4 of 40000 25.9 and 27.4; one of 16000 18.6 and 17.2).
+    int c = 1;
+    while (c < kMaxCluster && (int64_t)c * 16384 < p.context_limit) c *= 2;
     const int64_t slice = ((p.context_limit + c - 1) / c + 3) & ~int64_t(3);
     int rc = 0;
     if (slice <= kMaxSlice) {
@@ -555,8 +560,13 @@ int launch_evict(const EvictParams &p, int sms, cudaStream_t stream) {
         rc = cudaGetLastError() == cudaSuccess ? 0 : -1;
     }
     if (rc != 0) return rc;
+    // the movement's clusters fill the SMs, but have no more CTAs than one wave takes (50 tokens of 8
+    // kv heads: 8.5 -> 7.9 us in all)
+    int m = cluster_for(rows * 2, sms);
+    const int64_t wave = std::min<int64_t>(kMoveThreads, kMoveThreads * kMoveUnroll / (p.planes[0].row_bytes / 16));
+    while (m > 1 && (m / 2) * wave >= p.keep_limit) m /= 2;
     return launch_cluster(p.planes[0].side ? evict_move_kernel<true> : evict_move_kernel<false>, p.num_kv_heads,
-                          p.num_seqs, 2, cluster_for(rows * 2, sms), kMoveThreads, 0, stream, p);
+                          p.num_seqs, 2, m, kMoveThreads, 0, stream, p);
 }
 
 }  // namespace pa
