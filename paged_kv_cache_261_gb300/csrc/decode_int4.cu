@@ -675,24 +675,24 @@ __global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_int4_kernel(
 }
 
 // Joins the partials of the rows that several runs share: M = max m_i, L = sum l_i
-// 2^(m_i - M), out = sum o_i 2^(m_i - M) / L. Warps per (query head, sequence): one where a
-// row has few partials, four (joined through shared memory) where it has many. A warp reads
+// 2^(m_i - M), out = sum o_i 2^(m_i - M) / L. Warps per (query head, sequence), WPR: one where a
+// row has few partials, 4 or 16 (joined through shared memory) where it has many. A warp reads
 // 32 partials' pairs at once, one a lane, and then their outputs, kJoinBatch in flight.
-constexpr int kJoinThreads = 128;
+constexpr int kJoinWarps(int wpr) { return wpr < 4 ? 4 : wpr; }      // of a CTA
 constexpr int kJoinBatch = 8;
 
-template <typename T, int D, int WPR>
-__global__ __launch_bounds__(kJoinThreads) void decode_int4_join_kernel(const DecodeParams p, const Int4Work ws) {
+template <typename T, int D, int WPR, int kWarps = kJoinWarps(WPR)>
+__global__ __launch_bounds__(kWarps * 32) void decode_int4_join_kernel(const DecodeParams p, const Int4Work ws) {
     constexpr int N = D / 32;                          // channels of a lane
-    __shared__ float2 ml_s[4];
-    __shared__ float o_s[4][D];
+    __shared__ float2 ml_s[kWarps];
+    __shared__ float o_s[WPR > 1 ? kWarps : 1][D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = warp % WPR;
-    const int64_t head = (int64_t)blockIdx.x * (4 / WPR) + warp / WPR;   // (sequence, query head)
+    const int64_t head = (int64_t)blockIdx.x * (kWarps / WPR) + warp / WPR;   // (sequence, query head)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // after the wait: the accumulation of the weights relies on the decode having finished
     asm volatile("griddepcontrol.launch_dependents;");
-    if (head >= (int64_t)p.num_seqs * p.num_heads) return;   // with WPR 4, the whole CTA
+    if (head >= (int64_t)p.num_seqs * p.num_heads) return;   // with WPR > 1, the whole CTA
     const int G = p.group;
     const int64_t row = head / G;
     const int g = (int)(head - row * G);
@@ -757,9 +757,9 @@ __global__ __launch_bounds__(kJoinThreads) void decode_int4_join_kernel(const De
 #pragma unroll
         for (int u = 0; u < N; ++u) acc[u] = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) M = fmaxf(M, ml_s[w].x);
+        for (int w = 0; w < WPR; ++w) M = fmaxf(M, ml_s[w].x);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < WPR; ++w) {
             const float2 v = ml_s[w];
             const float f = v.x == -INFINITY ? (v.y == v.y ? 0.f : v.y) : fast_exp2(v.x - M);
             l = fmaf(v.y, f, l);
@@ -789,13 +789,17 @@ int launch_t(const DecodeParams &p, const Int4Work &ws, int grid, cudaStream_t s
     }
     const int rc = launch_pdl(kern, dim3((unsigned)grid), dim3(C::kThreads), C::kSmem, stream, p, ws);
     if (rc != 0) return rc;
-    // partials a row, about: (runs + rows) / rows
+    // Partials a row: about runs / rows, for contexts of the limit's length. (8 kv heads, us with up to
+    // 4 warps a row and with 16: one context of 16,000 tokens 21.2 and 13.2, of 131,072 44.9 and 35.9,
+    // three of 40,000 to 120,000 60.0 and 55.4; with 11 partials a row, 16 warps are 0.15 slower.)
     const int64_t heads = (int64_t)p.num_seqs * p.num_heads, rows = (int64_t)p.num_seqs * p.num_kv_heads;
-    if ((int64_t)grid * C::kWarps <= 8 * rows)
-        return launch_pdl(decode_int4_join_kernel<T, D, 1>, dim3((unsigned)((heads + 3) / 4)),
-                          dim3(kJoinThreads), 0, stream, p, ws);
-    return launch_pdl(decode_int4_join_kernel<T, D, 4>, dim3((unsigned)heads), dim3(kJoinThreads), 0, stream, p,
-                      ws);
+    const int64_t stages = (p.context_limit + (int64_t)C::kTok - 1) / C::kTok;
+    const int64_t runs = std::min<int64_t>((int64_t)grid * C::kWarps, rows * stages);
+    const int wpr = runs <= 8 * rows ? 1 : (runs <= 32 * rows ? 4 : 16), cta = kJoinWarps(wpr);
+    auto join = wpr == 1   ? decode_int4_join_kernel<T, D, 1>
+                : wpr == 4 ? decode_int4_join_kernel<T, D, 4>
+                           : decode_int4_join_kernel<T, D, 16>;
+    return launch_pdl(join, dim3((unsigned)((heads * wpr + cta - 1) / cta)), dim3(cta * 32), 0, stream, p, ws);
 }
 
 template <typename T, int D> int launch_g(const DecodeParams &p, const Int4Work &ws, int grid, cudaStream_t stream) {
