@@ -60,7 +60,12 @@ __global__ __launch_bounds__(kThreads) void decode_mass_kernel(const DecodeParam
     // by side; this one waits for it at its end, so that whatever follows comes after both.
     const bool beside = ws.rows != nullptr;
     if (!beside) asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
+    // Over planes of several heads the decode, and so most likely the next call's, is a persistent
+    // kernel of one CTA per SM, whose early start pays (8B-shaped batch 114.0 -> 112.2 us, of the
+    // 4-bit cache 48.7 -> 47.3). The SIMT decode's CTAs would be packed onto whatever SMs are free
+    // first (32 sequences of 8 heads, 1 kv head, head_dim 64: 152.6 us a call against 69.3), and an
+    // eviction's are, a little (4-bit decode and eviction 71.3 -> 77.6).
+    if constexpr (V > 1) asm volatile("griddepcontrol.launch_dependents;");
     int ctx = p.context_lens[b];
     ctx = ctx < 0 ? 0 : min(ctx, p.context_limit);
     const int64_t c0 = (int64_t)blockIdx.x * rounds * kChunk;
