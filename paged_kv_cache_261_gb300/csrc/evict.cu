@@ -5,7 +5,7 @@
 // the largest mass (equal masses: the lower index first; a NaN counts below every
 // number). The staying tokens keep their order; token kept[i] becomes token i.
 //
-// Selection (evict_select_kernel, a cluster of CTAs per (sequence, kv head)): the row's
+// Selection (evict_select_kernel, a CTA or a cluster of them per (sequence, kv head)): the row's
 // masses are read once, each CTA keeping a slice in shared memory. As unsigned keys of the
 // same order, a radix descent over three digits finds the (n - r)-th largest key and how
 // many of the tokens equal to it stay: each CTA counts its slice's digits, and every CTA
