@@ -560,8 +560,6 @@ int launch_evict(const EvictParams &p, int sms, cudaStream_t stream) {
         rc = cudaGetLastError() == cudaSuccess ? 0 : -1;
     }
     if (rc != 0) return rc;
-    // the movement's clusters fill the SMs, but have no more CTAs than one wave takes (50 tokens of 8
-    // kv heads: 8.5 -> 7.9 us in all)
     // Where few rows' clusters leave SMs idle, a row's vectors, which move independently, are
     // parted among clusters, to no less than 64 bytes (4-bit rows are no longer and stay whole):
     // 8 kv heads, bf16, one context of 100,000 cut to 4000 39.8 -> 30.9 us, two cut to 30,000
@@ -570,6 +568,8 @@ int launch_evict(const EvictParams &p, int sms, cudaStream_t stream) {
     const int vecs = p.planes[0].row_bytes / 16;
     while (rows * 2 * parts * kMaxCluster < 2 * (int64_t)sms && vecs % (2 * parts) == 0 && vecs / (2 * parts) >= 4)
         parts *= 2;
+    // the movement's clusters fill the SMs, but have no more CTAs than one wave takes (50 tokens of 8
+    // kv heads: 8.5 -> 7.9 us in all)
     int m = cluster_for(rows * 2 * parts, sms);
     const int64_t wave = std::min<int64_t>(kMoveThreads, kMoveThreads * kMoveUnroll / (vecs / parts));
     while (m > 1 && (m / 2) * wave >= p.keep_limit) m /= 2;
