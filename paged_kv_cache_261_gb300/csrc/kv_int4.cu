@@ -15,6 +15,8 @@
 #include "common.cuh"
 #include "kernels_compress.h"
 
+#include <type_traits>
+
 namespace pa {
 namespace {
 
@@ -209,6 +211,12 @@ __global__ __launch_bounds__(kThreads) void kv_write_int4_kernel(const T *__rest
     for (int w = 0; w < kWords; ++w) {
         float y[8];
         x[w].values(y);
+        // The clamp itself, above: it shows where the minimum rounds up to a zero next to 65504, as
+        // only float32 can (below, the zero is -65504 and the code 0 either way).
+        if constexpr (std::is_same_v<T, float>) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = fminf(y[i], 65504.f);
+        }
         codes[w] = scale > 0.f ? encode8(y, zero, scale, inv15) : 0u;
     }
     const uint32_t mine = (uint32_t)__half_as_ushort(scale_h) | ((uint32_t)__half_as_ushort(zero_h) << 16);
