@@ -470,7 +470,11 @@ size_t pa_decode_int4_workspace_bytes(int num_seqs, int num_heads, int num_kv_he
  *
  *   out[b,h,:] = sum_t softmax_t(scale * q[b,h,:] . K[b,t,h/G,:]) * V[b,t,h/G,:]
  *
- * with K and V the values held (code * scale + zero, unrounded). q and out:
+ * with K and V the values held (code * scale + zero, unrounded). The products of
+ * weights and V scales are rounded to 11 bits (f16 operands of the tensor cores; the
+ * softmax's sum, the zeros' part and mass take the weights unrounded). Of a context's
+ * largest weight times its largest V scale, products below 2^-22 lose bits: they are within
+ * 2^-33 of it, so V scales far apart cost the small ones their precision. q and out:
  * [num_seqs, num_heads, head_dim], PA_DTYPE_BF16 or PA_DTYPE_F16; head_dim 64 or 128,
  * num_heads / num_kv_heads <= 16. mass (NULL: none): float32 [num_seqs, num_kv_heads,
  * mass_len], accumulated as by pa_paged_attention_decode_scored, out staying the same.
@@ -508,8 +512,9 @@ size_t pa_decode_scored_workspace_bytes(int num_seqs, int num_heads, int num_kv_
  * they are. The weights are added in head order, in float32 from the unrounded scores.
  * A context longer than mass_len sets PA_DEVERR_CONTEXT and is cut to it. out is that of
  * pa_paged_attention_decode, bit for bit, with the same arguments (caches of float32,
- * f16 or bf16). The workspace (size from pa_decode_scored_workspace_bytes; NULL =
- * cudaMallocAsync on the stream) holds the scores: 4 bytes per query head and token, the
+ * f16 or bf16); where that runs on the tensor cores (16 bits, head_dim 128), out's weights
+ * are rounded to 16 bits, in its softmax's sum too. The workspace (size from
+ * pa_decode_scored_workspace_bytes; NULL = cudaMallocAsync on the stream) holds the scores: 4 bytes per query head and token, the
  * heads of a group rounded up to 2, 4, 8 or 16; it serves one call at a time.
  */
 int pa_paged_attention_decode_scored(void *out, const void *q, float *mass, int64_t mass_len, const void *key_cache,
@@ -544,6 +549,9 @@ int pa_paged_attention_decode_scored(void *out, const void *q, float *mass, int6
  * PA_DTYPE_INT4.
  * A length outside its range sets PA_DEVERR_CONTEXT and is cut; a bad block id sets
  * PA_DEVERR_BLOCK_ID and its row is not moved.
+ * The launch is sized by what the buffers hold, min(max_blocks_per_seq * block_size,
+ * mass_len) tokens, and kept and mass_out are written to their whole width: tables and
+ * masses much wider than the contexts cost time (see launch_evict for figures).
  */
 int pa_paged_kv_evict(int32_t *kept, int64_t kept_len, const float *mass, int64_t mass_len, float *mass_out,
                       int64_t mass_out_len, void *key_cache, void *value_cache, void *kv_params,

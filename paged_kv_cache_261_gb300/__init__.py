@@ -276,7 +276,8 @@ def _workspace(device, stream_ptr: int, nbytes: int):
     shared with other graphs, or go with the graph that it was first made for.
 
     The buffer is allocated on the stream that the call launches on, which need not be the
-    current one: the allocator hands its memory out again in the order of that stream alone."""
+    current one: the allocator hands its memory out again in the order of that stream alone.
+    (Of captures, the allocator knows those that torch.cuda.graph begins.)"""
     torch = _torch()
     c = torch._C
     if stream_ptr != c._cuda_getCurrentRawStream(device.index) or _elsewhere(device):
@@ -853,7 +854,8 @@ def paged_kv_evict(kept, mass, mass_out, key_cache, value_cache, block_tables, o
     i: its rows move to position i of out_block_tables [B, MB'], its mass to mass_out
     [B, Hk, M'] (0 past the kept ones). out_block_tables: blocks that no sequence of the call
     reads, or block_tables' own blocks for eviction in place (mass_out may then be mass).
-    Caches as the decode calls take them; kv_params with 4-bit ones."""
+    Caches as the decode calls take them; kv_params with 4-bit ones. The time follows the
+    widths of block_tables, mass, kept and mass_out: keep them near the longest context."""
     torch = _torch()
     dev = key_cache.device
     if kv_params is not None:

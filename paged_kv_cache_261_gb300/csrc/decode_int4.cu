@@ -23,9 +23,10 @@
 // W = p v_scale enters the product as f16 (11 bits; the row sums take p unrounded). Its
 // reference is a maximum of the scores (raised only when a score exceeds it by 2^7: no
 // reduction over the lanes before) and a power of two above every v_scale seen, so
-// weights are normal f16 numbers down to 2^-22 of the reference and rounded to 2^-33 of
-// it below, whatever the scale of V. The query enters as f16 times a power of two per
-// head: exact for bf16 and f16 at every channel within 2^-22 of the row's largest.
+// weights are normal f16 numbers down to 2^-22 of the reference times that power and within
+// 2^-33 of it below: a V row far larger than the others costs them bits. The query enters
+// as f16 times a power of two per head: exact for bf16 and f16 at every channel within
+// 2^-22 of the row's largest.
 //
 // The codes enter about their middle, 7.5, or the rounding of W would come out multiplied by
 // codes that are all of one sign, and the sums over a long context, which cancel against

@@ -14,8 +14,12 @@
 // numbers, so the result does not depend on timing, and every mass has been read before
 // the first is written, so mass_out may be mass.
 //
-// Rows too long for the shared memory of a cluster take evict_select_long_kernel: one CTA,
-// the masses read again for every digit, written in one ordered pass.
+// A call's tables and masses bound its rows before their lengths are known, so the cluster,
+// its shared memory and this choice follow what they hold, not the contexts: where they hold
+// more than 393,216 tokens, too many for a cluster's shared memory, every row of the call takes
+// evict_select_long_kernel: one CTA, the masses read again for every digit, written in one
+// ordered pass (8 kv heads, one context, cut to 4000: 393,216 tokens 54 us in all by clusters,
+// 393,232 by this kernel 489, a million 1229).
 //
 // Movement (evict_move_kernel, a cluster of CTAs per (sequence, kv head, plane)): the rows
 // move in waves, each read into registers by the whole cluster before any of it is
@@ -544,10 +548,12 @@ int launch_evict(const EvictParams &p, int sms, cudaStream_t stream) {
         attr_set[dev] = true;
     }
     const int64_t rows = (int64_t)p.num_seqs * p.num_kv_heads;
-    // The selection's clusters grow with the row alone, to 16384 masses a CTA: what a cluster's
-    // barriers cost is more than its other CTAs save (8 kv heads, whole call, us, against clusters
+    // The selection's clusters grow with the longest row that there may be, to 16384 masses a CTA:
+    // what a cluster's barriers cost is more than its other CTAs save (8 kv heads, whole call, us, against clusters
     // that fill the SMs: one sequence of 300 tokens 8.5 and 14.7, 16 of 2000 14.7 and 33.6, 16 of
-    // 16000 23.9 and 37.7, 4 of 40000 25.9 and 27.4; one of 16000 18.6 and 17.2).
+    // 16000 23.9 and 37.7, 4 of 40000 25.9 and 27.4; one of 16000 18.6 and 17.2). Short rows in wide
+    // tables and masses pay for it: 64 sequences of 512 to 4096, 8 kv heads, evicted in place to 1024
+    // again and again, 44 us in all where 4096 tokens fit, 50 at 16384, 85 at 32768, 250 at 131072.
     int c = 1;
     while (c < kMaxCluster && (int64_t)c * 16384 < p.context_limit) c *= 2;
     const int64_t slice = ((p.context_limit + c - 1) / c + 3) & ~int64_t(3);
