@@ -514,7 +514,8 @@ size_t pa_decode_scored_workspace_bytes(int num_seqs, int num_heads, int num_kv_
  * pa_paged_attention_decode, bit for bit, with the same arguments (caches of float32,
  * f16 or bf16); where that runs on the tensor cores (16 bits, head_dim 128), out's weights
  * are rounded to 16 bits, in its softmax's sum too. The workspace (size from
- * pa_decode_scored_workspace_bytes; NULL = cudaMallocAsync on the stream) holds the scores: 4 bytes per query head and token, the
+ * pa_decode_scored_workspace_bytes; NULL = cudaMallocAsync on the stream) holds the
+ * scores: 4 bytes per query head and token up to max_context_len for every sequence, the
  * heads of a group rounded up to 2, 4, 8 or 16; it serves one call at a time.
  */
 int pa_paged_attention_decode_scored(void *out, const void *q, float *mass, int64_t mass_len, const void *key_cache,
