@@ -778,7 +778,7 @@ __global__ __launch_bounds__(kWarps * 32) void decode_int4_join_kernel(const Dec
 }
 
 template <typename T, int D, int GT, bool kScore>
-int launch_t(const DecodeParams &p, const Int4Work &ws, int grid, cudaStream_t stream) {
+int launch_t(const DecodeParams &p, const Int4Work &ws, int64_t max_ctx, int grid, cudaStream_t stream) {
     using C = Cfg<D, GT>;
     auto kern = decode_int4_kernel<T, D, GT, kScore>;
     static bool attr_set[kMaxDevices] = {};
@@ -793,8 +793,11 @@ int launch_t(const DecodeParams &p, const Int4Work &ws, int grid, cudaStream_t s
     // Partials a row: about runs / rows, for contexts of the limit's length. (8 kv heads, us with up to
     // 4 warps a row and with 16: one context of 16,000 tokens 21.2 and 13.2, of 131,072 44.9 and 35.9,
     // three of 40,000 to 120,000 60.0 and 55.4; with 11 partials a row, 16 warps are 0.15 slower.)
+    // The limit is that of the call's arguments alone, before mass cuts p.context_limit: the warps
+    // decide the order of the sums, and out does not depend on whether weights are accumulated.
     const int64_t heads = (int64_t)p.num_seqs * p.num_heads, rows = (int64_t)p.num_seqs * p.num_kv_heads;
-    const int64_t stages = (p.context_limit + (int64_t)C::kTok - 1) / C::kTok;
+    const int64_t limit = std::min(max_ctx, (int64_t)p.max_blocks_per_seq * p.block_size);
+    const int64_t stages = (limit + C::kTok - 1) / C::kTok;
     const int64_t runs = std::min<int64_t>((int64_t)grid * C::kWarps, rows * stages);
     const int wpr = runs <= 8 * rows ? 1 : (runs <= 32 * rows ? 4 : 16), cta = kJoinWarps(wpr);
     auto join = wpr == 1   ? decode_int4_join_kernel<T, D, 1>
@@ -803,14 +806,19 @@ int launch_t(const DecodeParams &p, const Int4Work &ws, int grid, cudaStream_t s
     return launch_pdl(join, dim3((unsigned)((heads * wpr + cta - 1) / cta)), dim3(cta * 32), 0, stream, p, ws);
 }
 
-template <typename T, int D> int launch_g(const DecodeParams &p, const Int4Work &ws, int grid, cudaStream_t stream) {
+template <typename T, int D>
+int launch_g(const DecodeParams &p, const Int4Work &ws, int64_t max_ctx, int grid, cudaStream_t stream) {
     if (p.ws_logits)
-        return p.group <= 8 ? launch_t<T, D, 8, true>(p, ws, grid, stream) : launch_t<T, D, 16, true>(p, ws, grid, stream);
-    return p.group <= 8 ? launch_t<T, D, 8, false>(p, ws, grid, stream) : launch_t<T, D, 16, false>(p, ws, grid, stream);
+        return p.group <= 8 ? launch_t<T, D, 8, true>(p, ws, max_ctx, grid, stream)
+                            : launch_t<T, D, 16, true>(p, ws, max_ctx, grid, stream);
+    return p.group <= 8 ? launch_t<T, D, 8, false>(p, ws, max_ctx, grid, stream)
+                        : launch_t<T, D, 16, false>(p, ws, max_ctx, grid, stream);
 }
 
-template <typename T> int launch_d(const DecodeParams &p, const Int4Work &ws, int grid, cudaStream_t stream) {
-    return p.head_dim == 128 ? launch_g<T, 128>(p, ws, grid, stream) : launch_g<T, 64>(p, ws, grid, stream);
+template <typename T>
+int launch_d(const DecodeParams &p, const Int4Work &ws, int64_t max_ctx, int grid, cudaStream_t stream) {
+    return p.head_dim == 128 ? launch_g<T, 128>(p, ws, max_ctx, grid, stream)
+                             : launch_g<T, 64>(p, ws, max_ctx, grid, stream);
 }
 
 int64_t row_stages(int64_t max_ctx) { return (max_ctx + kInt4StageTokens - 1) / kInt4StageTokens; }
@@ -865,8 +873,8 @@ int launch_decode_int4(const DecodeParams &p, const Int4Work &ws, int64_t max_ct
             c.ws_score_ml = p.ws_score_ml + rows * 2;
         }
         const int grid = launch_grid(c.num_seqs, c.num_kv_heads, max_ctx, sms);
-        int rc = dtype == PA_DTYPE_BF16 ? launch_d<__nv_bfloat16>(c, ws, grid, stream)
-                                        : launch_d<__half>(c, ws, grid, stream);
+        int rc = dtype == PA_DTYPE_BF16 ? launch_d<__nv_bfloat16>(c, ws, max_ctx, grid, stream)
+                                        : launch_d<__half>(c, ws, max_ctx, grid, stream);
         if (rc == 0 && mass)
             rc = launch_decode_mass(c, 2, mass + (int64_t)b0 * p.num_kv_heads * mass_len, mass_len, &ws, stream);
         if (rc != 0) return rc;

@@ -69,3 +69,21 @@ def test_one_v_row_far_larger_than_the_others(pa, size, D):
         assert (err <= tol).all(), (b, float((err - tol).max()))
     # each head's weights sum to 1, off by float32 sums of n terms and by exp2
     assert np.abs(mass.double().cpu().numpy().sum(-1) - 4).max() <= 4 * (n * 2.0 ** -24 + 2.0 ** -20)
+
+
+@pytest.mark.parametrize("B,n,Hk,D", [(18, 430, 3, 64), (18, 430, 3, 128), (1, 1900, 1, 128), (2, 1000, 1, 64)])
+@pytest.mark.parametrize("width", [0, 5])
+def test_weights_leave_the_output_as_it_is(pa, B, n, Hk, D, width):
+    """Bit for bit, also where mass holds fewer tokens than the tables and max_context_len, so that the
+    longest context the call may have differs with and without it: as many partials a row as one warp
+    joins, or as four do, and more."""
+    rng = np.random.default_rng(B + n)
+    lens = rng.integers(n // 4, n, B)
+    lens[0] = n
+    case = Case(rng, lens, 8 * Hk, Hk, D, 16, "bf16", reserve=130)
+    for max_ctx in (0, 4 * n, n):
+        mass = torch.zeros((B, Hk, n + width), device=dev())
+        out = case.run(pa, mass, max_context_len=max_ctx)
+        assert torch.equal(out, case.run(pa, max_context_len=max_ctx))
+        case.check(out, mass)
+    assert pa.get_device_error() == 0
