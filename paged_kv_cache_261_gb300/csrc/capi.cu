@@ -300,7 +300,7 @@ int scored_workspace(pa::DecodeParams &p, int64_t P, int64_t max_ctx, void *work
 // Workspace of a 4-bit decode: the partials, then (with_mass) every row's (max, sum) pair
 // and the scores.
 size_t int4_workspace_bytes(int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_ctx, bool with_mass) {
-    const pa::Int4WorkSizes z = pa::decode_int4_work_sizes(B, H, Hk, D, max_ctx, device_sm_count());
+    const pa::RunWorkSizes z = pa::decode_int4_work_sizes(B, H, Hk, D, max_ctx, device_sm_count());
     return align256(z.rows) + align256(z.part_ml) + align256(z.part_o) +
            (with_mass ? align256((size_t)(B * H * 8)) + logits_bytes(B, H, Hk, max_ctx) : 0);
 }
@@ -897,10 +897,10 @@ int pa_paged_attention_decode_int4(void *out, const void *q, const void *key_cac
         if (cudaMallocAsync(&ws, need, s) != cudaSuccess) return PA_ERR_CUDA;
         owned = ws;
     }
-    const pa::Int4WorkSizes z =
+    const pa::RunWorkSizes z =
         pa::decode_int4_work_sizes(num_seqs, num_heads, num_kv_heads, head_dim, max_ctx, device_sm_count());
     char *at = static_cast<char *>(ws);
-    pa::Int4Work w;
+    pa::RunWork w;
     w.rows = reinterpret_cast<int2 *>(at);
     at += align256(z.rows);
     w.part_ml = reinterpret_cast<float2 *>(at);

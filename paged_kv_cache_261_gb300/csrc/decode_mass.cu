@@ -48,7 +48,7 @@ template <int V> __device__ __forceinline__ void load_vec(const float *src, floa
 // NP planes of V heads, of which the first `group` exist.
 template <int V, int NP>
 __global__ __launch_bounds__(kThreads) void decode_mass_kernel(const DecodeParams p, float *__restrict__ mass,
-                                                               int64_t mass_len, int rounds, const Int4Work ws) {
+                                                               int64_t mass_len, int rounds, const RunWork ws) {
     constexpr int kHeads = V * NP, kTok = tokens_per_thread(kHeads);
     constexpr int kChunk = kThreads * kTok;
     __shared__ float M_s[kMaxG], inv_s[kMaxG];
@@ -138,7 +138,7 @@ __global__ __launch_bounds__(kThreads) void decode_mass_kernel(const DecodeParam
 }
 
 template <int V, int NP>
-int launch_t(const DecodeParams &p, float *mass, int64_t mass_len, const Int4Work &ws, cudaStream_t stream) {
+int launch_t(const DecodeParams &p, float *mass, int64_t mass_len, const RunWork &ws, cudaStream_t stream) {
     constexpr int chunk = kThreads * tokens_per_thread(V * NP);
     const int64_t chunks = (p.context_limit + chunk - 1) / chunk;
     // a CTA takes several chunks where there are many of them, so that the joining of its heads'
@@ -151,9 +151,9 @@ int launch_t(const DecodeParams &p, float *mass, int64_t mass_len, const Int4Wor
 
 }  // namespace
 
-int launch_decode_mass(const DecodeParams &p, int heads_per_plane, float *mass, int64_t mass_len, const Int4Work *work,
+int launch_decode_mass(const DecodeParams &p, int heads_per_plane, float *mass, int64_t mass_len, const RunWork *work,
                        cudaStream_t stream) {
-    const Int4Work ws = work ? *work : Int4Work{};
+    const RunWork ws = work ? *work : RunWork{};
     if (p.context_limit <= 0) return 0;
     const int planes = (p.group + heads_per_plane - 1) / heads_per_plane;
     switch (heads_per_plane) {

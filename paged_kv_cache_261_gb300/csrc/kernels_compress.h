@@ -34,16 +34,16 @@ int launch_copy_params_int4(void *params, const int32_t *pairs, int64_t num_pair
 constexpr int kInt4StageTokens = 64;
 __host__ __device__ constexpr int kInt4Warps(int gt) { return gt == 8 ? 12 : 8; }
 
-// Workspace of the 4-bit decode's partials.
-struct Int4Work {
+// Workspace of the partials of a decode whose work is cut into equal runs (decode_runs.cuh).
+struct RunWork {
     int2 *rows;                // [sequence][kv head] of a launch: first partial, how many
     float2 *part_ml;           // [partial][head of the group]: reference (log2 units), sum
     float *part_o;             // [partial][head of the group][head_dim]
 };
-struct Int4WorkSizes {
+struct RunWorkSizes {
     size_t rows, part_ml, part_o;
 };
-Int4WorkSizes decode_int4_work_sizes(int64_t num_seqs, int64_t num_heads, int64_t num_kv_heads, int64_t head_dim,
+RunWorkSizes decode_int4_work_sizes(int64_t num_seqs, int64_t num_heads, int64_t num_kv_heads, int64_t head_dim,
                                      int64_t max_ctx, int sms);
 
 // Decode attention over a 4-bit cache (p.key_cache, p.value_cache, p.kv_params) of contexts
@@ -51,14 +51,14 @@ Int4WorkSizes decode_int4_work_sizes(int64_t num_seqs, int64_t num_heads, int64_
 // set, p.ws_logits and p.ws_score_ml hold the scores and the pairs of rows that one run
 // covers, and the weights are added to mass as by launch_decode_mass.
 bool decode_int4_supported(const DecodeParams &p, int dtype);
-int launch_decode_int4(const DecodeParams &p, const Int4Work &ws, int64_t max_ctx, int sms, float *mass,
+int launch_decode_int4(const DecodeParams &p, const RunWork &ws, int64_t max_ctx, int sms, float *mass,
                        int64_t mass_len, int dtype, cudaStream_t stream);
 
 // Adds each token's softmax weights, summed over the query heads of its kv head, to
 // mass [num_seqs, num_kv_heads, mass_len], from the scores (planes of heads_per_plane) and
 // (max, sum) pairs that a decode with p.ws_logits left in the workspace. ws: of a 4-bit decode,
 // whose joining kernel is the one before on the stream.
-int launch_decode_mass(const DecodeParams &p, int heads_per_plane, float *mass, int64_t mass_len, const Int4Work *ws,
+int launch_decode_mass(const DecodeParams &p, int heads_per_plane, float *mass, int64_t mass_len, const RunWork *ws,
                        cudaStream_t stream);
 // Heads per plane of the kernels: SIMT 1, 4-bit 2, and half the padded group here.
 inline int score_plane_tc(int group) { return group <= 4 ? 2 : (group <= 8 ? 4 : 8); }
