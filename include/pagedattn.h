@@ -38,7 +38,7 @@
  *
  * Launch chaining: the decode and merge kernels are launched as programmatic
  * dependents of the kernel before them on the stream, and the decode kernels (over
- * 4-bit caches too) read context_lens (and prefix_lens) before they wait for it. A
+ * 4-bit and block-scaled caches too) read context_lens (and prefix_lens) before they wait for it. A
  * kernel the caller launches just before a decode call therefore must not write those
  * two arrays after it signals its dependents early (griddepcontrol.launch_dependents); a
  * kernel that never signals is waited for in full, as usual.
@@ -79,9 +79,13 @@ extern "C" {
 #define PA_DEVERR_CONTEXT    0x4u  /* context_len < 0, > max_blocks_per_seq*bs,   */
                                    /* > max_context_len or > mass_len; eviction:  */
                                    /* a keep_len < 0, or more kept tokens than    */
-                                   /* the outputs hold                            */
+                                   /* the outputs hold; blocks_append: a request  */
+                                   /* that the table or the outputs do not hold   */
 #define PA_DEVERR_COPY_PAIR  0x8u  /* copy pair id outside [0, num_blocks)        */
 #define PA_DEVERR_WAIT       0x10u /* an internal pipeline wait hit its bound     */
+#define PA_DEVERR_FREE_BLOCKS 0x20u /* free list too short for a request's blocks */
+                                   /* (or, giving back, full), or its count out   */
+                                   /* of range                                    */
 
 /* Name of a status code (static string). */
 const char *pa_status_string(int status);
@@ -560,6 +564,188 @@ int pa_paged_kv_evict(int32_t *kept, int64_t kept_len, const float *mass, int64_
                       int out_max_blocks_per_seq, const int32_t *context_lens, const int32_t *keep_lens, int recent,
                       int num_seqs, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, int dtype,
                       void *stream);
+
+/* ---- a step's preparation on the GPU ---------------------------------------
+ * Not on the pages [P1-P3] as GPU code; what they have the host do at every step.
+ */
+
+/*
+ * Block tables and slot maps of a step, from the requests' lengths.
+ * [P2 demo 1: a new block only when a token starts one; P1 PagedKVManager: free ids on a
+ *  stack whose top is taken; P3 B.2: slot_mapping, query_start_loc]
+ *
+ * Request b holds c = context_lens[b] tokens, in the blocks of block_tables[b], and gets
+ * n = query_lens[b] >= 0 new ones. The free blocks are free_blocks[0 .. num_free[0]), a
+ * stack with its top at the end. In the order of the requests, each takes the
+ * ceil((c + n) / bs) - ceil(c / bs) blocks that it needs off the top and appends them to its
+ * table. Then
+ *
+ *   query_start_loc[b]   = the new tokens before request b; [num_seqs]: all of them
+ *   positions[t]         = c + i and
+ *   slot_mapping[t]      = the slot of that position, for t = query_start_loc[b] + i, i < n
+ *   new_context_lens[b]  = c + n
+ *   new_num_free[0]      = num_free[0] less the blocks taken
+ *
+ * and slot -1, position 0 for the entries of slot_mapping and positions [num_tokens] past the
+ * last token. A request is not served (its table and length stay, its tokens get slot -1 and
+ * position 0) when a length is negative or c + n is above max_blocks_per_seq * block_size, or
+ * when its tokens reach past num_tokens (PA_DEVERR_CONTEXT; query_start_loc ends at
+ * num_tokens), or when the stack is too short for its blocks (PA_DEVERR_FREE_BLOCKS); after
+ * one of the last kind, no later request is served that needs a block. An id outside
+ * [0, num_blocks) sets PA_DEVERR_BLOCK_ID; its tokens get slot -1, and a table -1 for it.
+ *
+ * new_context_lens may be context_lens and new_num_free num_free; no other array overlaps
+ * another. Tables that share blocks (pa_alloc_fork) stay with the host allocator: this
+ * stack counts no references. A request whose partly filled last block another table shares
+ * must not be served before that block was copied.
+ * Supported: block_size a power of two up to 256, num_seqs <= 16384, num_blocks * block_size
+ * <= 2^31 - 1; contexts up to 2^31 - 65537 tokens.
+ */
+int pa_paged_blocks_append(int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                           int32_t *new_context_lens, const int32_t *query_lens, int num_seqs,
+                           const int32_t *free_blocks, int64_t free_capacity, const int32_t *num_free,
+                           int32_t *new_num_free, int32_t *query_start_loc, int32_t *slot_mapping,
+                           int32_t *positions, int64_t num_tokens, int block_size, int64_t num_blocks,
+                           void *stream);
+
+/*
+ * Give back the blocks of finished requests. [P1 free_sequence]
+ * For every request b with finished[b] != 0 (bytes), in their order, the
+ * ceil(context_lens[b] / block_size) blocks of its table go onto the stack free_blocks
+ * [free_capacity], in the table's order (as pa_alloc_free_seq gives them back), and
+ * new_context_lens[b] = 0; other requests keep their lengths. new_num_free[0] is the stack's
+ * new height. The tables stay as they are. A length outside [0, max_blocks_per_seq *
+ * block_size] (PA_DEVERR_CONTEXT) or a full stack (PA_DEVERR_FREE_BLOCKS; then for every later
+ * request that holds a block too) leaves a request unreleased; an id outside [0, num_blocks)
+ * goes onto the stack as -1 (PA_DEVERR_BLOCK_ID). Aliasing and limits as
+ * pa_paged_blocks_append; releasing a block twice is a caller error.
+ */
+int pa_paged_blocks_release(const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                            int32_t *new_context_lens, const uint8_t *finished, int num_seqs, int32_t *free_blocks,
+                            int64_t free_capacity, const int32_t *num_free, int32_t *new_num_free, int block_size,
+                            int64_t num_blocks, void *stream);
+
+/*
+ * Rotary positions. With half = rotary_dim / 2 and the angle a = positions[t] * inv_freq[j], j <
+ * half, pair j of every head of token t becomes
+ *
+ *   (x1, x2) -> factor * (x1 cos a - x2 sin a, x2 cos a + x1 sin a),
+ *   (x1, x2) = (x[j], x[j + half]), or with interleaved != 0 (x[2 j], x[2 j + 1]),
+ *
+ * in float32, rounded once to the type; the channels from rotary_dim on are copied. inv_freq:
+ * float64 [half] on the device, finite, in radians per position (scaled as a model wants it;
+ * factor is what such scalings put on both cosine and sine). The angle is reduced to a turn in
+ * 64-bit fixed point: for positions of any size it is off by about positions[t] * inv_freq[j]
+ * * 2^-52, and cosine and sine by less than 2^-23 on top.
+ *
+ * q, q_out: [num_tokens, num_heads, head_dim]; k, k_out: [num_tokens, num_kv_heads, head_dim];
+ * row t of an array at t * its stride, in elements, a multiple of 16 bytes (so they may be
+ * views of a fused projection); outputs' strides are at least a row. An output may be its input
+ * (same pointer and stride). num_kv_heads may be 0, with k and k_out NULL.
+ * dtype: PA_DTYPE_F32, _F16 or _BF16. head_dim: a multiple of 16 up to 1024; rotary_dim: one up to head_dim.
+ */
+int pa_rotary_embedding(void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride, const void *q,
+                        int64_t q_stride, const void *k, int64_t k_stride, const int32_t *positions,
+                        const double *inv_freq, float factor, int interleaved, int64_t num_tokens, int num_heads,
+                        int num_kv_heads, int head_dim, int rotary_dim, int dtype, void *stream);
+
+/*
+ * pa_rotary_embedding of q into q_out and of k into key_cache, and v into value_cache, in one
+ * launch. [P1 write_kv; P3 B.2 for the slots, exactly as pa_paged_kv_write]
+ * key_cache, value_cache: [num_blocks, block_size, num_kv_heads, head_dim] of dtype. A token of
+ * slot -1 stores nothing (its query is rotated all the same). Caches of other types: rotate
+ * with pa_rotary_embedding, then their own scatter.
+ */
+int pa_paged_kv_write_rotary(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride, const void *k,
+                             int64_t k_stride, const void *v, int64_t v_stride, const int32_t *positions,
+                             const double *inv_freq, float factor, int interleaved, const int32_t *slot_mapping,
+                             int64_t num_tokens, void *key_cache, void *value_cache, int64_t num_blocks,
+                             int block_size, int num_heads, int num_kv_heads, int head_dim, int rotary_dim,
+                             int dtype, void *stream);
+
+/* ---- 8-bit KV cache with a scale for each block of tokens and kv head ---------
+ * Not on the pages [P1-P3]; an extension whose scales follow the data, where the _fp8 calls
+ * want one scale for all of K and one for all of V.
+ *   key_cache, value_cache : uint8 E4M3 codes [num_blocks, num_kv_heads, block_size, head_dim]
+ *   kv_scales              : float32 [num_blocks, num_kv_heads, 2] = (K scale, V scale)
+ * A channel stands for code * scale. A block's rows of one kv head are one contiguous run, as in
+ * the 4-bit cache. head_dim: 64 or 128; block_size: a power of two in [8, 256]. Slots, tables and
+ * lengths are those of the other caches.
+ */
+
+/*
+ * Scatter with quantisation. [P1 write_kv; P3 B.2 for the slots, exactly as
+ * pa_paged_kv_write]
+ * Per block written to, kv head and tensor, with a the largest finite magnitude of the call's
+ * tokens in it and s0 the scale it had:
+ *   s = the smallest 2^e, e >= -100, with a <= 448 * 2^e; if the call does not write the block's
+ *       first slot and s0 is positive and finite, the larger of that and s0
+ *   every code of the block, if the call does not write its first slot and s > s0 (positive and
+ *       finite): the code nearest to its code's number * (s0 / s)
+ *   the tokens' codes: those nearest to x / s
+ * (products and quotients in float32, exact where scales are powers of two, as the scatter's own
+ * are; nearest: ties to the even code, magnitudes beyond 448 and infinities to +-448, NaN to a NaN
+ * code). So a call that writes a block's first slot starts the block anew, and fills a block
+ * from its first slot on as sequences do. Empty caches need no initial scales.
+ * The tokens of one block stand next to each other in slot_mapping, with nothing between them (a
+ * packed batch's do); a block's tokens apart, like two tokens with the same slot, are a caller
+ * error (that block's contents are then undefined).
+ * k, v: [num_tokens, num_kv_heads, head_dim] of src_dtype (PA_DTYPE_F32, _F16 or _BF16), row t
+ * at t * its stride, in elements, a multiple of 16 bytes. Slot rules and errors as
+ * pa_paged_kv_write.
+ */
+int pa_paged_kv_write_fp8_block(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                const int32_t *slot_mapping, int64_t num_tokens, void *key_cache,
+                                void *value_cache, float *kv_scales, int64_t num_blocks, int block_size,
+                                int num_kv_heads, int head_dim, int src_dtype, void *stream);
+
+/*
+ * Read-back: k[t], v[t] = the values held at slot_mapping[t], rounded once to dst_dtype
+ * (PA_DTYPE_F32, _F16 or _BF16). A token of slot -1, or of a slot out of range (which sets
+ * PA_DEVERR_SLOT), keeps its row of k and v as it was. Slots may repeat. Read into
+ * a [num_blocks', block_size', num_kv_heads, head_dim] buffer, a cached context can be
+ * attended by pa_paged_attention_prefill.
+ */
+int pa_paged_kv_read_fp8_block(void *k, void *v, const int32_t *slot_mapping, int64_t num_tokens,
+                               const void *key_cache, const void *value_cache, const float *kv_scales,
+                               int64_t num_blocks, int block_size, int num_kv_heads, int head_dim, int dst_dtype,
+                               void *stream);
+
+/* pa_copy_blocks for such a cache: codes and scales of whole blocks. */
+int pa_copy_blocks_fp8_block(void *key_cache, void *value_cache, float *kv_scales, const int32_t *src_dst_pairs,
+                             int64_t num_pairs, int64_t num_blocks, int block_size, int num_kv_heads, int head_dim,
+                             void *stream);
+
+/* Bytes of workspace pa_paged_attention_decode_fp8_block needs for these sizes on the current
+ * device. */
+size_t pa_decode_fp8_block_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                           int max_context_len);
+
+/*
+ * Decode attention over such a cache. [P2 demo 2, eq. 4, as pa_paged_attention_decode]
+ *
+ *   out[b,h,:] = sum_t softmax_t(scale * q[b,h,:] . K[b,t,h/G,:]) * V[b,t,h/G,:]
+ *
+ * with K and V the values held (code * scale, unrounded). The products of weights and V scales
+ * are rounded to 11 bits (f16 operands of the tensor cores; the softmax's sum takes the weights
+ * unrounded). Of a context's largest weight times its largest V scale, products below 2^-22
+ * lose bits: they are within 2^-33 of it, so V scales far apart cost the small ones their
+ * precision; V scales below 2^-100 count as that for it. Values are below 2^90 in magnitude
+ * and queries below 2^118 (times |scale|; beyond, a head's output may be NaN). q and out:
+ * [num_seqs, num_heads, head_dim], PA_DTYPE_BF16 or PA_DTYPE_F16; num_heads / num_kv_heads <= 16.
+ * Codes and scales past a context's end are never used, whatever they hold; a NaN code or scale
+ * inside a context makes outputs of its heads NaN. The work is cut into equal runs of tokens
+ * over the device, whatever the lengths (there is no partition size). max_context_len, the
+ * workspace (size from pa_decode_fp8_block_workspace_bytes; NULL = cudaMallocAsync on the
+ * stream; it serves one call at a time, so calls that may run at the same time need one each)
+ * and the device error bits are those of pa_paged_attention_decode.
+ */
+int pa_paged_attention_decode_fp8_block(void *out, const void *q, const void *key_cache, const void *value_cache,
+                                        const float *kv_scales, const int32_t *block_tables, int max_blocks_per_seq,
+                                        const int32_t *context_lens, int num_seqs, int num_heads, int num_kv_heads,
+                                        int head_dim, int block_size, int64_t num_blocks, float scale,
+                                        int max_context_len, void *workspace, size_t workspace_bytes, int dtype,
+                                        void *stream);
 
 /*
  * Synchronise `stream`, then read and clear the current device's error word.

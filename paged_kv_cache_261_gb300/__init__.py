@@ -27,6 +27,17 @@ Entry points (same names as the C ABI, without the ``pa_`` prefix):
                                 block_tables, context_lens, scale)
   paged_kv_evict(kept, mass, mass_out, key_cache, value_cache, block_tables,
                  out_block_tables, context_lens, keep_lens, recent, kv_params=None)
+  paged_blocks_append(block_tables, context_lens, query_lens, free_blocks, num_free,
+                      query_start_loc, slot_mapping, positions, block_size, num_blocks)
+  paged_blocks_release(block_tables, context_lens, finished, free_blocks, num_free, block_size)
+  rotary_frequencies(rotary_dim, base=10000.0, ...)   (host)
+  rotary_embedding(q_out, k_out, q, k, positions, inv_freq, factor=1.0, interleaved=False)
+  paged_kv_write_rotary(q_out, q, k, v, positions, inv_freq, slot_mapping,
+                        key_cache, value_cache, factor=1.0, interleaved=False)
+  paged_kv_write_fp8_block(k, v, slot_mapping, key_cache, value_cache, kv_scales)
+  paged_kv_read_fp8_block(k, v, slot_mapping, key_cache, value_cache, kv_scales)
+  paged_attention_decode_fp8_block(out, q, key_cache, value_cache, kv_scales,
+                                   block_tables, context_lens, scale)
   get_device_error()
   BlockAllocator: the host block manager (free list, reference counts, fork,
   copy-on-write, block-table and slot-mapping export).
@@ -35,7 +46,10 @@ take 8-bit caches (torch.uint8 or torch.float8_e4m3fn) holding OCP FP8 E4M3
 codes with one float32 scale for K and one for V. The _int4 calls take caches
 [num_blocks, num_kv_heads, block_size, head_dim / 2] (torch.uint8, two codes a
 byte) with kv_params float16 [num_blocks, num_kv_heads, block_size, 4]: K scale,
-K zero, V scale, V zero of every token and kv head.
+K zero, V scale, V zero of every token and kv head. The _fp8_block calls take caches
+[num_blocks, num_kv_heads, block_size, head_dim] (torch.uint8 or torch.float8_e4m3fn) with
+kv_scales float32 [num_blocks, num_kv_heads, 2]: the K and the V scale of every block and
+kv head.
 """
 from __future__ import annotations
 
@@ -72,6 +86,7 @@ PA_DEVERR_BLOCK_ID = 0x2
 PA_DEVERR_CONTEXT = 0x4
 PA_DEVERR_COPY_PAIR = 0x8
 PA_DEVERR_WAIT = 0x10
+PA_DEVERR_FREE_BLOCKS = 0x20
 
 _vp, _i32, _i64, _sz, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 
@@ -118,6 +133,19 @@ _decl("pa_paged_attention_decode_scored", [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _
                                            _i32, _i64, _f, _i32, _i32, _vp, _sz, _i32, _vp])
 _decl("pa_paged_kv_evict", [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _i32,
                             _i32, _i32, _i32, _i32, _i64, _i32, _vp])
+_decl("pa_paged_blocks_append", [_vp, _i32, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i64,
+                                 _vp])
+_decl("pa_paged_blocks_release", [_vp, _i32, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _vp, _i32, _i64, _vp])
+_decl("pa_rotary_embedding", [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _f, _i32, _i64, _i32, _i32, _i32,
+                              _i32, _i32, _vp])
+_decl("pa_paged_kv_write_rotary", [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _f, _i32, _vp, _i64, _vp, _vp,
+                                   _i64, _i32, _i32, _i32, _i32, _i32, _i32, _vp])
+_decl("pa_paged_kv_write_fp8_block", [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp])
+_decl("pa_paged_kv_read_fp8_block", [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp])
+_decl("pa_copy_blocks_fp8_block", [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _vp])
+_decl("pa_decode_fp8_block_workspace_bytes", [_i32, _i32, _i32, _i32, _i32], _sz)
+_decl("pa_paged_attention_decode_fp8_block", [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32,
+                                              _i64, _f, _i32, _vp, _sz, _i32, _vp])
 
 
 class PagedAttnError(RuntimeError):
@@ -508,12 +536,25 @@ def paged_attention_decode_shared(out, q, key_cache, value_cache, block_tables, 
     _check(rc, "pa_paged_attention_decode_shared")
 
 
-def copy_blocks(key_cache, value_cache, src_dst_pairs, stream=None, kv_params=None) -> None:
+def copy_blocks(key_cache, value_cache, src_dst_pairs, stream=None, kv_params=None, kv_scales=None) -> None:
     """key_cache[dst] = key_cache[src] (and V) for each row (src, dst) of src_dst_pairs [P, 2].
 
-    kv_params: that of a 4-bit cache, copied along."""
+    kv_params: that of a 4-bit cache, copied along; kv_scales: that of a block-scaled 8-bit one."""
     torch = _torch()
     dev = key_cache.device
+    if kv_scales is not None:
+        if kv_params is not None:
+            raise ValueError("kv_params belongs to a 4-bit cache, kv_scales to a block-scaled 8-bit one")
+        nb, hk, bs, d = _fp8_block_caches(key_cache, value_cache, kv_scales, dev)
+        _cuda(src_dst_pairs, "src_dst_pairs", torch.int32, dev)
+        if src_dst_pairs.dim() != 2 or src_dst_pairs.shape[1] != 2:
+            raise ValueError("src_dst_pairs must be [P, 2]")
+        with _on(dev):
+            rc = _lib.pa_copy_blocks_fp8_block(key_cache.data_ptr(), value_cache.data_ptr(), kv_scales.data_ptr(),
+                                               src_dst_pairs.data_ptr(), src_dst_pairs.shape[0], nb, bs, hk, d,
+                                               _stream_ptr(stream, dev))
+        _check(rc, "pa_copy_blocks_fp8_block")
+        return
     if kv_params is not None:
         nb, hk, bs, d = _int4_caches(key_cache, value_cache, kv_params, dev)
         _cuda(src_dst_pairs, "src_dst_pairs", torch.int32, dev)
@@ -895,6 +936,306 @@ def paged_kv_evict(kept, mass, mass_out, key_cache, value_cache, block_tables, o
                                 _stream_ptr(stream, dev))
     if rc:
         _check(rc, "pa_paged_kv_evict")
+
+
+def paged_blocks_append(block_tables, context_lens, query_lens, free_blocks, num_free, query_start_loc, slot_mapping,
+                        positions, block_size: int, num_blocks: int, new_context_lens=None, new_num_free=None,
+                        stream=None) -> None:
+    """Make a step's block tables and slot maps from the requests' lengths.
+
+    Request b holds context_lens[b] tokens and gets query_lens[b] new ones; the blocks that it
+    needs are taken off the end of free_blocks[:num_free] and appended to block_tables[b].
+    query_start_loc [B + 1], slot_mapping [T] and positions [T] get the new tokens' starts, slots
+    (-1: not served, or past the last token) and positions; new_context_lens and new_num_free
+    (default: context_lens and num_free, in place) the lengths and the stack's height after the
+    step. All int32; block_tables [B, MB], num_free [1]."""
+    i32, dev = _torch().int32, block_tables.device
+    out_lens = context_lens if new_context_lens is None else new_context_lens
+    out_free = num_free if new_num_free is None else new_num_free
+    if not block_tables.is_cuda:
+        _cuda(block_tables, "block_tables")
+    _all_cuda(dev, (block_tables, "block_tables", i32), (context_lens, "context_lens", i32),
+              (query_lens, "query_lens", i32), (free_blocks, "free_blocks", i32), (num_free, "num_free", i32),
+              (query_start_loc, "query_start_loc", i32), (slot_mapping, "slot_mapping", i32),
+              (positions, "positions", i32), (out_lens, "new_context_lens", i32), (out_free, "new_num_free", i32))
+    if block_tables.dim() != 2 or free_blocks.dim() != 1 or slot_mapping.dim() != 1:
+        raise ValueError("block_tables must be [B, MB], free_blocks [F] and slot_mapping [T]")
+    B, mb = block_tables.shape
+    T = slot_mapping.shape[0]
+    if context_lens.shape != (B,) or query_lens.shape != (B,) or out_lens.shape != (B,) or \
+            query_start_loc.shape != (B + 1,):
+        raise ValueError("context_lens, query_lens and new_context_lens must be [B], query_start_loc [B + 1]")
+    if positions.shape != (T,) or num_free.numel() != 1 or out_free.numel() != 1:
+        raise ValueError("positions must be [T] as slot_mapping, num_free and new_num_free [1]")
+    if _elsewhere(dev):
+        with _on(dev):
+            return paged_blocks_append(block_tables, context_lens, query_lens, free_blocks, num_free, query_start_loc,
+                                       slot_mapping, positions, block_size, num_blocks, new_context_lens, new_num_free,
+                                       stream or _torch().cuda.current_stream(dev))
+    rc = _lib.pa_paged_blocks_append(block_tables.data_ptr(), mb, context_lens.data_ptr(), out_lens.data_ptr(),
+                                     query_lens.data_ptr(), B, free_blocks.data_ptr(), free_blocks.shape[0],
+                                     num_free.data_ptr(), out_free.data_ptr(), query_start_loc.data_ptr(),
+                                     slot_mapping.data_ptr(), positions.data_ptr(), T, int(block_size),
+                                     int(num_blocks), _stream_ptr(stream, dev))
+    if rc:
+        _check(rc, "pa_paged_blocks_append")
+
+
+def paged_blocks_release(block_tables, context_lens, finished, free_blocks, num_free, block_size: int,
+                         new_context_lens=None, new_num_free=None, num_blocks: int | None = None, stream=None) -> None:
+    """Give the blocks of every request b with finished[b] (torch.bool or uint8 [B]) back to the
+    stack free_blocks[:num_free] and set its length to 0; its table stays as it is.
+    new_context_lens and new_num_free: as paged_blocks_append. num_blocks (default: the length of
+    free_blocks): block ids are below it."""
+    torch = _torch()
+    i32, dev = torch.int32, block_tables.device
+    out_lens = context_lens if new_context_lens is None else new_context_lens
+    out_free = num_free if new_num_free is None else new_num_free
+    if not block_tables.is_cuda:
+        _cuda(block_tables, "block_tables")
+    if finished.dtype != torch.bool and finished.dtype != torch.uint8:
+        raise TypeError(f"finished must be torch.bool or torch.uint8, got {finished.dtype}")
+    _all_cuda(dev, (block_tables, "block_tables", i32), (context_lens, "context_lens", i32),
+              (finished, "finished", finished.dtype), (free_blocks, "free_blocks", i32), (num_free, "num_free", i32),
+              (out_lens, "new_context_lens", i32), (out_free, "new_num_free", i32))
+    if block_tables.dim() != 2 or free_blocks.dim() != 1:
+        raise ValueError("block_tables must be [B, MB] and free_blocks [F]")
+    B, mb = block_tables.shape
+    if context_lens.shape != (B,) or finished.shape != (B,) or out_lens.shape != (B,):
+        raise ValueError("context_lens, finished and new_context_lens must be [B]")
+    if num_free.numel() != 1 or out_free.numel() != 1:
+        raise ValueError("num_free and new_num_free must be [1]")
+    if _elsewhere(dev):
+        with _on(dev):
+            return paged_blocks_release(block_tables, context_lens, finished, free_blocks, num_free, block_size,
+                                        new_context_lens, new_num_free, num_blocks,
+                                        stream or torch.cuda.current_stream(dev))
+    cap = free_blocks.shape[0]
+    rc = _lib.pa_paged_blocks_release(block_tables.data_ptr(), mb, context_lens.data_ptr(), out_lens.data_ptr(),
+                                      finished.data_ptr(), B, free_blocks.data_ptr(), cap, num_free.data_ptr(),
+                                      out_free.data_ptr(), int(block_size), int(cap if num_blocks is None else num_blocks),
+                                      _stream_ptr(stream, dev))
+    if rc:
+        _check(rc, "pa_paged_blocks_release")
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | None = None, scale: float = 1.0,
+                       original_len: int = 8192, low: float = 1.0, high: float = 4.0) -> np.ndarray:
+    """Host: radians per position of the rotary_dim / 2 pairs, float64, for rotary_embedding.
+
+    base^(-2 j / rotary_dim), and for contexts `scale` times as long as original_len:
+      "linear"    every frequency divided by scale
+      "ntk"       base multiplied by scale^(rotary_dim / (rotary_dim - 2)): the slowest pair is
+                  divided by scale, the fastest kept
+      "by_turns"  a pair of at least `high` turns over original_len kept, one of at most `low`
+                  divided, in between a mean of both weighted by its turns
+      "by_index"  the same, weighted by the pair's index, from that of `high` turns, rounded down,
+                  to that of `low` turns, rounded up (usually 32 and 1)."""
+    if rotary_dim <= 0 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be a positive even number")
+    if not (base > 1 and scale > 0):
+        raise ValueError("base must be above 1 and scale positive")
+    half = rotary_dim // 2
+    if scaling == "ntk" and rotary_dim > 2:
+        base = base * scale ** (rotary_dim / (rotary_dim - 2))
+    f = np.float64(base) ** (-np.arange(half, dtype=np.float64) / half)
+    if scaling is None or scaling == "ntk":
+        return f
+    if scaling == "linear":
+        return f / scale
+    if scaling not in ("by_turns", "by_index"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if not 0 < low < high:
+        raise ValueError("low and high must be 0 < low < high")
+    if scaling == "by_turns":
+        keep = np.clip((original_len * f / (2 * np.pi) - low) / (high - low), 0.0, 1.0)
+    else:
+        first, last = (half * np.log(original_len / (n * 2 * np.pi)) / np.log(base) for n in (high, low))
+        first, last = max(np.floor(first), 0.0), min(np.ceil(last), half - 1.0)
+        keep = 1.0 - np.clip((np.arange(half) - first) / max(last - first, 0.001), 0.0, 1.0)
+    return f / scale * (1.0 - keep) + f * keep
+
+
+def _rows_of(t, name, T, heads, d, dtype, dev) -> int:
+    """Checks rows [T, heads, d] that may be strided over T; the stride."""
+    if t.device != dev or t.dtype != dtype:
+        _cuda(t, name, dtype, dev)
+    if t.shape != (T, heads, d):
+        raise ValueError(f"{name} must be [{T}, {heads}, {d}]")
+    row, head, one = t.stride()
+    if T <= 1:
+        row = heads * d
+    if one != 1 or (head != d and heads > 1) or row < 0:
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return row
+
+
+def _rotary_args(q_out, q, k, positions, inv_freq, dev):
+    """Checks what both rotary calls take; (T, H, Hk, D, rotary_dim, strides of q_out, q and k)."""
+    torch = _torch()
+    if not q.is_cuda:
+        _cuda(q, "q")
+    if q.dim() != 3 or (k is not None and k.dim() != 3):
+        raise ValueError("q must be [T, H, head_dim] and k [T, Hk, head_dim]")
+    T, H, D = q.shape
+    _all_cuda(dev, (positions, "positions", torch.int32), (inv_freq, "inv_freq", torch.float64))
+    if positions.shape != (T,) or inv_freq.dim() != 1:
+        raise ValueError("positions must be [T] and inv_freq [rotary_dim / 2]")
+    hk = 0 if k is None else k.shape[1]
+    ks = 0 if k is None else _rows_of(k, "k", T, hk, D, q.dtype, dev)
+    return (T, H, hk, D, 2 * inv_freq.shape[0], _rows_of(q_out, "q_out", T, H, D, q.dtype, dev),
+            _rows_of(q, "q", T, H, D, q.dtype, dev), ks)
+
+
+def rotary_embedding(q_out, k_out, q, k, positions, inv_freq, factor: float = 1.0, interleaved: bool = False,
+                     stream=None) -> None:
+    """Rotary positions: q_out [T, H, D] and k_out [T, Hk, D] = q and k with pair j of every head,
+    j < rotary_dim / 2, turned by positions[t] * inv_freq[j] and multiplied by factor; the channels
+    from rotary_dim on are copied. Pairs are (x[j], x[j + rotary_dim / 2]), or (x[2 j], x[2 j + 1])
+    if interleaved. positions int32 [T]; inv_freq float64 [rotary_dim / 2] (rotary_frequencies).
+    Rows may be strided over T (views of a fused projection); an output may be its input; k and
+    k_out may be None."""
+    dev = q.device
+    T, H, hk, D, rd, qos, qs, ks = _rotary_args(q_out, q, k, positions, inv_freq, dev)
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out must both be given, or neither")
+    kos = 0 if k is None else _rows_of(k_out, "k_out", T, hk, D, q.dtype, dev)
+    if _elsewhere(dev):
+        with _on(dev):
+            return rotary_embedding(q_out, k_out, q, k, positions, inv_freq, factor, interleaved,
+                                    stream or _torch().cuda.current_stream(dev))
+    rc = _lib.pa_rotary_embedding(q_out.data_ptr(), qos, None if k is None else k_out.data_ptr(), kos, q.data_ptr(), qs,
+                                  None if k is None else k.data_ptr(), ks, positions.data_ptr(), inv_freq.data_ptr(),
+                                  float(factor), int(interleaved), T, H, hk, D, rd, _dtype_code(q),
+                                  _stream_ptr(stream, dev))
+    if rc:
+        _check(rc, "pa_rotary_embedding")
+
+
+def paged_kv_write_rotary(q_out, q, k, v, positions, inv_freq, slot_mapping, key_cache, value_cache,
+                          factor: float = 1.0, interleaved: bool = False, stream=None) -> None:
+    """rotary_embedding of q [T, H, D] into q_out and of k [T, Hk, D] into key_cache, and v into
+    value_cache [NB, bs, Hk, D], at slot_mapping[T] as paged_kv_write, in one launch."""
+    dev, dt = key_cache.device, key_cache.dtype
+    T, H, hk, D, rd, qos, qs, ks = _rotary_args(q_out, q, k, positions, inv_freq, dev)
+    vs = _rows_of(v, "v", T, hk, D, dt, dev)
+    _all_cuda(dev, (slot_mapping, "slot_mapping", _torch_module.int32), (key_cache, "key_cache", dt),
+              (value_cache, "value_cache", dt))
+    if q.dtype != dt:
+        raise TypeError(f"q must be {dt}, got {q.dtype}")
+    shape = key_cache.shape
+    if len(shape) != 4 or value_cache.shape != shape or shape[2] != hk or shape[3] != D:
+        raise ValueError(f"key_cache and value_cache must be [num_blocks, block_size, {hk}, {D}]")
+    if slot_mapping.shape != (T,):
+        raise ValueError("slot_mapping must be [T]")
+    if _elsewhere(dev):
+        with _on(dev):
+            return paged_kv_write_rotary(q_out, q, k, v, positions, inv_freq, slot_mapping, key_cache, value_cache,
+                                         factor, interleaved, stream or _torch().cuda.current_stream(dev))
+    rc = _lib.pa_paged_kv_write_rotary(q_out.data_ptr(), qos, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                                       positions.data_ptr(), inv_freq.data_ptr(), float(factor), int(interleaved),
+                                       slot_mapping.data_ptr(), T, key_cache.data_ptr(), value_cache.data_ptr(),
+                                       shape[0], shape[1], H, hk, D, rd, _dtype_code(q), _stream_ptr(stream, dev))
+    if rc:
+        _check(rc, "pa_paged_kv_write_rotary")
+
+
+def _fp8_block_caches(key_cache, value_cache, kv_scales, dev):
+    """Checks the tensors of a block-scaled 8-bit cache; (num_blocks, num_kv_heads, block_size, head_dim)."""
+    torch = _torch()
+    dt = key_cache.dtype
+    if not (key_cache.is_cuda and key_cache.is_contiguous() and value_cache.device == dev and
+            value_cache.dtype == dt and value_cache.is_contiguous() and kv_scales.device == dev and
+            kv_scales.dtype == torch.float32 and kv_scales.is_contiguous()):
+        _cuda(key_cache, "key_cache")
+        _cuda(value_cache, "value_cache", dt, dev)
+        _cuda(kv_scales, "kv_scales", torch.float32, dev)
+    if not _is_fp8_cache(key_cache):
+        raise TypeError(f"8-bit caches must be torch.uint8 or torch.float8_e4m3fn, got {dt}")
+    shape = key_cache.shape
+    if len(shape) != 4 or value_cache.shape != shape:
+        raise ValueError("key_cache and value_cache must be [num_blocks, num_kv_heads, block_size, head_dim]")
+    if kv_scales.shape != (shape[0], shape[1], 2):
+        raise ValueError(f"kv_scales must be [{shape[0]}, {shape[1]}, 2]")
+    return shape
+
+
+def paged_kv_write_fp8_block(k, v, slot_mapping, key_cache, value_cache, kv_scales, stream=None) -> None:
+    """Scatter k/v [T, Hk, D] (fp32/fp16/bf16, rows may be strided over T) into block-scaled 8-bit
+    caches [NB, Hk, bs, D] with kv_scales [NB, Hk, 2] at slot_mapping[T]. A block's scale is the
+    smallest power of two that its values need; when it grows, the block's older codes are
+    re-encoded; a call that writes a block's first slot starts the block anew. The tokens of a
+    block stand next to each other in slot_mapping."""
+    dev = key_cache.device
+    nb, hk, bs, d = _fp8_block_caches(key_cache, value_cache, kv_scales, dev)
+    if slot_mapping.dim() != 1:
+        raise ValueError("slot_mapping must be [T]")
+    T = slot_mapping.shape[0]
+    ks, vs = _rows_of(k, "k", T, hk, d, k.dtype, dev), _rows_of(v, "v", T, hk, d, k.dtype, dev)
+    _all_cuda(dev, (slot_mapping, "slot_mapping", _torch_module.int32))
+    if _elsewhere(dev):
+        with _on(dev):
+            return paged_kv_write_fp8_block(k, v, slot_mapping, key_cache, value_cache, kv_scales,
+                                            stream or _torch().cuda.current_stream(dev))
+    rc = _lib.pa_paged_kv_write_fp8_block(k.data_ptr(), ks, v.data_ptr(), vs, slot_mapping.data_ptr(), T,
+                                          key_cache.data_ptr(), value_cache.data_ptr(), kv_scales.data_ptr(), nb, bs, hk,
+                                          d, _dtype_code(k), _stream_ptr(stream, dev))
+    if rc:
+        _check(rc, "pa_paged_kv_write_fp8_block")
+
+
+def paged_kv_read_fp8_block(k, v, slot_mapping, key_cache, value_cache, kv_scales, stream=None) -> None:
+    """The inverse: k[t], v[t] [T, Hk, D] (fp32/fp16/bf16) = the values held at
+    slot_mapping[t]; rows of slot -1 stay as they are."""
+    dev = key_cache.device
+    nb, hk, bs, d = _fp8_block_caches(key_cache, value_cache, kv_scales, dev)
+    T = _int4_rows(k, v, slot_mapping, hk, d, dev)
+    if _elsewhere(dev):
+        with _on(dev):
+            return paged_kv_read_fp8_block(k, v, slot_mapping, key_cache, value_cache, kv_scales,
+                                           stream or _torch().cuda.current_stream(dev))
+    rc = _lib.pa_paged_kv_read_fp8_block(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), T, key_cache.data_ptr(),
+                                         value_cache.data_ptr(), kv_scales.data_ptr(), nb, bs, hk, d, _dtype_code(k),
+                                         _stream_ptr(stream, dev))
+    if rc:
+        _check(rc, "pa_paged_kv_read_fp8_block")
+
+
+def decode_fp8_block_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                     max_context_len: int, device=None) -> int:
+    """Workspace bytes of a paged_attention_decode_fp8_block call on `device` (default: the current one)."""
+    if device is not None:
+        with _torch().cuda.device(device):
+            return decode_fp8_block_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len)
+    return int(_lib.pa_decode_fp8_block_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len))
+
+
+def paged_attention_decode_fp8_block(out, q, key_cache, value_cache, kv_scales, block_tables, context_lens,
+                                     scale: float, max_context_len: int = 0, workspace=None, stream=None) -> None:
+    """Decode attention over block-scaled 8-bit caches [NB, Hk, bs, D] with kv_scales [NB, Hk, 2].
+
+    q, out [B, H, D] bf16 or fp16. Other arguments as paged_attention_decode."""
+    dev = key_cache.device
+    nb, hk, bs, d = _fp8_block_caches(key_cache, value_cache, kv_scales, dev)
+    B, H, mb = _decode_args(out, q, block_tables, context_lens, d, dev, q.dtype, max_context_len)
+    if _elsewhere(dev):
+        with _on(dev):
+            return paged_attention_decode_fp8_block(out, q, key_cache, value_cache, kv_scales, block_tables,
+                                                    context_lens, scale, max_context_len, workspace,
+                                                    stream or _torch().cuda.current_stream(dev))
+    sp = _stream_ptr(stream, dev)
+    if workspace is None:
+        workspace = _workspace(dev, sp, _memo(decode_fp8_block_workspace_bytes, B, H, hk, d, max_context_len or mb * bs,
+                                              dev.index))
+    else:
+        _cuda(workspace, "workspace", _torch_module.uint8, dev)
+    rc = _lib.pa_paged_attention_decode_fp8_block(out.data_ptr(), q.data_ptr(), key_cache.data_ptr(),
+                                                  value_cache.data_ptr(), kv_scales.data_ptr(), block_tables.data_ptr(),
+                                                  mb, context_lens.data_ptr(), B, H, hk, d, bs, nb, float(scale),
+                                                  int(max_context_len), workspace.data_ptr(), workspace.numel(),
+                                                  _dtype_code(q), sp)
+    if rc:
+        _check(rc, "pa_paged_attention_decode_fp8_block")
 
 
 def get_device_error(stream=None, device=None) -> int:

@@ -13,6 +13,8 @@
 #include "kernels.h"
 #include "kernels_compress.h"
 #include "kernels_fp8.h"
+#include "kernels_fp8_block.h"
+#include "kernels_step.h"
 
 namespace {
 
@@ -334,6 +336,95 @@ int int4_setup(pa::Int4Cache &c, const void *k, const void *v, const int32_t *sl
     c.num_kv_heads = num_kv_heads;
     c.head_dim = head_dim;
     c.log2_block_size = ilog2(block_size);
+    return PA_OK;
+}
+
+// A row stride, in elements, of `row` elements of es bytes: a multiple of 16 bytes whose offsets
+// of num_tokens rows fit; an output's rows do not overlap.
+bool row_stride_ok(int64_t stride, int64_t row, int es, int64_t num_tokens, bool output) {
+    return stride >= (output ? row : 0) && stride * es % 16 == 0 &&
+           (num_tokens <= 1 || stride <= INT64_MAX / 16 / num_tokens);
+}
+
+// Validation shared by the scatter and read-back of the block-scaled 8-bit cache; fills c.
+int fp8_block_setup(pa::Fp8BlockCache &c, const void *k, const void *v, const int32_t *slot_mapping,
+                    int64_t num_tokens, void *key_cache, void *value_cache, float *kv_scales, int64_t num_blocks,
+                    int block_size, int num_kv_heads, int head_dim, int dtype) {
+    if (elem_size(dtype) == 0 || num_tokens < 0 || num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0 ||
+        head_dim <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (!pow2(block_size) || block_size < 8 || block_size > 256 || num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return kNothingToDo;
+    if (!k || !v || !slot_mapping || !key_cache || !value_cache || !kv_scales) return PA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(key_cache) || !aligned16(value_cache) || !aligned16(kv_scales))
+        return PA_ERR_INVALID_ARG;
+    if (num_blocks > INT64_MAX / ((int64_t)block_size * num_kv_heads * head_dim)) return PA_ERR_INVALID_ARG;
+    if (num_tokens > (INT32_MAX - 65536) / num_kv_heads) return PA_ERR_UNSUPPORTED;   // rows are counted in 31 bits
+    c.key = key_cache;
+    c.value = value_cache;
+    c.scales = reinterpret_cast<float2 *>(kv_scales);
+    c.num_slots = num_blocks * block_size;
+    c.num_kv_heads = num_kv_heads;
+    c.head_dim = head_dim;
+    c.log2_block_size = ilog2(block_size);
+    return PA_OK;
+}
+
+size_t fp8_block_workspace_bytes(int64_t B, int64_t H, int64_t Hk, int64_t D, int64_t max_ctx) {
+    const pa::RunWorkSizes z = pa::decode_fp8_block_work_sizes(B, H, Hk, D, max_ctx, device_sm_count());
+    return align256(z.rows) + align256(z.part_ml) + align256(z.part_o);
+}
+
+// Validation shared by the calls that turn lengths into tables.
+int layout_setup(int max_blocks_per_seq, int num_seqs, int64_t free_capacity, int block_size, int64_t num_blocks) {
+    if (max_blocks_per_seq <= 0 || num_seqs < 0 || free_capacity < 0 || block_size <= 0 || num_blocks <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (!pow2(block_size) || block_size > 256 || num_seqs > pa::kMaxLayoutSeqs || free_capacity > INT32_MAX ||
+        num_blocks > INT32_MAX / block_size)
+        return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+int64_t table_tokens(int max_blocks_per_seq, int block_size) {
+    return std::min((int64_t)max_blocks_per_seq * block_size, kMaxTokens);
+}
+
+// Validation shared by the rotary calls; fills p but for the destination of the keys.
+int rotary_setup(pa::RotaryParams &p, void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride,
+                 const void *k, int64_t k_stride, const int32_t *positions, const double *inv_freq, float factor,
+                 int interleaved, int64_t num_tokens, int num_heads, int num_kv_heads, int head_dim, int rotary_dim,
+                 int dtype) {
+    const int es = elem_size(dtype);
+    if (es == 0 || num_tokens < 0 || num_heads <= 0 || num_kv_heads < 0 || head_dim <= 0 || rotary_dim <= 0 ||
+        rotary_dim > head_dim || !(factor == factor))
+        return PA_ERR_INVALID_ARG;
+    if (head_dim % 16 != 0 || rotary_dim % 16 != 0 || head_dim > 1024 || num_heads > 65535 || num_kv_heads > 65535)
+        return PA_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return kNothingToDo;
+    if (num_tokens > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    if (!q_out || !q || !positions || !inv_freq || (num_kv_heads && !k) || !aligned16(q_out) || !aligned16(q) ||
+        !aligned16(k) || (reinterpret_cast<uintptr_t>(inv_freq) & 7u) != 0)
+        return PA_ERR_INVALID_ARG;
+    const int64_t q_row = (int64_t)num_heads * head_dim, k_row = (int64_t)num_kv_heads * head_dim;
+    if (!row_stride_ok(q_stride, q_row, es, num_tokens, false) ||
+        !row_stride_ok(q_out_stride, q_row, es, num_tokens, true) ||
+        !row_stride_ok(k_stride, k_row, es, num_tokens, false))
+        return PA_ERR_INVALID_ARG;
+    p.q = q;
+    p.k = k;
+    p.q_out = q_out;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.q_out_stride = q_out_stride;
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.num_tokens = num_tokens;
+    p.factor = factor;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.head_dim = head_dim;
+    p.rotary_dim = rotary_dim;
+    p.interleaved = interleaved != 0;
     return PA_OK;
 }
 
@@ -916,6 +1007,236 @@ int pa_paged_attention_decode_int4(void *out, const void *q, const void *key_cac
     p.max_partitions = 1;                     // as the accumulation of the weights sees it
     p.partition_size = INT32_MAX;
     const int krc = pa::launch_decode_int4(p, w, max_ctx, device_sm_count(), mass, mass_len, dtype, s);
+    if (owned) cudaFreeAsync(owned, s);
+    if (krc == -2) return PA_ERR_UNSUPPORTED;
+    return krc == 0 ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_paged_blocks_append(int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                           int32_t *new_context_lens, const int32_t *query_lens, int num_seqs,
+                           const int32_t *free_blocks, int64_t free_capacity, const int32_t *num_free,
+                           int32_t *new_num_free, int32_t *query_start_loc, int32_t *slot_mapping,
+                           int32_t *positions, int64_t num_tokens, int block_size, int64_t num_blocks,
+                           void *stream) {
+    const pa::CallRange range(__func__);
+    int rc = layout_setup(max_blocks_per_seq, num_seqs, free_capacity, block_size, num_blocks);
+    if (rc != PA_OK) return rc;
+    if (num_tokens < 0) return PA_ERR_INVALID_ARG;
+    if (num_tokens > kMaxTokens) return PA_ERR_UNSUPPORTED;
+    if ((num_seqs > 0 && (!block_tables || !context_lens || !new_context_lens || !query_lens)) ||
+        (free_capacity > 0 && !free_blocks) || !num_free || !new_num_free || !query_start_loc ||
+        (num_tokens > 0 && (!slot_mapping || !positions)))
+        return PA_ERR_INVALID_ARG;
+    pa::BlocksAppendParams p{};
+    if ((rc = error_word(&p.err)) != PA_OK) return rc;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.new_context_lens = new_context_lens;
+    p.query_lens = query_lens;
+    p.free_blocks = free_blocks;
+    p.num_free = num_free;
+    p.new_num_free = new_num_free;
+    p.query_start_loc = query_start_loc;
+    p.slot_mapping = slot_mapping;
+    p.positions = positions;
+    p.num_blocks = num_blocks;
+    p.table_tokens = table_tokens(max_blocks_per_seq, block_size);
+    p.num_seqs = num_seqs;
+    p.max_blocks = max_blocks_per_seq;
+    p.free_cap = (int)free_capacity;
+    p.num_tokens = (int)num_tokens;
+    p.log2_block_size = ilog2(block_size);
+    return pa::launch_blocks_append(p, static_cast<cudaStream_t>(stream)) == 0 ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_paged_blocks_release(const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                            int32_t *new_context_lens, const uint8_t *finished, int num_seqs, int32_t *free_blocks,
+                            int64_t free_capacity, const int32_t *num_free, int32_t *new_num_free, int block_size,
+                            int64_t num_blocks, void *stream) {
+    const pa::CallRange range(__func__);
+    int rc = layout_setup(max_blocks_per_seq, num_seqs, free_capacity, block_size, num_blocks);
+    if (rc != PA_OK) return rc;
+    if ((num_seqs > 0 && (!block_tables || !context_lens || !new_context_lens || !finished)) ||
+        (free_capacity > 0 && !free_blocks) || !num_free || !new_num_free)
+        return PA_ERR_INVALID_ARG;
+    pa::BlocksReleaseParams p{};
+    if ((rc = error_word(&p.err)) != PA_OK) return rc;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.new_context_lens = new_context_lens;
+    p.finished = finished;
+    p.free_blocks = free_blocks;
+    p.num_free = num_free;
+    p.new_num_free = new_num_free;
+    p.num_blocks = num_blocks;
+    p.table_tokens = table_tokens(max_blocks_per_seq, block_size);
+    p.num_seqs = num_seqs;
+    p.max_blocks = max_blocks_per_seq;
+    p.free_cap = (int)free_capacity;
+    p.log2_block_size = ilog2(block_size);
+    return pa::launch_blocks_release(p, static_cast<cudaStream_t>(stream)) == 0 ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_rotary_embedding(void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride, const void *q,
+                        int64_t q_stride, const void *k, int64_t k_stride, const int32_t *positions,
+                        const double *inv_freq, float factor, int interleaved, int64_t num_tokens, int num_heads,
+                        int num_kv_heads, int head_dim, int rotary_dim, int dtype, void *stream) {
+    const pa::CallRange range(__func__);
+    pa::RotaryParams p{};
+    int rc = rotary_setup(p, q_out, q_out_stride, q, q_stride, k, k_stride, positions, inv_freq, factor, interleaved,
+                          num_tokens, num_heads, num_kv_heads, head_dim, rotary_dim, dtype);
+    if (rc == kNothingToDo) return PA_OK;
+    if (rc != PA_OK) return rc;
+    if ((num_kv_heads && !k_out) || !aligned16(k_out) ||
+        !row_stride_ok(k_out_stride, (int64_t)num_kv_heads * head_dim, elem_size(dtype), num_tokens, true))
+        return PA_ERR_INVALID_ARG;
+    p.k_out = k_out;
+    p.k_out_stride = k_out_stride;
+    if ((rc = error_word(&p.err)) != PA_OK) return rc;
+    return pa::launch_rotary(p, dtype, static_cast<cudaStream_t>(stream)) == 0 ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_paged_kv_write_rotary(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride, const void *k,
+                             int64_t k_stride, const void *v, int64_t v_stride, const int32_t *positions,
+                             const double *inv_freq, float factor, int interleaved, const int32_t *slot_mapping,
+                             int64_t num_tokens, void *key_cache, void *value_cache, int64_t num_blocks,
+                             int block_size, int num_heads, int num_kv_heads, int head_dim, int rotary_dim,
+                             int dtype, void *stream) {
+    const pa::CallRange range(__func__);
+    if (num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0) return PA_ERR_INVALID_ARG;
+    pa::RotaryParams p{};
+    int rc = rotary_setup(p, q_out, q_out_stride, q, q_stride, k, k_stride, positions, inv_freq, factor, interleaved,
+                          num_tokens, num_heads, num_kv_heads, head_dim, rotary_dim, dtype);
+    if (rc == kNothingToDo) return PA_OK;
+    if (rc != PA_OK) return rc;
+    const int64_t row = (int64_t)num_kv_heads * head_dim;
+    if (!v || !slot_mapping || !key_cache || !value_cache || !aligned16(v) || !aligned16(key_cache) ||
+        !aligned16(value_cache) || !row_stride_ok(v_stride, row, elem_size(dtype), num_tokens, false) ||
+        num_blocks > INT64_MAX / 16 / block_size / row)
+        return PA_ERR_INVALID_ARG;
+    p.v = v;
+    p.v_stride = v_stride;
+    p.k_out = key_cache;
+    p.v_out = value_cache;
+    p.slots = slot_mapping;
+    p.num_slots = num_blocks * block_size;
+    if ((rc = error_word(&p.err)) != PA_OK) return rc;
+    return pa::launch_rotary(p, dtype, static_cast<cudaStream_t>(stream)) == 0 ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_paged_kv_write_fp8_block(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                const int32_t *slot_mapping, int64_t num_tokens, void *key_cache,
+                                void *value_cache, float *kv_scales, int64_t num_blocks, int block_size,
+                                int num_kv_heads, int head_dim, int src_dtype, void *stream) {
+    const pa::CallRange range(__func__);
+    pa::Fp8BlockCache c{};
+    int rc = fp8_block_setup(c, k, v, slot_mapping, num_tokens, key_cache, value_cache, kv_scales, num_blocks,
+                             block_size, num_kv_heads, head_dim, src_dtype);
+    if (rc == kNothingToDo) return PA_OK;
+    if (rc != PA_OK) return rc;
+    const int64_t row = (int64_t)num_kv_heads * head_dim;
+    if (!row_stride_ok(k_stride, row, elem_size(src_dtype), num_tokens, false) ||
+        !row_stride_ok(v_stride, row, elem_size(src_dtype), num_tokens, false))
+        return PA_ERR_INVALID_ARG;
+    unsigned int *err = nullptr;
+    if ((rc = error_word(&err)) != PA_OK) return rc;
+    return pa::launch_kv_write_fp8_block(k, v, k_stride, v_stride, src_dtype, slot_mapping, num_tokens, c, err,
+                                         static_cast<cudaStream_t>(stream)) == 0
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+int pa_paged_kv_read_fp8_block(void *k, void *v, const int32_t *slot_mapping, int64_t num_tokens,
+                               const void *key_cache, const void *value_cache, const float *kv_scales,
+                               int64_t num_blocks, int block_size, int num_kv_heads, int head_dim, int dst_dtype,
+                               void *stream) {
+    const pa::CallRange range(__func__);
+    pa::Fp8BlockCache c{};
+    int rc = fp8_block_setup(c, k, v, slot_mapping, num_tokens, const_cast<void *>(key_cache),
+                             const_cast<void *>(value_cache), const_cast<float *>(kv_scales), num_blocks, block_size,
+                             num_kv_heads, head_dim, dst_dtype);
+    if (rc == kNothingToDo) return PA_OK;
+    if (rc != PA_OK) return rc;
+    unsigned int *err = nullptr;
+    if ((rc = error_word(&err)) != PA_OK) return rc;
+    return pa::launch_kv_read_fp8_block(k, v, dst_dtype, slot_mapping, num_tokens, c, err,
+                                        static_cast<cudaStream_t>(stream)) == 0
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+int pa_copy_blocks_fp8_block(void *key_cache, void *value_cache, float *kv_scales, const int32_t *src_dst_pairs,
+                             int64_t num_pairs, int64_t num_blocks, int block_size, int num_kv_heads, int head_dim,
+                             void *stream) {
+    const pa::CallRange range(__func__);
+    if (num_pairs < 0 || num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0 || head_dim <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (!pow2(block_size) || block_size < 8 || block_size > 256 || num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+    if (num_pairs == 0) return PA_OK;
+    if (num_pairs > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    if (!key_cache || !value_cache || !kv_scales || !src_dst_pairs) return PA_ERR_INVALID_ARG;
+    if (!aligned16(key_cache) || !aligned16(value_cache) || !aligned16(kv_scales)) return PA_ERR_INVALID_ARG;
+    unsigned int *err = nullptr;
+    if (int rc = error_word(&err)) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t bytes = (int64_t)block_size * num_kv_heads * head_dim;
+    if (pa::launch_copy_blocks(key_cache, value_cache, src_dst_pairs, num_pairs, num_blocks, bytes, err, s) != 0 ||
+        pa::launch_copy_scales_fp8_block(reinterpret_cast<float2 *>(kv_scales), src_dst_pairs, num_pairs, num_blocks,
+                                         num_kv_heads, err, s) != 0)
+        return PA_ERR_CUDA;
+    return PA_OK;
+}
+
+size_t pa_decode_fp8_block_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                           int max_context_len) {
+    if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
+        (head_dim != 64 && head_dim != 128) || max_context_len < 0 || num_heads / num_kv_heads > 16)
+        return 0;
+    return fp8_block_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len);
+}
+
+int pa_paged_attention_decode_fp8_block(void *out, const void *q, const void *key_cache, const void *value_cache,
+                                        const float *kv_scales, const int32_t *block_tables, int max_blocks_per_seq,
+                                        const int32_t *context_lens, int num_seqs, int num_heads, int num_kv_heads,
+                                        int head_dim, int block_size, int64_t num_blocks, float scale,
+                                        int max_context_len, void *workspace, size_t workspace_bytes, int dtype,
+                                        void *stream) {
+    const pa::CallRange range(__func__);
+    if (dtype != PA_DTYPE_BF16 && dtype != PA_DTYPE_F16) return elem_size(dtype) ? PA_ERR_UNSUPPORTED
+                                                                                  : PA_ERR_INVALID_ARG;
+    pa::DecodeParams p{};
+    int64_t P = 0;
+    int rc = decode_setup(p, P, out, q, key_cache, value_cache, block_tables, max_blocks_per_seq, context_lens,
+                          num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                          max_context_len, 0);
+    if (rc == kNothingToDo) return PA_OK;
+    if (rc != PA_OK) return rc;
+    if (!kv_scales || !aligned16(kv_scales)) return PA_ERR_INVALID_ARG;
+    p.kv_params = kv_scales;
+    const int64_t max_ctx = call_max_context(max_blocks_per_seq, block_size, max_context_len);
+    if (!pa::decode_fp8_block_supported(p, dtype) || max_ctx > kMaxTokens) return PA_ERR_UNSUPPORTED;
+    if ((rc = error_word(&p.err)) != PA_OK) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t need = fp8_block_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_ctx);
+    void *ws = workspace, *owned = nullptr;
+    if (ws) {
+        if (workspace_bytes < need) return PA_ERR_WORKSPACE;
+        if (!aligned16(ws)) return PA_ERR_INVALID_ARG;
+    } else {
+        if (cudaMallocAsync(&ws, need, s) != cudaSuccess) return PA_ERR_CUDA;
+        owned = ws;
+    }
+    const pa::RunWorkSizes z =
+        pa::decode_fp8_block_work_sizes(num_seqs, num_heads, num_kv_heads, head_dim, max_ctx, device_sm_count());
+    char *at = static_cast<char *>(ws);
+    pa::RunWork w;
+    w.rows = reinterpret_cast<int2 *>(at);
+    at += align256(z.rows);
+    w.part_ml = reinterpret_cast<float2 *>(at);
+    at += align256(z.part_ml);
+    w.part_o = reinterpret_cast<float *>(at);
+    const int krc = pa::launch_decode_fp8_block(p, w, max_ctx, device_sm_count(), dtype, s);
     if (owned) cudaFreeAsync(owned, s);
     if (krc == -2) return PA_ERR_UNSUPPORTED;
     return krc == 0 ? PA_OK : PA_ERR_CUDA;

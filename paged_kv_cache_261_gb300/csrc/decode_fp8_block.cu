@@ -1,0 +1,577 @@
+// Decode attention over an 8-bit paged cache that has a scale for each block of tokens and kv
+// head (format: kv_fp8_block.cu).
+//
+// What is computed is the decode attention of "CS349E lecture 7: 01_paged_attention.py",
+// demo 2, paper eq. 4 (block-wise scores through the block table, one softmax over the whole
+// context, block-wise V accumulation) over the cache's values, K = code * k_scale and
+// V = code * v_scale with the scales of the token's block:
+//   q . K_t          = k_scale_t (q . n_t)
+//   sum_t p_t V_t[c] = sum_t (p_t v_scale_t) n_t[c]
+//
+// E4M3 codes are exact in f16, so a pair of codes becomes a pair of matrix operands by one
+// conversion. Per 16 tokens a warp multiplies, with mma.m16n8k16 (f16 operands, f32 sums),
+//   S^T[16 tok x 8 heads] = n_K[16 x D] . Q^T        A = codes, row = token
+//   O^T[D x 8 heads]     += n_V^T[D x 16 tok] . W^T   A = codes, row = channel
+// The order of the channels inside a contraction, and of the output's rows over the
+// instructions, is free; it is chosen so that every lane's codes are consecutive bytes
+// of a row (D / 4 for K, D / 8 for V). S^T's fragments turn into W^T's with one 8x8
+// transpose in registers. (An instruction of E4M3 operands would want query and weights as
+// sums of three E4M3 terms to keep the 11 bits that f16 has.)
+//
+// W = p v_scale enters the product as f16 (11 bits; the row sums take p unrounded). Its
+// reference is a maximum of the scores (raised only when a score exceeds it by 2^7: no
+// reduction over the lanes before) and a power of two above every v_scale seen, so weights are
+// normal f16 numbers down to 2^-22 of the reference times that power and within 2^-33 of it
+// below. The query enters as f16 times a power of two per head: exact for bf16 and f16 at
+// every channel within 2^-22 of the row's largest.
+//
+// Work: the stages (kTok tokens of one sequence and kv head) of the whole call, in order, are
+// cut into equal runs, one for each warp of the persistent grid (decode_runs.cuh). Warps share
+// nothing. Each warp fetches its own stages, one ahead and across rows, into its own ring: a
+// block of one kv head is one contiguous run for K and V each, so a stage is a few untiled bulk
+// copies, and its blocks' scales one 8-byte copy each, all on one mbarrier.
+//
+// Every wait is bounded; on a timeout the kernel sets PA_DEVERR_WAIT, waits (bounded)
+// for its copies in flight and returns.
+#include "decode_runs.cuh"
+#include "kernels_fp8_block.h"
+
+#include <type_traits>
+
+namespace pa {
+namespace {
+
+constexpr int kStages = 2;
+constexpr int kMaxSeqs = 1536;                    // sequences per launch (the host splits larger batches)
+
+// The softmax reference of a head is not raised before a score exceeds it by this many
+// powers of two: the weights (f16, up to 2^kWeightExp times 2^kSlack) have the room.
+constexpr float kSlack = 7.f;
+constexpr int kWeightExp = 8;
+constexpr int kMinScaleExp = -100, kMaxScaleExp = 121;   // of the V scales' reference
+
+__host__ __device__ constexpr int stage_tokens(int D) { return 4096 / D; }
+__host__ __device__ constexpr int warps_of(int GT) { return GT == 8 ? 12 : 8; }
+
+// GT: query heads padded to 8 or 16.
+template <int D, int GT> struct Cfg {
+    static constexpr int kWarps = warps_of(GT);
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kTok = stage_tokens(D);              // tokens per stage
+    static constexpr int kRow = D;                            // bytes of a token's codes
+    static constexpr int kPieces = kTok / 8;                  // blocks per stage, at most
+    static constexpr int kOffV = kTok * kRow;
+    static constexpr int kOffScale = 2 * kTok * kRow;
+    static constexpr int kSlot = kOffScale + kPieces * 8;
+    static constexpr int kRing = kWarps * kStages * kSlot;
+    // after the ring
+    static constexpr int kOffBar = kRing;                             // [kWarps][kStages]
+    static constexpr int kOffMisc = kOffBar + kWarps * kStages * 8;   // abort flag; warp sums of the prefix
+    static constexpr int kOffPre = kOffMisc + 16 + kWarps * 4;        // int [kMaxSeqs + 1]
+    static constexpr int kSmem = kOffPre + (kMaxSeqs + 1) * 4;
+    static_assert(kSmem <= 232448, "shared memory budget");
+    static_assert(kSlot % 16 == 0 && kOffV % 16 == 0 && kOffScale % 16 == 0, "bulk copies start on 16 bytes");
+    static_assert(kPieces <= 8, "a lane per piece");
+};
+
+// Two codes, in 16 bits, as two f16.
+__device__ __forceinline__ uint32_t widen(uint32_t two) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
+    return r;
+}
+__device__ __forceinline__ uint32_t widen_high(uint32_t two) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(two));
+    return r;
+}
+// 8 bytes copied asynchronously.
+__device__ __forceinline__ void copy8_async(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+// An arrival once this thread's asynchronous copies have landed (one of the phase's count).
+__device__ __forceinline__ void arrive_after_copies(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+template <typename T, int D, int GT>
+__global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_fp8_block_kernel(const DecodeParams p,
+                                                                                     const RunWork ws) {
+    using C = Cfg<D, GT>;
+    constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
+    constexpr int NT = GT / 8;                         // tiles of 8 heads
+    constexpr int kSteps = D / 16;                     // instructions per 16 tokens, S and O alike
+    constexpr int kSub = C::kTok / 16;
+    extern __shared__ __align__(128) unsigned char smem[];
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc);
+    int *warp_sums = reinterpret_cast<int *>(smem + C::kOffMisc + 16);
+    int *pre = reinterpret_cast<int *>(smem + C::kOffPre);   // stages of a kv head before sequence b
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int li = lane >> 2, lj = lane & 3;           // fragment row and column group
+    const int G = p.group, B = p.num_seqs, Hk = p.num_kv_heads;
+
+    if (tid == 0) {
+        // a phase: the bytes of the bulk copies, and the lanes that copy scales
+        for (int i = 0; i < kWarps * kStages; ++i) mbar_init(&bars[i], 1 + C::kPieces);
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    // as the other decode kernels: the set-up and the cut of the work (which reads only the
+    // call's lengths) overlap the preceding kernel
+    asm volatile("griddepcontrol.launch_dependents;");
+    auto context = [&](int b) { return clamped_context(p, b); };
+    count_stages<kThreads, C::kTok>(p, pre, warp_sums);
+    __syncthreads();
+    const uint32_t total = (uint32_t)pre[B] * Hk;      // below 2^31: the host sees to it
+    const uint32_t num_runs = max(1u, min(gridDim.x * kWarps, total));
+    const Runs runs(total, num_runs);
+    // runs go to the SMs in turn, so few of them still use all
+    const uint32_t run = warp * gridDim.x + blockIdx.x;
+    int todo = 0;
+    Cursor at = {};
+    if (run < num_runs && total > 0) {
+        const uint32_t run0 = runs.first(run);
+        todo = (int)(runs.len + (run < runs.longer ? 1 : 0));
+        int lo = 0, hi = B - 1;                        // the first b whose stages end after run0
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if ((uint32_t)pre[mid + 1] * Hk > run0) hi = mid; else lo = mid + 1;
+        }
+        at.b = lo;
+        at.ns = pre[lo + 1] - pre[lo];
+        const uint32_t rest = run0 - (uint32_t)pre[lo] * Hk;
+        at.kvh = (int)(rest / (uint32_t)at.ns);
+        at.s = (int)(rest - (uint32_t)at.kvh * at.ns);
+        at.ctx = context(lo);
+    }
+    // the next row that has stages (there is one)
+    auto next_row = [&](Cursor &c) {
+        c.s = 0;
+        if (++c.kvh < Hk) return;
+        c.kvh = 0;
+        do ++c.b; while (pre[c.b + 1] == pre[c.b]);
+        c.ns = pre[c.b + 1] - pre[c.b];
+        c.ctx = context(c.b);
+    };
+
+    // ---- fetching: lanes 0-7 the K runs, 8-15 the V runs, 16-23 the scales of a stage's
+    // blocks (at most 8: block_size >= 8)
+    unsigned char *ring = smem + warp * kStages * C::kSlot;
+    uint64_t *full = bars + warp * kStages;
+    const int kind = lane >> 3;
+    const int piece_tok = min(p.block_size, C::kTok), log2_piece = 31 - __clz(piece_tok);
+    const int piece_off = (lane & 7) * piece_tok;      // the piece's first token of the stage
+    const bool fetches = kind < 3 && piece_off < C::kTok;
+    const unsigned char *src_base = static_cast<const unsigned char *>(
+        kind == 2 ? p.kv_params : (kind == 1 ? p.value_cache : p.key_cache));
+    const uint32_t dst_off = kind == 2 ? C::kOffScale + (lane & 7) * 8 : (kind == 1 ? C::kOffV : 0) + piece_off * C::kRow;
+    const uint32_t piece_bytes = kind == 2 ? 8 : piece_tok * C::kRow;
+    const uint32_t run_bytes = (uint32_t)C::kRow << p.log2_block_size;     // a block's rows of one kv head
+    const uint32_t block_bytes = run_bytes * (uint32_t)Hk;                 // at most 2^16 * 2^8 * 128, less 2^15
+
+    // whether this lane has a piece of the stage to fetch, and its table entry
+    auto has_piece = [&](const Cursor &c) { return fetches && c.s * C::kTok + piece_off < c.ctx; };
+    auto look_up = [&](const Cursor &c) {
+        const int t = c.s * C::kTok + piece_off;
+        return has_piece(c) ? p.block_tables[(int64_t)c.b * p.max_blocks_per_seq + (t >> p.log2_block_size)] : -1;
+    };
+    auto step = [&](Cursor &c) {
+        if (++c.s == c.ns) next_row(c);
+    };
+    // fetch a stage into a slot of the ring (which no lane reads any more)
+    auto fetch = [&](const Cursor &nx, int entry, int sl) {
+        unsigned char *dst = ring + sl * C::kSlot + dst_off;
+        uint64_t *bar = &full[sl];
+        const bool live = has_piece(nx), good = live && entry >= 0 && entry < p.num_blocks;
+        const uint32_t blocks = __popc(__ballot_sync(0xffffffffu, good) & 0xFFu);
+        if (lane == 0) mbar_arrive_expect_tx(bar, blocks * piece_tok * (2 * C::kRow));
+        __syncwarp();
+        if (good) {
+            if (kind == 2) {
+                copy8_async(dst, src_base + ((int64_t)entry * Hk + nx.kvh) * 8);
+            } else {
+                const uint32_t off = (uint32_t)nx.kvh * run_bytes +
+                                     (uint32_t)((nx.s * C::kTok + piece_off) & (p.block_size - 1)) * C::kRow;
+                bulk_load(dst, src_base + ((uint64_t)(uint32_t)entry * block_bytes + off), piece_bytes, bar);
+            }
+        } else if (live) {
+            // a bad block id: zeros, so its tokens have score and value 0
+            if (kind == 0) raise_error(p.err, PA_DEVERR_BLOCK_ID);
+            for (uint32_t i = 0; i < piece_bytes; i += 8) *reinterpret_cast<uint2 *>(dst + i) = make_uint2(0, 0);
+            fence_proxy_async_smem();
+        }
+        if (kind == 2 && (lane & 7) < C::kPieces) arrive_after_copies(bar);
+        __syncwarp();
+    };
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the first stages, their look-ups in flight together; then one look-up ahead
+    Cursor nx = at;
+    int entry = -1;
+    if (todo > 0) {
+        Cursor c[kStages];
+        int e[kStages];
+#pragma unroll
+        for (int i = 0; i < kStages; ++i)
+            if (i < todo) {
+                c[i] = nx;
+                e[i] = look_up(nx);
+                if (i + 1 < todo) step(nx);
+            }
+#pragma unroll
+        for (int i = 0; i < kStages; ++i)
+            if (i < todo) fetch(c[i], e[i], i);
+        entry = look_up(nx);
+    }
+    describe_rows<kThreads>(p, ws.rows, pre, runs);
+    zero_empty_rows<T, D, kThreads>(p, pre);
+
+    if (todo == 0) return;
+    int left = todo;                                   // stages to consume
+    int unfetched = todo - min(todo, kStages);         // and to fetch
+    int sl = 0;                                        // the slot of the next stage
+    uint32_t phase = 0;                                // and its barrier's phase
+    bool ok = true;
+
+    T *out = reinterpret_cast<T *>(p.out);
+    const T *q = reinterpret_cast<const T *>(p.q);
+    while (left > 0) {
+        // ---- the part of row (b, kvh) that lies in this run
+        const int I_b = at.b, I_kvh = at.kvh;
+        const int s_end = min(at.ns, at.s + left);
+        const bool whole = at.s == 0 && s_end == at.ns;
+        const int64_t head0 = (int64_t)I_b * p.num_heads + (int64_t)I_kvh * G;
+
+        // the group's query as B fragments, and the factors of x = S * (k_scale * sa) of the
+        // heads of S^T's columns
+        uint32_t qb[NT][kSteps][2];
+        float2 sa[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            constexpr int N = D / 4;                   // channels of a lane
+            const int g = nt * 8 + li;
+            float x[N];
+            const T *src = q + (head0 + min(g, G - 1)) * D + lj * N;
+#pragma unroll
+            for (int u = 0; u < N / 8; ++u) Vec16<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(src) + u), x + 8 * u);
+            float amax = 0.f;
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+                if (g >= G) x[u] = 0.f;
+                amax = fmaxf(amax, fabsf(x[u]));
+            }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            // amax = 1.f * 2^(E - 127), scaled into [2^12, 2^13)
+            const int E = (int)((__float_as_uint(amax) >> 23) & 0xFF);
+            const int e2 = E == 0 ? 100 : max(-116, min(100, 139 - E));
+            const float up = pow2f(e2);
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u) {
+                qb[nt][u][0] = pack_half2(x[4 * u] * up, x[4 * u + 1] * up);
+                qb[nt][u][1] = pack_half2(x[4 * u + 2] * up, x[4 * u + 3] * up);
+            }
+            const float a = p.scale_log2 * pow2f(-e2);
+            sa[nt] = make_float2(__shfl_sync(0xffffffffu, a, 8 * lj), __shfl_sync(0xffffffffu, a, 8 * lj + 4));
+        }
+        float O[NT][kSteps][4];
+        float2 nm[NT], l[NT];                          // nm: the negated references
+        int r_exp = kMinScaleExp;                      // 2^r_exp = r_top > every v_scale seen
+        float r_top = 0.f, cr = 0.f;                   // v_scale * cr < 2^kWeightExp
+        bool first = true;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) O[nt][u][c] = 0.f;
+            nm[nt] = make_float2(INFINITY, INFINITY);
+            l[nt] = make_float2(0.f, 0.f);
+        }
+        // one stage; kTail: only its first n tokens belong to the row
+        auto stage = [&](auto tail, const unsigned char *slot, int n) {
+            constexpr bool kTail = decltype(tail)::value;
+            // ---- scores, S^T: rows li and li + 8 of each 16 tokens
+            float S[kSub][NT][4];
+            float vs[kSub][2];
+            float rmax = 0.f;
+#pragma unroll
+            for (int sub = 0; sub < kSub; ++sub) {
+                float S2[NT][4];                       // a second chain of sums
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) S[sub][nt][c] = S2[nt][c] = 0.f;
+                uint32_t ka[D / 16], kb[D / 16];       // this lane's words of the two rows
+                const unsigned char *kr = slot + (sub * 16 + li) * C::kRow + lj * (D / 4);
+#pragma unroll
+                for (int w = 0; w < D / 64; ++w) {
+                    reinterpret_cast<uint4 *>(ka)[w] = reinterpret_cast<const uint4 *>(kr)[w];
+                    reinterpret_cast<uint4 *>(kb)[w] = reinterpret_cast<const uint4 *>(kr + 8 * C::kRow)[w];
+                }
+#pragma unroll
+                for (int u = 0; u < kSteps; ++u) {
+                    const uint32_t a0 = widen(ka[u]), a1 = widen(kb[u]), a2 = widen_high(ka[u]), a3 = widen_high(kb[u]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma16816(u & 1 ? S2[nt] : S[sub][nt], a0, a1, a2, a3, qb[nt][u][0], qb[nt][u][1]);
+                }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int t = sub * 16 + li + 8 * r;
+                    const float2 sc = *reinterpret_cast<const float2 *>(slot + C::kOffScale + (t >> log2_piece) * 8);
+                    const bool valid = !kTail || t < n;
+                    vs[sub][r] = valid ? sc.y : 0.f;
+                    rmax = fmaxf(rmax, fabsf(vs[sub][r]));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float2 dot = add2(make_float2(S[sub][nt][2 * r], S[sub][nt][2 * r + 1]),
+                                                make_float2(S2[nt][2 * r], S2[nt][2 * r + 1]));
+                        const float2 x = mul2(dot, make_float2(sc.x * sa[nt].x, sc.x * sa[nt].y));
+                        S[sub][nt][2 * r] = valid ? x.x : -INFINITY;
+                        S[sub][nt][2 * r + 1] = valid ? x.y : -INFINITY;
+                    }
+                }
+            }
+            // ---- this lane's V words of every 16 tokens (2 lj, 2 lj + 1, 2 lj + 8, 2 lj + 9), read
+            // before the references are looked at
+            uint32_t vw[kSub][4][D / 32];
+#pragma unroll
+            for (int sub = 0; sub < kSub; ++sub) {
+                const unsigned char *vr = slot + C::kOffV + (sub * 16 + 2 * lj) * C::kRow + li * (D / 8);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int t = (k & 1) + (k & 2) * 4;
+                    const unsigned char *src = vr + t * C::kRow;
+                    if constexpr (D == 128) *reinterpret_cast<uint4 *>(vw[sub][k]) = *reinterpret_cast<const uint4 *>(src);
+                    else *reinterpret_cast<uint2 *>(vw[sub][k]) = *reinterpret_cast<const uint2 *>(src);
+                    // past the row's end anything may lie, NaN codes too
+                    if (kTail && sub * 16 + 2 * lj + t >= n) {
+#pragma unroll
+                        for (int w = 0; w < D / 32; ++w) vw[sub][k][w] = 0;
+                    }
+                }
+            }
+            // ---- the references, raised where a score or a V scale outgrew them
+            float over = -INFINITY;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float v = S[0][nt][c];
+#pragma unroll
+                    for (int sub = 0; sub < kSub; ++sub) v = fmaxf(v, fmaxf(S[sub][nt][c], S[sub][nt][2 + c]));
+                    over = fmaxf(over, v + (c ? nm[nt].y : nm[nt].x));
+                }
+            if (__any_sync(0xffffffffu, first || over > kSlack || rmax >= r_top)) {
+                const int r_new = max(r_exp, min(kMaxScaleExp, (int)((__float_as_uint(rows_max(rmax)) >> 23) & 0xFF) - 126));
+                const float rs = r_exp - r_new < -126 ? 0.f : pow2f(r_exp - r_new);
+                r_exp = r_new;
+                r_top = pow2f(r_new);
+                cr = pow2f(kWeightExp - r_new);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float a[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float &neg = c ? nm[nt].y : nm[nt].x;
+                        float v = -neg;
+#pragma unroll
+                        for (int sub = 0; sub < kSub; ++sub) v = fmaxf(v, fmaxf(S[sub][nt][c], S[sub][nt][2 + c]));
+                        v = rows_max(v);
+                        a[c] = first ? 0.f : fast_exp2(-neg - v);
+                        neg = -v;
+                    }
+                    if (!first) {
+                        l[nt] = mul2(l[nt], make_float2(a[0], a[1]));
+#pragma unroll
+                        for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) O[nt][u][c] *= a[c & 1] * rs;
+                    }
+                }
+                first = false;
+            }
+            // ---- weights and O^T
+#pragma unroll
+            for (int sub = 0; sub < kSub; ++sub) {
+                uint32_t wb[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float2 d = add2(make_float2(S[sub][nt][2 * r], S[sub][nt][2 * r + 1]), nm[nt]);
+                        const float2 w = make_float2(fast_exp2(d.x), fast_exp2(d.y));
+                        l[nt] = add2(l[nt], w);
+                        const float v = vs[sub][r] * cr;
+                        wb[nt][r] = transpose8x8(pack_half2(w.x * v, w.y * v));
+                    }
+                // two tokens' bytes of two channels side by side
+#pragma unroll
+                for (int u = 0; u < kSteps; ++u) {
+                    const uint32_t sel = u & 1 ? 0x7362u : 0x5140u;
+                    const uint32_t x = __byte_perm(vw[sub][0][u / 2], vw[sub][1][u / 2], sel);
+                    const uint32_t y = __byte_perm(vw[sub][2][u / 2], vw[sub][3][u / 2], sel);
+                    const uint32_t a0 = widen(x), a1 = widen_high(x), a2 = widen(y), a3 = widen_high(y);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816(O[nt][u], a0, a1, a2, a3, wb[nt][0], wb[nt][1]);
+                }
+            }
+        };
+        for (; at.s < s_end; ++at.s) {
+            const unsigned char *slot = ring + sl * C::kSlot;
+            if (!__all_sync(0xffffffffu, mbar_try_wait(&full[sl], phase)) &&
+                (__any_sync(0xffffffffu, *abort_flag != 0) || !warp_wait(&full[sl], phase))) {
+                ok = false;
+                break;
+            }
+            const int n = at.ctx - at.s * C::kTok;     // valid tokens, at least 1
+            if (n >= C::kTok) stage(std::false_type{}, slot, n);
+            else stage(std::true_type{}, slot, n);
+            __syncwarp();                              // every lane has read the slot
+            --left;
+            if (unfetched > 0) {
+                fetch(nx, entry, sl);
+                if (--unfetched > 0) {
+                    step(nx);
+                    entry = look_up(nx);               // on its way until the next fetch
+                }
+            }
+            if (++sl == kStages) {
+                sl = 0;
+                phase ^= 1;
+            }
+        }
+        if (!ok) break;
+
+        // ---- the row, or this run's partial of it (unnormalised, with its reference and sum).
+        // A lane has channels li D / 8 + 2 u + r of heads 2 lj and 2 lj + 1.
+        const int r = I_b * Hk + I_kvh;
+        const float unit = pow2f(r_exp - kWeightExp);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float ls = rows_sum(c ? l[nt].y : l[nt].x);
+                const int g = nt * 8 + 2 * lj + c;
+                if (g >= G) continue;
+                const float inv = whole ? 1.f / ls : 1.f;
+                const int d0 = li * (D / 8);
+#pragma unroll
+                for (int u0 = 0; u0 < kSteps; u0 += 4) {
+                    float v[8];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+#pragma unroll
+                        for (int rr = 0; rr < 2; ++rr) v[2 * u + rr] = O[nt][u0 + u][2 * rr + c] * inv * unit;
+                    if (whole) {
+                        alignas(16) T h[8];
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) h[u] = Elem<T>::from_f(v[u]);
+                        *reinterpret_cast<uint4 *>(out + (head0 + g) * D + d0 + 2 * u0) = *reinterpret_cast<uint4 *>(h);
+                    } else {
+                        float *dst = ws.part_o + ((int64_t)(run + r) * G + g) * D + d0 + 2 * u0;
+                        *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+                        *reinterpret_cast<float4 *>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
+                    }
+                }
+                if (li == 0 && !whole) ws.part_ml[(int64_t)(run + r) * G + g] = make_float2(-(c ? nm[nt].y : nm[nt].x), ls);
+            }
+        if (left > 0) next_row(at);
+    }
+    if (!ok) {
+        *abort_flag = 1;
+        raise_error(p.err, PA_DEVERR_WAIT);
+        // copies still in flight land before the CTA's shared memory goes away
+        for (; left > unfetched; --left) {
+            mbar_wait(&full[sl], phase);
+            if (++sl == kStages) {
+                sl = 0;
+                phase ^= 1;
+            }
+        }
+    }
+}
+
+template <typename T, int D, int GT>
+int launch_t(const DecodeParams &p, const RunWork &ws, int64_t max_ctx, int grid, cudaStream_t stream) {
+    using C = Cfg<D, GT>;
+    auto kern = decode_fp8_block_kernel<T, D, GT>;
+    static bool attr_set[kMaxDevices] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
+    if (!attr_set[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return -1;
+        attr_set[dev] = true;
+    }
+    const int rc = launch_pdl(kern, dim3((unsigned)grid), dim3(C::kThreads), C::kSmem, stream, p, ws);
+    return rc != 0 ? rc : launch_join<T, D>(p, ws, max_ctx, C::kTok, (int64_t)grid * C::kWarps, stream);
+}
+
+template <typename T>
+int launch_d(const DecodeParams &p, const RunWork &ws, int64_t max_ctx, int grid, cudaStream_t stream) {
+    if (p.head_dim == 128)
+        return p.group <= 8 ? launch_t<T, 128, 8>(p, ws, max_ctx, grid, stream)
+                            : launch_t<T, 128, 16>(p, ws, max_ctx, grid, stream);
+    return p.group <= 8 ? launch_t<T, 64, 8>(p, ws, max_ctx, grid, stream)
+                        : launch_t<T, 64, 16>(p, ws, max_ctx, grid, stream);
+}
+
+int64_t row_stages(int64_t max_ctx, int64_t head_dim) {
+    const int tok = stage_tokens((int)head_dim);
+    return (max_ctx + tok - 1) / tok;
+}
+
+// Sequences per launch: what the kernel's prefix holds, and a launch's stages in 31 bits.
+int64_t seqs_per_launch(int64_t stages, int64_t kv_heads) {
+    return std::max<int64_t>(1, std::min<int64_t>(kMaxSeqs, INT32_MAX / std::max<int64_t>(stages * kv_heads, 1)));
+}
+
+// One CTA per SM, and no more than there can be stages.
+int launch_grid(int64_t rows, int64_t stages, int sms) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>(sms, rows * stages));
+}
+
+}  // namespace
+
+bool decode_fp8_block_supported(const DecodeParams &p, int dtype) {
+    return (dtype == PA_DTYPE_BF16 || dtype == PA_DTYPE_F16) && (p.head_dim == 64 || p.head_dim == 128) &&
+           p.group >= 1 && p.group <= 16 && p.block_size >= 8 && p.block_size <= 256 && p.num_blocks < INT32_MAX &&
+           (int64_t)p.num_seqs * p.num_heads < INT32_MAX;
+}
+
+// At most one partial per run and one more per row: runs + rows of a launch.
+RunWorkSizes decode_fp8_block_work_sizes(int64_t num_seqs, int64_t num_heads, int64_t num_kv_heads, int64_t head_dim,
+                                         int64_t max_ctx, int sms) {
+    const int64_t group = num_heads / num_kv_heads, stages = row_stages(max_ctx, head_dim);
+    const int64_t rows = std::min(num_seqs, seqs_per_launch(stages, num_kv_heads)) * num_kv_heads;
+    const int64_t parts = (int64_t)launch_grid(rows, stages, sms) * warps_of(group <= 8 ? 8 : 16) + rows;
+    RunWorkSizes s;
+    s.rows = (size_t)(rows * 8);
+    s.part_ml = (size_t)(parts * group * 8);
+    s.part_o = (size_t)(parts * group * head_dim * 4);
+    return s;
+}
+
+int launch_decode_fp8_block(const DecodeParams &p, const RunWork &ws, int64_t max_ctx, int sms, int dtype,
+                            cudaStream_t stream) {
+    const int64_t stages = row_stages(max_ctx, p.head_dim);
+    if (!decode_fp8_block_supported(p, dtype) || stages * p.num_kv_heads > INT32_MAX) return -2;
+    const int chunk = (int)std::min<int64_t>(p.num_seqs, seqs_per_launch(stages, p.num_kv_heads));
+    for (int b0 = 0; b0 < p.num_seqs; b0 += chunk) {
+        DecodeParams c = p;
+        const int64_t first = (int64_t)b0 * p.num_heads * p.head_dim * 2;
+        c.num_seqs = std::min(chunk, p.num_seqs - b0);
+        c.q = static_cast<const char *>(p.q) + first;
+        c.out = static_cast<char *>(p.out) + first;
+        c.block_tables = p.block_tables + (int64_t)b0 * p.max_blocks_per_seq;
+        c.context_lens = p.context_lens + b0;
+        const int grid = launch_grid((int64_t)c.num_seqs * c.num_kv_heads, stages, sms);
+        const int rc = dtype == PA_DTYPE_BF16 ? launch_d<__nv_bfloat16>(c, ws, max_ctx, grid, stream)
+                                              : launch_d<__half>(c, ws, max_ctx, grid, stream);
+        if (rc != 0) return rc;
+    }
+    return 0;
+}
+
+}  // namespace pa
