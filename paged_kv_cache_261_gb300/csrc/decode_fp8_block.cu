@@ -18,18 +18,28 @@
 // transpose in registers. (An instruction of E4M3 operands would want query and weights as
 // sums of three E4M3 terms to keep the 11 bits that f16 has.)
 //
-// W = p v_scale enters the product as f16 (11 bits; the row sums take p unrounded). Its
-// reference is a maximum of the scores (raised only when a score exceeds it by 2^7: no
-// reduction over the lanes before) and a power of two above every v_scale seen, so weights are
-// normal f16 numbers down to 2^-22 of the reference times that power and within 2^-33 of it
-// below. The query enters as f16 times a power of two per head: exact for bf16 and f16 at
-// every channel within 2^-22 of the row's largest.
+// W = p v_scale enters the product as f16 (11 bits; the row sums take p unrounded), and where the
+// outputs are f16, whose own rounding is no coarser, what that rounding left enters as a second
+// f16 (22 bits; us with one and two: 8B-shaped batch 53.3, 53.7, long contexts 201.5, 202.2, 16 query
+// heads to a kv head 63.2, 69.7). Its reference is a maximum of the scores (raised only when a
+// score exceeds it by 2^7: no reduction over the lanes before) and a power of two above every
+// v_scale seen, so weights are normal f16 numbers down to 2^-22 of the reference times that power
+// and within 2^-33 of it below. The query enters as f16 times a power of two per head: exact for
+// bf16 and f16 at every channel within 2^-22 of the row's largest.
 //
 // Work: the stages (kTok tokens of one sequence and kv head) of the whole call, in order, are
 // cut into equal runs, one for each warp of the persistent grid (decode_runs.cuh). Warps share
 // nothing. Each warp fetches its own stages, one ahead and across rows, into its own ring: a
 // block of one kv head is one contiguous run for K and V each, so a stage is a few untiled bulk
-// copies, and its blocks' scales one 8-byte copy each, all on one mbarrier.
+// copies, and its blocks' scales one 8-byte copy each, all on one mbarrier. (Boxes that TMA
+// swizzles, so that the lanes of a fragment do not meet on few banks, changed nothing: 52.9 and
+// 201.7 us on the two cases below.)
+//
+// What bounds it (one GB300): HBM. Long contexts, 1.34 GB, take 202 us, 6.65 TB/s, as fast as a copy;
+// the 8B-shaped batch, 303 MB, 53.4 us, 3 of them the join and about 3 the start. 8 warps with two
+// stages of 8 KB each keep 131 KB an SM on their way; more of them is slower, as is less work a
+// stage (us, batch / long: 10 warps 53.0 / 214, 12 54.9 / 216, 8 with three stages 55.0 / 217, 12 with
+// three of 4 KB 53.2 / 205, 8 with three of 4 KB 61.7 / 241). 16 query heads to a kv head: 63.5 us on the batch, instructions.
 //
 // Every wait is bounded; on a timeout the kernel sets PA_DEVERR_WAIT, waits (bounded)
 // for its copies in flight and returns.
@@ -51,11 +61,9 @@ constexpr int kWeightExp = 8;
 constexpr int kMinScaleExp = -100, kMaxScaleExp = 121;   // of the V scales' reference
 
 __host__ __device__ constexpr int stage_tokens(int D) { return 4096 / D; }
-__host__ __device__ constexpr int warps_of(int GT) { return GT == 8 ? 12 : 8; }
+constexpr int kWarps = 8;                         // of a CTA, one CTA an SM
 
-// GT: query heads padded to 8 or 16.
-template <int D, int GT> struct Cfg {
-    static constexpr int kWarps = warps_of(GT);
+template <int D> struct Cfg {
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kTok = stage_tokens(D);              // tokens per stage
     static constexpr int kRow = D;                            // bytes of a token's codes
@@ -94,14 +102,16 @@ __device__ __forceinline__ void arrive_after_copies(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
+// GT: query heads padded to 8 or 16.
 template <typename T, int D, int GT>
-__global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_fp8_block_kernel(const DecodeParams p,
+__global__ __launch_bounds__(Cfg<D>::kThreads, 1) void decode_fp8_block_kernel(const DecodeParams p,
                                                                                      const RunWork ws) {
-    using C = Cfg<D, GT>;
-    constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
+    using C = Cfg<D>;
+    constexpr int kThreads = C::kThreads;
     constexpr int NT = GT / 8;                         // tiles of 8 heads
     constexpr int kSteps = D / 16;                     // instructions per 16 tokens, S and O alike
     constexpr int kSub = C::kTok / 16;
+    constexpr bool kTwoTerms = std::is_same_v<T, __half>;
     extern __shared__ __align__(128) unsigned char smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc);
@@ -396,6 +406,7 @@ __global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_fp8_block_ke
 #pragma unroll
             for (int sub = 0; sub < kSub; ++sub) {
                 uint32_t wb[NT][2];
+                [[maybe_unused]] uint32_t we[NT][2];   // what the rounding of W left, for f16 outputs
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -404,7 +415,14 @@ __global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_fp8_block_ke
                         const float2 w = make_float2(fast_exp2(d.x), fast_exp2(d.y));
                         l[nt] = add2(l[nt], w);
                         const float v = vs[sub][r] * cr;
-                        wb[nt][r] = transpose8x8(pack_half2(w.x * v, w.y * v));
+                        const float2 wv = mul2(w, make_float2(v, v));
+                        const uint32_t wh = pack_half2(wv.x, wv.y);
+                        wb[nt][r] = transpose8x8(wh);
+                        if constexpr (kTwoTerms) {
+                            const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&wh));
+                            const float2 lo = add2(wv, make_float2(-hi.x, -hi.y));
+                            we[nt][r] = transpose8x8(pack_half2(lo.x, lo.y));
+                        }
                     }
                 // two tokens' bytes of two channels side by side
 #pragma unroll
@@ -414,7 +432,10 @@ __global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_fp8_block_ke
                     const uint32_t y = __byte_perm(vw[sub][2][u / 2], vw[sub][3][u / 2], sel);
                     const uint32_t a0 = widen(x), a1 = widen_high(x), a2 = widen(y), a3 = widen_high(y);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma16816(O[nt][u], a0, a1, a2, a3, wb[nt][0], wb[nt][1]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma16816(O[nt][u], a0, a1, a2, a3, wb[nt][0], wb[nt][1]);
+                        if constexpr (kTwoTerms) mma16816(O[nt][u], a0, a1, a2, a3, we[nt][0], we[nt][1]);
+                    }
                 }
             }
         };
@@ -495,7 +516,7 @@ __global__ __launch_bounds__((Cfg<D, GT>::kThreads), 1) void decode_fp8_block_ke
 
 template <typename T, int D, int GT>
 int launch_t(const DecodeParams &p, const RunWork &ws, int64_t max_ctx, int grid, cudaStream_t stream) {
-    using C = Cfg<D, GT>;
+    using C = Cfg<D>;
     auto kern = decode_fp8_block_kernel<T, D, GT>;
     static bool attr_set[kMaxDevices] = {};
     int dev = 0;
@@ -505,7 +526,7 @@ int launch_t(const DecodeParams &p, const RunWork &ws, int64_t max_ctx, int grid
         attr_set[dev] = true;
     }
     const int rc = launch_pdl(kern, dim3((unsigned)grid), dim3(C::kThreads), C::kSmem, stream, p, ws);
-    return rc != 0 ? rc : launch_join<T, D>(p, ws, max_ctx, C::kTok, (int64_t)grid * C::kWarps, stream);
+    return rc != 0 ? rc : launch_join<T, D>(p, ws, max_ctx, C::kTok, (int64_t)grid * kWarps, stream);
 }
 
 template <typename T>
@@ -545,7 +566,7 @@ RunWorkSizes decode_fp8_block_work_sizes(int64_t num_seqs, int64_t num_heads, in
                                          int64_t max_ctx, int sms) {
     const int64_t group = num_heads / num_kv_heads, stages = row_stages(max_ctx, head_dim);
     const int64_t rows = std::min(num_seqs, seqs_per_launch(stages, num_kv_heads)) * num_kv_heads;
-    const int64_t parts = (int64_t)launch_grid(rows, stages, sms) * warps_of(group <= 8 ? 8 : 16) + rows;
+    const int64_t parts = (int64_t)launch_grid(rows, stages, sms) * kWarps + rows;
     RunWorkSizes s;
     s.rows = (size_t)(rows * 8);
     s.part_ml = (size_t)(parts * group * 8);
