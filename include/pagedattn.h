@@ -678,13 +678,13 @@ int pa_paged_kv_write_rotary(void *q_out, int64_t q_out_stride, const void *q, i
  * pa_paged_kv_write]
  * Per block written to, kv head and tensor, with a the largest finite magnitude of the call's
  * tokens in it and s0 the scale it had:
- *   s = the smallest 2^e, e >= -100, with a <= 448 * 2^e; if the call does not write the block's
- *       first slot and s0 is positive and finite, the larger of that and s0
- *   every code of the block, if the call does not write its first slot and s > s0 (positive and
- *       finite): the code nearest to its code's number * (s0 / s)
+ *   s = the smallest 2^e, e >= -100, with a <= 448 * 2^e and, if the call does not write the
+ *       block's first slot and 0 < s0 <= 2^126, s0 <= 2^e
+ *   every code of the block, where s0 counted and s > s0: the code nearest to its code's number *
+ *       (s0 / s)
  *   the tokens' codes: those nearest to x / s
- * (products and quotients in float32, exact where scales are powers of two, as the scatter's own
- * are; nearest: ties to the even code, magnitudes beyond 448 and infinities to +-448, NaN to a NaN
+ * (all exact in float32 where s0 is a power of two, as the scatter's own scales are; nearest: ties
+ * to the even code, magnitudes beyond 448 and infinities to +-448, NaN to a NaN
  * code). So a call that writes a block's first slot starts the block anew, and fills a block
  * from its first slot on as sequences do. Empty caches need no initial scales.
  * The tokens of one block stand next to each other in slot_mapping, with nothing between them (a
@@ -746,6 +746,22 @@ int pa_paged_attention_decode_fp8_block(void *out, const void *q, const void *ke
                                         int head_dim, int block_size, int64_t num_blocks, float scale,
                                         int max_context_len, void *workspace, size_t workspace_bytes, int dtype,
                                         void *stream);
+
+/*
+ * One of the calls above with its arguments in an array of 8-byte words: the call (PA_CALL_*), the
+ * number of words after the third, the stream, and then the arguments in the order of the
+ * declaration, pointers and integers as int64_t, floats as double. The same checks and results;
+ * for bindings in which every argument of a call costs time (Python's ctypes, on the GPU's host:
+ * 18 arguments 1.7 us, packed 0.4). A wrong call or number: PA_ERR_INVALID_ARG.
+ */
+#define PA_CALL_BLOCKS_APPEND    1
+#define PA_CALL_BLOCKS_RELEASE   2
+#define PA_CALL_ROTARY_EMBEDDING 3
+#define PA_CALL_KV_WRITE_ROTARY  4
+#define PA_CALL_KV_WRITE_FP8_BLOCK 5
+#define PA_CALL_KV_READ_FP8_BLOCK  6
+#define PA_CALL_DECODE_FP8_BLOCK   7
+int pa_call_packed(const void *words);
 
 /*
  * Synchronise `stream`, then read and clear the current device's error word.

@@ -55,7 +55,9 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
+import struct
 
 import numpy as np
 
@@ -146,6 +148,25 @@ _decl("pa_copy_blocks_fp8_block", [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _
 _decl("pa_decode_fp8_block_workspace_bytes", [_i32, _i32, _i32, _i32, _i32], _sz)
 _decl("pa_paged_attention_decode_fp8_block", [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32,
                                               _i64, _f, _i32, _vp, _sz, _i32, _vp])
+_decl("pa_call_packed", [ctypes.c_char_p])
+
+_packed = _lib.pa_call_packed
+
+
+def _words(call: int, name: str):
+    """Packs (stream, arguments of a call in the order of its declaration) for _packed."""
+    args = getattr(_lib, name).argtypes[:-1]
+    form = struct.Struct("3q" + "".join("d" if a is _f else "q" for a in args))
+    return functools.partial(form.pack, call, len(args))
+
+
+_append_words = _words(1, "pa_paged_blocks_append")
+_release_words = _words(2, "pa_paged_blocks_release")
+_rotary_words = _words(3, "pa_rotary_embedding")
+_write_rotary_words = _words(4, "pa_paged_kv_write_rotary")
+_write_block_words = _words(5, "pa_paged_kv_write_fp8_block")
+_read_block_words = _words(6, "pa_paged_kv_read_fp8_block")
+_decode_block_words = _words(7, "pa_paged_attention_decode_fp8_block")
 
 
 class PagedAttnError(RuntimeError):
@@ -233,6 +254,14 @@ def _stream_ptr(stream, device) -> int:
         # the pointer alone, without a Stream object around it (0.1 against 1.9 us)
         return int(torch._C._cuda_getCurrentRawStream(device.index))
     return int(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _stream_here(stream, device):
+    """The pointer of the stream that a call goes to, or None where it has to go through _on first."""
+    c, i = _torch_module._C, device.index
+    if i != c._cuda_getDevice():
+        return None
+    return c._cuda_getCurrentRawStream(i) if stream is None else int(stream.cuda_stream)
 
 
 def _cuda(t, name: str, dtype=None, device=None):
@@ -938,6 +967,15 @@ def paged_kv_evict(kept, mass, mass_out, key_cache, value_cache, block_tables, o
         _check(rc, "pa_paged_kv_evict")
 
 
+def _lengths(what, *tensors):
+    """The lengths of tensors that have to be one-dimensional."""
+    shapes = [t.shape for t in tensors]
+    for x in shapes:
+        if len(x) != 1:
+            raise ValueError(f"{what} must be one-dimensional")
+    return [x[0] for x in shapes]
+
+
 def paged_blocks_append(block_tables, context_lens, query_lens, free_blocks, num_free, query_start_loc, slot_mapping,
                         positions, block_size: int, num_blocks: int, new_context_lens=None, new_num_free=None,
                         stream=None) -> None:
@@ -952,31 +990,42 @@ def paged_blocks_append(block_tables, context_lens, query_lens, free_blocks, num
     i32, dev = _torch().int32, block_tables.device
     out_lens = context_lens if new_context_lens is None else new_context_lens
     out_free = num_free if new_num_free is None else new_num_free
-    if not block_tables.is_cuda:
-        _cuda(block_tables, "block_tables")
-    _all_cuda(dev, (block_tables, "block_tables", i32), (context_lens, "context_lens", i32),
-              (query_lens, "query_lens", i32), (free_blocks, "free_blocks", i32), (num_free, "num_free", i32),
-              (query_start_loc, "query_start_loc", i32), (slot_mapping, "slot_mapping", i32),
-              (positions, "positions", i32), (out_lens, "new_context_lens", i32), (out_free, "new_num_free", i32))
-    if block_tables.dim() != 2 or free_blocks.dim() != 1 or slot_mapping.dim() != 1:
-        raise ValueError("block_tables must be [B, MB], free_blocks [F] and slot_mapping [T]")
-    B, mb = block_tables.shape
-    T = slot_mapping.shape[0]
-    if context_lens.shape != (B,) or query_lens.shape != (B,) or out_lens.shape != (B,) or \
-            query_start_loc.shape != (B + 1,):
+    # what every tensor has to be, in one expression where nothing is wrong
+    if not (block_tables.is_cuda and block_tables.dtype == i32 and block_tables.is_contiguous() and
+            context_lens.device == dev and context_lens.dtype == i32 and context_lens.is_contiguous() and
+            query_lens.device == dev and query_lens.dtype == i32 and query_lens.is_contiguous() and
+            free_blocks.device == dev and free_blocks.dtype == i32 and free_blocks.is_contiguous() and
+            num_free.device == dev and num_free.dtype == i32 and query_start_loc.device == dev and
+            query_start_loc.dtype == i32 and query_start_loc.is_contiguous() and slot_mapping.device == dev and
+            slot_mapping.dtype == i32 and slot_mapping.is_contiguous() and positions.device == dev and
+            positions.dtype == i32 and positions.is_contiguous() and
+            (out_lens is context_lens or (out_lens.device == dev and out_lens.dtype == i32 and out_lens.is_contiguous())) and
+            (out_free is num_free or (out_free.device == dev and out_free.dtype == i32))):
+        _cuda(block_tables, "block_tables", i32)
+        _all_cuda(dev, (context_lens, "context_lens", i32), (query_lens, "query_lens", i32),
+                  (free_blocks, "free_blocks", i32), (num_free, "num_free", i32),
+                  (query_start_loc, "query_start_loc", i32), (slot_mapping, "slot_mapping", i32),
+                  (positions, "positions", i32), (out_lens, "new_context_lens", i32), (out_free, "new_num_free", i32))
+    table, (cap, T) = block_tables.shape, _lengths("free_blocks [F] and slot_mapping [T]", free_blocks, slot_mapping)
+    if len(table) != 2:
+        raise ValueError("block_tables must be [B, MB]")
+    B, mb = table
+    batch = (B,)
+    if context_lens.shape != batch or query_lens.shape != batch or query_start_loc.shape != (B + 1,) or \
+            (out_lens is not context_lens and out_lens.shape != batch):
         raise ValueError("context_lens, query_lens and new_context_lens must be [B], query_start_loc [B + 1]")
     if positions.shape != (T,) or num_free.numel() != 1 or out_free.numel() != 1:
         raise ValueError("positions must be [T] as slot_mapping, num_free and new_num_free [1]")
-    if _elsewhere(dev):
+    sp = _stream_here(stream, dev)
+    if sp is None:
         with _on(dev):
             return paged_blocks_append(block_tables, context_lens, query_lens, free_blocks, num_free, query_start_loc,
                                        slot_mapping, positions, block_size, num_blocks, new_context_lens, new_num_free,
-                                       stream or _torch().cuda.current_stream(dev))
-    rc = _lib.pa_paged_blocks_append(block_tables.data_ptr(), mb, context_lens.data_ptr(), out_lens.data_ptr(),
-                                     query_lens.data_ptr(), B, free_blocks.data_ptr(), free_blocks.shape[0],
-                                     num_free.data_ptr(), out_free.data_ptr(), query_start_loc.data_ptr(),
-                                     slot_mapping.data_ptr(), positions.data_ptr(), T, int(block_size),
-                                     int(num_blocks), _stream_ptr(stream, dev))
+                                       stream or _torch_module.cuda.current_stream(dev))
+    rc = _packed(_append_words(sp, block_tables.data_ptr(), mb, context_lens.data_ptr(),
+                               out_lens.data_ptr(), query_lens.data_ptr(), B, free_blocks.data_ptr(), cap,
+                               num_free.data_ptr(), out_free.data_ptr(), query_start_loc.data_ptr(),
+                               slot_mapping.data_ptr(), positions.data_ptr(), T, int(block_size), int(num_blocks)))
     if rc:
         _check(rc, "pa_paged_blocks_append")
 
@@ -991,30 +1040,37 @@ def paged_blocks_release(block_tables, context_lens, finished, free_blocks, num_
     i32, dev = torch.int32, block_tables.device
     out_lens = context_lens if new_context_lens is None else new_context_lens
     out_free = num_free if new_num_free is None else new_num_free
-    if not block_tables.is_cuda:
-        _cuda(block_tables, "block_tables")
-    if finished.dtype != torch.bool and finished.dtype != torch.uint8:
-        raise TypeError(f"finished must be torch.bool or torch.uint8, got {finished.dtype}")
-    _all_cuda(dev, (block_tables, "block_tables", i32), (context_lens, "context_lens", i32),
-              (finished, "finished", finished.dtype), (free_blocks, "free_blocks", i32), (num_free, "num_free", i32),
-              (out_lens, "new_context_lens", i32), (out_free, "new_num_free", i32))
-    if block_tables.dim() != 2 or free_blocks.dim() != 1:
-        raise ValueError("block_tables must be [B, MB] and free_blocks [F]")
-    B, mb = block_tables.shape
-    if context_lens.shape != (B,) or finished.shape != (B,) or out_lens.shape != (B,):
+    flag = finished.dtype
+    if flag != torch.bool and flag != torch.uint8:
+        raise TypeError(f"finished must be torch.bool or torch.uint8, got {flag}")
+    if not (block_tables.is_cuda and block_tables.dtype == i32 and block_tables.is_contiguous() and
+            context_lens.device == dev and context_lens.dtype == i32 and context_lens.is_contiguous() and
+            finished.device == dev and finished.is_contiguous() and free_blocks.device == dev and
+            free_blocks.dtype == i32 and free_blocks.is_contiguous() and num_free.device == dev and num_free.dtype == i32 and
+            (out_lens is context_lens or (out_lens.device == dev and out_lens.dtype == i32 and out_lens.is_contiguous())) and
+            (out_free is num_free or (out_free.device == dev and out_free.dtype == i32))):
+        _cuda(block_tables, "block_tables", i32)
+        _all_cuda(dev, (context_lens, "context_lens", i32), (finished, "finished", flag), (free_blocks, "free_blocks", i32),
+                  (num_free, "num_free", i32), (out_lens, "new_context_lens", i32), (out_free, "new_num_free", i32))
+    table, (cap,) = block_tables.shape, _lengths("free_blocks [F]", free_blocks)
+    if len(table) != 2:
+        raise ValueError("block_tables must be [B, MB]")
+    B, mb = table
+    batch = (B,)
+    if context_lens.shape != batch or finished.shape != batch or (out_lens is not context_lens and out_lens.shape != batch):
         raise ValueError("context_lens, finished and new_context_lens must be [B]")
     if num_free.numel() != 1 or out_free.numel() != 1:
         raise ValueError("num_free and new_num_free must be [1]")
-    if _elsewhere(dev):
+    sp = _stream_here(stream, dev)
+    if sp is None:
         with _on(dev):
             return paged_blocks_release(block_tables, context_lens, finished, free_blocks, num_free, block_size,
                                         new_context_lens, new_num_free, num_blocks,
                                         stream or torch.cuda.current_stream(dev))
-    cap = free_blocks.shape[0]
-    rc = _lib.pa_paged_blocks_release(block_tables.data_ptr(), mb, context_lens.data_ptr(), out_lens.data_ptr(),
-                                      finished.data_ptr(), B, free_blocks.data_ptr(), cap, num_free.data_ptr(),
-                                      out_free.data_ptr(), int(block_size), int(cap if num_blocks is None else num_blocks),
-                                      _stream_ptr(stream, dev))
+    rc = _packed(_release_words(sp, block_tables.data_ptr(), mb, context_lens.data_ptr(),
+                                out_lens.data_ptr(), finished.data_ptr(), B, free_blocks.data_ptr(), cap,
+                                num_free.data_ptr(), out_free.data_ptr(), int(block_size), int(cap if num_blocks is
+                                None else num_blocks)))
     if rc:
         _check(rc, "pa_paged_blocks_release")
 
@@ -1056,35 +1112,41 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | No
     return f / scale * (1.0 - keep) + f * keep
 
 
-def _rows_of(t, name, T, heads, d, dtype, dev) -> int:
+def _rows_of(t, name, shape, dtype, dev) -> int:
     """Checks rows [T, heads, d] that may be strided over T; the stride."""
     if t.device != dev or t.dtype != dtype:
-        _cuda(t, name, dtype, dev)
-    if t.shape != (T, heads, d):
-        raise ValueError(f"{name} must be [{T}, {heads}, {d}]")
+        if not t.is_cuda or t.device != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
     row, head, one = t.stride()
-    if T <= 1:
-        row = heads * d
+    T, heads, d = shape
     if one != 1 or (head != d and heads > 1) or row < 0:
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return row
+    return row if T > 1 else heads * d
 
 
 def _rotary_args(q_out, q, k, positions, inv_freq, dev):
     """Checks what both rotary calls take; (T, H, Hk, D, rotary_dim, strides of q_out, q and k)."""
     torch = _torch()
+    dt, shape = q.dtype, q.shape
     if not q.is_cuda:
         _cuda(q, "q")
-    if q.dim() != 3 or (k is not None and k.dim() != 3):
+    if len(shape) != 3 or (k is not None and k.dim() != 3):
         raise ValueError("q must be [T, H, head_dim] and k [T, Hk, head_dim]")
-    T, H, D = q.shape
-    _all_cuda(dev, (positions, "positions", torch.int32), (inv_freq, "inv_freq", torch.float64))
-    if positions.shape != (T,) or inv_freq.dim() != 1:
+    T, H, D = shape
+    if not (positions.device == dev and positions.dtype == torch.int32 and positions.is_contiguous() and
+            inv_freq.device == dev and inv_freq.dtype == torch.float64 and inv_freq.is_contiguous()):
+        _all_cuda(dev, (positions, "positions", torch.int32), (inv_freq, "inv_freq", torch.float64))
+    freqs = inv_freq.shape
+    if positions.shape != (T,) or len(freqs) != 1:
         raise ValueError("positions must be [T] and inv_freq [rotary_dim / 2]")
-    hk = 0 if k is None else k.shape[1]
-    ks = 0 if k is None else _rows_of(k, "k", T, hk, D, q.dtype, dev)
-    return (T, H, hk, D, 2 * inv_freq.shape[0], _rows_of(q_out, "q_out", T, H, D, q.dtype, dev),
-            _rows_of(q, "q", T, H, D, q.dtype, dev), ks)
+    hk, ks = 0, 0
+    if k is not None:
+        hk = k.shape[1]
+        ks = _rows_of(k, "k", (T, hk, D), dt, dev)
+    return T, H, hk, D, 2 * freqs[0], _rows_of(q_out, "q_out", shape, dt, dev), _rows_of(q, "q", shape, dt, dev), ks
 
 
 def rotary_embedding(q_out, k_out, q, k, positions, inv_freq, factor: float = 1.0, interleaved: bool = False,
@@ -1099,15 +1161,16 @@ def rotary_embedding(q_out, k_out, q, k, positions, inv_freq, factor: float = 1.
     T, H, hk, D, rd, qos, qs, ks = _rotary_args(q_out, q, k, positions, inv_freq, dev)
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out must both be given, or neither")
-    kos = 0 if k is None else _rows_of(k_out, "k_out", T, hk, D, q.dtype, dev)
-    if _elsewhere(dev):
+    kos = 0 if k is None else _rows_of(k_out, "k_out", (T, hk, D), q.dtype, dev)
+    sp = _stream_here(stream, dev)
+    if sp is None:
         with _on(dev):
             return rotary_embedding(q_out, k_out, q, k, positions, inv_freq, factor, interleaved,
-                                    stream or _torch().cuda.current_stream(dev))
-    rc = _lib.pa_rotary_embedding(q_out.data_ptr(), qos, None if k is None else k_out.data_ptr(), kos, q.data_ptr(), qs,
-                                  None if k is None else k.data_ptr(), ks, positions.data_ptr(), inv_freq.data_ptr(),
-                                  float(factor), int(interleaved), T, H, hk, D, rd, _dtype_code(q),
-                                  _stream_ptr(stream, dev))
+                                    stream or _torch_module.cuda.current_stream(dev))
+    rc = _packed(_rotary_words(sp, q_out.data_ptr(), qos, 0 if k is None else
+                               k_out.data_ptr(), kos, q.data_ptr(), qs, 0 if k is None else k.data_ptr(), ks,
+                               positions.data_ptr(), inv_freq.data_ptr(), float(factor), int(interleaved), T, H, hk,
+                               D, rd, _dtype_code(q)))
     if rc:
         _check(rc, "pa_rotary_embedding")
 
@@ -1118,24 +1181,27 @@ def paged_kv_write_rotary(q_out, q, k, v, positions, inv_freq, slot_mapping, key
     value_cache [NB, bs, Hk, D], at slot_mapping[T] as paged_kv_write, in one launch."""
     dev, dt = key_cache.device, key_cache.dtype
     T, H, hk, D, rd, qos, qs, ks = _rotary_args(q_out, q, k, positions, inv_freq, dev)
-    vs = _rows_of(v, "v", T, hk, D, dt, dev)
-    _all_cuda(dev, (slot_mapping, "slot_mapping", _torch_module.int32), (key_cache, "key_cache", dt),
-              (value_cache, "value_cache", dt))
     if q.dtype != dt:
         raise TypeError(f"q must be {dt}, got {q.dtype}")
+    vs, i32 = _rows_of(v, "v", (T, hk, D), dt, dev), _torch_module.int32
+    if not (slot_mapping.device == dev and slot_mapping.dtype == i32 and slot_mapping.is_contiguous() and
+            key_cache.is_contiguous() and value_cache.device == dev and value_cache.dtype == dt and
+            value_cache.is_contiguous()):
+        _all_cuda(dev, (slot_mapping, "slot_mapping", i32), (key_cache, "key_cache", dt), (value_cache, "value_cache", dt))
     shape = key_cache.shape
     if len(shape) != 4 or value_cache.shape != shape or shape[2] != hk or shape[3] != D:
         raise ValueError(f"key_cache and value_cache must be [num_blocks, block_size, {hk}, {D}]")
     if slot_mapping.shape != (T,):
         raise ValueError("slot_mapping must be [T]")
-    if _elsewhere(dev):
+    sp = _stream_here(stream, dev)
+    if sp is None:
         with _on(dev):
             return paged_kv_write_rotary(q_out, q, k, v, positions, inv_freq, slot_mapping, key_cache, value_cache,
-                                         factor, interleaved, stream or _torch().cuda.current_stream(dev))
-    rc = _lib.pa_paged_kv_write_rotary(q_out.data_ptr(), qos, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-                                       positions.data_ptr(), inv_freq.data_ptr(), float(factor), int(interleaved),
-                                       slot_mapping.data_ptr(), T, key_cache.data_ptr(), value_cache.data_ptr(),
-                                       shape[0], shape[1], H, hk, D, rd, _dtype_code(q), _stream_ptr(stream, dev))
+                                         factor, interleaved, stream or _torch_module.cuda.current_stream(dev))
+    rc = _packed(_write_rotary_words(sp, q_out.data_ptr(), qos, q.data_ptr(), qs, k.data_ptr(),
+                                     ks, v.data_ptr(), vs, positions.data_ptr(), inv_freq.data_ptr(), float(factor),
+                                     int(interleaved), slot_mapping.data_ptr(), T, key_cache.data_ptr(),
+                                     value_cache.data_ptr(), shape[0], shape[1], H, hk, D, rd, _dtype_code(q)))
     if rc:
         _check(rc, "pa_paged_kv_write_rotary")
 
@@ -1168,18 +1234,19 @@ def paged_kv_write_fp8_block(k, v, slot_mapping, key_cache, value_cache, kv_scal
     block stand next to each other in slot_mapping."""
     dev = key_cache.device
     nb, hk, bs, d = _fp8_block_caches(key_cache, value_cache, kv_scales, dev)
-    if slot_mapping.dim() != 1:
-        raise ValueError("slot_mapping must be [T]")
-    T = slot_mapping.shape[0]
-    ks, vs = _rows_of(k, "k", T, hk, d, k.dtype, dev), _rows_of(v, "v", T, hk, d, k.dtype, dev)
-    _all_cuda(dev, (slot_mapping, "slot_mapping", _torch_module.int32))
-    if _elsewhere(dev):
+    if not (slot_mapping.device == dev and slot_mapping.dtype == _torch_module.int32 and slot_mapping.is_contiguous()):
+        _cuda(slot_mapping, "slot_mapping", _torch_module.int32, dev)
+    (T,), dt = _lengths("slot_mapping [T]", slot_mapping), k.dtype
+    rows = (T, hk, d)
+    ks, vs = _rows_of(k, "k", rows, dt, dev), _rows_of(v, "v", rows, dt, dev)
+    sp = _stream_here(stream, dev)
+    if sp is None:
         with _on(dev):
             return paged_kv_write_fp8_block(k, v, slot_mapping, key_cache, value_cache, kv_scales,
-                                            stream or _torch().cuda.current_stream(dev))
-    rc = _lib.pa_paged_kv_write_fp8_block(k.data_ptr(), ks, v.data_ptr(), vs, slot_mapping.data_ptr(), T,
-                                          key_cache.data_ptr(), value_cache.data_ptr(), kv_scales.data_ptr(), nb, bs, hk,
-                                          d, _dtype_code(k), _stream_ptr(stream, dev))
+                                            stream or _torch_module.cuda.current_stream(dev))
+    rc = _packed(_write_block_words(sp, k.data_ptr(), ks, v.data_ptr(), vs,
+                                    slot_mapping.data_ptr(), T, key_cache.data_ptr(), value_cache.data_ptr(),
+                                    kv_scales.data_ptr(), nb, bs, hk, d, _dtype_code(k)))
     if rc:
         _check(rc, "pa_paged_kv_write_fp8_block")
 
@@ -1190,13 +1257,14 @@ def paged_kv_read_fp8_block(k, v, slot_mapping, key_cache, value_cache, kv_scale
     dev = key_cache.device
     nb, hk, bs, d = _fp8_block_caches(key_cache, value_cache, kv_scales, dev)
     T = _int4_rows(k, v, slot_mapping, hk, d, dev)
-    if _elsewhere(dev):
+    sp = _stream_here(stream, dev)
+    if sp is None:
         with _on(dev):
             return paged_kv_read_fp8_block(k, v, slot_mapping, key_cache, value_cache, kv_scales,
-                                           stream or _torch().cuda.current_stream(dev))
-    rc = _lib.pa_paged_kv_read_fp8_block(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), T, key_cache.data_ptr(),
-                                         value_cache.data_ptr(), kv_scales.data_ptr(), nb, bs, hk, d, _dtype_code(k),
-                                         _stream_ptr(stream, dev))
+                                           stream or _torch_module.cuda.current_stream(dev))
+    rc = _packed(_read_block_words(sp, k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), T,
+                                   key_cache.data_ptr(), value_cache.data_ptr(), kv_scales.data_ptr(), nb, bs, hk, d,
+                                   _dtype_code(k)))
     if rc:
         _check(rc, "pa_paged_kv_read_fp8_block")
 
@@ -1218,22 +1286,21 @@ def paged_attention_decode_fp8_block(out, q, key_cache, value_cache, kv_scales, 
     dev = key_cache.device
     nb, hk, bs, d = _fp8_block_caches(key_cache, value_cache, kv_scales, dev)
     B, H, mb = _decode_args(out, q, block_tables, context_lens, d, dev, q.dtype, max_context_len)
-    if _elsewhere(dev):
+    sp = _stream_here(stream, dev)
+    if sp is None:
         with _on(dev):
             return paged_attention_decode_fp8_block(out, q, key_cache, value_cache, kv_scales, block_tables,
                                                     context_lens, scale, max_context_len, workspace,
-                                                    stream or _torch().cuda.current_stream(dev))
-    sp = _stream_ptr(stream, dev)
+                                                    stream or _torch_module.cuda.current_stream(dev))
     if workspace is None:
         workspace = _workspace(dev, sp, _memo(decode_fp8_block_workspace_bytes, B, H, hk, d, max_context_len or mb * bs,
                                               dev.index))
     else:
         _cuda(workspace, "workspace", _torch_module.uint8, dev)
-    rc = _lib.pa_paged_attention_decode_fp8_block(out.data_ptr(), q.data_ptr(), key_cache.data_ptr(),
-                                                  value_cache.data_ptr(), kv_scales.data_ptr(), block_tables.data_ptr(),
-                                                  mb, context_lens.data_ptr(), B, H, hk, d, bs, nb, float(scale),
-                                                  int(max_context_len), workspace.data_ptr(), workspace.numel(),
-                                                  _dtype_code(q), sp)
+    rc = _packed(_decode_block_words(sp, out.data_ptr(), q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                                     kv_scales.data_ptr(), block_tables.data_ptr(), mb, context_lens.data_ptr(), B, H,
+                                     hk, d, bs, nb, float(scale), int(max_context_len), workspace.data_ptr(),
+                                     workspace.numel(), _dtype_code(q)))
     if rc:
         _check(rc, "pa_paged_attention_decode_fp8_block")
 

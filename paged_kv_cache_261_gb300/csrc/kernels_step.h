@@ -26,7 +26,7 @@ struct BlocksAppendParams {
     int64_t num_blocks, table_tokens;   // table_tokens: max_blocks * block_size
     int num_seqs, max_blocks, free_cap, num_tokens, log2_block_size;
 };
-int launch_blocks_append(const BlocksAppendParams &p, cudaStream_t stream);
+int launch_blocks_append(const BlocksAppendParams &p, int sms, cudaStream_t stream);
 
 struct BlocksReleaseParams {
     const int32_t *block_tables;

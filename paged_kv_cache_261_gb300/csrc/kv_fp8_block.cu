@@ -7,48 +7,105 @@
 // for K and one for V; a channel stands for code * scale. The scatter makes a scale the
 // smallest power of two 2^e, e >= -100, for which the largest finite magnitude in the block is
 // at most 448 * 2^e (E4M3 is a floating-point format, so a scale between two powers of two would
-// buy no precision, and dividing by a power of two is exact). When new tokens make it grow, the
+// buy no precision, and dividing by a power of two is exact; a foreign scale becomes the next
+// power of two). When new tokens make it grow, the
 // codes that the block held are re-encoded: exact, but for those that come to lie below E4M3's
 // normal numbers. A call that writes a block's first slot starts the block anew: what else it
 // held, its scales too, counts no more.
 //
 // Tokens of one block stand next to each other in slot_mapping, so a block's new tokens are a
 // run of it, which starts where the block of the token before is another. A team of warps takes
-// a run of one kv head and of K or V: it finds the run's largest magnitude, then the scale,
-// re-encodes the block's older codes where the scale grew, and writes the new ones. (Atomic
-// maxima over all tokens, whatever their order, would need the old scales kept beside the new
-// ones and two more launches.)
+// a run of one kv head and of K or V: it reads the run's rows into registers, finds their largest
+// magnitude, then the scale, re-encodes the block's older codes where the scale grew, and writes
+// the new ones. A run of a single token (a decode step's) takes the lanes of one row, several
+// side by side in a warp. (Atomic maxima over all tokens, whatever their order, would need the
+// old scales kept beside the new ones and two more launches.)
 #include "common.cuh"
 #include "kernels_fp8_block.h"
+
+#include <algorithm>
+#include <type_traits>
 
 namespace pa {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kKeep = 4;                         // rows of a lane held in registers
 constexpr int kMinScaleExp = -100;
+constexpr int kWriteCtas = 4;                    // of the scatter, on an SM
+constexpr int64_t kFewTokens = 1024;             // written with a warp for a few rows each
+// Channels per lane in reading: more where there are enough rows to fill the SMs all the same.
+constexpr int kFewChannels = 8, kManyChannels = 32;
+constexpr int64_t kManyRows = 4096;              // (token, kv head) pairs
 
-// 16 channels of a row as floats.
-template <typename T> __device__ __forceinline__ void load16(const T *src, float *x) {
-    constexpr int N = Vec16<T>::N;
+template <typename T2> __device__ __forceinline__ T2 as2(uint32_t u) { return *reinterpret_cast<T2 *>(&u); }
+template <typename T2> __device__ __forceinline__ uint32_t bits2(T2 v) { return *reinterpret_cast<uint32_t *>(&v); }
+// The largest magnitude of some 16-bit (packed maxima) or float32 channels; NaN is passed over.
+template <typename T2, int N> __device__ __forceinline__ uint32_t packed_largest(const uint4 (&raw)[N]) {
+    uint32_t a = 0;
 #pragma unroll
-    for (int u = 0; u < 16 / N; ++u) Vec16<T>::unpack(reinterpret_cast<const uint4 *>(src)[u], x + u * N);
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (uint32_t w : {raw[i].x, raw[i].y, raw[i].z, raw[i].w})
+            a = bits2(__hmax2(as2<T2>(a), as2<T2>(w & 0x7FFF7FFFu)));
+    return bits2(__hmax2(as2<T2>(a), as2<T2>(__byte_perm(a, a, 0x1032))));
+}
+template <typename T, int N> __device__ __forceinline__ float largest_or_inf(const uint4 (&raw)[N]) {
+    if constexpr (sizeof(T) == 2) {
+        using T2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
+        return Elem<T>::to_f(as2<T2>(packed_largest<T2>(raw)).x);
+    } else {
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (uint32_t w : {raw[i].x, raw[i].y, raw[i].z, raw[i].w}) a = fmaxf(a, fabsf(__uint_as_float(w)));
+        return a;
+    }
 }
 
-// Codes of x[0..15] / scale (code i in byte i): nearest, ties to the even code, saturating at
-// +-448, NaN to a NaN code. inv: 1 / scale where scale is a power of two (the product is then
-// the quotient), else 0.
-__device__ __forceinline__ uint4 encode16(const float *x, float scale, float inv) {
-    float y[16];
+// 16 channels of a row as loaded.
+template <typename T> struct Run16 {
+    uint4 raw[sizeof(T)];
+    __device__ __forceinline__ void load(const T *src) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = inv != 0.f ? x[i] * inv : __fdiv_rn(x[i], scale);
+        for (int u = 0; u < (int)sizeof(T); ++u) raw[u] = reinterpret_cast<const uint4 *>(src)[u];
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int u = 0; u < (int)sizeof(T); ++u) raw[u] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void values(float *x) const {
+#pragma unroll
+        for (int u = 0; u < (int)sizeof(T); ++u) Vec16<T>::unpack(raw[u], x + u * Vec16<T>::N);
+    }
+    // the largest finite magnitude
+    __device__ __forceinline__ float largest() const {
+        float x[16], a = largest_or_inf<T>(raw);
+        if (a == INFINITY) {
+            values(x);
+            a = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
+        }
+        return a;
+    }
+};
+
+// Codes of x[0..15] * f (code i in byte i): nearest, ties to the even code, saturating at +-448,
+// NaN to a NaN code.
+__device__ __forceinline__ uint4 encode16(const float *x, float f) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        uint16_t lo, hi;
-        // the first source operand lands in the upper byte
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[4 * i + 1]), "f"(y[4 * i]));
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y[4 * i + 3]), "f"(y[4 * i + 2]));
-        w[i] = (uint32_t)lo | ((uint32_t)hi << 16);
+        // products in pairs; of a conversion, the first source operand lands in the upper byte
+        asm("{\n\t.reg .b64 a, b, s;\n\t.reg .f32 x0, x1, x2, x3;\n\t.reg .b16 lo, hi;\n\t"
+            "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tmov.b64 s, {%5, %5};\n\t"
+            "mul.rn.f32x2 a, a, s;\n\tmul.rn.f32x2 b, b, s;\n\tmov.b64 {x0, x1}, a;\n\tmov.b64 {x2, x3}, b;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 lo, x1, x0;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, x3, x2;\n\t"
+            "mov.b32 %0, {lo, hi};\n\t}"
+            : "=r"(w[i])
+            : "f"(x[4 * i]), "f"(x[4 * i + 1]), "f"(x[4 * i + 2]), "f"(x[4 * i + 3]), "f"(f));
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -69,31 +126,52 @@ __device__ __forceinline__ void decode16(const uint4 &c, float *x) {
     decode4(c.w, x + 12);
 }
 
-// The smallest 2^e, e >= kMinScaleExp, with amax <= 448 * 2^e = 1.75 * 2^(e + 8).
-__device__ __forceinline__ float scale_for(float amax) {
-    const uint32_t b = __float_as_uint(amax);
-    const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    return __uint_as_float((uint32_t)(max(e, kMinScaleExp) + 127) << 23);
-}
-// 1 / s where s is a power of two whose reciprocal is exact, else 0.
-__device__ __forceinline__ float exact_inverse(float s) {
-    const uint32_t b = __float_as_uint(s), e = b >> 23;
-    return (b & 0x7FFFFFu) == 0 && e >= 1 && e <= 253 ? __uint_as_float((254 - e) << 23) : 0.f;
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126..127
+
+// The exponent of the scale of a block whose new tokens have magnitudes up to amax: the smallest
+// e >= kMinScaleExp with amax <= 448 * 2^e = 1.75 * 2^(e + 8) and, where what the block holds under
+// the scale `old` counts, old <= 2^e. (2^126 has an exact normal reciprocal.)
+__device__ __forceinline__ int next_scale(float amax, float old, bool fresh, bool &held) {
+    const uint32_t b = __float_as_uint(amax), o = __float_as_uint(old);
+    const int e = max(kMinScaleExp, (int)(b >> 23) - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0));
+    held = !fresh && old > 0.f && old <= 0x1p126f;
+    return held ? max(e, (int)(o >> 23) - 127 + ((o & 0x7FFFFFu) != 0 ? 1 : 0)) : e;
 }
 
 // The block of a slot, or -1: no token.
-__device__ __forceinline__ int64_t block_of(const Fp8BlockCache &c, int64_t slot) {
+__device__ __forceinline__ int block_of(const Fp8BlockCache &c, int32_t slot) {
     return slot < 0 || slot >= c.num_slots ? -1 : slot >> c.log2_block_size;
 }
 
-// team: warps that share a run (a power of two, at most kWarps); chunk: tokens of
+// Re-encodes a block's rows first, first + step, ... of this lane's 16 channels, a few in flight
+// at once; codes: of row 0.
+template <int kLanes>
+__device__ __forceinline__ void reencode(uint4 *codes, int first, int step, int bs, float ratio) {
+    constexpr int kBatch = 4;
+#pragma unroll 1
+    for (int i0 = first; i0 < bs; i0 += kBatch * step) {
+        uint4 old[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (i0 + u * step < bs) old[u] = codes[(i0 + u * step) * kLanes];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (i0 + u * step >= bs) break;
+            float x[16];
+            decode16(old[u], x);
+            codes[(i0 + u * step) * kLanes] = encode16(x, ratio);
+        }
+    }
+}
+
+// 2^log2_team: warps that share a run (at most kWarps); chunk: tokens of
 // slot_mapping whose runs a CTA column takes (at most 32).
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads) void kv_write_fp8_block_kernel(const T *__restrict__ k, const T *__restrict__ v,
+__global__ __launch_bounds__(kThreads, kWriteCtas) void kv_write_fp8_block_kernel(const T *__restrict__ k, const T *__restrict__ v,
                                                                       int64_t k_stride, int64_t v_stride,
                                                                       const int32_t *__restrict__ slots,
                                                                       int64_t num_tokens, const Fp8BlockCache c,
-                                                                      int team, int chunk, unsigned int *err) {
+                                                                      int log2_team, int chunk, unsigned int *err) {
     constexpr int kLanes = D / 16, kRows = 32 / kLanes;   // lanes of a row; rows of a warp
     __shared__ float maxima[kWarps];
     // launched as a dependent of the kernel before; a kernel launched after this one may start
@@ -101,100 +179,185 @@ __global__ __launch_bounds__(kThreads) void kv_write_fp8_block_kernel(const T *_
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group = warp / team, member = warp - group * team, groups = kWarps / team;
-    const int row0 = member * kRows + lane / kLanes, part = (lane % kLanes) * 16;
-    const int row_step = team * kRows;
+    const int row = lane / kLanes, part = (lane % kLanes) * 16;
     const int Hk = c.num_kv_heads, bs = 1 << c.log2_block_size;
+    // the runs that start in this CTA's tokens, from a window of 64: whether a token has a block,
+    // continues the run of the token before, is its block's first
+    const int64_t t0 = (int64_t)blockIdx.x * chunk;
+    int32_t slot[2];
+    int block[2];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const int64_t t = t0 + 32 * w + lane;
+        slot[w] = t < num_tokens ? slots[t] : -1;
+        block[w] = block_of(c, slot[w]);
+    }
+    const int last = lane == 0 && t0 > 0 ? block_of(c, slots[t0 - 1]) : -1;
+    if (block[0] < 0 && slot[0] != -1 && lane < chunk && blockIdx.y == 0 && warp == 0) raise_error(err, PA_DEVERR_SLOT);
+    uint64_t goes_on = 0, firsts = 0;
+    uint32_t starts = 0;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        int before = __shfl_up_sync(0xffffffffu, block[w], 1);
+        const int end = __shfl_sync(0xffffffffu, block[0], 31);
+        if (lane == 0) before = w == 0 ? last : end;
+        goes_on |= (uint64_t)__ballot_sync(0xffffffffu, block[w] >= 0 && block[w] == before) << (32 * w);
+        firsts |= (uint64_t)__ballot_sync(0xffffffffu, block[w] >= 0 && (slot[w] & (bs - 1)) == 0) << (32 * w);
+        if (w == 0) starts = __ballot_sync(0xffffffffu, block[0] >= 0 && block[0] != before && lane < chunk);
+    }
+    // a slot of the window's token i (each lane asks for its own)
+    auto slot_at = [&](int i) {
+        const int32_t lo = __shfl_sync(0xffffffffu, slot[0], i & 31), hi = __shfl_sync(0xffffffffu, slot[1], i & 31);
+        return i < 32 ? lo : hi;
+    };
+
+    const int units = 2 * Hk, quads = (units + kRows - 1) / kRows;   // of a run: (kv head, K or V)
+    const int warps = gridDim.y * kWarps, my_warp = blockIdx.y * kWarps + warp;
+    const int team = 1 << log2_team, group = warp >> log2_team, member = warp & (team - 1);
+    const int teams = warps >> log2_team, my_team = my_warp >> log2_team;
     auto sync = [&] {
         if (team == 1) __syncwarp();
         else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(team * 32) : "memory");
     };
-
-    // the runs that start in this CTA's tokens
-    const int64_t t0 = (int64_t)blockIdx.x * chunk;
-    uint32_t starts;
-    {
-        const int64_t t = t0 + lane;
-        const bool in = lane < chunk && t < num_tokens;
-        const int64_t slot = in ? slots[t] : -1, b = block_of(c, slot);
-        if (in && b < 0 && slot != -1 && blockIdx.y == 0 && warp == 0) raise_error(err, PA_DEVERR_SLOT);
-        starts = __ballot_sync(0xffffffffu, b >= 0 && (t == 0 || block_of(c, slots[t - 1]) != b));
-    }
-    const int64_t units = (int64_t)__popc(starts) * Hk * 2;
-    for (int64_t u = (int64_t)blockIdx.y * groups + group; u < units; u += (int64_t)gridDim.y * groups) {
-        const int r = (int)(u / (2 * Hk)), kvh = (int)(u - (int64_t)r * 2 * Hk) >> 1;
-        const bool is_v = u & 1;
-        uint32_t m = starts;
-        for (int i = 0; i < r; ++i) m &= m - 1;
-        const int64_t first = t0 + __ffs(m) - 1, block = block_of(c, slots[first]);
-        // its length, and whether it starts the block
-        int64_t n = 0;
-        bool fresh = false;
-        for (int len = 32; len == 32; n += len) {
-            const int64_t t = first + n + lane;
-            const int64_t slot = t < num_tokens ? slots[t] : -1;
-            const uint32_t other = ~__ballot_sync(0xffffffffu, block_of(c, slot) == block);
-            len = other ? __ffs(other) - 1 : 32;
-            fresh |= __any_sync(0xffffffffu, lane < len && (slot & (bs - 1)) == 0);
-        }
-        const T *src = (is_v ? v + first * v_stride : k + first * k_stride) + kvh * D + part;
-        const int64_t stride = is_v ? v_stride : k_stride;
-        float amax = 0.f;
-        for (int64_t i = row0; i < n; i += row_step) {
-            float x[16];
-            load16(src + i * stride, x);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const float a = fabsf(x[j]);
-                amax = fmaxf(amax, a < INFINITY ? a : 0.f);
+    int turn = 0;                                      // runs are dealt from one warp on to the next
+    for (; starts; starts &= starts - 1) {
+        const int s = __ffs(starts) - 1;
+        const int64_t first = t0 + s;
+        const int b = slot_at(s) >> c.log2_block_size;
+        // tokens of the run that the window shows, and beyond it
+        int n = __ffsll((long long)~(goes_on >> (s + 1)));
+        bool fresh = (firsts >> s & (~0ull >> (64 - n))) != 0;
+        if (s + n == 64) {
+            for (int len = 32; len == 32; n += len) {
+                const int64_t t = first + n + lane;
+                const int32_t next = t < num_tokens ? slots[t] : -1;
+                const uint32_t other = ~__ballot_sync(0xffffffffu, block_of(c, next) == b);
+                len = other ? __ffs(other) - 1 : 32;
+                fresh |= __any_sync(0xffffffffu, lane < len && (next & (bs - 1)) == 0);
             }
         }
+        if (n == 1) {
+            // a unit for each row of the warp
+            const int off = slot_at(s) & (bs - 1);
+#pragma unroll 1
+            for (int q = my_warp - turn + (my_warp < turn ? warps : 0); q < quads; q += warps) {
+                const int u = q * kRows + row;
+                const bool live = u < units, is_v = u & 1;
+                const int kvh = min(u >> 1, Hk - 1);
+                float *scale_at = reinterpret_cast<float *>(c.scales + ((int64_t)b * Hk + kvh)) + is_v;
+                Run16<T> x;
+                x.load((is_v ? v + first * v_stride : k + first * k_stride) + kvh * D + part);
+                const float old = *scale_at;
+                float amax = x.largest();
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        float *scale_at = reinterpret_cast<float *>(c.scales + block * Hk + kvh) + is_v;
-        const float old = *scale_at;
-        if (lane == 0) maxima[warp] = amax;
-        sync();
-        for (int w = 0; w < team; ++w) amax = fmaxf(amax, maxima[group * team + w]);
-        const bool held = !fresh && old > 0.f && old < INFINITY;
-        const float scale = held ? fmaxf(old, scale_for(amax)) : scale_for(amax), inv = exact_inverse(scale);
-        uint4 *codes = reinterpret_cast<uint4 *>(static_cast<unsigned char *>(is_v ? c.value : c.key) +
-                                                 ((block * Hk + kvh) << c.log2_block_size) * D + part);
-        if (held && scale > old) {
-            const float ratio = __fdiv_rn(old, scale);
-            for (int i = row0; i < bs; i += row_step) {
-                float x[16];
-                decode16(codes[i * kLanes], x);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] *= ratio;
-                codes[i * kLanes] = encode16(x, 1.f, 1.f);
+                for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                bool held;
+                const int e = next_scale(amax, old, fresh, held);
+                const float scale = pow2f(e);
+                uint4 *codes = reinterpret_cast<uint4 *>(static_cast<unsigned char *>(is_v ? c.value : c.key) +
+                                                         (((int64_t)b * Hk + kvh) << c.log2_block_size) * D + part);
+                // the older codes of these units, each by the whole warp
+                uint32_t grown = __ballot_sync(0xffffffffu, live && held && scale > old && part == 0);
+                for (; grown; grown &= grown - 1) {
+                    const int from = __ffs(grown) - 1;
+                    const uint64_t at = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(codes), from);
+                    const float ratio = __shfl_sync(0xffffffffu, old * pow2f(-e), from);
+                    reencode<kLanes>(reinterpret_cast<uint4 *>(at + part), row, kRows, bs, ratio);
+                }
+                __syncwarp();                          // older codes before new ones
+                if (live) {
+                    float y[16];
+                    x.values(y);
+                    codes[off * kLanes] = encode16(y, pow2f(-e));
+                    if (part == 0) *scale_at = scale;
+                }
             }
+            for (turn += quads; turn >= warps;) turn -= warps;
+            continue;
         }
-        sync();                                        // older codes before new ones; the old scale is read
-        for (int64_t i = row0; i < n; i += row_step) {
-            float x[16];
-            load16(src + i * stride, x);
-            codes[(slots[first + i] & (bs - 1)) * kLanes] = encode16(x, scale, inv);
+#pragma unroll 1
+        for (int u = my_team - (turn >> log2_team) + (my_team < turn >> log2_team ? teams : 0); u < units; u += teams) {
+            const bool is_v = u & 1;
+            const int kvh = u >> 1;
+            const T *src = (is_v ? v + first * v_stride : k + first * k_stride) + kvh * D + part;
+            const int64_t stride = is_v ? v_stride : k_stride;
+            const int row0 = member * kRows + row, step = team * kRows;
+            Run16<T> x[kKeep];
+            int off[kKeep];
+            float *scale_at = reinterpret_cast<float *>(c.scales + ((int64_t)b * Hk + kvh)) + is_v;
+            const float old = *scale_at;
+#pragma unroll
+            for (int j = 0; j < kKeep; ++j) {
+                const int i = row0 + j * step;
+                x[j].clear();
+                if (i < n) x[j].load(src + i * stride);
+            }
+#pragma unroll
+            for (int j = 0; j < kKeep; ++j) {
+                const int i = row0 + j * step;
+                const int32_t in_window = slot_at(min(s + i, 63));
+                off[j] = i >= n ? -1 : (s + i < 64 ? in_window : slots[first + i]) & (bs - 1);
+            }
+            float amax = 0.f;
+#pragma unroll
+            for (int j = 0; j < kKeep; ++j) amax = fmaxf(amax, x[j].largest());
+#pragma unroll 1
+            for (int i = row0 + kKeep * step; i < n; i += step) {   // a long run of a large block
+                Run16<T> more;
+                more.load(src + i * stride);
+                amax = fmaxf(amax, more.largest());
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            if (team > 1) {
+                if (lane == 0) maxima[warp] = amax;
+                sync();
+                for (int w = 0; w < team; ++w) amax = fmaxf(amax, maxima[group * team + w]);
+            }
+            bool held;
+            const int e = next_scale(amax, old, fresh, held);
+            const float scale = pow2f(e), inv = pow2f(-e);
+            uint4 *codes = reinterpret_cast<uint4 *>(static_cast<unsigned char *>(is_v ? c.value : c.key) +
+                                                     (((int64_t)b * Hk + kvh) << c.log2_block_size) * D + part);
+            if (held && scale > old) reencode<kLanes>(codes, row0, step, bs, old * inv);
+            sync();                                    // older codes before new ones; maxima and the old scale are read
+#pragma unroll
+            for (int j = 0; j < kKeep; ++j) {
+                float y[16];
+                x[j].values(y);
+                if (off[j] >= 0) codes[off[j] * kLanes] = encode16(y, inv);
+                asm volatile("" ::: "memory");         // one row after the other, for fewer registers
+            }
+#pragma unroll 1
+            for (int i = row0 + kKeep * step; i < n; i += step) {
+                Run16<T> more;
+                more.load(src + i * stride);
+                float y[16];
+                more.values(y);
+                codes[(slots[first + i] & (bs - 1)) * kLanes] = encode16(y, inv);
+            }
+            if (member == 0 && lane == 0) *scale_at = scale;
         }
-        if (member == 0 && lane == 0) *scale_at = scale;
+        for (turn += units << log2_team; turn >= warps;) turn -= warps;
     }
 }
 
-template <typename T> __device__ __forceinline__ void store16(T *dst, const float *x) {
-    alignas(16) T v[16];
+template <typename T> __device__ __forceinline__ void store8(T *dst, const float *x) {
+    alignas(16) T v[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = Elem<T>::from_f(x[i]);
+    for (int i = 0; i < 8; ++i) v[i] = Elem<T>::from_f(x[i]);
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T); ++i) reinterpret_cast<uint4 *>(dst)[i] = reinterpret_cast<const uint4 *>(v)[i];
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4 *>(dst)[i] = reinterpret_cast<const uint4 *>(v)[i];
 }
 
-// A lane has 16 channels of a row; a K row and its V row are side by side.
-template <typename T, int D>
+// Reading: a lane has kCh channels of a row, in words of 8 a row's lanes apart, so that loads and
+// stores of a warp are contiguous; a K row and its V row are side by side.
+template <typename T, int D, int kCh>
 __global__ __launch_bounds__(kThreads) void kv_read_fp8_block_kernel(T *__restrict__ k, T *__restrict__ v,
                                                                      const int32_t *__restrict__ slots,
                                                                      uint32_t num_tokens, const Fp8BlockCache c,
                                                                      unsigned int *err) {
-    constexpr int kLanes = D / 16, kPairs = kThreads / kLanes / 2;
+    constexpr int kLanes = D / kCh, kWords = kCh / 8, kPairs = kThreads / kLanes / 2;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int part = threadIdx.x % kLanes;
@@ -203,20 +366,29 @@ __global__ __launch_bounds__(kThreads) void kv_read_fp8_block_kernel(T *__restri
     const uint32_t t = th / (uint32_t)c.num_kv_heads;
     const int h = (int)(th - t * c.num_kv_heads);
     if (t >= num_tokens) return;
-    const int64_t slot = slots[t], block = block_of(c, slot);
+    const int32_t slot = slots[t];
+    const int64_t block = block_of(c, slot);
     if (block < 0) {
         if (slot != -1 && part == 0 && h == 0 && !is_v) raise_error(err, PA_DEVERR_SLOT);
         return;
     }
     const int64_t run = block * c.num_kv_heads + h;
     const int64_t row = (run << c.log2_block_size) + (slot & ((1 << c.log2_block_size) - 1));
-    const float2 s = c.scales[run];
-    const float scale = is_v ? s.y : s.x;
-    float x[16];
-    decode16(__ldcs(static_cast<const uint4 *>(is_v ? c.value : c.key) + row * kLanes + part), x);
+    const uint2 *src = static_cast<const uint2 *>(is_v ? c.value : c.key) + row * (D / 8) + part;
+    uint2 codes[kWords];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] *= scale;
-    store16((is_v ? v : k) + (int64_t)th * D + part * 16, x);
+    for (int w = 0; w < kWords; ++w) codes[w] = __ldcs(src + w * kLanes);
+    const float scale = reinterpret_cast<const float *>(c.scales + run)[is_v];
+    T *dst = (is_v ? v : k) + (int64_t)th * D + part * 8;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+        float x[8];
+        decode4(codes[w].x, x);
+        decode4(codes[w].y, x + 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= scale;
+        store8(dst + w * kLanes * 8, x);
+    }
 }
 
 // scales[dst] = scales[src] for each pair of blocks.
@@ -235,22 +407,30 @@ __global__ __launch_bounds__(kThreads) void copy_scales_kernel(float2 *scales, c
 template <typename T, int D>
 int write_t(const void *k, const void *v, int64_t ks, int64_t vs, const int32_t *slots, int64_t n,
             const Fp8BlockCache &c, unsigned int *err, cudaStream_t s) {
-    // a warp per 16 rows of a block
-    const int team = std::max(1, std::min(kWarps, (1 << c.log2_block_size) / 16));
-    const int chunk = 32;
-    const int64_t units = (int64_t)chunk * 2 * c.num_kv_heads, groups = kWarps / team;
-    const int64_t x = (n + chunk - 1) / chunk;
-    const int64_t y = std::min<int64_t>((units + groups - 1) / groups, 2 * c.num_kv_heads);
-    return launch_pdl(kv_write_fp8_block_kernel<T, D>, dim3((unsigned)x, (unsigned)std::min<int64_t>(y, 65535)),
-                      dim3(kThreads), 0, s, (const T *)k, (const T *)v, ks, vs, slots, n, c, team, chunk, err);
+    constexpr int kRows = 32 / (D / 16);               // of a warp
+    // as many warps a team as hold a block's rows in registers
+    int log2_team = 0;
+    while (1 << log2_team < kWarps && kRows * kKeep << log2_team < 1 << c.log2_block_size) ++log2_team;
+    // Few tokens: a warp for each step of the work, if they are single ones. Many: columns of 32, with
+    // warps for half of the units of a run of as many (8 kv heads, us with half, all and twice the
+    // rows of CTAs: 16,384 tokens, blocks of 16 22.2, 23.8, 30.7; 8192, of 32 12.6, 12.1, 14.3; of 256, f32
+    // 65, 39, 26).
+    const int chunk = n <= kFewTokens ? 4 : 32, Hk = c.num_kv_heads;
+    const int64_t y = chunk == 4 ? ((2 * Hk + kRows - 1) / kRows * chunk + kWarps - 1) / kWarps
+                                 : ((Hk << log2_team) + 1) / 2;
+    return launch_pdl(kv_write_fp8_block_kernel<T, D>,
+                      dim3((unsigned)((n + chunk - 1) / chunk), (unsigned)std::min<int64_t>(y, 65535)), dim3(kThreads), 0,
+                      s, (const T *)k, (const T *)v, ks, vs, slots, n, c, log2_team, chunk, err);
 }
 
 template <typename T, int D>
 int read_t(void *k, void *v, const int32_t *slots, int64_t n, const Fp8BlockCache &c, unsigned int *err,
            cudaStream_t s) {
-    const int pairs = kThreads / (D / 16) / 2;         // of a CTA
-    return launch_pdl(kv_read_fp8_block_kernel<T, D>, dim3((unsigned)((n * c.num_kv_heads + pairs - 1) / pairs)),
-                      dim3(kThreads), 0, s, (T *)k, (T *)v, slots, (uint32_t)n, c, err);
+    const bool many = n * c.num_kv_heads >= kManyRows;
+    const int pairs = kThreads / (D / (many ? kManyChannels : kFewChannels)) / 2;   // of a CTA
+    return launch_pdl(many ? kv_read_fp8_block_kernel<T, D, kManyChannels> : kv_read_fp8_block_kernel<T, D, kFewChannels>,
+                      dim3((unsigned)((n * c.num_kv_heads + pairs - 1) / pairs)), dim3(kThreads), 0, s, (T *)k, (T *)v,
+                      slots, (uint32_t)n, c, err);
 }
 
 template <typename T>

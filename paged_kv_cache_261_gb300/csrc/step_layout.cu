@@ -11,10 +11,11 @@
 // in which requests served one after another would have popped them. Two prefix sums over the
 // requests (rows and needs) are all that connects the requests.
 //
-// One cluster does a call: every CTA of it takes the sums over all requests by itself (they are
-// few), and the tokens and blocks are dealt among all threads; a token finds its request by a
-// binary search of the sums in shared memory. The cluster's barrier stands between the last
-// read of the lengths and the first write of the new ones, which may be the same arrays.
+// Every CTA takes the sums over all requests by itself (they are few), and the tokens and blocks
+// are dealt among all threads; a token finds its request by a binary search of the sums in shared
+// memory. The new lengths may be written over the old, so their writer has to come after every
+// reader: one cluster does a whole call, its barrier between the two, or, where there are many
+// tokens, a second launch of one CTA takes the sums again and writes the lengths.
 // What bounds it is latency: a chain of loads, the sums, a barrier, a search, loads and stores.
 #include "common.cuh"
 #include "kernels_step.h"
@@ -26,14 +27,10 @@ namespace {
 
 constexpr int kMaxThreads = 1024;
 constexpr int kMaxCluster = 8;
-constexpr int kScratch = 68;                     // 64-bit words of the sums
-constexpr int kPerThread = 4;                    // tokens (or blocks) of a thread that the launch aims at
+constexpr int kScratch = 66;                     // 64-bit words of the sums
+constexpr int kPerThread = 4;                    // table entries of a thread that a release aims at
+constexpr int kClusterTokens = 8192;             // an append's tokens that one cluster takes
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -59,28 +56,14 @@ __device__ __forceinline__ Sums prefix_sums(Sums mine, int64_t *scratch, Sums &t
         scratch[2 * warp + 1] = inc.b;
     }
     __syncthreads();
-    if (warp == 0) {
-        Sums w{0, 0};
-        if (lane < warps) w = {scratch[2 * lane], scratch[2 * lane + 1]};
-        Sums s = w;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t a = __shfl_up_sync(0xffffffffu, s.a, o), b = __shfl_up_sync(0xffffffffu, s.b, o);
-            if (lane >= o) {
-                s.a += a;
-                s.b += b;
-            }
-        }
-        scratch[2 * lane] = s.a - w.a;
-        scratch[2 * lane + 1] = s.b - w.b;
-        if (lane == 31) {
-            scratch[64] = s.a;
-            scratch[65] = s.b;
-        }
+    total = {0, 0};
+    Sums before{0, 0};
+    for (int w = 0; w < warps; ++w) {
+        if (w == warp) before = total;
+        total.a += scratch[2 * w];
+        total.b += scratch[2 * w + 1];
     }
-    __syncthreads();
-    total = {scratch[64], scratch[65]};
-    return {scratch[2 * warp] + inc.a - mine.a, scratch[2 * warp + 1] + inc.b - mine.b};
+    return {before.a + inc.a - mine.a, before.b + inc.b - mine.b};
 }
 
 // The last b in [0, n) with first[b] <= x, for ascending first with first[0] <= x.
@@ -108,6 +91,12 @@ __device__ __forceinline__ int checked_block(int entry, int64_t num_blocks, unsi
     return -1;
 }
 
+// What a launch of blocks_append_kernel does: a whole call by one cluster; all of a call but the
+// lengths and the stack's height, by any number of CTAs; or these two, after such a launch.
+enum class Append { kCall, kMaps, kLengths };
+
+// G: tokens that a thread takes together.
+template <Append kWhat, int G>
 __global__ __launch_bounds__(kMaxThreads) void blocks_append_kernel(const BlocksAppendParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
     int64_t *scratch = reinterpret_cast<int64_t *>(smem);
@@ -115,11 +104,14 @@ __global__ __launch_bounds__(kMaxThreads) void blocks_append_kernel(const Blocks
     int *start = reinterpret_cast<int *>(scratch + kScratch);          // [B + 1] rows before a request
     int *taken = start + p.num_seqs + 1;                               // [B] blocks needed before it
     int *ctx = taken + p.num_seqs;                                     // [B] tokens held, -1: not served
-    // no early signal: a decode launched next reads the new lengths before it waits
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // No early signal but to the second launch of a call: a decode launched next reads the new
+    // lengths before it waits. That second launch reads what was there before the call, and
+    // waits before it writes.
+    if constexpr (kWhat != Append::kLengths) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if constexpr (kWhat == Append::kMaps) asm volatile("griddepcontrol.launch_dependents;");
     const int B = p.num_seqs, T = p.num_tokens, l2 = p.log2_block_size, bs = 1 << l2;
-    const uint32_t rank = cluster_rank(), gid = rank * blockDim.x + threadIdx.x, threads = gridDim.x * blockDim.x;
-    const bool report = rank == 0;
+    const uint32_t gid = blockIdx.x * blockDim.x + threadIdx.x, threads = gridDim.x * blockDim.x;
+    const bool report = blockIdx.x == 0 && kWhat != Append::kLengths;
     if (threadIdx.x == 0) *all_taken = 0;
     const int height = stack_height(p.num_free, p.free_cap, report && threadIdx.x == 0, p.err);
 
@@ -168,35 +160,75 @@ __global__ __launch_bounds__(kMaxThreads) void blocks_append_kernel(const Blocks
     if (mine_taken) atomicMax(all_taken, mine_taken);
     if (report && bits) raise_error(p.err, bits);
     __syncthreads();
-    cluster_sync();                              // every CTA has read the lengths and the height
+    // every CTA that reads the lengths and the height has done so
+    if constexpr (kWhat == Append::kCall) cluster_sync();
+    if constexpr (kWhat == Append::kLengths) asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    for (int b = gid; b <= B; b += threads) {
-        p.query_start_loc[b] = start[b];
-        if (b < B) p.new_context_lens[b] = ctx[b] >= 0 ? ctx[b] + start[b + 1] - start[b] : p.context_lens[b];
+    if constexpr (kWhat != Append::kMaps) {
+        for (int b = gid; b < B; b += threads)
+            p.new_context_lens[b] = ctx[b] >= 0 ? ctx[b] + start[b + 1] - start[b] : p.context_lens[b];
+        if (gid == 0) *p.new_num_free = height - *all_taken;
     }
-    if (gid == 0) *p.new_num_free = height - *all_taken;
-    // the entries of the blocks taken
-    for (int j = gid; j < *all_taken; j += threads) {
-        const int b = owner(taken, B, j), col = ((ctx[b] + bs - 1) >> l2) + j - taken[b];
-        p.block_tables[(int64_t)b * p.max_blocks + col] = checked_block(p.free_blocks[height - 1 - j], p.num_blocks, p.err);
-    }
-    // slots and positions
-    for (int t = gid, b = 0; t < T; t += threads) {
-        int slot = -1, pos = 0;
-        if (t < start[B]) {
-            b += owner(start + b, B - b, t);
-            const int c = ctx[b];
-            if (c >= 0) {
-                pos = c + t - start[b];
-                const int held = (c + bs - 1) >> l2, col = pos >> l2;
-                const int entry = col < held ? p.block_tables[(int64_t)b * p.max_blocks + col]
-                                             : p.free_blocks[height - 1 - (taken[b] + col - held)];
-                const int block = checked_block(entry, p.num_blocks, p.err);
-                slot = block < 0 ? -1 : (block << l2) + (pos & (bs - 1));
+    if constexpr (kWhat != Append::kLengths) {
+        for (int b = gid; b <= B; b += threads) p.query_start_loc[b] = start[b];
+        // the entries of the blocks taken
+        for (int j = gid; j < *all_taken; j += threads) {
+            const int b = owner(taken, B, j), col = ((ctx[b] + bs - 1) >> l2) + j - taken[b];
+            p.block_tables[(int64_t)b * p.max_blocks + col] = checked_block(p.free_blocks[height - 1 - j], p.num_blocks, p.err);
+        }
+        // Slots and positions, of G tokens in a row. Their entries are loaded together; tokens of one
+        // block load one.
+        const bool wide = ((reinterpret_cast<uintptr_t>(p.slot_mapping) | reinterpret_cast<uintptr_t>(p.positions)) & 15) == 0;
+        const int live = start[B];
+        for (int64_t t0 = (int64_t)gid * G; t0 < T; t0 += (int64_t)threads * G) {
+            alignas(16) int slot[G], pos[G];
+            const int32_t *from[G];                        // the place of a token's entry, null: none or as before
+            bool served[G];
+            int b = 0, next = 0, col = -1;                 // tokens before `next` are request b's; its last column
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                const int t = (int)t0 + i;                 // (T is below 2^31 - 65536)
+                pos[i] = 0;
+                from[i] = nullptr;
+                served[i] = false;
+                if (t >= live) continue;
+                if (t >= next) {
+                    b += owner(start + b, B - b, t);
+                    next = start[b + 1];
+                    col = -1;
+                }
+                const int c = ctx[b];
+                if (c < 0) continue;
+                served[i] = true;
+                pos[i] = c + t - start[b];
+                if (pos[i] >> l2 != col) {
+                    col = pos[i] >> l2;
+                    const int held = (c + bs - 1) >> l2;
+                    from[i] = col < held ? p.block_tables + (int64_t)b * p.max_blocks + col
+                                         : p.free_blocks + (height - 1 - (taken[b] + col - held));
+                }
+            }
+            int entry[G];
+#pragma unroll
+            for (int i = 0; i < G; ++i) entry[i] = from[i] ? *from[i] : 0;
+            int block = -1;
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                if (from[i]) block = checked_block(entry[i], p.num_blocks, p.err);
+                slot[i] = served[i] && block >= 0 ? (block << l2) + (pos[i] & (bs - 1)) : -1;
+            }
+            if (G == 4 && wide && t0 + G <= T) {
+                *reinterpret_cast<int4 *>(p.slot_mapping + t0) = *reinterpret_cast<int4 *>(slot);
+                *reinterpret_cast<int4 *>(p.positions + t0) = *reinterpret_cast<int4 *>(pos);
+            } else {
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+                    if (t0 + i < T) {
+                        p.slot_mapping[t0 + i] = slot[i];
+                        p.positions[t0 + i] = pos[i];
+                    }
             }
         }
-        p.slot_mapping[t] = slot;
-        p.positions[t] = pos;
     }
 }
 
@@ -208,8 +240,8 @@ __global__ __launch_bounds__(kMaxThreads) void blocks_release_kernel(const Block
     int *ctx = back + p.num_seqs;                                      // [B] its new length
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int B = p.num_seqs, l2 = p.log2_block_size, bs = 1 << l2;
-    const uint32_t rank = cluster_rank(), gid = rank * blockDim.x + threadIdx.x, threads = gridDim.x * blockDim.x;
-    const bool report = rank == 0;
+    const uint32_t gid = blockIdx.x * blockDim.x + threadIdx.x, threads = gridDim.x * blockDim.x;
+    const bool report = blockIdx.x == 0;
     if (threadIdx.x == 0) *all_back = 0;
     const int height = stack_height(p.num_free, p.free_cap, report && threadIdx.x == 0, p.err);
     const int room = p.free_cap - height;
@@ -265,14 +297,9 @@ __global__ __launch_bounds__(kMaxThreads) void blocks_release_kernel(const Block
     }
 }
 
-// One cluster with about kPerThread of `items` (and of the requests) a thread.
+// Launch of `ctas` CTAs, as one cluster or none.
 template <typename P>
-int launch_cluster(void (*kern)(P), const P &p, int64_t items, int words, cudaStream_t stream) {
-    const int64_t work = std::max<int64_t>(items, p.num_seqs);
-    const int threads = (int)std::min<int64_t>(kMaxThreads, std::max<int64_t>(128, (work + 127) / 128 * 128));
-    const int64_t want = (work + (int64_t)threads * kPerThread - 1) / ((int64_t)threads * kPerThread);
-    int ctas = 1;
-    while (ctas < kMaxCluster && ctas < want) ctas *= 2;
+int launch(void (*kern)(P), const P &p, int ctas, int threads, bool cluster, int words, cudaStream_t stream) {
     const size_t smem = kScratch * 8 + (size_t)words * 4;
     // (set on every call: the attribute is the device's own)
     if (smem > 48 * 1024 &&
@@ -290,18 +317,42 @@ int launch_cluster(void (*kern)(P), const P &p, int64_t items, int words, cudaSt
     attr[1].val.clusterDim.x = (unsigned)ctas;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = cluster ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? 0 : -1;
+}
+
+// Threads of a CTA for this much work, at least one for each request.
+int cta_threads(int64_t work, int num_seqs) {
+    return (int)std::min<int64_t>(kMaxThreads, std::max<int64_t>(128, (std::max<int64_t>(work, num_seqs) + 127) / 128 * 128));
+}
+int cluster_ctas(int64_t work, int threads) {
+    int ctas = 1;
+    while (ctas < kMaxCluster && (int64_t)ctas * threads < work) ctas *= 2;
+    return ctas;
 }
 
 }  // namespace
 
-int launch_blocks_append(const BlocksAppendParams &p, cudaStream_t stream) {
-    return launch_cluster(blocks_append_kernel, p, p.num_tokens, 3 * p.num_seqs + 1, stream);
+int launch_blocks_append(const BlocksAppendParams &p, int sms, cudaStream_t stream) {
+    const int T = p.num_tokens, words = 3 * p.num_seqs + 1;
+    if (T <= kClusterTokens) {
+        const int threads = cta_threads(T, p.num_seqs);
+        return launch(blocks_append_kernel<Append::kCall, 1>, p, cluster_ctas(T, threads), threads, true, words, stream);
+    }
+    const int threads = cta_threads(512, p.num_seqs);
+    const int64_t ctas = (T / 4 + threads - 1) / threads;
+    const int rc = launch(blocks_append_kernel<Append::kMaps, 4>, p, (int)std::min<int64_t>(sms, ctas), threads, false,
+                          words, stream);
+    if (rc != 0) return rc;
+    return launch(blocks_append_kernel<Append::kLengths, 1>, p, 1, cta_threads(0, p.num_seqs), false, words, stream);
 }
 
 int launch_blocks_release(const BlocksReleaseParams &p, cudaStream_t stream) {
-    return launch_cluster(blocks_release_kernel, p, 0, 2 * p.num_seqs, stream);
+    // a thread for every kPerThread entries that the tables could hold: which requests are
+    // finished is known on the device alone
+    const int64_t work = ((int64_t)p.num_seqs * p.max_blocks + kPerThread - 1) / kPerThread;
+    const int threads = cta_threads(work, p.num_seqs);
+    return launch(blocks_release_kernel, p, cluster_ctas(work, threads), threads, true, 2 * p.num_seqs, stream);
 }
 
 }  // namespace pa

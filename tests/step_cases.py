@@ -63,14 +63,14 @@ def write_blocks(kc, vc, sc, k, v, slots):
                 a = np.abs(new[np.isfinite(new)])
                 s = scale_for(a.max(initial=0.0))
                 old = float(sc[b, h, j])
-                if 0 not in off and 0 < old < np.inf:
-                    s = max(s, old)
+                if 0 not in off and 0 < old <= 2.0 ** 126:
+                    while s < old:
+                        s *= 2
                     if s > old:                       # the product in float32: scales may be foreign ones
                         with np.errstate(all="ignore"):
-                            x32 = E4M3[c[b, h]].astype(np.float32) * (np.float32(old) / np.float32(s))
+                            x32 = E4M3[c[b, h]].astype(np.float32) * np.float32(old / s)
                         c[b, h] = encode(x32)
-                with np.errstate(all="ignore"):
-                    c[b, h, off] = encode(new.astype(np.float32) / np.float32(s))
+                c[b, h, off] = encode(new / s)
                 sc[b, h, j] = s
 
 
