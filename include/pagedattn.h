@@ -748,22 +748,6 @@ int pa_paged_attention_decode_fp8_block(void *out, const void *q, const void *ke
                                         void *stream);
 
 /*
- * One of the calls above with its arguments in an array of 8-byte words: the call (PA_CALL_*), the
- * number of words after the third, the stream, and then the arguments in the order of the
- * declaration, pointers and integers as int64_t, floats as double. The same checks and results;
- * for bindings in which every argument of a call costs time (Python's ctypes, on the GPU's host:
- * 18 arguments 1.7 us, packed 0.4). A wrong call or number: PA_ERR_INVALID_ARG.
- */
-#define PA_CALL_BLOCKS_APPEND    1
-#define PA_CALL_BLOCKS_RELEASE   2
-#define PA_CALL_ROTARY_EMBEDDING 3
-#define PA_CALL_KV_WRITE_ROTARY  4
-#define PA_CALL_KV_WRITE_FP8_BLOCK 5
-#define PA_CALL_KV_READ_FP8_BLOCK  6
-#define PA_CALL_DECODE_FP8_BLOCK   7
-int pa_call_packed(const void *words);
-
-/*
  * Synchronise `stream`, then read and clear the current device's error word.
  * *bits receives the PA_DEVERR_* bits seen since the last call. Returns
  * PA_ERR_DEVICE_INDEX when any bit was set, PA_OK otherwise.

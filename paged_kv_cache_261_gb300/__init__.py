@@ -1,8 +1,8 @@
 """Paged KV cache decode path for GB300 (sm_103a): Python binding of libpagedattn.
 
 A thin ctypes layer over the C ABI in ``include/pagedattn.h``: it reads shapes,
-dtypes and pointers off torch tensors and calls the library. Every step of the
-computation runs in the library's CUDA kernels; there is no fallback. Importing
+dtypes and pointers off torch tensors and calls the library (the calls of a serving step
+through a small compiled module where that fits). Every step of the computation runs in the library's CUDA kernels; there is no fallback. Importing
 this package fails when ``_build/libpagedattn.so`` has not been built (run
 ``python paged_kv_cache_261_gb300/build.py``).
 
@@ -55,9 +55,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import functools
+import importlib.util
 import os
-import struct
 
 import numpy as np
 
@@ -148,25 +147,6 @@ _decl("pa_copy_blocks_fp8_block", [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _
 _decl("pa_decode_fp8_block_workspace_bytes", [_i32, _i32, _i32, _i32, _i32], _sz)
 _decl("pa_paged_attention_decode_fp8_block", [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32,
                                               _i64, _f, _i32, _vp, _sz, _i32, _vp])
-_decl("pa_call_packed", [ctypes.c_char_p])
-
-_packed = _lib.pa_call_packed
-
-
-def _words(call: int, name: str):
-    """Packs (stream, arguments of a call in the order of its declaration) for _packed."""
-    args = getattr(_lib, name).argtypes[:-1]
-    form = struct.Struct("3q" + "".join("d" if a is _f else "q" for a in args))
-    return functools.partial(form.pack, call, len(args))
-
-
-_append_words = _words(1, "pa_paged_blocks_append")
-_release_words = _words(2, "pa_paged_blocks_release")
-_rotary_words = _words(3, "pa_rotary_embedding")
-_write_rotary_words = _words(4, "pa_paged_kv_write_rotary")
-_write_block_words = _words(5, "pa_paged_kv_write_fp8_block")
-_read_block_words = _words(6, "pa_paged_kv_read_fp8_block")
-_decode_block_words = _words(7, "pa_paged_attention_decode_fp8_block")
 
 
 class PagedAttnError(RuntimeError):
@@ -199,12 +179,28 @@ def _check(rc: int, what: str) -> None:
 
 _torch_module = None
 _dtype_codes: dict = {}
+# The short way of a serving step's calls into the library (csrc/binding.cpp), once torch is there.
+# Its functions answer None where a call is not as plain as it wants it; the Python code below
+# them then checks, refuses or adapts. Built for one version of torch; without it, all calls go
+# the Python code's way.
+_binding = None
+
+
+def _load_binding(torch_version: str):
+    path = os.path.join(_HERE, "_build", f"_pagedattn_binding_{torch_version}.so")
+    if not os.path.exists(path):
+        return None
+    spec = importlib.util.spec_from_file_location("_pagedattn_binding", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
 
 
 def _torch():
-    global _torch_module
+    global _torch_module, _binding
     if _torch_module is None:
         import torch
+        _binding = _load_binding(torch.__version__)
         _dtype_codes.update({torch.float32: PA_DTYPE_F32, torch.float16: PA_DTYPE_F16,
                              torch.bfloat16: PA_DTYPE_BF16})
         _torch_module = torch
@@ -987,6 +983,14 @@ def paged_blocks_append(block_tables, context_lens, query_lens, free_blocks, num
     (-1: not served, or past the last token) and positions; new_context_lens and new_num_free
     (default: context_lens and num_free, in place) the lengths and the stack's height after the
     step. All int32; block_tables [B, MB], num_free [1]."""
+    if _binding is not None:
+        rc = _binding.blocks_append(block_tables, context_lens, query_lens, free_blocks, num_free, query_start_loc,
+                                    slot_mapping, positions, block_size, num_blocks, new_context_lens, new_num_free,
+                                    stream)
+        if rc is not None:
+            if rc:
+                _check(rc, "pa_paged_blocks_append")
+            return
     i32, dev = _torch().int32, block_tables.device
     out_lens = context_lens if new_context_lens is None else new_context_lens
     out_free = num_free if new_num_free is None else new_num_free
@@ -1022,10 +1026,10 @@ def paged_blocks_append(block_tables, context_lens, query_lens, free_blocks, num
             return paged_blocks_append(block_tables, context_lens, query_lens, free_blocks, num_free, query_start_loc,
                                        slot_mapping, positions, block_size, num_blocks, new_context_lens, new_num_free,
                                        stream or _torch_module.cuda.current_stream(dev))
-    rc = _packed(_append_words(sp, block_tables.data_ptr(), mb, context_lens.data_ptr(),
-                               out_lens.data_ptr(), query_lens.data_ptr(), B, free_blocks.data_ptr(), cap,
-                               num_free.data_ptr(), out_free.data_ptr(), query_start_loc.data_ptr(),
-                               slot_mapping.data_ptr(), positions.data_ptr(), T, int(block_size), int(num_blocks)))
+    rc = _lib.pa_paged_blocks_append(block_tables.data_ptr(), mb, context_lens.data_ptr(), out_lens.data_ptr(),
+                                     query_lens.data_ptr(), B, free_blocks.data_ptr(), cap, num_free.data_ptr(),
+                                     out_free.data_ptr(), query_start_loc.data_ptr(), slot_mapping.data_ptr(),
+                                     positions.data_ptr(), T, int(block_size), int(num_blocks), sp)
     if rc:
         _check(rc, "pa_paged_blocks_append")
 
@@ -1036,6 +1040,13 @@ def paged_blocks_release(block_tables, context_lens, finished, free_blocks, num_
     stack free_blocks[:num_free] and set its length to 0; its table stays as it is.
     new_context_lens and new_num_free: as paged_blocks_append. num_blocks (default: the length of
     free_blocks): block ids are below it."""
+    if _binding is not None:
+        rc = _binding.blocks_release(block_tables, context_lens, finished, free_blocks, num_free, block_size,
+                                     new_context_lens, new_num_free, num_blocks, stream)
+        if rc is not None:
+            if rc:
+                _check(rc, "pa_paged_blocks_release")
+            return
     torch = _torch()
     i32, dev = torch.int32, block_tables.device
     out_lens = context_lens if new_context_lens is None else new_context_lens
@@ -1067,10 +1078,10 @@ def paged_blocks_release(block_tables, context_lens, finished, free_blocks, num_
             return paged_blocks_release(block_tables, context_lens, finished, free_blocks, num_free, block_size,
                                         new_context_lens, new_num_free, num_blocks,
                                         stream or torch.cuda.current_stream(dev))
-    rc = _packed(_release_words(sp, block_tables.data_ptr(), mb, context_lens.data_ptr(),
-                                out_lens.data_ptr(), finished.data_ptr(), B, free_blocks.data_ptr(), cap,
-                                num_free.data_ptr(), out_free.data_ptr(), int(block_size), int(cap if num_blocks is
-                                None else num_blocks)))
+    rc = _lib.pa_paged_blocks_release(block_tables.data_ptr(), mb, context_lens.data_ptr(), out_lens.data_ptr(),
+                                      finished.data_ptr(), B, free_blocks.data_ptr(), cap, num_free.data_ptr(),
+                                      out_free.data_ptr(), int(block_size), int(cap if num_blocks is None else
+                                      num_blocks), sp)
     if rc:
         _check(rc, "pa_paged_blocks_release")
 
@@ -1157,6 +1168,12 @@ def rotary_embedding(q_out, k_out, q, k, positions, inv_freq, factor: float = 1.
     if interleaved. positions int32 [T]; inv_freq float64 [rotary_dim / 2] (rotary_frequencies).
     Rows may be strided over T (views of a fused projection); an output may be its input; k and
     k_out may be None."""
+    if _binding is not None:
+        rc = _binding.rotary_embedding(q_out, k_out, q, k, positions, inv_freq, factor, interleaved, stream)
+        if rc is not None:
+            if rc:
+                _check(rc, "pa_rotary_embedding")
+            return
     dev = q.device
     T, H, hk, D, rd, qos, qs, ks = _rotary_args(q_out, q, k, positions, inv_freq, dev)
     if (k is None) != (k_out is None):
@@ -1167,10 +1184,9 @@ def rotary_embedding(q_out, k_out, q, k, positions, inv_freq, factor: float = 1.
         with _on(dev):
             return rotary_embedding(q_out, k_out, q, k, positions, inv_freq, factor, interleaved,
                                     stream or _torch_module.cuda.current_stream(dev))
-    rc = _packed(_rotary_words(sp, q_out.data_ptr(), qos, 0 if k is None else
-                               k_out.data_ptr(), kos, q.data_ptr(), qs, 0 if k is None else k.data_ptr(), ks,
-                               positions.data_ptr(), inv_freq.data_ptr(), float(factor), int(interleaved), T, H, hk,
-                               D, rd, _dtype_code(q)))
+    rc = _lib.pa_rotary_embedding(q_out.data_ptr(), qos, None if k is None else k_out.data_ptr(), kos, q.data_ptr(), qs,
+                                  None if k is None else k.data_ptr(), ks, positions.data_ptr(), inv_freq.data_ptr(),
+                                  float(factor), int(interleaved), T, H, hk, D, rd, _dtype_code(q), sp)
     if rc:
         _check(rc, "pa_rotary_embedding")
 
@@ -1179,6 +1195,13 @@ def paged_kv_write_rotary(q_out, q, k, v, positions, inv_freq, slot_mapping, key
                           factor: float = 1.0, interleaved: bool = False, stream=None) -> None:
     """rotary_embedding of q [T, H, D] into q_out and of k [T, Hk, D] into key_cache, and v into
     value_cache [NB, bs, Hk, D], at slot_mapping[T] as paged_kv_write, in one launch."""
+    if _binding is not None:
+        rc = _binding.kv_write_rotary(q_out, q, k, v, positions, inv_freq, slot_mapping, key_cache, value_cache,
+                                      factor, interleaved, stream)
+        if rc is not None:
+            if rc:
+                _check(rc, "pa_paged_kv_write_rotary")
+            return
     dev, dt = key_cache.device, key_cache.dtype
     T, H, hk, D, rd, qos, qs, ks = _rotary_args(q_out, q, k, positions, inv_freq, dev)
     if q.dtype != dt:
@@ -1198,10 +1221,10 @@ def paged_kv_write_rotary(q_out, q, k, v, positions, inv_freq, slot_mapping, key
         with _on(dev):
             return paged_kv_write_rotary(q_out, q, k, v, positions, inv_freq, slot_mapping, key_cache, value_cache,
                                          factor, interleaved, stream or _torch_module.cuda.current_stream(dev))
-    rc = _packed(_write_rotary_words(sp, q_out.data_ptr(), qos, q.data_ptr(), qs, k.data_ptr(),
-                                     ks, v.data_ptr(), vs, positions.data_ptr(), inv_freq.data_ptr(), float(factor),
-                                     int(interleaved), slot_mapping.data_ptr(), T, key_cache.data_ptr(),
-                                     value_cache.data_ptr(), shape[0], shape[1], H, hk, D, rd, _dtype_code(q)))
+    rc = _lib.pa_paged_kv_write_rotary(q_out.data_ptr(), qos, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                                       positions.data_ptr(), inv_freq.data_ptr(), float(factor), int(interleaved),
+                                       slot_mapping.data_ptr(), T, key_cache.data_ptr(), value_cache.data_ptr(),
+                                       shape[0], shape[1], H, hk, D, rd, _dtype_code(q), sp)
     if rc:
         _check(rc, "pa_paged_kv_write_rotary")
 
@@ -1232,6 +1255,12 @@ def paged_kv_write_fp8_block(k, v, slot_mapping, key_cache, value_cache, kv_scal
     smallest power of two that its values need; when it grows, the block's older codes are
     re-encoded; a call that writes a block's first slot starts the block anew. The tokens of a
     block stand next to each other in slot_mapping."""
+    if _binding is not None:
+        rc = _binding.kv_write_fp8_block(k, v, slot_mapping, key_cache, value_cache, kv_scales, stream)
+        if rc is not None:
+            if rc:
+                _check(rc, "pa_paged_kv_write_fp8_block")
+            return
     dev = key_cache.device
     nb, hk, bs, d = _fp8_block_caches(key_cache, value_cache, kv_scales, dev)
     if not (slot_mapping.device == dev and slot_mapping.dtype == _torch_module.int32 and slot_mapping.is_contiguous()):
@@ -1244,9 +1273,9 @@ def paged_kv_write_fp8_block(k, v, slot_mapping, key_cache, value_cache, kv_scal
         with _on(dev):
             return paged_kv_write_fp8_block(k, v, slot_mapping, key_cache, value_cache, kv_scales,
                                             stream or _torch_module.cuda.current_stream(dev))
-    rc = _packed(_write_block_words(sp, k.data_ptr(), ks, v.data_ptr(), vs,
-                                    slot_mapping.data_ptr(), T, key_cache.data_ptr(), value_cache.data_ptr(),
-                                    kv_scales.data_ptr(), nb, bs, hk, d, _dtype_code(k)))
+    rc = _lib.pa_paged_kv_write_fp8_block(k.data_ptr(), ks, v.data_ptr(), vs, slot_mapping.data_ptr(), T,
+                                          key_cache.data_ptr(), value_cache.data_ptr(), kv_scales.data_ptr(), nb, bs,
+                                          hk, d, _dtype_code(k), sp)
     if rc:
         _check(rc, "pa_paged_kv_write_fp8_block")
 
@@ -1254,6 +1283,12 @@ def paged_kv_write_fp8_block(k, v, slot_mapping, key_cache, value_cache, kv_scal
 def paged_kv_read_fp8_block(k, v, slot_mapping, key_cache, value_cache, kv_scales, stream=None) -> None:
     """The inverse: k[t], v[t] [T, Hk, D] (fp32/fp16/bf16) = the values held at
     slot_mapping[t]; rows of slot -1 stay as they are."""
+    if _binding is not None:
+        rc = _binding.kv_read_fp8_block(k, v, slot_mapping, key_cache, value_cache, kv_scales, stream)
+        if rc is not None:
+            if rc:
+                _check(rc, "pa_paged_kv_read_fp8_block")
+            return
     dev = key_cache.device
     nb, hk, bs, d = _fp8_block_caches(key_cache, value_cache, kv_scales, dev)
     T = _int4_rows(k, v, slot_mapping, hk, d, dev)
@@ -1262,9 +1297,9 @@ def paged_kv_read_fp8_block(k, v, slot_mapping, key_cache, value_cache, kv_scale
         with _on(dev):
             return paged_kv_read_fp8_block(k, v, slot_mapping, key_cache, value_cache, kv_scales,
                                            stream or _torch_module.cuda.current_stream(dev))
-    rc = _packed(_read_block_words(sp, k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), T,
-                                   key_cache.data_ptr(), value_cache.data_ptr(), kv_scales.data_ptr(), nb, bs, hk, d,
-                                   _dtype_code(k)))
+    rc = _lib.pa_paged_kv_read_fp8_block(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), T, key_cache.data_ptr(),
+                                         value_cache.data_ptr(), kv_scales.data_ptr(), nb, bs, hk, d, _dtype_code(k),
+                                         sp)
     if rc:
         _check(rc, "pa_paged_kv_read_fp8_block")
 
@@ -1283,6 +1318,13 @@ def paged_attention_decode_fp8_block(out, q, key_cache, value_cache, kv_scales, 
     """Decode attention over block-scaled 8-bit caches [NB, Hk, bs, D] with kv_scales [NB, Hk, 2].
 
     q, out [B, H, D] bf16 or fp16. Other arguments as paged_attention_decode."""
+    if _binding is not None:
+        rc = _binding.attention_decode_fp8_block(out, q, key_cache, value_cache, kv_scales, block_tables,
+                                                 context_lens, scale, max_context_len, workspace, stream)
+        if rc is not None:
+            if rc:
+                _check(rc, "pa_paged_attention_decode_fp8_block")
+            return
     dev = key_cache.device
     nb, hk, bs, d = _fp8_block_caches(key_cache, value_cache, kv_scales, dev)
     B, H, mb = _decode_args(out, q, block_tables, context_lens, d, dev, q.dtype, max_context_len)
@@ -1297,10 +1339,11 @@ def paged_attention_decode_fp8_block(out, q, key_cache, value_cache, kv_scales, 
                                               dev.index))
     else:
         _cuda(workspace, "workspace", _torch_module.uint8, dev)
-    rc = _packed(_decode_block_words(sp, out.data_ptr(), q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
-                                     kv_scales.data_ptr(), block_tables.data_ptr(), mb, context_lens.data_ptr(), B, H,
-                                     hk, d, bs, nb, float(scale), int(max_context_len), workspace.data_ptr(),
-                                     workspace.numel(), _dtype_code(q)))
+    rc = _lib.pa_paged_attention_decode_fp8_block(out.data_ptr(), q.data_ptr(), key_cache.data_ptr(),
+                                                  value_cache.data_ptr(), kv_scales.data_ptr(),
+                                                  block_tables.data_ptr(), mb, context_lens.data_ptr(), B, H, hk, d,
+                                                  bs, nb, float(scale), int(max_context_len), workspace.data_ptr(),
+                                                  workspace.numel(), _dtype_code(q), sp)
     if rc:
         _check(rc, "pa_paged_attention_decode_fp8_block")
 

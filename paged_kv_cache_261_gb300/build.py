@@ -2,8 +2,9 @@
 
 Each translation unit compiles in its own nvcc process, in parallel, then one
 nvcc call links the shared library. The output lands in
-``paged_kv_cache_261_gb300/_build/`` (git-ignored). Run as a script or call
-``build_library()``.
+``paged_kv_cache_261_gb300/_build/`` (git-ignored). Where torch is installed, g++ builds
+the Python module of csrc/binding.cpp beside it, for that version of torch. Run as a script
+or call ``build_library()``.
 """
 from __future__ import annotations
 
@@ -28,6 +29,50 @@ SOURCES = ["capi.cu", "kv_write.cu", "kv_write_fp8.cu", "decode_simt.cu", "decod
            "selftest.cu", "kv_fp8_block.cu", "decode_fp8_block.cu", "step_layout.cu", "rotary.cu", "allocator.cpp"]
 
 
+BINDING = "binding.cpp"
+
+
+def _torch_version():
+    try:
+        from importlib.metadata import version
+        version("torch")
+    except Exception:
+        return None
+    import torch
+    return torch.__version__
+
+
+def binding_path(torch_version: str) -> str:
+    return os.path.join(BUILD, f"_pagedattn_binding_{torch_version}.so")
+
+
+def _binding_command(obj: str):
+    import sysconfig
+
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__), "include")
+    nvcc_include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    include = [root, os.path.join(root, "torch", "csrc", "api", "include"), nvcc_include, sysconfig.get_paths()["include"]]
+    return ["g++", "-std=c++17", "-O2", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *("-I" + d for d in include), "-c", os.path.join(CSRC, BINDING), "-o", obj]
+
+
+def _link_binding(obj: str, torch_version: str) -> None:
+    import torch
+    tmp = binding_path(torch_version) + f".tmp{os.getpid()}"
+    _run(["g++", "-shared", "-o", tmp, obj, "-L" + BUILD, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
+          "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+          "-ltorch_python"], "linking the binding")
+    os.replace(tmp, binding_path(torch_version))
+
+
+def _run(cmd, what: str):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    return r
+
+
 def _nvcc() -> str:
     for cand in (os.environ.get("NVCC"), shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
         if cand and os.path.exists(cand):
@@ -48,29 +93,29 @@ def _stale(target: str) -> bool:
 
 
 def build_library(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
-    if not force and not _stale(LIB):
+    torch_version = _torch_version()
+    if not force and not _stale(LIB) and (torch_version is None or not _stale(binding_path(torch_version))):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
 
     def compile_one(src: str) -> str:
         obj = os.path.join(BUILD, src + f".{os.getpid()}.o")
-        cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+        cmd = _binding_command(obj) if src == BINDING else \
+            [nvcc, *ARCH, *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+        r = _run(cmd, f"compiling {src}")
         if verbose and (r.stdout or r.stderr):
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=jobs or len(SOURCES)) as ex:
-        objs = list(ex.map(compile_one, SOURCES))
+    sources = SOURCES + ([BINDING] if torch_version else [])
+    with ThreadPoolExecutor(max_workers=jobs or len(sources)) as ex:
+        objs = list(ex.map(compile_one, sources))
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs[:len(SOURCES)]], "link")
     os.replace(tmp, LIB)
+    if torch_version:
+        _link_binding(objs[-1], torch_version)
     for o in objs:
         os.remove(o)
     return LIB

@@ -6,8 +6,6 @@
 #include <string.h>
 
 #include <algorithm>
-#include <type_traits>
-#include <utility>
 
 #include "../../include/pagedattn.h"
 #include "call_range.h"
@@ -428,32 +426,6 @@ int rotary_setup(pa::RotaryParams &p, void *q_out, int64_t q_out_stride, const v
     p.rotary_dim = rotary_dim;
     p.interleaved = interleaved != 0;
     return PA_OK;
-}
-
-// A call's arguments from 8-byte words (pa_call_packed): each by the type of its parameter.
-template <typename T> T from_word(int64_t w) {
-    if constexpr (std::is_pointer_v<T>) {
-        return reinterpret_cast<T>(static_cast<uintptr_t>(w));
-    } else if constexpr (std::is_floating_point_v<T>) {
-        double d;
-        memcpy(&d, &w, sizeof d);
-        return static_cast<T>(d);
-    } else {
-        return static_cast<T>(w);
-    }
-}
-template <typename... A, size_t... I>
-int call_unpacked(int (*fn)(A...), const int64_t *w, std::index_sequence<I...>) {
-    return fn(from_word<A>(w[I])...);
-}
-// fn's last parameter is the stream, which stands before the others in `words`.
-template <typename... A> int call_words(int (*fn)(A...), const int64_t *words) {
-    constexpr size_t n = sizeof...(A);
-    if (words[1] != (int64_t)(n - 1)) return PA_ERR_INVALID_ARG;
-    int64_t w[n];
-    memcpy(w, words + 3, (n - 1) * sizeof w[0]);
-    w[n - 1] = words[2];
-    return call_unpacked(fn, w, std::make_index_sequence<n>());
 }
 
 }  // namespace
@@ -1268,21 +1240,6 @@ int pa_paged_attention_decode_fp8_block(void *out, const void *q, const void *ke
     if (owned) cudaFreeAsync(owned, s);
     if (krc == -2) return PA_ERR_UNSUPPORTED;
     return krc == 0 ? PA_OK : PA_ERR_CUDA;
-}
-
-int pa_call_packed(const void *words) {
-    if (!words || (reinterpret_cast<uintptr_t>(words) & 7u) != 0) return PA_ERR_INVALID_ARG;
-    const int64_t *w = static_cast<const int64_t *>(words);
-    switch (w[0]) {
-    case PA_CALL_BLOCKS_APPEND: return call_words(pa_paged_blocks_append, w);
-    case PA_CALL_BLOCKS_RELEASE: return call_words(pa_paged_blocks_release, w);
-    case PA_CALL_ROTARY_EMBEDDING: return call_words(pa_rotary_embedding, w);
-    case PA_CALL_KV_WRITE_ROTARY: return call_words(pa_paged_kv_write_rotary, w);
-    case PA_CALL_KV_WRITE_FP8_BLOCK: return call_words(pa_paged_kv_write_fp8_block, w);
-    case PA_CALL_KV_READ_FP8_BLOCK: return call_words(pa_paged_kv_read_fp8_block, w);
-    case PA_CALL_DECODE_FP8_BLOCK: return call_words(pa_paged_attention_decode_fp8_block, w);
-    default: return PA_ERR_INVALID_ARG;
-    }
 }
 
 int pa_paged_kv_evict(int32_t *kept, int64_t kept_len, const float *mass, int64_t mass_len, float *mass_out,

@@ -157,8 +157,13 @@ __global__ __launch_bounds__(kMaxThreads) void blocks_append_kernel(const Blocks
         ctx[b] = good ? c : -1;
     }
     if (threadIdx.x == 0) start[B] = (int)min(total.a, (int64_t)T);
-    if (mine_taken) atomicMax(all_taken, mine_taken);
-    if (report && bits) raise_error(p.err, bits);
+    // (one lane a warp: a thousand threads on one word took 2 us)
+    mine_taken = __reduce_max_sync(0xffffffffu, mine_taken);
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    if ((threadIdx.x & 31) == 0) {
+        if (mine_taken) atomicMax(all_taken, mine_taken);
+        if (report && bits) raise_error(p.err, bits);
+    }
     __syncthreads();
     // every CTA that reads the lengths and the height has done so
     if constexpr (kWhat == Append::kCall) cluster_sync();
@@ -283,8 +288,12 @@ __global__ __launch_bounds__(kMaxThreads) void blocks_release_kernel(const Block
         }
         ctx[b] = c;
     }
-    if (mine_back) atomicMax(all_back, mine_back);
-    if (report && bits) raise_error(p.err, bits);
+    mine_back = __reduce_max_sync(0xffffffffu, mine_back);
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    if ((threadIdx.x & 31) == 0) {
+        if (mine_back) atomicMax(all_back, mine_back);
+        if (report && bits) raise_error(p.err, bits);
+    }
     __syncthreads();
     cluster_sync();                              // every CTA has read the lengths and the height
 

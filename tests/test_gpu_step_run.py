@@ -328,9 +328,10 @@ def test_context_read_back_for_prefill(pa):
     assert pa.get_device_error() == 0
 
 
-def test_two_branches_of_one_graph(pa, monkeypatch):
+@pytest.mark.parametrize("plain", [False, True])
+def test_two_branches_of_one_graph(pa, monkeypatch, plain):
     """One capture forks: decodes go to a side stream through stream=, others and torch operations that allocate run
-    beside them on the capture's own stream; each has a workspace of its own, and replays equal the calls alone."""
+    beside them on the capture's own stream; replays equal the calls alone, whichever way the calls go."""
     from test_gpu_fp8_block import Case
     cases = [Case(np.random.default_rng(60 + i), lens, 16, 4, 128, 16, "f16") for i, lens in
              enumerate(([2500, 900, 1300], [1100, 3000, 2049, 5]))]
@@ -343,6 +344,8 @@ def test_two_branches_of_one_graph(pa, monkeypatch):
         return buf
 
     monkeypatch.setattr(pa, "_workspace", spy)
+    if plain:
+        monkeypatch.setattr(pa, "_binding", None)
     outs = [torch.empty_like(w) for w in want]
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
@@ -356,7 +359,8 @@ def test_two_branches_of_one_graph(pa, monkeypatch):
             cases[1].run(pa, out=outs[1])
             junk = junk + 1
         cur.wait_stream(side)
-    assert {s for s, _, _ in seen} == {cur.cuda_stream, side.cuda_stream}
+    # a stream that is not the current one is the Python code's affair
+    assert {s for s, _, _ in seen} == ({cur.cuda_stream, side.cuda_stream} if plain else {side.cuda_stream})
     for s, a, b in seen:
         for t, c, d in seen:
             assert s == t or b <= c or d <= a
@@ -366,4 +370,77 @@ def test_two_branches_of_one_graph(pa, monkeypatch):
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    assert pa.get_device_error() == 0
+
+
+def test_python_code_and_compiled_way_agree(pa, monkeypatch):
+    """The steps through the compiled module and through the Python code alone leave the same tensors; what the
+    module does not take, as a tensor subclass's rows that are not dense, the Python code refuses."""
+    def run(plain):
+        if plain:
+            monkeypatch.setattr(pa, "_binding", None)
+        loop = Loop(pa, 70, 6, 40)
+        store = Loop(pa, 71, 3, 20)
+        cache = [torch.zeros((20, 16, 2, 128), dtype=torch.bfloat16, device=dev()) for _ in range(2)]
+        rows = [torch.zeros((96, 2, 128), dtype=torch.bfloat16, device=dev()) for _ in range(2)]
+        for new, done in plan(np.random.default_rng(72), loop, 6):
+            loop.feed(new, done)
+            loop.step()
+            store.feed(new[:3], done[:3])
+            pa.paged_blocks_append(store.table, store.lens, store.new, store.free, store.num_free, store.start,
+                                   store.slots, store.pos, 16, 20)
+            q, k, v = store.qkv[:, :8], store.qkv[:, 8:10], store.qkv[:, 10:]
+            pa.paged_kv_write_rotary(q, q, k, v, store.pos, store.freq, store.slots, *cache, factor=1.5)
+            pa.paged_kv_read_fp8_block(*rows, loop.slots, loop.kc, loop.vc, loop.sc)
+        pa.get_device_error()
+        return [loop.out, loop.kc, loop.vc, loop.table, loop.lens, loop.free, loop.qkv, store.qkv, *cache, *rows]
+
+    assert pa._binding is not None
+    a = run(False)
+    for x, y in zip(a, run(True)):
+        assert torch.equal(x, y)
+
+
+def test_refusals_are_the_same_both_ways(pa, monkeypatch):
+    """Statuses of the library and the Python code's errors, with and without the compiled module."""
+    d = dev()
+    x = torch.zeros((4, 2, 128), dtype=torch.bfloat16, device=d)
+    c = torch.zeros((4, 2, 16, 128), dtype=torch.uint8, device=d)
+    s, i = torch.zeros((4, 2, 2), device=d), torch.zeros(4, dtype=torch.int32, device=d)
+    one, t = torch.zeros(1, dtype=torch.int32, device=d), torch.zeros((4, 3), dtype=torch.int32, device=d)
+    f = torch.zeros(64, dtype=torch.float64, device=d)
+    cases = [
+        (ValueError, lambda: pa.paged_kv_write_fp8_block(x[:3], x, i, c, c, s)),
+        (TypeError, lambda: pa.paged_kv_write_fp8_block(x.double(), x.double(), i, c, c, s)),
+        (TypeError, lambda: pa.paged_kv_write_fp8_block(x, x, i, x.view(1, 4, 2, 128), x.view(1, 4, 2, 128), s)),
+        (TypeError, lambda: pa.paged_kv_write_fp8_block(x, x, i.long(), c, c, s)),
+        (ValueError, lambda: pa.paged_kv_write_fp8_block(x, x, i, c, c, s[:2])),
+        (ValueError, lambda: pa.paged_kv_write_fp8_block(x, x.cpu(), i, c, c, s)),
+        (ValueError, lambda: pa.paged_kv_read_fp8_block(x.transpose(0, 1), x, i, c, c, s)),
+        (pa.PagedAttnError, lambda: pa.paged_kv_write_fp8_block(x[..., :96].contiguous(), x[..., :96].contiguous(), i,
+                                                              c[..., :96].contiguous(), c[..., :96].contiguous(), s)),
+        (ValueError, lambda: pa.paged_attention_decode_fp8_block(x, x, c, c, s, t, i[:3], 1.0)),
+        (ValueError, lambda: pa.paged_attention_decode_fp8_block(x, x, c, c, s, t, i, 1.0, max_context_len=-1)),
+        (pa.PagedAttnError, lambda: pa.paged_attention_decode_fp8_block(x, x, c, c, s, t, i, float("nan"))),
+        (pa.PagedAttnError, lambda: pa.paged_attention_decode_fp8_block(x.float(), x.float(), c, c, s, t, i, 1.0)),
+        (TypeError, lambda: pa.paged_attention_decode_fp8_block(x, x, c, c, s, t, i, 1.0, workspace=s)),
+        (pa.PagedAttnError, lambda: pa.rotary_embedding(x, None, x, None, i, f[:12])),
+        (ValueError, lambda: pa.rotary_embedding(x, None, x, x, i, f)),
+        (TypeError, lambda: pa.rotary_embedding(x.float(), None, x, None, i, f)),
+        (ValueError, lambda: pa.paged_kv_write_rotary(x, x, x, x, i, f, i, x, x)),
+        (pa.PagedAttnError, lambda: pa.paged_blocks_append(t, i, i, i, one, torch.zeros(5, dtype=torch.int32, device=d), i,
+                                                          i, 12, 4)),
+        (ValueError, lambda: pa.paged_blocks_append(t, i, i, i, i, i, i, i, 16, 4)),
+        (TypeError, lambda: pa.paged_blocks_release(t, i, i, i, one, 16)),
+        (pa.PagedAttnError, lambda: pa.paged_blocks_release(t, i, i.bool(), i, one, 16, num_blocks=0)),
+    ]
+    for _ in range(2):
+        for exc, call in cases:
+            with pytest.raises(exc):
+                call()
+        # what is left open works: empty calls, a given stream, flags as numbers
+        pa.paged_kv_write_fp8_block(x[:0], x[:0], i[:0], c, c, s)
+        pa.rotary_embedding(x, x, x, x, i, f, 1, 1, stream=torch.cuda.current_stream())
+        pa.paged_blocks_release(t, i, i.to(torch.uint8), i, one, 16)
+        monkeypatch.setattr(pa, "_binding", None)
     assert pa.get_device_error() == 0

@@ -266,28 +266,3 @@ def test_host_allocator_serves_in_the_same_order(pa):
             al.free_seq(int(b))
             al.add_seq(int(b))
     assert al.stats().num_free == nf
-
-
-def test_packed_calls(pa):
-    """pa_call_packed takes the arguments of a call in its order, and refuses what it does not know."""
-    import ctypes
-    import struct
-
-    def call(*words):
-        return pa.lib().pa_call_packed(struct.pack(f"{len(words)}q", *words))
-
-    assert pa.lib().pa_call_packed(None) == INVALID
-    assert call(0, 0, 0) == INVALID and call(99, 0, 0) == INVALID
-    good = [16, 256, 16, 256, 16, 0, 16, 16, 16, 8, 16, 2, 128, 2]           # a scatter of no tokens
-    assert call(5, len(good), 0, *good) == 0
-    assert call(5, len(good) - 1, 0, *good) == INVALID and call(5, len(good) + 1, 0, *good, 0) == INVALID
-    for i, bad, code in ((12, 96, UNSUPPORTED), (10, 12, UNSUPPORTED), (9, 0, INVALID), (13, 3, INVALID)):
-        words = list(good)
-        words[i] = bad
-        assert call(5, len(words), 0, *words) == code
-    # floats as doubles: a NaN factor is refused, 1.0 is not
-    for factor, code in ((1.0, 0), (float("nan"), INVALID)):
-        w = struct.pack("3q10qd7q", 3, 18, 0, 16, 512, 16, 256, 16, 512, 16, 256, 16, 16, factor, 0, 0, 4, 2, 128, 128, 2)
-        assert pa.lib().pa_call_packed(w) == code
-    buf = ctypes.create_string_buffer(64)
-    assert pa.lib().pa_call_packed(ctypes.cast(ctypes.addressof(buf) + 4, ctypes.c_char_p)) == INVALID
