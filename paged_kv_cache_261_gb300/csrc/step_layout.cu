@@ -29,7 +29,15 @@ constexpr int kMaxThreads = 1024;
 constexpr int kMaxCluster = 8;
 constexpr int kScratch = 66;                     // 64-bit words of the sums
 constexpr int kPerThread = 4;                    // table entries of a thread that a release aims at
-constexpr int kClusterTokens = 8192;             // an append's tokens that one cluster takes
+// An append's tokens that one cluster takes: up to about here its single launch is as fast as the two
+// (us on the device: 68 tokens 3.4; 1500 of 300 requests 6.5 against 4.4, 4000 of four 5.6 against 3.7).
+constexpr int kClusterTokens = 512;
+// Threads of a CTA. Many are slow to start and to agree: maps of 17,500 tokens with 256 3.9 us, 512 4.5,
+// 1024 6.4; lengths after 139,000 tokens of 1024 requests with 256 6.4 (the call), 1024 8.2; a release of
+// 64 requests with 256 2.8, 512 3.1, 1024 4.2, of 1024 requests 5.1, 4.3, 5.0.
+// (More where there are many requests: no thread sums up more than kPerThread of them, or they are 1024.)
+constexpr int kCallThreads = 512, kMapThreads = 256, kLengthThreads = 256;
+constexpr int kMapCtas = 2;                      // on an SM, at most
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -95,8 +103,7 @@ __device__ __forceinline__ int checked_block(int entry, int64_t num_blocks, unsi
 // lengths and the stack's height, by any number of CTAs; or these two, after such a launch.
 enum class Append { kCall, kMaps, kLengths };
 
-// G: tokens that a thread takes together.
-template <Append kWhat, int G>
+template <Append kWhat>
 __global__ __launch_bounds__(kMaxThreads) void blocks_append_kernel(const BlocksAppendParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
     int64_t *scratch = reinterpret_cast<int64_t *>(smem);
@@ -157,7 +164,6 @@ __global__ __launch_bounds__(kMaxThreads) void blocks_append_kernel(const Blocks
         ctx[b] = good ? c : -1;
     }
     if (threadIdx.x == 0) start[B] = (int)min(total.a, (int64_t)T);
-    // (one lane a warp: a thousand threads on one word took 2 us)
     mine_taken = __reduce_max_sync(0xffffffffu, mine_taken);
     bits = __reduce_or_sync(0xffffffffu, bits);
     if ((threadIdx.x & 31) == 0) {
@@ -181,58 +187,25 @@ __global__ __launch_bounds__(kMaxThreads) void blocks_append_kernel(const Blocks
             const int b = owner(taken, B, j), col = ((ctx[b] + bs - 1) >> l2) + j - taken[b];
             p.block_tables[(int64_t)b * p.max_blocks + col] = checked_block(p.free_blocks[height - 1 - j], p.num_blocks, p.err);
         }
-        // Slots and positions, of G tokens in a row. Their entries are loaded together; tokens of one
-        // block load one.
-        const bool wide = ((reinterpret_cast<uintptr_t>(p.slot_mapping) | reinterpret_cast<uintptr_t>(p.positions)) & 15) == 0;
+        // Slots and positions, a token a thread. (Four tokens in a row a thread, with one search and vector
+        // stores where they share a request: 10.2 us against 7.5 for 139,000 tokens of 1024 requests, 6.6
+        // against 4.7 for 17,500 of 192.)
         const int live = start[B];
-        for (int64_t t0 = (int64_t)gid * G; t0 < T; t0 += (int64_t)threads * G) {
-            alignas(16) int slot[G], pos[G];
-            const int32_t *from[G];                        // the place of a token's entry, null: none or as before
-            bool served[G];
-            int b = 0, next = 0, col = -1;                 // tokens before `next` are request b's; its last column
-#pragma unroll
-            for (int i = 0; i < G; ++i) {
-                const int t = (int)t0 + i;                 // (T is below 2^31 - 65536)
-                pos[i] = 0;
-                from[i] = nullptr;
-                served[i] = false;
-                if (t >= live) continue;
-                if (t >= next) {
-                    b += owner(start + b, B - b, t);
-                    next = start[b + 1];
-                    col = -1;
-                }
-                const int c = ctx[b];
-                if (c < 0) continue;
-                served[i] = true;
-                pos[i] = c + t - start[b];
-                if (pos[i] >> l2 != col) {
-                    col = pos[i] >> l2;
-                    const int held = (c + bs - 1) >> l2;
-                    from[i] = col < held ? p.block_tables + (int64_t)b * p.max_blocks + col
-                                         : p.free_blocks + (height - 1 - (taken[b] + col - held));
+        for (int t = gid; t < T; t += threads) {       // (T is below 2^31 - 65536)
+            int slot = -1, pos = 0;
+            if (t < live) {
+                const int b = owner(start, B, t), c = ctx[b];
+                if (c >= 0) {
+                    pos = c + t - start[b];
+                    const int held = (c + bs - 1) >> l2, col = pos >> l2;
+                    const int entry = col < held ? p.block_tables[(int64_t)b * p.max_blocks + col]
+                                                 : p.free_blocks[height - 1 - (taken[b] + col - held)];
+                    const int block = checked_block(entry, p.num_blocks, p.err);
+                    if (block >= 0) slot = (block << l2) + (pos & (bs - 1));
                 }
             }
-            int entry[G];
-#pragma unroll
-            for (int i = 0; i < G; ++i) entry[i] = from[i] ? *from[i] : 0;
-            int block = -1;
-#pragma unroll
-            for (int i = 0; i < G; ++i) {
-                if (from[i]) block = checked_block(entry[i], p.num_blocks, p.err);
-                slot[i] = served[i] && block >= 0 ? (block << l2) + (pos[i] & (bs - 1)) : -1;
-            }
-            if (G == 4 && wide && t0 + G <= T) {
-                *reinterpret_cast<int4 *>(p.slot_mapping + t0) = *reinterpret_cast<int4 *>(slot);
-                *reinterpret_cast<int4 *>(p.positions + t0) = *reinterpret_cast<int4 *>(pos);
-            } else {
-#pragma unroll
-                for (int i = 0; i < G; ++i)
-                    if (t0 + i < T) {
-                        p.slot_mapping[t0 + i] = slot[i];
-                        p.positions[t0 + i] = pos[i];
-                    }
-            }
+            p.slot_mapping[t] = slot;
+            p.positions[t] = pos;
         }
     }
 }
@@ -330,9 +303,10 @@ int launch(void (*kern)(P), const P &p, int ctas, int threads, bool cluster, int
     return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? 0 : -1;
 }
 
-// Threads of a CTA for this much work, at least one for each request.
-int cta_threads(int64_t work, int num_seqs) {
-    return (int)std::min<int64_t>(kMaxThreads, std::max<int64_t>(128, (std::max<int64_t>(work, num_seqs) + 127) / 128 * 128));
+// Threads of a CTA for this much work and as many requests, up to `most` if the work alone asks.
+int cta_threads(int64_t work, int num_seqs, int most) {
+    const int64_t want = std::max<int64_t>(std::min<int64_t>(work, most), num_seqs / kPerThread);
+    return (int)std::min<int64_t>(kMaxThreads, std::max<int64_t>(128, (want + 127) / 128 * 128));
 }
 int cluster_ctas(int64_t work, int threads) {
     int ctas = 1;
@@ -345,22 +319,23 @@ int cluster_ctas(int64_t work, int threads) {
 int launch_blocks_append(const BlocksAppendParams &p, int sms, cudaStream_t stream) {
     const int T = p.num_tokens, words = 3 * p.num_seqs + 1;
     if (T <= kClusterTokens) {
-        const int threads = cta_threads(T, p.num_seqs);
-        return launch(blocks_append_kernel<Append::kCall, 1>, p, cluster_ctas(T, threads), threads, true, words, stream);
+        const int threads = cta_threads(std::max(T, p.num_seqs), p.num_seqs, kCallThreads);
+        return launch(blocks_append_kernel<Append::kCall>, p, cluster_ctas(T, threads), threads, true, words, stream);
     }
-    const int threads = cta_threads(512, p.num_seqs);
-    const int64_t ctas = (T / 4 + threads - 1) / threads;
-    const int rc = launch(blocks_append_kernel<Append::kMaps, 4>, p, (int)std::min<int64_t>(sms, ctas), threads, false,
-                          words, stream);
+    const int threads = cta_threads(T, p.num_seqs, kMapThreads);
+    const int64_t ctas = ((int64_t)T + threads - 1) / threads;
+    const int rc = launch(blocks_append_kernel<Append::kMaps>, p, (int)std::min<int64_t>(kMapCtas * sms, ctas), threads,
+                          false, words, stream);
     if (rc != 0) return rc;
-    return launch(blocks_append_kernel<Append::kLengths, 1>, p, 1, cta_threads(0, p.num_seqs), false, words, stream);
+    return launch(blocks_append_kernel<Append::kLengths>, p, 1, cta_threads(p.num_seqs, p.num_seqs, kLengthThreads), false,
+                  words, stream);
 }
 
 int launch_blocks_release(const BlocksReleaseParams &p, cudaStream_t stream) {
     // a thread for every kPerThread entries that the tables could hold: which requests are
     // finished is known on the device alone
     const int64_t work = ((int64_t)p.num_seqs * p.max_blocks + kPerThread - 1) / kPerThread;
-    const int threads = cta_threads(work, p.num_seqs);
+    const int threads = cta_threads(std::max<int64_t>(work, p.num_seqs), p.num_seqs, p.num_seqs > 256 ? 512 : 256);
     return launch(blocks_release_kernel, p, cluster_ctas(work, threads), threads, true, 2 * p.num_seqs, stream);
 }
 
