@@ -14,10 +14,15 @@
 // short enough for float32 (an error of 2^-28 turns at most), and sincospif takes it.
 // The angle is off by position * inv_freq * 2^-52 and that, nothing else.
 //
-// A CTA takes one or two tokens: its threads first make the tokens' cosines and sines, in shared
-// memory, then each takes units of 16 channels, the 8 pairs of which lie in one thread for both
-// kinds of pairs. The first units are loaded before the angles are made. What bounds it is HBM:
-// every row is read and written once.
+// A CTA takes a few tokens: its threads first make the tokens' cosines and sines, in shared
+// memory, then take units of 16 channels, the 8 pairs of which lie in one thread for both kinds
+// of pairs. The first units are loaded before the angles are made.
+//
+// What bounds it (one GB300, inputs and outputs not in L2): HBM, every row being read and written
+// once. 8192 tokens of 32 + 8 + 8 heads, 201 MB, 32.6 us, 6.2 TB/s; 4096 of 128 + 8 + 8, 302 MB, 47.4;
+// 2047 of 64 + 8, 75 MB, 15.0. Two units a thread in flight: with one 33.6 us, three 34.6 (the 8192
+// tokens). With all of a CTA's rows copied asynchronously into shared memory, so more on its way:
+// 46.6. Without the streaming hints 33.4; loads alone hinted 34.4, stores alone 33.7.
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "kernels_step.h"
@@ -29,8 +34,9 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kUnits = 2;                        // of a thread, in flight together
-constexpr int kMaxTokens = 2;                    // of a CTA
-constexpr int64_t kManyTokens = 1200;            // from here on a CTA takes kMaxTokens
+constexpr int kTurns = 4;                        // units of a thread that a CTA's tokens are chosen for
+constexpr int kMaxTokens = 8;                    // of a CTA
+constexpr int64_t kManyTokens = 1200;            // up to here a CTA takes one
 
 // inv_freq radians as a number of 2^-64 turns, modulo one turn.
 __device__ __forceinline__ uint64_t turn_step(double inv_freq) {
@@ -57,11 +63,11 @@ template <typename T> struct Run8 {
     uint4 raw[sizeof(T) / 2];
     __device__ __forceinline__ void load(const T *src) {
 #pragma unroll
-        for (int u = 0; u < (int)sizeof(T) / 2; ++u) raw[u] = reinterpret_cast<const uint4 *>(src)[u];
+        for (int u = 0; u < (int)sizeof(T) / 2; ++u) raw[u] = __ldcs(reinterpret_cast<const uint4 *>(src) + u);
     }
     __device__ __forceinline__ void store(T *dst) const {
 #pragma unroll
-        for (int u = 0; u < (int)sizeof(T) / 2; ++u) reinterpret_cast<uint4 *>(dst)[u] = raw[u];
+        for (int u = 0; u < (int)sizeof(T) / 2; ++u) __stcs(reinterpret_cast<uint4 *>(dst) + u, raw[u]);
     }
     __device__ __forceinline__ void values(float *x) const {
 #pragma unroll
@@ -76,12 +82,15 @@ template <typename T> struct Run8 {
 
 template <typename T, bool kInterleaved>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(const RotaryParams p, int tokens) {
-    extern __shared__ __align__(16) float turn[];          // [tokens][2][half] cosines, sines; then the steps [half]
+    // [tokens][2][half] cosines and sines, the steps [half] and the tokens' rows in the cache [tokens]
+    extern __shared__ __align__(16) float turn[];
     // launched as a dependent of the kernel before; a kernel launched after this one may start
     // its set-up once everything before this one has finished
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int half = p.rotary_dim / 2, D = p.head_dim, parts = D / 16;
+    uint64_t *steps = reinterpret_cast<uint64_t *>(turn + 2 * tokens * half);
+    int64_t *cache = reinterpret_cast<int64_t *>(steps + half);
     const int64_t t0 = (int64_t)blockIdx.x * tokens;
     const int n = (int)min((int64_t)tokens, p.num_tokens - t0);
     const int H = p.num_heads, Hk = p.num_kv_heads, heads = H + Hk * (p.slots ? 2 : 1);
@@ -89,40 +98,71 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(const RotaryParams p, 
     const int part = threadIdx.x % parts, rows = kThreads / parts;
     const bool turned = part * 8 < half;
     const int a = kInterleaved || !turned ? part * 16 : part * 8, b = kInterleaved || !turned ? a + 8 : a + half;
-    const int h0 = threadIdx.x / parts;
 
     struct Unit {
         Run8<T> x[2];
-        T *dst;                                            // null: none
-        bool turns;
+        int i, h;                                          // token, head of the queries, keys and values in turn
     };
-    // head h of the queries, keys and values in turn, of token t; cache: its row there, -1: none
-    auto load = [&](Unit &u, int h, int64_t t, int64_t cache) {
-        u.dst = nullptr;
-        if (h >= heads) return;
-        const T *src;
-        if (h < H) {
-            src = static_cast<const T *>(p.q) + t * p.q_stride + h * D;
-            u.dst = static_cast<T *>(p.q_out) + t * p.q_out_stride + h * D;
-            u.turns = turned;
-        } else {
-            const bool is_v = h >= H + Hk;
-            const int at = (h - H - (is_v ? Hk : 0)) * D;
-            if (cache < 0) return;
-            src = (is_v ? static_cast<const T *>(p.v) + t * p.v_stride : static_cast<const T *>(p.k) + t * p.k_stride) + at;
-            u.dst = static_cast<T *>(is_v ? p.v_out : p.k_out) + cache + at;
-            u.turns = turned && !is_v;
+    // the next row of this thread
+    int i = 0, h = threadIdx.x / parts;
+    if (h >= rows) i = n;                                  // threads that a row's parts do not divide are idle
+    auto load = [&](Unit &u) {
+        while (h >= heads) {
+            h -= heads;
+            ++i;
         }
+        u.i = i;
+        u.h = h;
+        h += rows;
+        if (u.i >= n) return;
+        const int64_t t = t0 + u.i;
+        const T *src = u.h < H        ? static_cast<const T *>(p.q) + t * p.q_stride + u.h * D
+                       : u.h < H + Hk ? static_cast<const T *>(p.k) + t * p.k_stride + (u.h - H) * D
+                                      : static_cast<const T *>(p.v) + t * p.v_stride + (u.h - H - Hk) * D;
         u.x[0].load(src + a);
         u.x[1].load(src + b);
     };
-    auto finish = [&](Unit &u, const float *cs) {
-        if (!u.dst) return;
-        if (u.turns) {
-            float x[16], y[16];
+    Unit u[kUnits];
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) load(u[k]);           // on their way while the angles are made
+
+    // where a token's keys and values go, in elements from the outputs' start; -1: nowhere
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const int64_t t = t0 + i;
+        int64_t row = t * p.k_out_stride;
+        if (p.slots) {
+            const int64_t slot = p.slots[t];
+            const bool good = slot >= 0 && slot < p.num_slots;
+            if (!good && slot != -1) raise_error(p.err, PA_DEVERR_SLOT);
+            row = good ? slot * Hk * D : -1;
+        }
+        cache[i] = row;
+    }
+    for (int j = threadIdx.x; j < half; j += kThreads) steps[j] = turn_step(p.inv_freq[j]);
+    __syncthreads();
+    for (int e = threadIdx.x; e < n * half; e += kThreads) {
+        const int i = e / half, j = e - i * half;
+        const float2 cs = cos_sin(steps[j], p.positions[t0 + i]);
+        turn[2 * i * half + j] = cs.x * p.factor;
+        turn[(2 * i + 1) * half + j] = cs.y * p.factor;
+    }
+    __syncthreads();
+
+    auto finish = [&](Unit &u) {
+        if (u.i >= n) return;
+        const bool is_v = u.h >= H + Hk;
+        T *dst;
+        if (u.h < H) {
+            dst = static_cast<T *>(p.q_out) + (t0 + u.i) * p.q_out_stride + u.h * D;
+        } else {
+            if (cache[u.i] < 0) return;
+            dst = static_cast<T *>(is_v ? p.v_out : p.k_out) + cache[u.i] + (u.h - H - (is_v ? Hk : 0)) * D;
+        }
+        if (turned && !is_v) {
+            const float *cs = turn + 2 * u.i * half + part * 8;
+            float x[16], y[16], c[8], s[8];
             u.x[0].values(x);
             u.x[1].values(x + 8);
-            float c[8], s[8];
 #pragma unroll
             for (int j = 0; j < 8; j += 4) {
                 *reinterpret_cast<float4 *>(c + j) = *reinterpret_cast<const float4 *>(cs + j);
@@ -143,62 +183,24 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(const RotaryParams p, 
             u.x[0].round(y);
             u.x[1].round(y + 8);
         }
-        u.x[0].store(u.dst + a);
-        u.x[1].store(u.dst + b);
+        u.x[0].store(dst + a);
+        u.x[1].store(dst + b);
     };
-    // where a token's keys and values go, in elements from the outputs' start
-    auto cache_row = [&](int64_t t) {
-        if (!p.slots) return t * p.k_out_stride;
-        const int64_t slot = p.slots[t];
-        if (slot >= 0 && slot < p.num_slots) return slot * Hk * D;
-        if (slot != -1 && threadIdx.x == 0) raise_error(p.err, PA_DEVERR_SLOT);
-        return (int64_t)-1;
-    };
-    const bool works = h0 < rows;                          // threads that a row's parts do not divide are idle
-    int64_t cache = cache_row(t0);
-    Unit u[kUnits];
+    while (u[0].i < n) {
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-        u[k].dst = nullptr;
-        if (works) load(u[k], h0 + k * rows, t0, cache);   // on their way while the angles are made
-    }
-
-    uint64_t *steps = reinterpret_cast<uint64_t *>(turn + 2 * tokens * half);
-    for (int j = threadIdx.x; j < half; j += kThreads) steps[j] = turn_step(p.inv_freq[j]);
-    __syncthreads();
-    for (int e = threadIdx.x; e < n * half; e += kThreads) {
-        const int i = e / half, j = e - i * half;
-        const float2 cs = cos_sin(steps[j], p.positions[t0 + i]);
-        turn[2 * i * half + j] = cs.x * p.factor;
-        turn[(2 * i + 1) * half + j] = cs.y * p.factor;
-    }
-    __syncthreads();
-    if (!works) return;
-
-    for (int i = 0; i < n; ++i) {
-        const float *cs = turn + 2 * i * half + part * 8;
-        const int64_t t = t0 + i, next = i + 1 < n ? cache_row(t + 1) : -1;
-        for (int h = h0; h < heads; h += kUnits * rows) {
+        for (int k = 0; k < kUnits; ++k) finish(u[k]);
 #pragma unroll
-            for (int k = 0; k < kUnits; ++k) finish(u[k], cs);
-            // the next ones of this token, or the first of the next
-            const bool same = h + kUnits * rows < heads;
-#pragma unroll
-            for (int k = 0; k < kUnits; ++k) {
-                if (same) load(u[k], h + (kUnits + k) * rows, t, cache);
-                else if (i + 1 < n) load(u[k], h0 + k * rows, t + 1, next);
-            }
-        }
-        cache = next;
+        for (int k = 0; k < kUnits; ++k) load(u[k]);
     }
 }
 
 template <typename T>
 int launch_t(const RotaryParams &p, cudaStream_t stream) {
-    const int tokens = p.num_tokens >= kManyTokens ? kMaxTokens : 1;
-    const int64_t grid = (p.num_tokens + tokens - 1) / tokens;
-    return launch_pdl(p.interleaved ? rotary_kernel<T, true> : rotary_kernel<T, false>, dim3((unsigned)grid),
-                      dim3(kThreads), (size_t)(tokens + 1) * p.rotary_dim * sizeof(float), stream, p, tokens);
+    const int rows = kThreads / (p.head_dim / 16), heads = p.num_heads + p.num_kv_heads * (p.slots ? 2 : 1);
+    const int tokens = p.num_tokens < kManyTokens ? 1 : std::max(1, std::min(kMaxTokens, kTurns * rows / heads));
+    const size_t smem = (size_t)(tokens + 1) * p.rotary_dim * sizeof(float) + tokens * sizeof(int64_t);
+    return launch_pdl(p.interleaved ? rotary_kernel<T, true> : rotary_kernel<T, false>,
+                      dim3((unsigned)((p.num_tokens + tokens - 1) / tokens)), dim3(kThreads), smem, stream, p, tokens);
 }
 
 }  // namespace
