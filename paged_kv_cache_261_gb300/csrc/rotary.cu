@@ -19,10 +19,10 @@
 // of pairs. The first units are loaded before the angles are made.
 //
 // What bounds it (one GB300, inputs and outputs not in L2): HBM, every row being read and written
-// once. 8192 tokens of 32 + 8 + 8 heads, 201 MB, 32.6 us, 6.2 TB/s; 4096 of 128 + 8 + 8, 302 MB, 47.4;
-// 2047 of 64 + 8, 75 MB, 15.0. Two units a thread in flight: with one 33.6 us, three 34.6 (the 8192
-// tokens). With all of a CTA's rows copied asynchronously into shared memory, so more on its way:
-// 46.6. Without the streaming hints 33.4; loads alone hinted 34.4, stores alone 33.7.
+// once. 8192 tokens of 32 + 8 + 8 heads, 201 MB, 32.4 us, 6.2 TB/s; 4096 of 128 + 8 + 8, 302 MB, 47.9;
+// 2047 of 64 + 8, 75 MB, 14.7. Three units a thread in flight: with two 33.4 us (the 8192 tokens). With all of a
+// CTA's rows copied asynchronously into shared memory, so more on its way: 46.6. The streaming hints gain
+// 2 to 3 %, on the loads or the stores alone nothing.
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "kernels_step.h"
@@ -33,10 +33,12 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kUnits = 2;                        // of a thread, in flight together
+constexpr int kUnits = 3;                        // of a thread, in flight together
 constexpr int kTurns = 4;                        // units of a thread that a CTA's tokens are chosen for
 constexpr int kMaxTokens = 8;                    // of a CTA
-constexpr int64_t kManyTokens = 1200;            // up to here a CTA takes one
+// Up to here a CTA takes one token (8 + 1 + 1 heads of 64 channels, us with one and 6: 200 tokens 2.9, 3.4,
+// 1100 3.7, 3.5, 2000 5.8, 3.7).
+constexpr int64_t kManyTokens = 1200;
 
 // inv_freq radians as a number of 2^-64 turns, modulo one turn.
 __device__ __forceinline__ uint64_t turn_step(double inv_freq) {
@@ -82,15 +84,14 @@ template <typename T> struct Run8 {
 
 template <typename T, bool kInterleaved>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(const RotaryParams p, int tokens) {
-    // [tokens][2][half] cosines and sines, the steps [half] and the tokens' rows in the cache [tokens]
+    // [tokens][2][half] cosines and sines, and the tokens' rows in the cache [tokens]
     extern __shared__ __align__(16) float turn[];
     // launched as a dependent of the kernel before; a kernel launched after this one may start
     // its set-up once everything before this one has finished
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int half = p.rotary_dim / 2, D = p.head_dim, parts = D / 16;
-    uint64_t *steps = reinterpret_cast<uint64_t *>(turn + 2 * tokens * half);
-    int64_t *cache = reinterpret_cast<int64_t *>(steps + half);
+    int64_t *cache = reinterpret_cast<int64_t *>(turn + 2 * tokens * half);
     const int64_t t0 = (int64_t)blockIdx.x * tokens;
     const int n = (int)min((int64_t)tokens, p.num_tokens - t0);
     const int H = p.num_heads, Hk = p.num_kv_heads, heads = H + Hk * (p.slots ? 2 : 1);
@@ -138,13 +139,16 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(const RotaryParams p, 
         }
         cache[i] = row;
     }
-    for (int j = threadIdx.x; j < half; j += kThreads) steps[j] = turn_step(p.inv_freq[j]);
-    __syncthreads();
-    for (int e = threadIdx.x; e < n * half; e += kThreads) {
-        const int i = e / half, j = e - i * half;
-        const float2 cs = cos_sin(steps[j], p.positions[t0 + i]);
-        turn[2 * i * half + j] = cs.x * p.factor;
-        turn[(2 * i + 1) * half + j] = cs.y * p.factor;
+    // a thread has a frequency and every groups-th token
+    const int groups = max(1, kThreads / half);
+    for (int e = threadIdx.x; e < groups * half; e += kThreads) {
+        const int g = e / half, j = e - g * half;
+        const uint64_t step = turn_step(p.inv_freq[j]);
+        for (int t = g; t < n; t += groups) {
+            const float2 cs = cos_sin(step, p.positions[t0 + t]);
+            turn[2 * t * half + j] = cs.x * p.factor;
+            turn[(2 * t + 1) * half + j] = cs.y * p.factor;
+        }
     }
     __syncthreads();
 
@@ -198,7 +202,7 @@ template <typename T>
 int launch_t(const RotaryParams &p, cudaStream_t stream) {
     const int rows = kThreads / (p.head_dim / 16), heads = p.num_heads + p.num_kv_heads * (p.slots ? 2 : 1);
     const int tokens = p.num_tokens < kManyTokens ? 1 : std::max(1, std::min(kMaxTokens, kTurns * rows / heads));
-    const size_t smem = (size_t)(tokens + 1) * p.rotary_dim * sizeof(float) + tokens * sizeof(int64_t);
+    const size_t smem = tokens * (p.rotary_dim * sizeof(float) + sizeof(int64_t));
     return launch_pdl(p.interleaved ? rotary_kernel<T, true> : rotary_kernel<T, false>,
                       dim3((unsigned)((p.num_tokens + tokens - 1) / tokens)), dim3(kThreads), smem, stream, p, tokens);
 }
