@@ -599,7 +599,7 @@ int pa_paged_kv_evict(int32_t *kept, int64_t kept_len, const float *mass, int64_
  * stack counts no references. A request whose partly filled last block another table shares
  * must not be served before that block was copied.
  * Supported: block_size a power of two up to 256, num_seqs <= 16384, num_blocks * block_size
- * <= 2^31 - 1; contexts up to 2^31 - 65537 tokens.
+ * <= 2^31 - 1, num_tokens and free_capacity <= 2^30; contexts up to 2^31 - 65537 tokens.
  */
 int pa_paged_blocks_append(int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
                            int32_t *new_context_lens, const int32_t *query_lens, int num_seqs,

@@ -1038,8 +1038,8 @@ def paged_blocks_release(block_tables, context_lens, finished, free_blocks, num_
                          new_context_lens=None, new_num_free=None, num_blocks: int | None = None, stream=None) -> None:
     """Give the blocks of every request b with finished[b] (torch.bool or uint8 [B]) back to the
     stack free_blocks[:num_free] and set its length to 0; its table stays as it is.
-    new_context_lens and new_num_free: as paged_blocks_append. num_blocks (default: the length of
-    free_blocks): block ids are below it."""
+    new_context_lens and new_num_free: as paged_blocks_append. num_blocks (default: no bound): ids at
+    or above it are bad."""
     if _binding is not None:
         rc = _binding.blocks_release(block_tables, context_lens, finished, free_blocks, num_free, block_size,
                                      new_context_lens, new_num_free, num_blocks, stream)
@@ -1080,8 +1080,8 @@ def paged_blocks_release(block_tables, context_lens, finished, free_blocks, num_
                                         stream or torch.cuda.current_stream(dev))
     rc = _lib.pa_paged_blocks_release(block_tables.data_ptr(), mb, context_lens.data_ptr(), out_lens.data_ptr(),
                                       finished.data_ptr(), B, free_blocks.data_ptr(), cap, num_free.data_ptr(),
-                                      out_free.data_ptr(), int(block_size), int(cap if num_blocks is None else
-                                      num_blocks), sp)
+                                      out_free.data_ptr(), int(block_size),
+                                      0x7FFFFFFF // max(int(block_size), 1) if num_blocks is None else int(num_blocks), sp)
     if rc:
         _check(rc, "pa_paged_blocks_release")
 

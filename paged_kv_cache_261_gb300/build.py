@@ -39,7 +39,7 @@ def _torch_version():
     except Exception:
         return None
     import torch
-    return torch.__version__
+    return torch.__version__ if torch.version.cuda else None
 
 
 def binding_path(torch_version: str) -> str:

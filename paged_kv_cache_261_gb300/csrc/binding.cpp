@@ -172,7 +172,7 @@ PyObject *blocks_release(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const int bs = a.small(5);
     const Tensor *new_lens = a.none(6) ? lens : a.vector(6, at::kInt, B), *new_height = a.none(7) ? height : a.scalar(7);
     if (!a.ok) Py_RETURN_NONE;
-    const int64_t blocks = a.none(8) ? free->size(0) : a.integer(8);
+    const int64_t blocks = a.none(8) ? INT_MAX / std::max(bs, 1) : a.integer(8);
     a.on_stream(9);
     if (!a.ok || width > INT_MAX || B > INT_MAX) Py_RETURN_NONE;
     return status(pa_paged_blocks_release(ptr<int32_t>(table), (int)width, ptr<int32_t>(lens), ptr<int32_t>(new_lens),
@@ -335,11 +335,7 @@ PyObject *attention_decode_fp8_block(PyObject *, PyObject *const *args, Py_ssize
         // on another stream than the current one the buffer would have to be allocated there
         if (!a.none(10) && a.stream != c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)a.device).stream()) Py_RETURN_NONE;
         const size_t need = pa_decode_fp8_block_workspace_bytes((int)B, (int)H, (int)c.Hk, (int)c.D, (int)longest);
-        try {
-            ws = workspace(a.device, a.stream, (int64_t)need);
-        } catch (const std::exception &) {
-            Py_RETURN_NONE;                            // refused there too, as torch does it
-        }
+        ws = workspace(a.device, a.stream, (int64_t)need);
     } else {
         const Tensor *given = a.dense(9, at::kByte, 1);
         if (!a.ok) Py_RETURN_NONE;
@@ -351,7 +347,20 @@ PyObject *attention_decode_fp8_block(PyObject *, PyObject *const *args, Py_ssize
         (size_t)ws.numel(), element_code(type), a.stream));
 }
 
-#define PA_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(name)), METH_FASTCALL, nullptr}
+// torch reports failures (a CUDA error left by earlier work, no memory) as exceptions, which must not pass
+// through Python's frames: the Python code meets them again, in its own way.
+template <PyObject *(*kFunction)(PyObject *, PyObject *const *, Py_ssize_t)>
+PyObject *guarded(PyObject *self, PyObject *const *args, Py_ssize_t n) {
+    try {
+        return kFunction(self, args, n);
+    } catch (...) {
+        PyErr_Clear();
+        Py_RETURN_NONE;
+    }
+}
+
+#define PA_METHOD(name) \
+    {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(guarded<name>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {PA_METHOD(blocks_append),      PA_METHOD(blocks_release),    PA_METHOD(rotary_embedding),
                          PA_METHOD(kv_write_rotary),    PA_METHOD(kv_write_fp8_block), PA_METHOD(kv_read_fp8_block),
                          PA_METHOD(attention_decode_fp8_block), {nullptr, nullptr, 0, nullptr}};

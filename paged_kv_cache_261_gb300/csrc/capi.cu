@@ -376,11 +376,14 @@ size_t fp8_block_workspace_bytes(int64_t B, int64_t H, int64_t Hk, int64_t D, in
     return align256(z.rows) + align256(z.part_ml) + align256(z.part_o);
 }
 
+// Tokens of a step and blocks of a stack: a grid's stride beyond either stays in 31 bits.
+constexpr int64_t kMaxLayoutItems = int64_t(1) << 30;
+
 // Validation shared by the calls that turn lengths into tables.
 int layout_setup(int max_blocks_per_seq, int num_seqs, int64_t free_capacity, int block_size, int64_t num_blocks) {
     if (max_blocks_per_seq <= 0 || num_seqs < 0 || free_capacity < 0 || block_size <= 0 || num_blocks <= 0)
         return PA_ERR_INVALID_ARG;
-    if (!pow2(block_size) || block_size > 256 || num_seqs > pa::kMaxLayoutSeqs || free_capacity > INT32_MAX ||
+    if (!pow2(block_size) || block_size > 256 || num_seqs > pa::kMaxLayoutSeqs || free_capacity > kMaxLayoutItems ||
         num_blocks > INT32_MAX / block_size)
         return PA_ERR_UNSUPPORTED;
     return PA_OK;
@@ -1022,7 +1025,7 @@ int pa_paged_blocks_append(int32_t *block_tables, int max_blocks_per_seq, const 
     int rc = layout_setup(max_blocks_per_seq, num_seqs, free_capacity, block_size, num_blocks);
     if (rc != PA_OK) return rc;
     if (num_tokens < 0) return PA_ERR_INVALID_ARG;
-    if (num_tokens > kMaxTokens) return PA_ERR_UNSUPPORTED;
+    if (num_tokens > kMaxLayoutItems) return PA_ERR_UNSUPPORTED;
     if ((num_seqs > 0 && (!block_tables || !context_lens || !new_context_lens || !query_lens)) ||
         (free_capacity > 0 && !free_blocks) || !num_free || !new_num_free || !query_start_loc ||
         (num_tokens > 0 && (!slot_mapping || !positions)))

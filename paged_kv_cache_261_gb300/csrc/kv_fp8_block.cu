@@ -21,11 +21,11 @@
 // side by side in a warp. (Atomic maxima over all tokens, whatever their order, would need the
 // old scales kept beside the new ones and two more launches.)
 //
-// What bounds it (one GB300, 8 kv heads of 128 channels): a decode step's 64 tokens 2.7 us, the latency of
-// three dependent loads; 8192 tokens, 50 MB, 12.2 us, instructions and the same chain with 16 warps an
-// SM (118 registers: four CTAs an SM 12.1 us, three 13.2, five, which spill, 14.4; two rows a lane in
-// registers instead of four were slower). Reading back 131,071 tokens, 805 MB, takes 121 us, 6.65 TB/s, as fast
-// as a copy; 8192 just written 7.2.
+// What bounds it (one GB300, 8 kv heads of 128 channels): a decode step's 64 tokens 2.6 us, the latency of
+// three dependent loads; 8192 tokens, 50 MB, 10.8 us, instructions and the same chain with 16 warps an
+// SM (five CTAs an SM, which spill, 13.1). All CTAs of a few tokens stand next to each other in the grid, so
+// that their rows, which lie side by side, are read at the same time (heads far apart: 12.2). Reading back
+// 131,071 tokens, 805 MB, takes 121 us, 6.65 TB/s, as fast as a copy; 8192 just written 7.2.
 #include "common.cuh"
 #include "kernels_fp8_block.h"
 
@@ -36,11 +36,13 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 128, kWarps = kThreads / 32;
-constexpr int kKeep = 4;                         // rows of a lane held in registers
+// Rows of a lane held in registers: 16 a warp (8192 tokens of 64 channels with 16 and 32 rows a warp 7.8
+// and 9.0 us, of 128 channels with 8 and 16 15.2 and 10.8).
+template <int D> constexpr int kKeep = D / 32;
 constexpr int kMinScaleExp = -100;
-constexpr int kWriteCtas = 4;                    // of the scatter, on an SM
+constexpr int kWriteCtas = 4;                    // of the scatter, on an SM (one less for float32 rows)
 // Tokens written in columns of 4 rather than 32 (8 kv heads, us with 4 and 32: single tokens of 1024
-// sequences 5.6, 13.5, of 2048 9.9, 14.1; 400 tokens of one 3.3, 4.1, 2000 5.5, 4.7, 8192 23.0, 12.2).
+// sequences 5.1, 13.5, of 2048 8.9, 12.2; 400 tokens of one 3.3, 4.1, 2000 5.5, 4.7, 8192 23.0, 10.8).
 constexpr int64_t kFewTokens = 4096;
 // Channels per lane in reading: more where there are enough rows to fill the SMs all the same (us
 // with 8 and 32 channels, 8 kv heads: 100 tokens 1.4, 1.6; 700 1.9, 1.9; 1000 2.4, 2.1).
@@ -56,7 +58,7 @@ template <typename T2, int N> __device__ __forceinline__ uint32_t packed_largest
     for (int i = 0; i < N; ++i)
 #pragma unroll
         for (uint32_t w : {raw[i].x, raw[i].y, raw[i].z, raw[i].w})
-            a = bits2(__hmax2(as2<T2>(a), as2<T2>(w & 0x7FFF7FFFu)));
+            a = bits2(__hmax2(as2<T2>(a), __habs2(as2<T2>(w))));
     return bits2(__hmax2(as2<T2>(a), as2<T2>(__byte_perm(a, a, 0x1032))));
 }
 template <typename T, int N> __device__ __forceinline__ float largest_or_inf(const uint4 (&raw)[N]) {
@@ -173,14 +175,14 @@ __device__ __forceinline__ void reencode(uint4 *codes, int first, int step, int 
     }
 }
 
-// 2^log2_team: warps that share a run (at most kWarps); chunk: tokens of
-// slot_mapping whose runs a CTA column takes (at most 32).
+// 2^log2_team: warps that share a run (at most kWarps); chunk: tokens of slot_mapping whose runs
+// `split` CTAs in a row take (at most 32), so that their rows are read at the same time.
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads, kWriteCtas) void kv_write_fp8_block_kernel(const T *__restrict__ k, const T *__restrict__ v,
+__global__ __launch_bounds__(kThreads, sizeof(T) == 4 ? kWriteCtas - 1 : kWriteCtas) void kv_write_fp8_block_kernel(const T *__restrict__ k, const T *__restrict__ v,
                                                                       int64_t k_stride, int64_t v_stride,
                                                                       const int32_t *__restrict__ slots,
                                                                       int64_t num_tokens, const Fp8BlockCache c,
-                                                                      int log2_team, int chunk, unsigned int *err) {
+                                                                      int log2_team, int chunk, int split, unsigned int *err) {
     constexpr int kLanes = D / 16, kRows = 32 / kLanes;   // lanes of a row; rows of a warp
     __shared__ float maxima[kWarps];
     // launched as a dependent of the kernel before; a kernel launched after this one may start
@@ -192,7 +194,8 @@ __global__ __launch_bounds__(kThreads, kWriteCtas) void kv_write_fp8_block_kerne
     const int Hk = c.num_kv_heads, bs = 1 << c.log2_block_size;
     // the runs that start in this CTA's tokens, from a window of 64: whether a token has a block,
     // continues the run of the token before, is its block's first
-    const int64_t t0 = (int64_t)blockIdx.x * chunk;
+    const uint32_t column = blockIdx.x / (uint32_t)split, place = blockIdx.x - column * split;
+    const int64_t t0 = (int64_t)column * chunk;
     int32_t slot[2];
     int block[2];
 #pragma unroll
@@ -202,7 +205,7 @@ __global__ __launch_bounds__(kThreads, kWriteCtas) void kv_write_fp8_block_kerne
         block[w] = block_of(c, slot[w]);
     }
     const int last = lane == 0 && t0 > 0 ? block_of(c, slots[t0 - 1]) : -1;
-    if (block[0] < 0 && slot[0] != -1 && lane < chunk && blockIdx.y == 0 && warp == 0) raise_error(err, PA_DEVERR_SLOT);
+    if (block[0] < 0 && slot[0] != -1 && lane < chunk && place == 0 && warp == 0) raise_error(err, PA_DEVERR_SLOT);
     uint64_t goes_on = 0, firsts = 0;
     uint32_t starts = 0;
 #pragma unroll
@@ -221,7 +224,7 @@ __global__ __launch_bounds__(kThreads, kWriteCtas) void kv_write_fp8_block_kerne
     };
 
     const int units = 2 * Hk, quads = (units + kRows - 1) / kRows;   // of a run: (kv head, K or V)
-    const int warps = gridDim.y * kWarps, my_warp = blockIdx.y * kWarps + warp;
+    const int warps = split * kWarps, my_warp = place * kWarps + warp;
     const int team = 1 << log2_team, group = warp >> log2_team, member = warp & (team - 1);
     const int teams = warps >> log2_team, my_team = my_warp >> log2_team;
     auto sync = [&] {
@@ -291,27 +294,30 @@ __global__ __launch_bounds__(kThreads, kWriteCtas) void kv_write_fp8_block_kerne
             const T *src = (is_v ? v + first * v_stride : k + first * k_stride) + kvh * D + part;
             const int64_t stride = is_v ? v_stride : k_stride;
             const int row0 = member * kRows + row, step = team * kRows;
-            Run16<T> x[kKeep];
-            int off[kKeep];
+            Run16<T> x[kKeep<D>];
+            uint32_t offs = 0, lives = 0;              // a row's place in its block, a byte each; whether there is one
             float *scale_at = reinterpret_cast<float *>(c.scales + ((int64_t)b * Hk + kvh)) + is_v;
             const float old = *scale_at;
 #pragma unroll
-            for (int j = 0; j < kKeep; ++j) {
+            for (int j = 0; j < kKeep<D>; ++j) {
                 const int i = row0 + j * step;
                 x[j].clear();
                 if (i < n) x[j].load(src + i * stride);
             }
 #pragma unroll
-            for (int j = 0; j < kKeep; ++j) {
+            for (int j = 0; j < kKeep<D>; ++j) {
                 const int i = row0 + j * step;
                 const int32_t in_window = slot_at(min(s + i, 63));
-                off[j] = i >= n ? -1 : (s + i < 64 ? in_window : slots[first + i]) & (bs - 1);
+                if (i < n) {
+                    offs |= (uint32_t)((s + i < 64 ? in_window : slots[first + i]) & (bs - 1)) << (8 * j);
+                    lives |= 1u << j;
+                }
             }
             float amax = 0.f;
 #pragma unroll
-            for (int j = 0; j < kKeep; ++j) amax = fmaxf(amax, x[j].largest());
+            for (int j = 0; j < kKeep<D>; ++j) amax = fmaxf(amax, x[j].largest());
 #pragma unroll 1
-            for (int i = row0 + kKeep * step; i < n; i += step) {   // a long run of a large block
+            for (int i = row0 + kKeep<D> * step; i < n; i += step) {   // a long run of a large block
                 Run16<T> more;
                 more.load(src + i * stride);
                 amax = fmaxf(amax, more.largest());
@@ -331,14 +337,14 @@ __global__ __launch_bounds__(kThreads, kWriteCtas) void kv_write_fp8_block_kerne
             if (held && scale > old) reencode<kLanes>(codes, row0, step, bs, old * inv);
             sync();                                    // older codes before new ones; maxima and the old scale are read
 #pragma unroll
-            for (int j = 0; j < kKeep; ++j) {
+            for (int j = 0; j < kKeep<D>; ++j) {
                 float y[16];
                 x[j].values(y);
-                if (off[j] >= 0) codes[off[j] * kLanes] = encode16(y, inv);
+                if (lives >> j & 1) codes[(offs >> (8 * j) & 255) * kLanes] = encode16(y, inv);
                 asm volatile("" ::: "memory");         // one row after the other, for fewer registers
             }
 #pragma unroll 1
-            for (int i = row0 + kKeep * step; i < n; i += step) {
+            for (int i = row0 + kKeep<D> * step; i < n; i += step) {
                 Run16<T> more;
                 more.load(src + i * stride);
                 float y[16];
@@ -419,17 +425,17 @@ int write_t(const void *k, const void *v, int64_t ks, int64_t vs, const int32_t 
     constexpr int kRows = 32 / (D / 16);               // of a warp
     // as many warps a team as hold a block's rows in registers
     int log2_team = 0;
-    while (1 << log2_team < kWarps && kRows * kKeep << log2_team < 1 << c.log2_block_size) ++log2_team;
+    while (1 << log2_team < kWarps && kRows * kKeep<D> << log2_team < 1 << c.log2_block_size) ++log2_team;
     // Few tokens: a warp for each step of the work, if they are single ones. Many: columns of 32, with
-    // warps for half of the units of a run of as many (8 kv heads, us with half, all and twice the
-    // rows of CTAs: 16,384 tokens, blocks of 16 22.2, 23.8, 30.7; 8192, of 32 12.6, 12.1, 14.3; of 256, f32
-    // 65, 39, 26).
+    // a warp for each unit of a run of 8 (8 kv heads, us with half, as many and twice the CTAs: 16,384 tokens,
+    // blocks of 16 23.9, 21.5, 24.2; 8192, of 32 12.6, 10.8, 13.6; of 256, f32 32.4, 30.8, 36.7).
     const int chunk = n <= kFewTokens ? 4 : 32, Hk = c.num_kv_heads;
     const int64_t y = chunk == 4 ? ((2 * Hk + kRows - 1) / kRows * chunk + kWarps - 1) / kWarps
                                  : ((Hk << log2_team) + 1) / 2;
-    return launch_pdl(kv_write_fp8_block_kernel<T, D>,
-                      dim3((unsigned)((n + chunk - 1) / chunk), (unsigned)std::min<int64_t>(y, 65535)), dim3(kThreads), 0,
-                      s, (const T *)k, (const T *)v, ks, vs, slots, n, c, log2_team, chunk, err);
+    const int64_t columns = (n + chunk - 1) / chunk;
+    const int split = (int)std::max<int64_t>(1, std::min(y, INT32_MAX / columns));
+    return launch_pdl(kv_write_fp8_block_kernel<T, D>, dim3((unsigned)(columns * split)), dim3(kThreads), 0, s,
+                      (const T *)k, (const T *)v, ks, vs, slots, n, c, log2_team, chunk, split, err);
 }
 
 template <typename T, int D>

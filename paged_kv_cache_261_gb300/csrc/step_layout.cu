@@ -191,7 +191,7 @@ __global__ __launch_bounds__(kMaxThreads) void blocks_append_kernel(const Blocks
         // stores where they share a request: 10.2 us against 7.5 for 139,000 tokens of 1024 requests, 6.6
         // against 4.7 for 17,500 of 192.)
         const int live = start[B];
-        for (int t = gid; t < T; t += threads) {       // (T is below 2^31 - 65536)
+        for (int t = gid; t < T; t += threads) {       // (T is at most 2^30)
             int slot = -1, pos = 0;
             if (t < live) {
                 const int b = owner(start, B, t), c = ctx[b];

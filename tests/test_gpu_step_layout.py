@@ -140,6 +140,17 @@ def test_release_out_of_range(pa):
     run_release(pa, np.zeros((0, 4), np.int32), np.zeros(0, np.int32), [], free, 3, 8, NB)
 
 
+@pytest.mark.parametrize("plain", [False, True])
+def test_release_onto_a_stack_shorter_than_the_pool(pa, monkeypatch, plain):
+    """Without num_blocks every id goes back, whatever the stack's capacity."""
+    if plain:
+        monkeypatch.setattr(pa, "_binding", None)
+    table, lens, free, n = t32([[900, 3], [77, 5000]]), t32([20, 9]), t32([8, 0, 0, 0]), t32([1])
+    pa.paged_blocks_release(table, lens, torch.tensor([True, True], device=dev()), free, n, 16)
+    assert free.tolist() == [8, 900, 3, 77] and int(n) == 4 and lens.tolist() == [0, 0]
+    assert pa.get_device_error() == 0
+
+
 def test_python_refusals(pa):
     bt, x2, x3, x8, one = (t32(np.zeros(s)) for s in ((2, 4), 2, 3, 8, 1))
     ok = [bt, x2, x2.clone(), x8, one, x3, x8.clone(), x8.clone(), 16, 8]

@@ -28,7 +28,7 @@ def _append(pa, **kw):
     (dict(mb=0), INVALID), (dict(B=-1), INVALID), (dict(B=16385), UNSUPPORTED), (dict(cap=-1), INVALID),
     (dict(cap=1 << 31), UNSUPPORTED), (dict(bs=0), INVALID), (dict(bs=12), UNSUPPORTED), (dict(bs=512), UNSUPPORTED),
     (dict(nb=0), INVALID), (dict(nb=1 << 27), UNSUPPORTED), (dict(T=-1), INVALID), (dict(T=2 ** 31 - 1), UNSUPPORTED),
-    (dict(bt=None), INVALID), (dict(cl=None), INVALID), (dict(ncl=None), INVALID), (dict(ql=None), INVALID),
+    (dict(T=2 ** 30 + 1), UNSUPPORTED), (dict(cap=2 ** 30 + 1), UNSUPPORTED), (dict(bt=None), INVALID), (dict(cl=None), INVALID), (dict(ncl=None), INVALID), (dict(ql=None), INVALID),
     (dict(free=None), INVALID), (dict(nf=None), INVALID), (dict(nnf=None), INVALID), (dict(start=None), INVALID),
     (dict(slots=None), INVALID), (dict(pos=None), INVALID)])
 def test_append_refusals(pa, bad, code):
