@@ -735,7 +735,8 @@ size_t pa_decode_fp8_block_workspace_bytes(int num_seqs, int num_heads, int num_
  * [num_seqs, num_heads, head_dim], PA_DTYPE_BF16 or PA_DTYPE_F16; num_heads / num_kv_heads <= 16.
  * Codes and scales past a context's end are never used, whatever they hold; a NaN code or scale
  * inside a context makes outputs of its heads NaN. The work is cut into equal runs of tokens
- * over the device, whatever the lengths (there is no partition size). max_context_len, the
+ * over the device, whatever the lengths, or, where max_context_len is short and sequences are
+ * few, into equal parts of each sequence (there is no partition size). max_context_len, the
  * workspace (size from pa_decode_fp8_block_workspace_bytes; NULL = cudaMallocAsync on the
  * stream; it serves one call at a time, so calls that may run at the same time need one each)
  * and the device error bits are those of pa_paged_attention_decode.

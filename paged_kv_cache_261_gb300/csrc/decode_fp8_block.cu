@@ -29,7 +29,9 @@
 //
 // Work: the stages (kTok tokens of one sequence and kv head) of the whole call, in order, are
 // cut into equal runs, one for each warp of the persistent grid (decode_runs.cuh). Warps share
-// nothing. Each warp fetches its own stages, one ahead and across rows, into its own ring: a
+// nothing. Few rows of short contexts are too little work to cut so: there one to eight CTAs, a
+// cluster, take each row, its stages dealt to their warps in equal parts, and join the parts
+// through each other's shared memory, without a second kernel (row_cluster). Each warp fetches its own stages, one ahead and across rows, into its own ring: a
 // block of one kv head is one contiguous run for K and V each, so a stage is a few untiled bulk
 // copies, and its blocks' scales one 8-byte copy each, all on one mbarrier. (Boxes that TMA
 // swizzles, so that the lanes of a fragment do not meet on few banks, changed nothing: 52.9 and
@@ -46,6 +48,7 @@
 #include "decode_runs.cuh"
 #include "kernels_fp8_block.h"
 
+#include <mutex>
 #include <type_traits>
 
 namespace pa {
@@ -62,6 +65,8 @@ constexpr int kMinScaleExp = -100, kMaxScaleExp = 121;   // of the V scales' ref
 
 __host__ __device__ constexpr int stage_tokens(int D) { return 4096 / D; }
 constexpr int kWarps = 8;                         // of a CTA, one CTA an SM
+constexpr int kMaxCluster = 8;                    // CTAs of a row, where CTAs take rows
+constexpr int kRowStages = 7;                     // of a warp, then, at most
 
 template <int D> struct Cfg {
     static constexpr int kThreads = kWarps * 32;
@@ -77,7 +82,11 @@ template <int D> struct Cfg {
     static constexpr int kOffMisc = kOffBar + kWarps * kStages * 8;   // abort flag; warp sums of the prefix
     static constexpr int kOffPre = kOffMisc + 16 + kWarps * 4;        // int [kMaxSeqs + 1]
     static constexpr int kSmem = kOffPre + (kMaxSeqs + 1) * 4;
-    static_assert(kSmem <= 232448, "shared memory budget");
+    // where CTAs take rows, then: partials float [kWarps + 1][GT][D], the last of them the CTA's, and their
+    // float2 (reference, sum) [kWarps + 1][GT]
+    static constexpr int kOffPart = (kSmem + 15) / 16 * 16;
+    static constexpr int part_bytes(int GT) { return (kWarps + 1) * GT * (D * 4 + 8); }
+    static_assert(kOffPart + part_bytes(16) <= 232448, "shared memory budget");
     static_assert(kSlot % 16 == 0 && kOffV % 16 == 0 && kOffScale % 16 == 0, "bulk copies start on 16 bytes");
     static_assert(kPieces <= 8, "a lane per piece");
 };
@@ -102,8 +111,52 @@ __device__ __forceinline__ void arrive_after_copies(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// GT: query heads padded to 8 or 16.
-template <typename T, int D, int GT>
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return n;
+}
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Where CTA `rank` of the cluster has what this CTA has at p, and what is there.
+__device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float2 load_peer2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 load_peer4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+// Adds a partial (its reference and sum, its outputs) to a joined one whose reference is M.
+__device__ __forceinline__ void join_partial(float M, float2 ml, float4 o, float &L, float4 &acc) {
+    // a partial whose scores are all NaN has no reference and a NaN sum: keep the NaN
+    const float c = ml.x == -INFINITY ? (ml.y == ml.y ? 0.f : ml.y) : fast_exp2(ml.x - M);
+    L = fmaf(ml.y, c, L);
+    acc.x = fmaf(o.x, c, acc.x);
+    acc.y = fmaf(o.y, c, acc.y);
+    acc.z = fmaf(o.z, c, acc.z);
+    acc.w = fmaf(o.w, c, acc.w);
+}
+
+// GT: query heads padded to 8 or 16. kRowCta: a cluster of CTAs takes a row, its warps equal parts of it.
+template <typename T, int D, int GT, bool kRowCta>
 __global__ __launch_bounds__(Cfg<D>::kThreads, 1) void decode_fp8_block_kernel(const DecodeParams p,
                                                                                      const RunWork ws) {
     using C = Cfg<D>;
@@ -131,16 +184,36 @@ __global__ __launch_bounds__(Cfg<D>::kThreads, 1) void decode_fp8_block_kernel(c
     // call's lengths) overlap the preceding kernel
     asm volatile("griddepcontrol.launch_dependents;");
     auto context = [&](int b) { return clamped_context(p, b); };
-    count_stages<kThreads, C::kTok>(p, pre, warp_sums);
-    __syncthreads();
-    const uint32_t total = (uint32_t)pre[B] * Hk;      // below 2^31: the host sees to it
-    const uint32_t num_runs = max(1u, min(gridDim.x * kWarps, total));
-    const Runs runs(total, num_runs);
-    // runs go to the SMs in turn, so few of them still use all
-    const uint32_t run = warp * gridDim.x + blockIdx.x;
+    float *parts = reinterpret_cast<float *>(smem + C::kOffPart);                  // [kWarps + 1][G][D]
+    float2 *part_ml = reinterpret_cast<float2 *>(parts + (kWarps + 1) * GT * D);   // [kWarps + 1][G]
     int todo = 0;
     Cursor at = {};
-    if (run < num_runs && total > 0) {
+    [[maybe_unused]] uint32_t run = 0, total = 0, num_runs = 1;
+    if constexpr (kRowCta) {
+        const int row = blockIdx.x / cluster_size(), warps = cluster_size() * kWarps;
+        at.b = row / Hk;
+        at.kvh = row - at.b * Hk;
+        at.ctx = context(at.b);
+        at.ns = (at.ctx + C::kTok - 1) / C::kTok;
+        const int per = (at.ns + warps - 1) / warps;
+        at.s = min(at.ns, (int)(cluster_rank() * kWarps + warp) * per);
+        todo = min(at.ns, at.s + per) - at.s;
+        if (tid == 0 && at.kvh == 0 && cluster_rank() == 0 && at.ctx != p.context_lens[at.b])
+            raise_error(p.err, PA_DEVERR_CONTEXT);
+        // a warp without stages leaves a partial of nothing
+        for (int i = lane; i < G * D && todo == 0; i += 32) parts[warp * G * D + i] = 0.f;
+        for (int g = lane; g < G; g += 32) part_ml[warp * G + g] = make_float2(-INFINITY, 0.f);
+        __syncthreads();                               // the barriers stand
+    } else {
+        count_stages<kThreads, C::kTok>(p, pre, warp_sums);
+        __syncthreads();
+        total = (uint32_t)pre[B] * Hk;                 // below 2^31: the host sees to it
+        num_runs = max(1u, min(gridDim.x * kWarps, total));
+    }
+    const Runs runs(total, num_runs);
+    // runs go to the SMs in turn, so few of them still use all
+    if constexpr (!kRowCta) run = warp * gridDim.x + blockIdx.x;
+    if (!kRowCta && run < num_runs && total > 0) {
         const uint32_t run0 = runs.first(run);
         todo = (int)(runs.len + (run < runs.longer ? 1 : 0));
         int lo = 0, hi = B - 1;                        // the first b whose stages end after run0
@@ -157,6 +230,7 @@ __global__ __launch_bounds__(Cfg<D>::kThreads, 1) void decode_fp8_block_kernel(c
     }
     // the next row that has stages (there is one)
     auto next_row = [&](Cursor &c) {
+        if constexpr (kRowCta) return;                 // there is none
         c.s = 0;
         if (++c.kvh < Hk) return;
         c.kvh = 0;
@@ -233,10 +307,11 @@ __global__ __launch_bounds__(Cfg<D>::kThreads, 1) void decode_fp8_block_kernel(c
             if (i < todo) fetch(c[i], e[i], i);
         entry = look_up(nx);
     }
-    describe_rows<kThreads>(p, ws.rows, pre, runs);
-    zero_empty_rows<T, D, kThreads>(p, pre);
-
-    if (todo == 0) return;
+    if constexpr (!kRowCta) {
+        describe_rows<kThreads>(p, ws.rows, pre, runs);
+        zero_empty_rows<T, D, kThreads>(p, pre);
+        if (todo == 0) return;
+    }
     int left = todo;                                   // stages to consume
     int unfetched = todo - min(todo, kStages);         // and to fetch
     int sl = 0;                                        // the slot of the next stage
@@ -249,7 +324,7 @@ __global__ __launch_bounds__(Cfg<D>::kThreads, 1) void decode_fp8_block_kernel(c
         // ---- the part of row (b, kvh) that lies in this run
         const int I_b = at.b, I_kvh = at.kvh;
         const int s_end = min(at.ns, at.s + left);
-        const bool whole = at.s == 0 && s_end == at.ns;
+        const bool whole = !kRowCta && at.s == 0 && s_end == at.ns;
         const int64_t head0 = (int64_t)I_b * p.num_heads + (int64_t)I_kvh * G;
 
         // the group's query as B fragments, and the factors of x = S * (k_scale * sa) of the
@@ -491,12 +566,15 @@ __global__ __launch_bounds__(Cfg<D>::kThreads, 1) void decode_fp8_block_kernel(c
                         for (int u = 0; u < 8; ++u) h[u] = Elem<T>::from_f(v[u]);
                         *reinterpret_cast<uint4 *>(out + (head0 + g) * D + d0 + 2 * u0) = *reinterpret_cast<uint4 *>(h);
                     } else {
-                        float *dst = ws.part_o + ((int64_t)(run + r) * G + g) * D + d0 + 2 * u0;
+                        float *dst = (kRowCta ? parts + (warp * G + g) * D
+                                              : ws.part_o + ((int64_t)(run + r) * G + g) * D) + d0 + 2 * u0;
                         *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
                         *reinterpret_cast<float4 *>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
                     }
                 }
-                if (li == 0 && !whole) ws.part_ml[(int64_t)(run + r) * G + g] = make_float2(-(c ? nm[nt].y : nm[nt].x), ls);
+                if (li == 0 && !whole)
+                    (kRowCta ? part_ml[warp * G + g] : ws.part_ml[(int64_t)(run + r) * G + g]) =
+                        make_float2(-(c ? nm[nt].y : nm[nt].x), ls);
             }
         if (left > 0) next_row(at);
     }
@@ -512,12 +590,51 @@ __global__ __launch_bounds__(Cfg<D>::kThreads, 1) void decode_fp8_block_kernel(c
             }
         }
     }
+    if constexpr (kRowCta) {
+        // The warps' partials joined into the CTA's, and the CTAs' into the row, each CTA taking a part of it.
+        __syncthreads();
+        const int C4 = D / 4;
+        for (int i = tid; i < G * C4; i += kThreads) {
+            const int g = i / C4, d = (i - g * C4) * 4;
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, part_ml[w * G + g].x);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                join_partial(M, part_ml[w * G + g], *reinterpret_cast<const float4 *>(parts + (w * G + g) * D + d), L, acc);
+            *reinterpret_cast<float4 *>(parts + (kWarps * G + g) * D + d) = acc;
+            if (d == 0) part_ml[kWarps * G + g] = make_float2(M, L);
+        }
+        cluster_sync();
+        const int n = (int)cluster_size();
+        const int64_t head0 = (int64_t)at.b * p.num_heads + (int64_t)at.kvh * G;
+        for (int i = (int)cluster_rank() * kThreads + tid; i < G * C4; i += n * kThreads) {
+            const int g = i / C4, d = (i - g * C4) * 4;
+            float M = -INFINITY, L = 0.f;
+            for (int r = 0; r < n; ++r) M = fmaxf(M, load_peer2(peer_addr(part_ml + kWarps * G + g, r)).x);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int r = 0; r < n; ++r)
+                join_partial(M, load_peer2(peer_addr(part_ml + kWarps * G + g, r)),
+                             load_peer4(peer_addr(parts + (kWarps * G + g) * D + d, r)), L, acc);
+            const float inv = at.ctx > 0 ? 1.f / L : 0.f;          // an empty context: zeros
+            alignas(8) T h[4] = {Elem<T>::from_f(acc.x * inv), Elem<T>::from_f(acc.y * inv), Elem<T>::from_f(acc.z * inv),
+                                 Elem<T>::from_f(acc.w * inv)};
+            *reinterpret_cast<uint2 *>(out + (head0 + g) * D + d) = *reinterpret_cast<uint2 *>(h);
+        }
+        cluster_sync();                                // no CTA leaves while another reads its memory
+    }
+}
+
+// One CTA per SM, and no more than there can be stages.
+int launch_grid(int64_t rows, int64_t stages, int sms) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>(sms, rows * stages));
 }
 
 template <typename T, int D, int GT>
-int launch_t(const DecodeParams &p, const RunWork &ws, int64_t max_ctx, int grid, cudaStream_t stream) {
+int launch_runs(const DecodeParams &p, const RunWork &ws, int64_t max_ctx, int grid, cudaStream_t stream) {
     using C = Cfg<D>;
-    auto kern = decode_fp8_block_kernel<T, D, GT>;
+    auto kern = decode_fp8_block_kernel<T, D, GT, false>;
     static bool attr_set[kMaxDevices] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
@@ -529,13 +646,82 @@ int launch_t(const DecodeParams &p, const RunWork &ws, int64_t max_ctx, int grid
     return rc != 0 ? rc : launch_join<T, D>(p, ws, max_ctx, C::kTok, (int64_t)grid * kWarps, stream);
 }
 
+// CTAs that take rows, `cluster` to a row.
+template <typename T, int D, int GT> struct RowCtas {
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = {};
+    RowCtas(int64_t rows, int cluster, cudaStream_t stream) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)cluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.gridDim = dim3((unsigned)(rows * cluster));
+        cfg.blockDim = dim3(Cfg<D>::kThreads);
+        cfg.dynamicSmemBytes = Cfg<D>::kOffPart + Cfg<D>::part_bytes(GT);
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+    }
+    RowCtas(const RowCtas &) = delete;
+
+    // How many clusters of 2^i CTAs the device holds at once; -1 in [0] on an error.
+    static const int *room(int dev) {
+        static std::once_flag once[kMaxDevices];
+        static int n[kMaxDevices][4];
+        std::call_once(once[dev], [&] {
+            auto kern = decode_fp8_block_kernel<T, D, GT, true>;
+            for (int i = 0; i < 4; ++i) {
+                RowCtas l(1, 1 << i, nullptr);
+                if ((i == 0 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                    (int)l.cfg.dynamicSmemBytes) != cudaSuccess) ||
+                    cudaOccupancyMaxActiveClusters(&n[dev][i], kern, &l.cfg) != cudaSuccess) {
+                    n[dev][0] = -1;
+                    return;
+                }
+            }
+        });
+        return n[dev];
+    }
+};
+
+// CTAs of a row where CTAs take rows and join what their warps have themselves, or 0: runs and a joining kernel,
+// which costs about as much as a warp's stage, 1.6 us. So rows where no warp has more than one stage beyond what
+// runs would give it (and few at all: runs even out lengths below the bound). A cluster doubles while its CTAs
+// have stages and all clusters have room at once: 16 of eight CTAs, of which 14 have, are slower than runs.
+// us, runs and rows, of G 4 and D 128, by rows and stages of the longest: 8 and 2 5.7, 4.0; 8 and 10 5.6, 5.0;
+// 8 and 22 5.9, 5.1; 8 and 63 7.0, 5.6; 8 and 125 7.8, 7.0; 14 and 125 9.3, 7.5; 32 and 32 6.5, 5.7; 64 and 32 8.7, 6.7;
+// 64 and 63 10.7, 9.3; 96 and 32 9.5, 8.9; 128 and 4 6.5, 4.6; 128 and 32 10.7, 8.9; 144 and 54 13.4, 12.7; not taken: 128 and
+// 63 13.4, 13.9, 16 and 125 8.4, 12.1 (eight CTAs). 32 rows of 32 stages of G 16, f16: 9.5, 8.3.
+int row_cluster(int64_t rows, int64_t stages, int sms, const int *room) {
+    if (rows > room[0]) return 0;
+    int i = 0;
+    while ((2 << i) <= kMaxCluster && kWarps << i < stages && rows <= room[i + 1]) ++i;
+    const int64_t mine = (stages + (kWarps << i) - 1) / (kWarps << i);
+    const int64_t runs = (rows * stages + (int64_t)sms * kWarps - 1) / ((int64_t)sms * kWarps);
+    return mine <= std::min<int64_t>(runs + 1, kRowStages) ? 1 << i : 0;
+}
+
+template <typename T, int D, int GT>
+int launch_t(const DecodeParams &p, const RunWork &ws, int64_t max_ctx, int64_t stages, int sms, cudaStream_t stream) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
+    const int64_t rows = (int64_t)p.num_seqs * p.num_kv_heads;
+    const int *room = RowCtas<T, D, GT>::room(dev);
+    if (room[0] < 0) return -1;
+    const int cluster = row_cluster(rows, stages, sms, room);
+    if (cluster == 0) return launch_runs<T, D, GT>(p, ws, max_ctx, launch_grid(rows, stages, sms), stream);
+    RowCtas<T, D, GT> l(rows, cluster, stream);
+    return cudaLaunchKernelEx(&l.cfg, decode_fp8_block_kernel<T, D, GT, true>, p, ws) == cudaSuccess ? 0 : -1;
+}
+
 template <typename T>
-int launch_d(const DecodeParams &p, const RunWork &ws, int64_t max_ctx, int grid, cudaStream_t stream) {
+int launch_d(const DecodeParams &p, const RunWork &ws, int64_t max_ctx, int64_t stages, int sms, cudaStream_t stream) {
     if (p.head_dim == 128)
-        return p.group <= 8 ? launch_t<T, 128, 8>(p, ws, max_ctx, grid, stream)
-                            : launch_t<T, 128, 16>(p, ws, max_ctx, grid, stream);
-    return p.group <= 8 ? launch_t<T, 64, 8>(p, ws, max_ctx, grid, stream)
-                        : launch_t<T, 64, 16>(p, ws, max_ctx, grid, stream);
+        return p.group <= 8 ? launch_t<T, 128, 8>(p, ws, max_ctx, stages, sms, stream)
+                            : launch_t<T, 128, 16>(p, ws, max_ctx, stages, sms, stream);
+    return p.group <= 8 ? launch_t<T, 64, 8>(p, ws, max_ctx, stages, sms, stream)
+                        : launch_t<T, 64, 16>(p, ws, max_ctx, stages, sms, stream);
 }
 
 int64_t row_stages(int64_t max_ctx, int64_t head_dim) {
@@ -546,11 +732,6 @@ int64_t row_stages(int64_t max_ctx, int64_t head_dim) {
 // Sequences per launch: what the kernel's prefix holds, and a launch's stages in 31 bits.
 int64_t seqs_per_launch(int64_t stages, int64_t kv_heads) {
     return std::max<int64_t>(1, std::min<int64_t>(kMaxSeqs, INT32_MAX / std::max<int64_t>(stages * kv_heads, 1)));
-}
-
-// One CTA per SM, and no more than there can be stages.
-int launch_grid(int64_t rows, int64_t stages, int sms) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>(sms, rows * stages));
 }
 
 }  // namespace
@@ -587,9 +768,8 @@ int launch_decode_fp8_block(const DecodeParams &p, const RunWork &ws, int64_t ma
         c.out = static_cast<char *>(p.out) + first;
         c.block_tables = p.block_tables + (int64_t)b0 * p.max_blocks_per_seq;
         c.context_lens = p.context_lens + b0;
-        const int grid = launch_grid((int64_t)c.num_seqs * c.num_kv_heads, stages, sms);
-        const int rc = dtype == PA_DTYPE_BF16 ? launch_d<__nv_bfloat16>(c, ws, max_ctx, grid, stream)
-                                              : launch_d<__half>(c, ws, max_ctx, grid, stream);
+        const int rc = dtype == PA_DTYPE_BF16 ? launch_d<__nv_bfloat16>(c, ws, max_ctx, stages, sms, stream)
+                                              : launch_d<__half>(c, ws, max_ctx, stages, sms, stream);
         if (rc != 0) return rc;
     }
     return 0;

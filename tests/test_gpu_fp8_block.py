@@ -374,3 +374,32 @@ def test_offsets_past_32_bits(pa):
     ref, tol = expected(q[0].double().cpu().numpy(), hk, hv, D ** -0.5, "f16")
     assert (np.abs(out[0].double().cpu().numpy() - ref) <= tol).all()
     assert pa.get_device_error() == 0
+
+
+SHORT = [1, 7, 0, 15, 16, 17, 31, 33, 64, 127, 128, 129, 300, 513, 1000, 1024]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("H,Hk,D,bs", [(8, 8, 128, 16), (36, 9, 128, 16), (6, 2, 64, 8), (7, 1, 128, 32), (16, 2, 64, 64),
+                                       (12, 1, 128, 256), (32, 2, 128, 8), (10, 2, 64, 16), (16, 1, 64, 8),
+                                       (3, 3, 64, 128), (24, 4, 128, 16), (9, 3, 64, 32)])
+def test_decode_rows_of_ctas(pa, dtype, H, Hk, D, bs):
+    """Few rows of short contexts, which clusters of one to eight CTAs take: CTAs and warps without a stage, parts of a
+    stage, several; the same contexts under a longer bound, which are cut into runs."""
+    case = Case(np.random.default_rng(43 + H + D + bs), SHORT, H, Hk, D, bs, dtype, gain=2.0)
+    out = case.run(pa, max_context_len=1024)
+    case.check(out)
+    assert torch.equal(out, case.run(pa, max_context_len=1024))
+    case.check(case.run(pa, max_context_len=9000))
+    case.check(case.run(pa, max_context_len=40000))
+    assert (out[2] == 0).all() and pa.get_device_error() == 0
+    # NaN in one row's context, a bad block and bad lengths in others
+    want = out.clone()
+    case.t["kc"][int(case.bt[15, 0]), 0, 3, 9] = 0x7F
+    case.t["bt"][14, 1] = case.NB
+    case.t["lens"][:2] = torch.tensor([-1, 5000], dtype=torch.int32)
+    out = case.run(pa, max_context_len=1024)
+    assert pa.get_device_error() == pa.PA_DEVERR_BLOCK_ID | pa.PA_DEVERR_CONTEXT
+    G = H // Hk
+    assert torch.isnan(out[15, :G]).all() and torch.equal(out[15, G:], want[15, G:])
+    assert (out[0] == 0).all() and torch.isfinite(out[14]).all() and torch.equal(out[3:14], want[3:14])
