@@ -48,6 +48,7 @@
 #include "decode_runs.cuh"
 #include "kernels_fp8_block.h"
 
+#include <atomic>
 #include <mutex>
 #include <type_traits>
 
@@ -665,22 +666,23 @@ template <typename T, int D, int GT> struct RowCtas {
     }
     RowCtas(const RowCtas &) = delete;
 
-    // How many clusters of 2^i CTAs the device holds at once; -1 in [0] on an error.
+    // How many clusters of 2^i CTAs the device holds at once (asked for once); null on an error.
     static const int *room(int dev) {
-        static std::once_flag once[kMaxDevices];
+        static std::atomic<bool> known[kMaxDevices];
+        static std::mutex asking;
         static int n[kMaxDevices][4];
-        std::call_once(once[dev], [&] {
-            auto kern = decode_fp8_block_kernel<T, D, GT, true>;
-            for (int i = 0; i < 4; ++i) {
-                RowCtas l(1, 1 << i, nullptr);
-                if ((i == 0 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                    (int)l.cfg.dynamicSmemBytes) != cudaSuccess) ||
-                    cudaOccupancyMaxActiveClusters(&n[dev][i], kern, &l.cfg) != cudaSuccess) {
-                    n[dev][0] = -1;
-                    return;
-                }
-            }
-        });
+        if (known[dev].load(std::memory_order_acquire)) return n[dev];
+        const std::lock_guard<std::mutex> lock(asking);
+        if (known[dev].load(std::memory_order_relaxed)) return n[dev];
+        auto kern = decode_fp8_block_kernel<T, D, GT, true>;
+        for (int i = 0; i < 4; ++i) {
+            RowCtas l(1, 1 << i, nullptr);
+            if (i == 0 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)l.cfg.dynamicSmemBytes) != cudaSuccess)
+                return nullptr;
+            if (cudaOccupancyMaxActiveClusters(&n[dev][i], kern, &l.cfg) != cudaSuccess) return nullptr;
+        }
+        known[dev].store(true, std::memory_order_release);
         return n[dev];
     }
 };
@@ -708,7 +710,7 @@ int launch_t(const DecodeParams &p, const RunWork &ws, int64_t max_ctx, int64_t 
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
     const int64_t rows = (int64_t)p.num_seqs * p.num_kv_heads;
     const int *room = RowCtas<T, D, GT>::room(dev);
-    if (room[0] < 0) return -1;
+    if (room == nullptr) return -1;
     const int cluster = row_cluster(rows, stages, sms, room);
     if (cluster == 0) return launch_runs<T, D, GT>(p, ws, max_ctx, launch_grid(rows, stages, sms), stream);
     RowCtas<T, D, GT> l(rows, cluster, stream);

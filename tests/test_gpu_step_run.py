@@ -1,6 +1,10 @@
 """A serving loop's steps over a block-scaled 8-bit cache, as they would be used together: blocks given back
 and taken on the GPU, queries and keys rotated, keys and values stored, the cache attended and read back;
 eagerly, captured in graphs, on two streams, and beside the host allocator's forks."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -444,3 +448,34 @@ def test_refusals_are_the_same_both_ways(pa, monkeypatch):
         pa.paged_blocks_release(t, i, i.to(torch.uint8), i, one, 16)
         monkeypatch.setattr(pa, "_binding", None)
     assert pa.get_device_error() == 0
+
+
+FIRST_CALLS = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import numpy as np, torch
+from test_gpu_step_run import Loop, Model, plan
+import paged_kv_cache_261_gb300 as pa
+loop = Loop(pa, 30, 5, 40)
+model = Model(loop)
+steps = list(plan(np.random.default_rng(31), loop, 3))
+x = loop.feed(*steps[0])
+torch.index_select(loop.q, 0, loop.last)             # torch's own first calls
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    loop.step()
+for i, (new, done) in enumerate(steps):
+    if i:
+        x = loop.feed(new, done)
+    g.replay()
+    model.check(x, new, done)
+"""
+
+
+def test_first_calls_of_a_process_are_captured(pa):
+    """What the library asks the device once (kernels' shared memory, how many clusters have room) may be asked
+    inside a capture."""
+    tests = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=os.path.dirname(tests), tests=tests)],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
