@@ -246,6 +246,8 @@ def expected(q, k, v, scale, dtype):
     return ref, np.abs(ref) * eps / 2 + (1 + eps) * (rel * wv + small) + eps * 2.0 ** -14
 
 
+RUNS = 100000                                # a bound on the contexts at which any call is cut into runs
+
 RAGGED = [1, 7, 0, 15, 16, 17, 31, 33, 64, 127, 128, 129, 300, 513, 1000, 1025]
 
 
@@ -260,6 +262,7 @@ def test_decode_ragged(pa, dtype, H, Hk, D, bs):
     case.check(out)
     assert torch.equal(out, case.run(pa, max_context_len=max(RAGGED)))
     case.check(case.run(pa))
+    case.check(case.run(pa, max_context_len=RUNS))
     assert pa.get_device_error() == 0
 
 
@@ -269,7 +272,8 @@ def test_decode_ragged(pa, dtype, H, Hk, D, bs):
 def test_decode_cuts(pa, lens, H, Hk):
     """Rows that one run covers, rows cut into many, runs over many rows, batches of several launches."""
     case = Case(np.random.default_rng(3), lens, H, Hk, 128, 16, "f16")
-    case.check(case.run(pa, max_context_len=max(1, max(lens))))
+    for bound in (max(1, max(lens)), RUNS):
+        case.check(case.run(pa, max_context_len=bound))
     assert pa.get_device_error() == 0
 
 
@@ -281,6 +285,7 @@ def test_decode_ranges(pa, dtype, gain, k_size, v_size, spread, D):
     """Peaked and flat softmaxes; caches and queries of large and of tiny values; blocks of unlike size."""
     case = Case(np.random.default_rng(21), [400, 90], 8, 2, D, 16, dtype, gain, k_size, v_size, spread)
     case.check(case.run(pa))
+    case.check(case.run(pa, max_context_len=RUNS))
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -291,17 +296,19 @@ def test_decode_v_blocks_far_apart(pa, D):
     case.sc[case.bt[1, :19], :, 1] = np.float32(2.0 ** -100)
     case.t["sc"].copy_(torch.from_numpy(case.sc))
     case.check(case.run(pa))
+    case.check(case.run(pa, max_context_len=RUNS))
 
 
-def test_decode_nan_and_bad_blocks(pa):
+@pytest.mark.parametrize("bound", [0, RUNS])
+def test_decode_nan_and_bad_blocks(pa, bound):
     """A NaN code of K or V, or a NaN scale, reaches the outputs of its kv head and no other's; bad block
     ids read as zeros."""
     case = Case(np.random.default_rng(29), [100, 60, 100, 70], 8, 2, 128, 16, "bf16")
-    want = case.run(pa).clone()
+    want = case.run(pa, max_context_len=bound).clone()
     case.t["kc"][int(case.bt[0, 2]), 1, 3, 77] = 0x7F
     case.t["vc"][int(case.bt[1, 1]), 0, 9, 5] = 0xFF
     case.t["sc"][int(case.bt[2, 0]), 1, 1] = float("nan")
-    out = case.run(pa)
+    out = case.run(pa, max_context_len=bound)
     assert torch.isnan(out[0, 4:]).all() and torch.equal(out[0, :4], want[0, :4])
     assert torch.isnan(out[1, :4, 5]).all() and torch.equal(out[1, 4:], want[1, 4:])
     assert torch.isnan(out[2, 4:]).all() and torch.equal(out[2, :4], want[2, :4])
@@ -310,7 +317,7 @@ def test_decode_nan_and_bad_blocks(pa):
         b = case.bt[3, i]
         case.t["bt"][3, i] = bad
         case.kc[b], case.vc[b], case.sc[b] = 0, 0, 1.0
-        out = case.run(pa)
+        out = case.run(pa, max_context_len=bound)
         assert pa.get_device_error() == pa.PA_DEVERR_BLOCK_ID
         ref, tol = expected(cc.stored(case.q, "bf16")[3], *case.kv(3), case.scale, "bf16")
         assert (np.abs(out[3].double().cpu().numpy() - ref) <= tol).all()
@@ -328,23 +335,24 @@ def test_decode_bad_lengths(pa):
     assert np.abs(got - ref).max() <= 2e-3                # the same context, in other runs
 
 
+@pytest.mark.parametrize("bound", [0, RUNS])
 @pytest.mark.parametrize("dtype", [torch.uint8, torch.float8_e4m3fn])
-def test_decode_workspaces_and_cache_types(pa, dtype):
+def test_decode_workspaces_and_cache_types(pa, dtype, bound):
     case = Case(np.random.default_rng(37), [700, 1500], 16, 4, 128, 32, "bf16")
-    want = case.run(pa)
+    want = case.run(pa, max_context_len=bound)
     case.t["kc"], case.t["vc"] = case.t["kc"].view(dtype), case.t["vc"].view(dtype)
-    n = pa.decode_fp8_block_workspace_bytes(2, 16, 4, 128, case.bt.shape[1] * 32)
+    n = pa.decode_fp8_block_workspace_bytes(2, 16, 4, 128, bound or case.bt.shape[1] * 32)
     for fill in (0, 255):
         ws = torch.full((n,), fill, dtype=torch.uint8, device=dev())
-        assert torch.equal(case.run(pa, workspace=ws), want)
+        assert torch.equal(case.run(pa, workspace=ws, max_context_len=bound), want)
     with pytest.raises(pa.PagedAttnError) as e:
-        case.run(pa, workspace=ws[:n - 16])
+        case.run(pa, workspace=ws[:n - 16], max_context_len=bound)
     assert e.value.status == pa.PA_ERR_WORKSPACE
     # NULL: the library's own
     t, out = case.t, torch.empty_like(want)
     rc = pa.lib().pa_paged_attention_decode_fp8_block(
         out.data_ptr(), t["q"].data_ptr(), t["kc"].data_ptr(), t["vc"].data_ptr(), t["sc"].data_ptr(), t["bt"].data_ptr(),
-        case.bt.shape[1], t["lens"].data_ptr(), 2, 16, 4, 128, 32, case.NB, case.scale, 0, None, 0, pa.PA_DTYPE_BF16,
+        case.bt.shape[1], t["lens"].data_ptr(), 2, 16, 4, 128, 32, case.NB, case.scale, bound, None, 0, pa.PA_DTYPE_BF16,
         torch.cuda.current_stream().cuda_stream)
     torch.cuda.synchronize()
     assert rc == 0 and torch.equal(out, want)

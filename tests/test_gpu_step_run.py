@@ -12,7 +12,7 @@ import torch
 import compress_cases as cc
 import step_cases as sc
 from gpu_cases import dev, pa_mod
-from test_gpu_fp8_block import expected
+from test_gpu_fp8_block import RUNS, expected
 
 pytestmark = pytest.mark.gpu
 
@@ -32,7 +32,9 @@ def pa():
 class Loop:
     """Requests in B rows of one table over a pool of NB blocks; every tensor of a step lives here."""
 
-    def __init__(self, pa, seed, B, NB, H=8, Hk=2, D=128, bs=16, T=96, width=20, dtype="bf16", inter=False):
+    def __init__(self, pa, seed, B, NB, H=8, Hk=2, D=128, bs=16, T=96, width=20, dtype="bf16", inter=False,
+                 bound=0):
+        self.bound = bound                           # on the contexts: 0 the table's width, or RUNS
         self.pa, self.B, self.NB, self.H, self.Hk, self.D, self.bs, self.T = pa, B, NB, H, Hk, D, bs, T
         self.dtype, self.inter, self.rng, self.scale = dtype, inter, np.random.default_rng(seed), D ** -0.5
         i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev())
@@ -64,7 +66,7 @@ class Loop:
         if stream is None:
             torch.index_select(q, 0, (self.start[1:].long() - 1).clamp(min=0), out=self.q)
         pa.paged_attention_decode_fp8_block(self.out, self.q, self.kc, self.vc, self.sc, self.table, self.lens,
-                                            self.scale, **kw)
+                                            self.scale, max_context_len=self.bound, **kw)
 
     def feed(self, new, done):
         """The next step's inputs, written in place; their host copies."""
@@ -148,10 +150,11 @@ def test_steps_against_plain_forms(pa, dtype, D, bs, inter):
     assert pa.get_device_error() == sum(code[e] for e in model.err)
 
 
-def test_steps_without_synchronisation(pa):
+@pytest.mark.parametrize("bound", [0, RUNS])
+def test_steps_without_synchronisation(pa, bound):
     """The same steps enqueued in one go, and with a wait after every call, leave the same caches."""
     def run(wait):
-        loop = Loop(pa, 3, 6, 40)
+        loop = Loop(pa, 3, 6, 40, bound=bound)
         outs = []
         for new, done in plan(np.random.default_rng(4), loop, 10):
             loop.feed(new, done)
@@ -166,10 +169,11 @@ def test_steps_without_synchronisation(pa):
     pa.get_device_error()
 
 
-def test_two_graphs_replayed_in_turn(pa):
+@pytest.mark.parametrize("bound", [0, RUNS])
+def test_two_graphs_replayed_in_turn(pa, bound):
     """Two loops' steps captured, replayed in turn with new inputs written in place, beside the same steps run
     eagerly; the first graph is destroyed before the second runs on."""
-    loops, twins = ([Loop(pa, 10 + i, B, NB, H=H, Hk=2) for i, (B, NB, H) in enumerate(((5, 40, 8), (9, 60, 24)))]
+    loops, twins = ([Loop(pa, 10 + i, B, NB, H=H, Hk=2, bound=bound) for i, (B, NB, H) in enumerate(((5, 40, 8), (9, 60, 24)))]
                     for _ in range(2))
     plans = [list(plan(np.random.default_rng(20 + i), l, 8)) for i, l in enumerate(loops)]
     for l, t in zip(loops, twins):               # warm up without new tokens
@@ -201,10 +205,11 @@ def test_two_graphs_replayed_in_turn(pa):
     pa.get_device_error()
 
 
-def test_two_streams_at_once(pa):
+@pytest.mark.parametrize("bound", [0, RUNS])
+def test_two_streams_at_once(pa, bound):
     """Steps of two loops on two streams through stream=, their queries given; equal to the steps run alone."""
     def make():
-        loops = [Loop(pa, 30 + i, B, NB) for i, (B, NB) in enumerate(((4, 40), (7, 60)))]
+        loops = [Loop(pa, 30 + i, B, NB, bound=bound) for i, (B, NB) in enumerate(((4, 40), (7, 60)))]
         for l in loops:
             l.q.copy_(torch.from_numpy(np.random.default_rng(5).standard_normal(tuple(l.q.shape)).astype(np.float32)))
             l.feed(np.minimum(np.arange(l.B) * 7 + 1, 96 // l.B), np.zeros(l.B))
@@ -243,10 +248,10 @@ def test_lengths_and_decode_next_to_each_other(pa):
         outs, start, slots, pos = [], i32(B + 1), i32(T), i32(T)
         # a V block stands for its number's square root; with flat weights the output is the context's mean
         vs[..., 1] = torch.arange(NB, device=dev()).float().sqrt()[:, None]
-        for _ in range(8):
+        for i in range(8):
             pa.paged_blocks_append(table, lens, new, free, nf, start, slots, pos, bs, NB)
             out = torch.empty_like(q)
-            pa.paged_attention_decode_fp8_block(out, q, kc, kc, vs, table, lens, 1.0)
+            pa.paged_attention_decode_fp8_block(out, q, kc, kc, vs, table, lens, 1.0, max_context_len=i % 2 * RUNS)
             outs.append(out)
         torch.cuda.synchronize()
         tab = table.cpu().numpy()
@@ -332,14 +337,15 @@ def test_context_read_back_for_prefill(pa):
     assert pa.get_device_error() == 0
 
 
+@pytest.mark.parametrize("bound", [0, RUNS])
 @pytest.mark.parametrize("plain", [False, True])
-def test_two_branches_of_one_graph(pa, monkeypatch, plain):
+def test_two_branches_of_one_graph(pa, monkeypatch, plain, bound):
     """One capture forks: decodes go to a side stream through stream=, others and torch operations that allocate run
     beside them on the capture's own stream; replays equal the calls alone, whichever way the calls go."""
     from test_gpu_fp8_block import Case
     cases = [Case(np.random.default_rng(60 + i), lens, 16, 4, 128, 16, "f16") for i, lens in
              enumerate(([2500, 900, 1300], [1100, 3000, 2049, 5]))]
-    want = [c.run(pa) for c in cases]
+    want = [c.run(pa, max_context_len=bound) for c in cases]
     seen, inner = [], pa._workspace
 
     def spy(device, stream_ptr, nbytes):
@@ -358,9 +364,9 @@ def test_two_branches_of_one_graph(pa, monkeypatch, plain):
         cur = torch.cuda.current_stream()
         side.wait_stream(cur)
         for _ in range(4):
-            cases[0].run(pa, out=outs[0], stream=side)
+            cases[0].run(pa, out=outs[0], stream=side, max_context_len=bound)
             junk = torch.full((8 << 20,), 255, dtype=torch.uint8, device=dev())
-            cases[1].run(pa, out=outs[1])
+            cases[1].run(pa, out=outs[1], max_context_len=bound)
             junk = junk + 1
         cur.wait_stream(side)
     # a stream that is not the current one is the Python code's affair
