@@ -21,7 +21,7 @@
 // side by side in a warp. (Atomic maxima over all tokens, whatever their order, would need the
 // old scales kept beside the new ones and two more launches.)
 //
-// What bounds it (one GB300, 8 kv heads of 128 channels): a decode step's 64 tokens 2.6 us, the latency of
+// What bounds it (one GB300, 8 kv heads of 128 channels): a decode step's 64 tokens 1.9 us, the latency of
 // three dependent loads; 8192 tokens, 50 MB, 10.8 us, instructions and the same chain with 16 warps an
 // SM (five CTAs an SM, which spill, 13.1). All CTAs of a few tokens stand next to each other in the grid, so
 // that their rows, which lie side by side, are read at the same time (heads far apart: 12.2). Reading back
@@ -41,9 +41,11 @@ constexpr int kThreads = 128, kWarps = kThreads / 32;
 template <int D> constexpr int kKeep = D / 32;
 constexpr int kMinScaleExp = -100;
 constexpr int kWriteCtas = 4;                    // of the scatter, on an SM (one less for float32 rows)
-// Tokens written in columns of 4 rather than 32 (8 kv heads, us with 4 and 32: single tokens of 1024
-// sequences 5.1, 13.5, of 2048 8.9, 12.2; 400 tokens of one 3.3, 4.1, 2000 5.5, 4.7, 8192 23.0, 10.8).
-constexpr int64_t kFewTokens = 4096;
+constexpr int kColumn = 32;                      // tokens, a lane each, whose runs the scatter's CTAs take together
+// CTAs that it aims at where columns are few: as many as the device holds (8 kv heads, us
+// with three quarters, as many and one and a half times: single tokens of 1024 sequences 3.6, 3.0, 4.1, of 2048 5.0, 4.4,
+// 5.5; 2000 tokens of one 4.8, 3.6, 4.1, 50 of each of 40 5.6, 4.7, 5.8).
+constexpr int64_t kFillCtas = 152 * kWriteCtas;
 // Channels per lane in reading: more where there are enough rows to fill the SMs all the same (us
 // with 8 and 32 channels, 8 kv heads: 100 tokens 1.4, 1.6; 700 1.9, 1.9; 1000 2.4, 2.1).
 constexpr int kFewChannels = 8, kManyChannels = 32;
@@ -175,14 +177,15 @@ __device__ __forceinline__ void reencode(uint4 *codes, int first, int step, int 
     }
 }
 
-// 2^log2_team: warps that share a run (at most kWarps); chunk: tokens of slot_mapping whose runs
-// `split` CTAs in a row take (at most 32), so that their rows are read at the same time.
+// 2^log2_team: warps that share a run (at most kWarps). `split` CTAs in a row take the runs that start in
+// kColumn tokens of slot_mapping, so that their rows are read at the same time: the parts of all runs,
+// in order, are dealt to their warps in turn, and a warp finds its own without passing by the others.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 4 ? kWriteCtas - 1 : kWriteCtas) void kv_write_fp8_block_kernel(const T *__restrict__ k, const T *__restrict__ v,
                                                                       int64_t k_stride, int64_t v_stride,
                                                                       const int32_t *__restrict__ slots,
                                                                       int64_t num_tokens, const Fp8BlockCache c,
-                                                                      int log2_team, int chunk, int split, unsigned int *err) {
+                                                                      int log2_team, int split, unsigned int *err) {
     constexpr int kLanes = D / 16, kRows = 32 / kLanes;   // lanes of a row; rows of a warp
     __shared__ float maxima[kWarps];
     // launched as a dependent of the kernel before; a kernel launched after this one may start
@@ -195,7 +198,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 ? kWriteCtas - 1 : kWriteC
     // the runs that start in this CTA's tokens, from a window of 64: whether a token has a block,
     // continues the run of the token before, is its block's first
     const uint32_t column = blockIdx.x / (uint32_t)split, place = blockIdx.x - column * split;
-    const int64_t t0 = (int64_t)column * chunk;
+    const int64_t t0 = (int64_t)column * kColumn;
     int32_t slot[2];
     int block[2];
 #pragma unroll
@@ -205,7 +208,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 ? kWriteCtas - 1 : kWriteC
         block[w] = block_of(c, slot[w]);
     }
     const int last = lane == 0 && t0 > 0 ? block_of(c, slots[t0 - 1]) : -1;
-    if (block[0] < 0 && slot[0] != -1 && lane < chunk && place == 0 && warp == 0) raise_error(err, PA_DEVERR_SLOT);
+    if (block[0] < 0 && slot[0] != -1 && place == 0 && warp == 0) raise_error(err, PA_DEVERR_SLOT);
     uint64_t goes_on = 0, firsts = 0;
     uint32_t starts = 0;
 #pragma unroll
@@ -215,7 +218,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 ? kWriteCtas - 1 : kWriteC
         if (lane == 0) before = w == 0 ? last : end;
         goes_on |= (uint64_t)__ballot_sync(0xffffffffu, block[w] >= 0 && block[w] == before) << (32 * w);
         firsts |= (uint64_t)__ballot_sync(0xffffffffu, block[w] >= 0 && (slot[w] & (bs - 1)) == 0) << (32 * w);
-        if (w == 0) starts = __ballot_sync(0xffffffffu, block[0] >= 0 && block[0] != before && lane < chunk);
+        if (w == 0) starts = __ballot_sync(0xffffffffu, block[0] >= 0 && block[0] != before);
     }
     // a slot of the window's token i (each lane asks for its own)
     auto slot_at = [&](int i) {
@@ -231,9 +234,56 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 ? kWriteCtas - 1 : kWriteC
         if (team == 1) __syncwarp();
         else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(team * 32) : "memory");
     };
-    int turn = 0;                                      // runs are dealt from one warp on to the next
-    for (; starts; starts &= starts - 1) {
-        const int s = __ffs(starts) - 1;
+    // the place of the r-th bit of a mask
+    auto place_of = [&](uint32_t mask, int r) {
+        return __ffs(__ballot_sync(0xffffffffu, (mask >> lane & 1) && __popc(mask & ((1u << lane) - 1)) == r)) - 1;
+    };
+    // Runs of one token: a unit for each row of the warp, every run's warps dealt in turn.
+    const uint32_t singles = starts & ~(uint32_t)(goes_on >> 1);
+    const int single_tasks = __popc(singles) * quads;
+#pragma unroll 1
+    for (int task = my_warp; task < single_tasks; task += warps) {
+        const int r = task / quads, q = task - r * quads, s = place_of(singles, r);
+        const int64_t first = t0 + s;
+        const int at = slot_at(s), b = at >> c.log2_block_size, off = at & (bs - 1);
+        const bool fresh = firsts >> s & 1;
+        const int u = q * kRows + row;
+        const bool live = u < units, is_v = u & 1;
+        const int kvh = min(u >> 1, Hk - 1);
+        float *scale_at = reinterpret_cast<float *>(c.scales + ((int64_t)b * Hk + kvh)) + is_v;
+        Run16<T> x;
+        x.load((is_v ? v + first * v_stride : k + first * k_stride) + kvh * D + part);
+        const float old = *scale_at;
+        float amax = x.largest();
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        bool held;
+        const int e = next_scale(amax, old, fresh, held);
+        const float scale = pow2f(e);
+        uint4 *codes = reinterpret_cast<uint4 *>(static_cast<unsigned char *>(is_v ? c.value : c.key) +
+                                                 (((int64_t)b * Hk + kvh) << c.log2_block_size) * D + part);
+        // the older codes of these units, each by the whole warp
+        uint32_t grown = __ballot_sync(0xffffffffu, live && held && scale > old && part == 0);
+        for (; grown; grown &= grown - 1) {
+            const int from = __ffs(grown) - 1;
+            const uint64_t rows = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(codes), from);
+            const float ratio = __shfl_sync(0xffffffffu, old * pow2f(-e), from);
+            reencode<kLanes>(reinterpret_cast<uint4 *>(rows + part), row, kRows, bs, ratio);
+        }
+        __syncwarp();                                  // older codes before new ones
+        if (live) {
+            float y[16];
+            x.values(y);
+            codes[off * kLanes] = encode16(y, pow2f(-e));
+            if (part == 0) *scale_at = scale;
+        }
+    }
+    // Longer ones: a unit for each team, which follow where those ended.
+    const uint32_t longer = starts & ~singles;
+    const int tasks = __popc(longer) * units, skipped = single_tasks % warps >> log2_team;
+#pragma unroll 1
+    for (int task = my_team - skipped + (my_team < skipped ? teams : 0); task < tasks; task += teams) {
+        const int r = task / units, u = task - r * units, s = place_of(longer, r);
         const int64_t first = t0 + s;
         const int b = slot_at(s) >> c.log2_block_size;
         // tokens of the run that the window shows, and beyond it
@@ -248,112 +298,69 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 ? kWriteCtas - 1 : kWriteC
                 fresh |= __any_sync(0xffffffffu, lane < len && (next & (bs - 1)) == 0);
             }
         }
-        if (n == 1) {
-            // a unit for each row of the warp
-            const int off = slot_at(s) & (bs - 1);
-#pragma unroll 1
-            for (int q = my_warp - turn + (my_warp < turn ? warps : 0); q < quads; q += warps) {
-                const int u = q * kRows + row;
-                const bool live = u < units, is_v = u & 1;
-                const int kvh = min(u >> 1, Hk - 1);
-                float *scale_at = reinterpret_cast<float *>(c.scales + ((int64_t)b * Hk + kvh)) + is_v;
-                Run16<T> x;
-                x.load((is_v ? v + first * v_stride : k + first * k_stride) + kvh * D + part);
-                const float old = *scale_at;
-                float amax = x.largest();
+        const bool is_v = u & 1;
+        const int kvh = u >> 1;
+        const T *src = (is_v ? v + first * v_stride : k + first * k_stride) + kvh * D + part;
+        const int64_t stride = is_v ? v_stride : k_stride;
+        const int row0 = member * kRows + row, step = team * kRows;
+        Run16<T> x[kKeep<D>];
+        uint32_t offs = 0, lives = 0;                  // a row's place in its block, a byte each; whether there is one
+        float *scale_at = reinterpret_cast<float *>(c.scales + ((int64_t)b * Hk + kvh)) + is_v;
+        const float old = *scale_at;
 #pragma unroll
-                for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                bool held;
-                const int e = next_scale(amax, old, fresh, held);
-                const float scale = pow2f(e);
-                uint4 *codes = reinterpret_cast<uint4 *>(static_cast<unsigned char *>(is_v ? c.value : c.key) +
-                                                         (((int64_t)b * Hk + kvh) << c.log2_block_size) * D + part);
-                // the older codes of these units, each by the whole warp
-                uint32_t grown = __ballot_sync(0xffffffffu, live && held && scale > old && part == 0);
-                for (; grown; grown &= grown - 1) {
-                    const int from = __ffs(grown) - 1;
-                    const uint64_t at = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(codes), from);
-                    const float ratio = __shfl_sync(0xffffffffu, old * pow2f(-e), from);
-                    reencode<kLanes>(reinterpret_cast<uint4 *>(at + part), row, kRows, bs, ratio);
-                }
-                __syncwarp();                          // older codes before new ones
-                if (live) {
-                    float y[16];
-                    x.values(y);
-                    codes[off * kLanes] = encode16(y, pow2f(-e));
-                    if (part == 0) *scale_at = scale;
-                }
+        for (int j = 0; j < kKeep<D>; ++j) {
+            const int i = row0 + j * step;
+            x[j].clear();
+            if (i < n) x[j].load(src + i * stride);
+        }
+#pragma unroll
+        for (int j = 0; j < kKeep<D>; ++j) {
+            const int i = row0 + j * step;
+            const int32_t in_window = slot_at(min(s + i, 63));
+            if (i < n) {
+                offs |= (uint32_t)((s + i < 64 ? in_window : slots[first + i]) & (bs - 1)) << (8 * j);
+                lives |= 1u << j;
             }
-            for (turn += quads; turn >= warps;) turn -= warps;
-            continue;
+        }
+        float amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < kKeep<D>; ++j) amax = fmaxf(amax, x[j].largest());
+#pragma unroll 1
+        for (int i = row0 + kKeep<D> * step; i < n; i += step) {   // a long run of a large block
+            Run16<T> more;
+            more.load(src + i * stride);
+            amax = fmaxf(amax, more.largest());
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (team > 1) {
+            if (lane == 0) maxima[warp] = amax;
+            sync();
+            for (int w = 0; w < team; ++w) amax = fmaxf(amax, maxima[group * team + w]);
+        }
+        bool held;
+        const int e = next_scale(amax, old, fresh, held);
+        const float scale = pow2f(e), inv = pow2f(-e);
+        uint4 *codes = reinterpret_cast<uint4 *>(static_cast<unsigned char *>(is_v ? c.value : c.key) +
+                                                 (((int64_t)b * Hk + kvh) << c.log2_block_size) * D + part);
+        if (held && scale > old) reencode<kLanes>(codes, row0, step, bs, old * inv);
+        sync();                                    // older codes before new ones; maxima and the old scale are read
+#pragma unroll
+        for (int j = 0; j < kKeep<D>; ++j) {
+            float y[16];
+            x[j].values(y);
+            if (lives >> j & 1) codes[(offs >> (8 * j) & 255) * kLanes] = encode16(y, inv);
+            asm volatile("" ::: "memory");         // one row after the other, for fewer registers
         }
 #pragma unroll 1
-        for (int u = my_team - (turn >> log2_team) + (my_team < turn >> log2_team ? teams : 0); u < units; u += teams) {
-            const bool is_v = u & 1;
-            const int kvh = u >> 1;
-            const T *src = (is_v ? v + first * v_stride : k + first * k_stride) + kvh * D + part;
-            const int64_t stride = is_v ? v_stride : k_stride;
-            const int row0 = member * kRows + row, step = team * kRows;
-            Run16<T> x[kKeep<D>];
-            uint32_t offs = 0, lives = 0;              // a row's place in its block, a byte each; whether there is one
-            float *scale_at = reinterpret_cast<float *>(c.scales + ((int64_t)b * Hk + kvh)) + is_v;
-            const float old = *scale_at;
-#pragma unroll
-            for (int j = 0; j < kKeep<D>; ++j) {
-                const int i = row0 + j * step;
-                x[j].clear();
-                if (i < n) x[j].load(src + i * stride);
-            }
-#pragma unroll
-            for (int j = 0; j < kKeep<D>; ++j) {
-                const int i = row0 + j * step;
-                const int32_t in_window = slot_at(min(s + i, 63));
-                if (i < n) {
-                    offs |= (uint32_t)((s + i < 64 ? in_window : slots[first + i]) & (bs - 1)) << (8 * j);
-                    lives |= 1u << j;
-                }
-            }
-            float amax = 0.f;
-#pragma unroll
-            for (int j = 0; j < kKeep<D>; ++j) amax = fmaxf(amax, x[j].largest());
-#pragma unroll 1
-            for (int i = row0 + kKeep<D> * step; i < n; i += step) {   // a long run of a large block
-                Run16<T> more;
-                more.load(src + i * stride);
-                amax = fmaxf(amax, more.largest());
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            if (team > 1) {
-                if (lane == 0) maxima[warp] = amax;
-                sync();
-                for (int w = 0; w < team; ++w) amax = fmaxf(amax, maxima[group * team + w]);
-            }
-            bool held;
-            const int e = next_scale(amax, old, fresh, held);
-            const float scale = pow2f(e), inv = pow2f(-e);
-            uint4 *codes = reinterpret_cast<uint4 *>(static_cast<unsigned char *>(is_v ? c.value : c.key) +
-                                                     (((int64_t)b * Hk + kvh) << c.log2_block_size) * D + part);
-            if (held && scale > old) reencode<kLanes>(codes, row0, step, bs, old * inv);
-            sync();                                    // older codes before new ones; maxima and the old scale are read
-#pragma unroll
-            for (int j = 0; j < kKeep<D>; ++j) {
-                float y[16];
-                x[j].values(y);
-                if (lives >> j & 1) codes[(offs >> (8 * j) & 255) * kLanes] = encode16(y, inv);
-                asm volatile("" ::: "memory");         // one row after the other, for fewer registers
-            }
-#pragma unroll 1
-            for (int i = row0 + kKeep<D> * step; i < n; i += step) {
-                Run16<T> more;
-                more.load(src + i * stride);
-                float y[16];
-                more.values(y);
-                codes[(slots[first + i] & (bs - 1)) * kLanes] = encode16(y, inv);
-            }
-            if (member == 0 && lane == 0) *scale_at = scale;
+        for (int i = row0 + kKeep<D> * step; i < n; i += step) {
+            Run16<T> more;
+            more.load(src + i * stride);
+            float y[16];
+            more.values(y);
+            codes[(slots[first + i] & (bs - 1)) * kLanes] = encode16(y, inv);
         }
-        for (turn += units << log2_team; turn >= warps;) turn -= warps;
+        if (member == 0 && lane == 0) *scale_at = scale;
     }
 }
 
@@ -426,16 +433,17 @@ int write_t(const void *k, const void *v, int64_t ks, int64_t vs, const int32_t 
     // as many warps a team as hold a block's rows in registers
     int log2_team = 0;
     while (1 << log2_team < kWarps && kRows * kKeep<D> << log2_team < 1 << c.log2_block_size) ++log2_team;
-    // Few tokens: a warp for each step of the work, if they are single ones. Many: columns of 32, with
-    // a warp for each unit of a run of 8 (8 kv heads, us with half, as many and twice the CTAs: 16,384 tokens,
-    // blocks of 16 23.9, 21.5, 24.2; 8192, of 32 12.6, 10.8, 13.6; of 256, f32 32.4, 30.8, 36.7).
-    const int chunk = n <= kFewTokens ? 4 : 32, Hk = c.num_kv_heads;
-    const int64_t y = chunk == 4 ? ((2 * Hk + kRows - 1) / kRows * chunk + kWarps - 1) / kWarps
-                                 : ((Hk << log2_team) + 1) / 2;
-    const int64_t columns = (n + chunk - 1) / chunk;
-    const int split = (int)std::max<int64_t>(1, std::min(y, INT32_MAX / columns));
+    // CTAs of a column: a warp for each unit of runs of 8 (8 kv heads, us with half, as many and twice: 16,384 tokens,
+    // blocks of 16 23.9, 21.5, 24.2; 8192, of 32 12.6, 10.8, 13.6; of 256, f32 32.4, 30.8, 36.7), or more where columns
+    // are few, up to a warp for each step that single tokens need.
+    const int Hk = c.num_kv_heads;
+    const int64_t columns = (n + kColumn - 1) / kColumn;
+    const int64_t for_runs = ((Hk << log2_team) + 1) / 2;
+    const int64_t for_singles = ((2 * Hk + kRows - 1) / kRows * kColumn + kWarps - 1) / kWarps;
+    const int64_t ctas = std::max(for_runs, std::min(for_singles, kFillCtas / columns));
+    const int split = (int)std::max<int64_t>(1, std::min(ctas, INT32_MAX / columns));
     return launch_pdl(kv_write_fp8_block_kernel<T, D>, dim3((unsigned)(columns * split)), dim3(kThreads), 0, s,
-                      (const T *)k, (const T *)v, ks, vs, slots, n, c, log2_team, chunk, split, err);
+                      (const T *)k, (const T *)v, ks, vs, slots, n, c, log2_team, split, err);
 }
 
 template <typename T, int D>
