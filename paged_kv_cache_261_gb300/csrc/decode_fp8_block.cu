@@ -29,7 +29,7 @@
 //
 // Work: the stages (kTok tokens of one sequence and kv head) of the whole call, in order, are
 // cut into equal runs, one for each warp of the persistent grid (decode_runs.cuh). Warps share
-// nothing. Few rows of short contexts are too little work to cut so: there one to eight CTAs, a
+// nothing. Few rows of short contexts are too little work to cut so: there one to sixteen CTAs, a
 // cluster, take each row, its stages dealt to their warps in equal parts, and join the parts
 // through each other's shared memory, without a second kernel (row_cluster). Each warp fetches its own stages, one ahead and across rows, into its own ring: a
 // block of one kv head is one contiguous run for K and V each, so a stage is a few untiled bulk
@@ -66,7 +66,7 @@ constexpr int kMinScaleExp = -100, kMaxScaleExp = 121;   // of the V scales' ref
 
 __host__ __device__ constexpr int stage_tokens(int D) { return 4096 / D; }
 constexpr int kWarps = 8;                         // of a CTA, one CTA an SM
-constexpr int kMaxCluster = 8;                    // CTAs of a row, where CTAs take rows
+constexpr int kClusterSizes = 5;                  // 1, 2, ..., 16 CTAs of a row, where CTAs take rows
 constexpr int kRowStages = 7;                     // of a warp, then, at most
 
 template <int D> struct Cfg {
@@ -649,6 +649,7 @@ int launch_runs(const DecodeParams &p, const RunWork &ws, int64_t max_ctx, int g
 
 // CTAs that take rows, `cluster` to a row.
 template <typename T, int D, int GT> struct RowCtas {
+    static constexpr int kSmem = Cfg<D>::kOffPart + Cfg<D>::part_bytes(GT);
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = {};
     RowCtas(int64_t rows, int cluster, cudaStream_t stream) {
@@ -659,7 +660,7 @@ template <typename T, int D, int GT> struct RowCtas {
         attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
         cfg.gridDim = dim3((unsigned)(rows * cluster));
         cfg.blockDim = dim3(Cfg<D>::kThreads);
-        cfg.dynamicSmemBytes = Cfg<D>::kOffPart + Cfg<D>::part_bytes(GT);
+        cfg.dynamicSmemBytes = kSmem;
         cfg.stream = stream;
         cfg.attrs = attr;
         cfg.numAttrs = 2;
@@ -670,16 +671,16 @@ template <typename T, int D, int GT> struct RowCtas {
     static const int *room(int dev) {
         static std::atomic<bool> known[kMaxDevices];
         static std::mutex asking;
-        static int n[kMaxDevices][4];
+        static int n[kMaxDevices][kClusterSizes];
         if (known[dev].load(std::memory_order_acquire)) return n[dev];
         const std::lock_guard<std::mutex> lock(asking);
         if (known[dev].load(std::memory_order_relaxed)) return n[dev];
         auto kern = decode_fp8_block_kernel<T, D, GT, true>;
-        for (int i = 0; i < 4; ++i) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            return nullptr;
+        for (int i = 0; i < kClusterSizes; ++i) {
             RowCtas l(1, 1 << i, nullptr);
-            if (i == 0 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)l.cfg.dynamicSmemBytes) != cudaSuccess)
-                return nullptr;
             if (cudaOccupancyMaxActiveClusters(&n[dev][i], kern, &l.cfg) != cudaSuccess) return nullptr;
         }
         known[dev].store(true, std::memory_order_release);
@@ -694,11 +695,12 @@ template <typename T, int D, int GT> struct RowCtas {
 // us, runs and rows, of G 4 and D 128, by rows and stages of the longest: 8 and 2 5.7, 4.0; 8 and 10 5.6, 5.0;
 // 8 and 22 5.9, 5.1; 8 and 63 7.0, 5.6; 8 and 125 7.8, 7.0; 14 and 125 9.3, 7.5; 32 and 32 6.5, 5.7; 64 and 32 8.7, 6.7;
 // 64 and 63 10.7, 9.3; 96 and 32 9.5, 8.9; 128 and 4 6.5, 4.6; 128 and 32 10.7, 8.9; 144 and 54 13.4, 12.7; not taken: 128 and
-// 63 13.4, 13.9, 16 and 125 8.4, 12.1 (eight CTAs). 32 rows of 32 stages of G 16, f16: 9.5, 8.3.
+// 63 13.4, 13.9, 16 and 125 8.4, 12.1 (eight CTAs). Of sixteen CTAs, 7 have room: 1 and 250 8.0, 7.3; 4 and 250 8.9, 7.6; 7 and
+// 250 9.8, 8.4. 32 rows of 32 stages of G 16, f16: 9.5, 8.3.
 int row_cluster(int64_t rows, int64_t stages, int sms, const int *room) {
     if (rows > room[0]) return 0;
     int i = 0;
-    while ((2 << i) <= kMaxCluster && kWarps << i < stages && rows <= room[i + 1]) ++i;
+    while (i + 1 < kClusterSizes && kWarps << i < stages && rows <= room[i + 1]) ++i;
     const int64_t mine = (stages + (kWarps << i) - 1) / (kWarps << i);
     const int64_t runs = (rows * stages + (int64_t)sms * kWarps - 1) / ((int64_t)sms * kWarps);
     return mine <= std::min<int64_t>(runs + 1, kRowStages) ? 1 << i : 0;

@@ -266,7 +266,7 @@ def test_decode_ragged(pa, dtype, H, Hk, D, bs):
     assert pa.get_device_error() == 0
 
 
-@pytest.mark.parametrize("lens", [[2000, 1, 128, 700, 0, 1537], [31] * 700, [0, 0, 33], [0], [9000], [70, 5000] * 20,
+@pytest.mark.parametrize("lens", [[2000, 1, 128, 700, 0, 1537], [31] * 700, [0, 0, 33], [0], [9000], [5000], [4000, 2100, 0, 1], [70, 5000] * 20,
                                   [5] * 1600])
 @pytest.mark.parametrize("H,Hk", [(16, 4), (12, 1)])
 def test_decode_cuts(pa, lens, H, Hk):
@@ -392,7 +392,7 @@ SHORT = [1, 7, 0, 15, 16, 17, 31, 33, 64, 127, 128, 129, 300, 513, 1000, 1024]
                                        (12, 1, 128, 256), (32, 2, 128, 8), (10, 2, 64, 16), (16, 1, 64, 8),
                                        (3, 3, 64, 128), (24, 4, 128, 16), (9, 3, 64, 32)])
 def test_decode_rows_of_ctas(pa, dtype, H, Hk, D, bs):
-    """Few rows of short contexts, which clusters of one to eight CTAs take: CTAs and warps without a stage, parts of a
+    """Few rows of short contexts, which clusters of one to sixteen CTAs take: CTAs and warps without a stage, parts of a
     stage, several; the same contexts under a longer bound, which are cut into runs."""
     case = Case(np.random.default_rng(43 + H + D + bs), SHORT, H, Hk, D, bs, dtype, gain=2.0)
     out = case.run(pa, max_context_len=1024)
