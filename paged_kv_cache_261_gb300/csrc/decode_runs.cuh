@@ -235,8 +235,8 @@ __global__ __launch_bounds__(kWarps * 32) void decode_join_kernel(const DecodePa
     else *reinterpret_cast<uint32_t *>(dst) = *reinterpret_cast<uint32_t *>(h);
 }
 
-// The join after a kernel of `warps` warps and stages of `tok` tokens.
-template <typename T, int D>
+// The join after a kernel of `warps` warps and stages of `tok` tokens; kMost: warps of a row that has many partials.
+template <typename T, int D, int kMost = 16>
 int launch_join(const DecodeParams &p, const RunWork &ws, int64_t max_ctx, int tok, int64_t warps, cudaStream_t stream) {
     // Partials a row: about runs / rows, for contexts of the limit's length. (8 kv heads, us with up to
     // 4 warps a row and with 16: one context of 16,000 tokens 21.2 and 13.2, of 131,072 44.9 and 35.9,
@@ -247,10 +247,10 @@ int launch_join(const DecodeParams &p, const RunWork &ws, int64_t max_ctx, int t
     const int64_t limit = std::min(max_ctx, (int64_t)p.max_blocks_per_seq * p.block_size);
     const int64_t stages = (limit + tok - 1) / tok;
     const int64_t runs = std::min<int64_t>(warps, rows * stages);
-    const int wpr = runs <= 8 * rows ? 1 : (runs <= 32 * rows ? 4 : 16), cta = kJoinWarps(wpr);
+    const int wpr = runs <= 8 * rows ? 1 : (runs <= 32 * rows ? 4 : kMost), cta = kJoinWarps(wpr);
     auto join = wpr == 1   ? decode_join_kernel<T, D, 1>
                 : wpr == 4 ? decode_join_kernel<T, D, 4>
-                           : decode_join_kernel<T, D, 16>;
+                           : decode_join_kernel<T, D, kMost>;
     return launch_pdl(join, dim3((unsigned)((heads * wpr + cta - 1) / cta)), dim3(cta * 32), 0, stream, p, ws);
 }
 
