@@ -380,7 +380,6 @@ __global__ __launch_bounds__(kThreads) void kv_read_fp8_block_kernel(T *__restri
                                                                      uint32_t num_tokens, const Fp8BlockCache c,
                                                                      unsigned int *err) {
     constexpr int kLanes = D / kCh, kWords = kCh / 8, kPairs = kThreads / kLanes / 2;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int part = threadIdx.x % kLanes;
     const bool is_v = (threadIdx.x / kLanes) & 1;
@@ -451,9 +450,13 @@ int read_t(void *k, void *v, const int32_t *slots, int64_t n, const Fp8BlockCach
            cudaStream_t s) {
     const bool many = n * c.num_kv_heads >= kManyRows;
     const int pairs = kThreads / (D / (many ? kManyChannels : kFewChannels)) / 2;   // of a CTA
-    return launch_pdl(many ? kv_read_fp8_block_kernel<T, D, kManyChannels> : kv_read_fp8_block_kernel<T, D, kFewChannels>,
-                      dim3((unsigned)((n * c.num_kv_heads + pairs - 1) / pairs)), dim3(kThreads), 0, s, (T *)k, (T *)v,
-                      slots, (uint32_t)n, c, err);
+    // Not as a dependent of the kernel before: small CTAs that start early crowd the SMs that it leaves first (a
+    // read-back after a scatter, us of both as a dependent and so: 2159 tokens of 4 kv heads of 64 channels, f32 13.7,
+    // 7.2, bf16 9.5, 5.9; 2000 tokens of 8, f16 10.3, 9.0; 8192 22.4, 22.4).
+    auto kern = many ? kv_read_fp8_block_kernel<T, D, kManyChannels> : kv_read_fp8_block_kernel<T, D, kFewChannels>;
+    kern<<<dim3((unsigned)((n * c.num_kv_heads + pairs - 1) / pairs)), dim3(kThreads), 0, s>>>((T *)k, (T *)v, slots,
+                                                                                             (uint32_t)n, c, err);
+    return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
 template <typename T>
