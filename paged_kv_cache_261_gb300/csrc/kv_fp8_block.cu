@@ -45,11 +45,14 @@ constexpr int kColumn = 32;                      // tokens, a lane each, whose r
 // CTAs that it aims at where columns are few: as many as the device holds (8 kv heads, us
 // with three quarters, as many and one and a half times: single tokens of 1024 sequences 3.6, 3.0, 4.1, of 2048 5.0, 4.4,
 // 5.5; 2000 tokens of one 4.8, 3.6, 4.1, 50 of each of 40 5.6, 4.7, 5.8).
-constexpr int64_t kFillCtas = 152 * kWriteCtas;
+constexpr int kSms = 152;
+constexpr int64_t kFillCtas = kSms * kWriteCtas;
 // Channels per lane in reading: more where there are enough rows to fill the SMs all the same (us
 // with 8 and 32 channels, 8 kv heads: 100 tokens 1.4, 1.6; 700 1.9, 1.9; 1000 2.4, 2.1).
 constexpr int kFewChannels = 8, kManyChannels = 32;
 constexpr int64_t kManyRows = 4096;              // (token, kv head) pairs
+constexpr int kFullCtas = 14;                    // of reading, on an SM: there is little room for more
+constexpr int kSmemOfSm = 228 * 1024, kSmemOfCta = 1024;   // bytes an SM has, and of them what a CTA takes by itself
 
 template <typename T2> __device__ __forceinline__ T2 as2(uint32_t u) { return *reinterpret_cast<T2 *>(&u); }
 template <typename T2> __device__ __forceinline__ uint32_t bits2(T2 v) { return *reinterpret_cast<uint32_t *>(&v); }
@@ -380,6 +383,7 @@ __global__ __launch_bounds__(kThreads) void kv_read_fp8_block_kernel(T *__restri
                                                                      uint32_t num_tokens, const Fp8BlockCache c,
                                                                      unsigned int *err) {
     constexpr int kLanes = D / kCh, kWords = kCh / 8, kPairs = kThreads / kLanes / 2;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int part = threadIdx.x % kLanes;
     const bool is_v = (threadIdx.x / kLanes) & 1;
@@ -450,13 +454,23 @@ int read_t(void *k, void *v, const int32_t *slots, int64_t n, const Fp8BlockCach
            cudaStream_t s) {
     const bool many = n * c.num_kv_heads >= kManyRows;
     const int pairs = kThreads / (D / (many ? kManyChannels : kFewChannels)) / 2;   // of a CTA
-    // Not as a dependent of the kernel before: small CTAs that start early crowd the SMs that it leaves first (a
-    // read-back after a scatter, us of both as a dependent and so: 2159 tokens of 4 kv heads of 64 channels, f32 13.7,
-    // 7.2, bf16 9.5, 5.9; 2000 tokens of 8, f16 10.3, 9.0; 8192 22.4, 22.4).
+    const int64_t ctas = (n * c.num_kv_heads + pairs - 1) / pairs, each = (ctas + kSms - 1) / kSms;
+    // CTAs of a dependent start where the kernel before leaves room, and small ones crowd the SMs that it leaves
+    // first. Where the SMs are not full anyway, they ask for shared memory that no more fit into than spread
+    // evenly (read-backs after a scatter, us of both without and so: 2159 tokens of 4 kv heads of 64 channels, f32
+    // 13.9, 6.9, bf16 9.5, 5.7; 2000 of 8 10.5, 9.6; 560 4.2, 4.2; not launched as a dependent: 7.2, 5.9, 9.0, 4.0, but 1 to 2 us
+    // more each outside a graph).
+    const int smem = each < kFullCtas ? (int)(kSmemOfSm / each) - kSmemOfCta : 0;
     auto kern = many ? kv_read_fp8_block_kernel<T, D, kManyChannels> : kv_read_fp8_block_kernel<T, D, kFewChannels>;
-    kern<<<dim3((unsigned)((n * c.num_kv_heads + pairs - 1) / pairs)), dim3(kThreads), 0, s>>>((T *)k, (T *)v, slots,
-                                                                                             (uint32_t)n, c, err);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    static bool attr_set[2][kMaxDevices] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
+    if (!attr_set[many][dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOfSm - kSmemOfCta) != cudaSuccess)
+            return -1;
+        attr_set[many][dev] = true;
+    }
+    return launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), smem, s, (T *)k, (T *)v, slots, (uint32_t)n, c, err);
 }
 
 template <typename T>
