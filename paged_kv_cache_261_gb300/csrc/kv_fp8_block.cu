@@ -22,8 +22,8 @@
 // old scales kept beside the new ones and two more launches.)
 //
 // What bounds it (one GB300, 8 kv heads of 128 channels): a decode step's 64 tokens 1.9 us, the latency of
-// three dependent loads; 8192 tokens, 50 MB, 10.8 us, instructions and the same chain with 16 warps an
-// SM (five CTAs an SM, which spill, 13.1). All CTAs of a few tokens stand next to each other in the grid, so
+// three dependent loads; 8192 tokens, 50 MB, 10.7 us with the rows in L2 and 14.8 from HBM, instructions and the same chain
+// with 16 warps an SM (five CTAs an SM, which spill, 11.1 and 15.2). All CTAs of a few tokens stand next to each other in the grid, so
 // that their rows, which lie side by side, are read at the same time (heads far apart: 12.2). Reading back
 // 131,071 tokens, 805 MB, takes 121 us, 6.65 TB/s, as fast as a copy; 8192 just written 7.2.
 #include "common.cuh"
