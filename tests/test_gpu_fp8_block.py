@@ -79,6 +79,45 @@ def test_write_is_bit_exact(pa, src, Hk, D, bs):
     assert pa.get_device_error() == 0
 
 
+@pytest.mark.parametrize("T,Hk,D,bs", [(31, 5, 128, 16), (33, 8, 64, 8), (65, 3, 64, 32), (200, 1, 128, 16), (700, 2, 128, 64),
+                                       (1000, 7, 64, 256), (6000, 1, 64, 8)])
+def test_write_and_read_mixed_batches(pa, T, Hk, D, bs):
+    """Single tokens, runs of a few and of more than a block, side by side, between them tokens without a slot and
+    with a bad one; read back at once, and again a call later."""
+    rng = np.random.default_rng(T + Hk + bs)
+    total = 4 * bs
+    bt, NB, _ = cc.tables(rng, [total] * T, bs)
+    s, at = Store(NB, Hk, bs, D), np.zeros(T, int)
+    for call in range(2):
+        slots, bad = [], 0
+        for b in rng.permutation(T):
+            n = int(rng.choice([1, 1, 1, 1, 2, 3, 17, 40, bs + 5]))
+            n = min(n, total - at[b], T - len(slots))
+            slots += list(cc.slots_of(bt[b], total, bs)[at[b]:at[b] + n])
+            at[b] += n
+            if rng.random() < 0.2 and len(slots) < T:
+                slots.append(-1 if rng.random() < 0.7 else NB * bs + int(rng.integers(0, 9)))
+                bad += slots[-1] >= 0
+            if len(slots) >= T:
+                break
+        slots = np.asarray(slots[:T], np.int32)
+        big = np.where(rng.random((T, 1, 1)) < 0.3, np.float32(30.0), np.float32(1.0)).astype(np.float32)
+        good = np.where(slots < NB * bs, slots, -1)
+        k, v = rows(rng, (T, Hk, D), "k") * big, rows(rng, (T, Hk, D)) * big
+        kt, vt = (torch.from_numpy(x).to(dev()).to(torch.bfloat16) for x in (k, v))
+        st = torch.from_numpy(slots).to(dev())
+        pa.paged_kv_write_fp8_block(kt, vt, st, *s.t)
+        ko, vo = (torch.full((T, Hk, D), 7.0, device=dev()) for _ in range(2))
+        pa.paged_kv_read_fp8_block(ko, vo, st, *s.t)
+        sc.write_blocks(s.kc, s.vc, s.sc, cc.stored(k, "bf16"), cc.stored(v, "bf16"), good)
+        s.check()
+        blk, off = good // bs, good % bs
+        for got, cache, i in ((ko, s.kc, 0), (vo, s.vc, 1)):
+            want = np.where((good >= 0)[:, None, None], sc.E4M3[cache[blk, :, off]] * s.sc[blk, :, i][..., None].astype(np.float64), 7.0)
+            assert np.array_equal(got.double().cpu().numpy(), want)          # a code times a power of two: exact
+        assert pa.get_device_error() == (pa.PA_DEVERR_SLOT if bad else 0)
+
+
 @pytest.mark.parametrize("bs", [8, 32])
 def test_write_order_within_a_block(pa, bs):
     """The tokens of a block next to each other, in any order; the first slot last."""
