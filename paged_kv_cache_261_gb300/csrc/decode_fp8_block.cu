@@ -18,13 +18,13 @@
 // transpose in registers. (An instruction of E4M3 operands would want query and weights as
 // sums of three E4M3 terms to keep the 11 bits that f16 has.)
 //
-// W = p v_scale enters the product as f16 (11 bits; the row sums take p unrounded), and where the
-// outputs are f16, whose own rounding is no coarser, what that rounding left enters as a second
-// f16 (22 bits; us with one and two: 8B-shaped batch 53.3, 53.7, long contexts 201.5, 202.2, 16 query
-// heads to a kv head 63.2, 69.7). Its reference is a maximum of the scores (raised only when a
-// score exceeds it by 2^7: no reduction over the lanes before) and a power of two above every
-// v_scale seen, so weights are normal f16 numbers down to 2^-22 of the reference times that power
-// and within 2^-33 of it below. The query enters as f16 times a power of two per head: exact for
+// W = p v_scale enters the product as two f16, its rounding and what that left (22 bits; the row sums
+// take p unrounded): as one (11 bits) the weights' rounding reached the outputs, 4 to 9 % of the bf16 ones
+// rounded to a neighbour of what float32 weights give (us with one and two, bf16: 8B-shaped batch 53.8, 54.2, long contexts
+// 202.6, 202.8, one sequence of 700 tokens 5.1, 5.35, 16 query heads to a kv head 63.9, 70.4). Its reference is a
+// maximum of the scores (raised only when a score exceeds it by 2^7: no reduction over the lanes before) and a
+// power of two above every v_scale seen, so the terms are normal f16 numbers down to 2^-22 of the reference times that
+// power and within 2^-33 of it below. The query enters as f16 times a power of two per head: exact for
 // bf16 and f16 at every channel within 2^-22 of the row's largest.
 //
 // Work: the stages (kTok tokens of one sequence and kv head) of the whole call, in order, are
@@ -38,10 +38,10 @@
 // 201.7 us on the two cases below.)
 //
 // What bounds it (one GB300): HBM. Long contexts, 1.34 GB, take 202 us, 6.65 TB/s, as fast as a copy;
-// the 8B-shaped batch, 303 MB, 53.4 us, 3 of them the join and about 3 the start. 8 warps with two
+// the 8B-shaped batch, 303 MB, 54.2 us, 3 of them the join and about 3 the start. 8 warps with two
 // stages of 8 KB each keep 131 KB an SM on their way; more of them is slower, as is less work a
-// stage (us, batch / long: 10 warps 53.0 / 214, 12 54.9 / 216, 8 with three stages 55.0 / 217, 12 with
-// three of 4 KB 53.2 / 205, 8 with three of 4 KB 61.7 / 241). 16 query heads to a kv head: 63.5 us on the batch, instructions.
+// stage (us with weights as one f16, batch / long, of which 53.3 / 201.5 with two stages of 8 warps: 10 warps 53.0 / 214, 12 54.9 / 216, 8 with three stages 55.0 / 217, 12 with
+// three of 4 KB 53.2 / 205, 8 with three of 4 KB 61.7 / 241). 16 query heads to a kv head: 70.4 us on the batch, instructions.
 //
 // Every wait is bounded; on a timeout the kernel sets PA_DEVERR_WAIT, waits (bounded)
 // for its copies in flight and returns.
@@ -165,7 +165,6 @@ __global__ __launch_bounds__(Cfg<D>::kThreads, 1) void decode_fp8_block_kernel(c
     constexpr int NT = GT / 8;                         // tiles of 8 heads
     constexpr int kSteps = D / 16;                     // instructions per 16 tokens, S and O alike
     constexpr int kSub = C::kTok / 16;
-    constexpr bool kTwoTerms = std::is_same_v<T, __half>;
     extern __shared__ __align__(128) unsigned char smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc);
@@ -481,8 +480,7 @@ __global__ __launch_bounds__(Cfg<D>::kThreads, 1) void decode_fp8_block_kernel(c
             // ---- weights and O^T
 #pragma unroll
             for (int sub = 0; sub < kSub; ++sub) {
-                uint32_t wb[NT][2];
-                [[maybe_unused]] uint32_t we[NT][2];   // what the rounding of W left, for f16 outputs
+                uint32_t wb[NT][2], we[NT][2];         // W as f16, and what that rounding left
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -494,11 +492,9 @@ __global__ __launch_bounds__(Cfg<D>::kThreads, 1) void decode_fp8_block_kernel(c
                         const float2 wv = mul2(w, make_float2(v, v));
                         const uint32_t wh = pack_half2(wv.x, wv.y);
                         wb[nt][r] = transpose8x8(wh);
-                        if constexpr (kTwoTerms) {
-                            const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&wh));
-                            const float2 lo = add2(wv, make_float2(-hi.x, -hi.y));
-                            we[nt][r] = transpose8x8(pack_half2(lo.x, lo.y));
-                        }
+                        const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&wh));
+                        const float2 lo = add2(wv, make_float2(-hi.x, -hi.y));
+                        we[nt][r] = transpose8x8(pack_half2(lo.x, lo.y));
                     }
                 // two tokens' bytes of two channels side by side
 #pragma unroll
@@ -510,7 +506,7 @@ __global__ __launch_bounds__(Cfg<D>::kThreads, 1) void decode_fp8_block_kernel(c
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         mma16816(O[nt][u], a0, a1, a2, a3, wb[nt][0], wb[nt][1]);
-                        if constexpr (kTwoTerms) mma16816(O[nt][u], a0, a1, a2, a3, we[nt][0], we[nt][1]);
+                        mma16816(O[nt][u], a0, a1, a2, a3, we[nt][0], we[nt][1]);
                     }
                 }
             }
