@@ -1097,7 +1097,8 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | No
       "by_turns"  a pair of at least `high` turns over original_len kept, one of at most `low`
                   divided, in between a mean of both weighted by its turns
       "by_index"  the same, weighted by the pair's index, from that of `high` turns, rounded down,
-                  to that of `low` turns, rounded up (usually 32 and 1)."""
+                  to that of `low` turns, rounded up (usually 32 and 1), both within
+                  [0, rotary_dim - 1], so the ramp may end behind the last pair."""
     if rotary_dim <= 0 or rotary_dim % 2:
         raise ValueError("rotary_dim must be a positive even number")
     if not (base > 1 and scale > 0):
@@ -1118,7 +1119,7 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | No
         keep = np.clip((original_len * f / (2 * np.pi) - low) / (high - low), 0.0, 1.0)
     else:
         first, last = (half * np.log(original_len / (n * 2 * np.pi)) / np.log(base) for n in (high, low))
-        first, last = max(np.floor(first), 0.0), min(np.ceil(last), half - 1.0)
+        first, last = max(np.floor(first), 0.0), min(np.ceil(last), rotary_dim - 1.0)
         keep = 1.0 - np.clip((np.arange(half) - first) / max(last - first, 0.001), 0.0, 1.0)
     return f / scale * (1.0 - keep) + f * keep
 
