@@ -1101,8 +1101,8 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | No
                   [0, rotary_dim - 1], so the ramp may end behind the last pair."""
     if rotary_dim <= 0 or rotary_dim % 2:
         raise ValueError("rotary_dim must be a positive even number")
-    if not (base > 1 and scale > 0):
-        raise ValueError("base must be above 1 and scale positive")
+    if not (1 < base < np.inf and 0 < scale < np.inf):
+        raise ValueError("base must be finite and above 1, scale finite and positive")
     half = rotary_dim // 2
     if scaling == "ntk" and rotary_dim > 2:
         base = base * scale ** (rotary_dim / (rotary_dim - 2))
@@ -1113,8 +1113,10 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | No
         return f / scale
     if scaling not in ("by_turns", "by_index"):
         raise ValueError(f"unknown scaling {scaling!r}")
-    if not 0 < low < high:
-        raise ValueError("low and high must be 0 < low < high")
+    if not 0 < low < high < np.inf:
+        raise ValueError("low and high must be finite, 0 < low < high")
+    if not 0 < original_len < np.inf:
+        raise ValueError("original_len must be finite and positive")
     if scaling == "by_turns":
         keep = np.clip((original_len * f / (2 * np.pi) - low) / (high - low), 0.0, 1.0)
     else:

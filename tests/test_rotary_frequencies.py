@@ -44,3 +44,12 @@ def test_by_index_at_the_last_pair(pa):
     r = (63 - 40) / (65 - 40)
     assert math.isclose(f[63], plain * (1 - r) + plain / 8 * r, rel_tol=1e-12)
     assert math.isclose(f[40], 1e4 ** (-40 / 64), rel_tol=1e-12) and f[41] < 0.99 * 1e4 ** (-41 / 64)
+
+
+@pytest.mark.parametrize("scaling", ["by_turns", "by_index"])
+@pytest.mark.parametrize("bad", [dict(original_len=0), dict(original_len=-8192), dict(original_len=float("nan")),
+                                 dict(high=float("inf")), dict(high=float("nan")), dict(scale=float("nan")),
+                                 dict(base=float("inf")), dict(original_len=float("inf")), dict(scale=float("inf"))])
+def test_what_gives_no_frequencies_is_refused(pa, scaling, bad):
+    with pytest.raises(ValueError):
+        pa.rotary_frequencies(8, scaling=scaling, **{**dict(scale=2.0), **bad})
