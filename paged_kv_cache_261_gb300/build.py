@@ -3,7 +3,8 @@
 Each translation unit compiles in its own nvcc process, in parallel, then one
 nvcc call links the shared library. The output lands in
 ``paged_kv_cache_261_gb300/_build/`` (git-ignored). Where torch is installed, g++ builds
-the Python module of csrc/binding.cpp beside it, for that version of torch. Run as a script
+the Python module of csrc/binding.cpp beside it, for that version of torch; the package works
+without it, so failing to build it is a warning. Run as a script
 or call ``build_library()``.
 """
 from __future__ import annotations
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -33,13 +35,17 @@ BINDING = "binding.cpp"
 
 
 def _torch_version():
+    """The version of the torch that is there, if it has CUDA; torch is not imported for it."""
+    import importlib.util
+    import runpy
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return None
     try:
-        from importlib.metadata import version
-        version("torch")
+        v = runpy.run_path(os.path.join(spec.submodule_search_locations[0], "version.py"))
     except Exception:
         return None
-    import torch
-    return torch.__version__ if torch.version.cuda else None
+    return v.get("__version__") if v.get("cuda") else None
 
 
 def binding_path(torch_version: str) -> str:
@@ -92,32 +98,62 @@ def _stale(target: str) -> bool:
     return any(os.path.getmtime(d) > t for d in _deps())
 
 
+def _binding_wanted(torch_version: str | None) -> bool:
+    """Whether there is a binding to build: none is there, or an old one, and building these sources has not failed."""
+    return torch_version is not None and _stale(binding_path(torch_version)) and \
+        _stale(binding_path(torch_version) + ".failed")
+
+
+def _no_binding(torch_version: str, why: Exception) -> None:
+    """The package works without its binding, more slowly: a failure to build it is told, and not tried again
+    before a source changes."""
+    with open(binding_path(torch_version) + ".failed", "w") as f:
+        f.write(f"{why}\n")
+    warnings.warn(f"the compiled module of the serving step's calls was not built; they go through ctypes. {why}")
+
+
 def build_library(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
     torch_version = _torch_version()
-    if not force and not _stale(LIB) and (torch_version is None or not _stale(binding_path(torch_version))):
+    lib = force or _stale(LIB)
+    binding = torch_version is not None if lib else _binding_wanted(torch_version)
+    if not lib and not binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    nvcc = _nvcc()
 
-    def compile_one(src: str) -> str:
-        obj = os.path.join(BUILD, src + f".{os.getpid()}.o")
-        cmd = _binding_command(obj) if src == BINDING else \
-            [nvcc, *ARCH, *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
-        r = _run(cmd, f"compiling {src}")
+    def object_of(src: str) -> str:
+        return os.path.join(BUILD, src + f".{os.getpid()}.o")
+
+    def compile_one(src: str):
+        """None, or why the binding did not compile."""
+        try:
+            cmd = _binding_command(object_of(src)) if src == BINDING else \
+                [_nvcc(), *ARCH, *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", object_of(src)]
+            r = _run(cmd, f"compiling {src}")
+        except Exception as e:
+            if src == BINDING:
+                return e
+            raise
         if verbose and (r.stdout or r.stderr):
             sys.stderr.write(r.stdout + r.stderr)
-        return obj
+        return None
 
-    sources = SOURCES + ([BINDING] if torch_version else [])
+    sources = (SOURCES if lib else []) + ([BINDING] if binding else [])
     with ThreadPoolExecutor(max_workers=jobs or len(sources)) as ex:
-        objs = list(ex.map(compile_one, sources))
-    tmp = LIB + f".tmp{os.getpid()}"
-    _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs[:len(SOURCES)]], "link")
-    os.replace(tmp, LIB)
-    if torch_version:
-        _link_binding(objs[-1], torch_version)
-    for o in objs:
-        os.remove(o)
+        why = list(ex.map(compile_one, sources))[-1]
+    if lib:
+        tmp = LIB + f".tmp{os.getpid()}"
+        _run([_nvcc(), *ARCH, "-shared", "-o", tmp, *map(object_of, SOURCES)], "link")
+        os.replace(tmp, LIB)
+    if binding:
+        try:
+            if why is not None:
+                raise why
+            _link_binding(object_of(BINDING), torch_version)
+        except Exception as e:
+            _no_binding(torch_version, e)
+    for src in sources:
+        if os.path.exists(object_of(src)):
+            os.remove(object_of(src))
     return LIB
 
 
