@@ -57,6 +57,8 @@ import contextlib
 import ctypes
 import importlib.util
 import os
+import warnings
+from importlib.machinery import EXTENSION_SUFFIXES
 
 import numpy as np
 
@@ -181,18 +183,22 @@ _torch_module = None
 _dtype_codes: dict = {}
 # The short way of a serving step's calls into the library (csrc/binding.cpp), once torch is there.
 # Its functions answer None where a call is not as plain as it wants it; the Python code below
-# them then checks, refuses or adapts. Built for one version of torch; without it, all calls go
+# them then checks, refuses or adapts. Built for one version of torch and of Python; without it, all calls go
 # the Python code's way.
 _binding = None
 
 
 def _load_binding(torch_version: str):
-    path = os.path.join(_HERE, "_build", f"_pagedattn_binding_{torch_version}.so")
+    path = os.path.join(_HERE, "_build", f"_pagedattn_binding_{torch_version}{EXTENSION_SUFFIXES[0]}")
     if not os.path.exists(path):
         return None
-    spec = importlib.util.spec_from_file_location("_pagedattn_binding", path)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
+    try:
+        spec = importlib.util.spec_from_file_location("_pagedattn_binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except Exception as e:
+        warnings.warn(f"{path} cannot be loaded; the serving step's calls go through ctypes. {e}")
+        return None
     return module
 
 

@@ -3,7 +3,7 @@
 Each translation unit compiles in its own nvcc process, in parallel, then one
 nvcc call links the shared library. The output lands in
 ``paged_kv_cache_261_gb300/_build/`` (git-ignored). Where torch is installed, g++ builds
-the Python module of csrc/binding.cpp beside it, for that version of torch; the package works
+the Python module of csrc/binding.cpp beside it, for that torch and that Python; the package works
 without it, so failing to build it is a warning. Run as a script
 or call ``build_library()``.
 """
@@ -15,6 +15,7 @@ import subprocess
 import sys
 import warnings
 from concurrent.futures import ThreadPoolExecutor
+from importlib.machinery import EXTENSION_SUFFIXES
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -49,7 +50,8 @@ def _torch_version():
 
 
 def binding_path(torch_version: str) -> str:
-    return os.path.join(BUILD, f"_pagedattn_binding_{torch_version}.so")
+    """Of this interpreter: its tag is in the name, as an extension module's."""
+    return os.path.join(BUILD, f"_pagedattn_binding_{torch_version}{EXTENSION_SUFFIXES[0]}")
 
 
 def _binding_command(obj: str):
