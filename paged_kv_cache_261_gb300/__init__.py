@@ -196,6 +196,9 @@ def _load_binding(torch_version: str):
         spec = importlib.util.spec_from_file_location("_pagedattn_binding", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
+        compiled, library, at = module.interface()
+        if compiled != library or at != ctypes.cast(_lib.pa_version, ctypes.c_void_p).value:
+            raise ImportError("it was built for another libpagedattn.so")
     except Exception as e:
         warnings.warn(f"{path} cannot be loaded; the serving step's calls go through ctypes. {e}")
         return None

@@ -9,6 +9,7 @@ or call ``build_library()``.
 """
 from __future__ import annotations
 
+import hashlib
 import os
 import shutil
 import subprocess
@@ -54,6 +55,12 @@ def binding_path(torch_version: str) -> str:
     return os.path.join(BUILD, f"_pagedattn_binding_{torch_version}{EXTENSION_SUFFIXES[0]}")
 
 
+def interface() -> str:
+    """What the library and its callers have to agree on: a number made of the header, compiled into both."""
+    with open(HEADER, "rb") as f:
+        return f"-DPA_INTERFACE=0x{hashlib.sha256(f.read()).hexdigest()[:16]}ull"
+
+
 def _binding_command(obj: str):
     import sysconfig
 
@@ -62,16 +69,15 @@ def _binding_command(obj: str):
     nvcc_include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
     include = [root, os.path.join(root, "torch", "csrc", "api", "include"), nvcc_include, sysconfig.get_paths()["include"]]
     return ["g++", "-std=c++17", "-O2", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-            *("-I" + d for d in include), "-c", os.path.join(CSRC, BINDING), "-o", obj]
+            interface(), *("-I" + d for d in include), "-c", os.path.join(CSRC, BINDING), "-o", obj]
 
 
-def _link_binding(obj: str, torch_version: str) -> None:
+def _link_binding(obj: str, folder: str, to: str) -> None:
+    """Links the binding with the library in `folder`; it will look for that beside itself."""
     import torch
-    tmp = binding_path(torch_version) + f".tmp{os.getpid()}"
-    _run(["g++", "-shared", "-o", tmp, obj, "-L" + BUILD, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
+    _run(["g++", "-shared", "-o", to, obj, "-L" + folder, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
           "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
           "-ltorch_python"], "linking the binding")
-    os.replace(tmp, binding_path(torch_version))
 
 
 def _run(cmd, what: str):
@@ -129,7 +135,7 @@ def build_library(force: bool = False, verbose: bool = False, jobs: int | None =
         """None, or why the binding did not compile."""
         try:
             cmd = _binding_command(object_of(src)) if src == BINDING else \
-                [_nvcc(), *ARCH, *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", object_of(src)]
+                [_nvcc(), *ARCH, *NVCC_FLAGS, interface(), "-c", os.path.join(CSRC, src), "-o", object_of(src)]
             r = _run(cmd, f"compiling {src}")
         except Exception as e:
             if src == BINDING:
@@ -142,17 +148,28 @@ def build_library(force: bool = False, verbose: bool = False, jobs: int | None =
     sources = (SOURCES if lib else []) + ([BINDING] if binding else [])
     with ThreadPoolExecutor(max_workers=jobs or len(sources)) as ex:
         why = list(ex.map(compile_one, sources))[-1]
+    # Both are linked before either is put in place, and a new library leaves no binding of an old one beside it,
+    # for whatever torch or Python that was.
+    new = os.path.join(BUILD, f"new.{os.getpid()}")
+    os.makedirs(new, exist_ok=True)
     if lib:
-        tmp = LIB + f".tmp{os.getpid()}"
-        _run([_nvcc(), *ARCH, "-shared", "-o", tmp, *map(object_of, SOURCES)], "link")
-        os.replace(tmp, LIB)
-    if binding:
+        _run([_nvcc(), *ARCH, "-shared", "-o", os.path.join(new, os.path.basename(LIB)), *map(object_of, SOURCES)], "link")
+    if binding and why is None:
         try:
-            if why is not None:
-                raise why
-            _link_binding(object_of(BINDING), torch_version)
+            _link_binding(object_of(BINDING), new if lib else BUILD, os.path.join(new, BINDING + ".so"))
         except Exception as e:
-            _no_binding(torch_version, e)
+            why = e
+    if lib:
+        for f in os.listdir(BUILD):
+            if f.startswith("_pagedattn_binding_"):
+                os.remove(os.path.join(BUILD, f))
+        os.replace(os.path.join(new, os.path.basename(LIB)), LIB)
+    if binding:
+        if why is None:
+            os.replace(os.path.join(new, BINDING + ".so"), binding_path(torch_version))
+        else:
+            _no_binding(torch_version, why)
+    shutil.rmtree(new)
     for src in sources:
         if os.path.exists(object_of(src)):
             os.remove(object_of(src))

@@ -3,7 +3,7 @@
 // position, and answers with the status of the C call, or with None where anything is not as the
 // plain call has it (a tensor of another type, shape or device, a foreign device current, numbers
 // that are none): then nothing was done, and the Python function, which knows how to refuse or
-// adapt, goes its own way. So this file raises nothing and checks everything.
+// adapt, goes its own way. So this file raises nothing and checks everything. (interface() alone is another thing.)
 //
 // (On a GB300's host, us of host time with the checks in Python and here: the two layout calls of a
 // step 13.2 and 4.5, a rotary call 8.4 and 2.7, a write and its read-back 12.3 and 4.6, one decode
@@ -22,6 +22,8 @@
 #include <utility>
 
 #include "../../include/pagedattn.h"
+
+extern "C" uint64_t pa_internal_interface(void);   // the library's PA_INTERFACE
 
 namespace {
 
@@ -359,11 +361,19 @@ PyObject *guarded(PyObject *self, PyObject *const *args, Py_ssize_t n) {
     }
 }
 
+// The header that this module was built with, that of the library which it calls, and where that library is: the
+// package takes the module only if the two are one and the library is its own.
+PyObject *interface(PyObject *, PyObject *) {
+    return Py_BuildValue("KKK", (unsigned long long)PA_INTERFACE, (unsigned long long)pa_internal_interface(),
+                         (unsigned long long)reinterpret_cast<uintptr_t>(&pa_version));
+}
+
 #define PA_METHOD(name) \
     {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(guarded<name>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {PA_METHOD(blocks_append),      PA_METHOD(blocks_release),    PA_METHOD(rotary_embedding),
                          PA_METHOD(kv_write_rotary),    PA_METHOD(kv_write_fp8_block), PA_METHOD(kv_read_fp8_block),
-                         PA_METHOD(attention_decode_fp8_block), {nullptr, nullptr, 0, nullptr}};
+                         PA_METHOD(attention_decode_fp8_block), {"interface", interface, METH_NOARGS, nullptr},
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pagedattn_binding", nullptr, -1, methods};
 
 }  // namespace

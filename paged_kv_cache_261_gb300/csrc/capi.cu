@@ -452,6 +452,10 @@ const char *pa_status_string(int status) {
 
 int pa_version(void) { return 100; }
 
+// Not part of the ABI: the header that this library was built with, as a number, for the compiled module
+// that calls it (binding.cpp).
+uint64_t pa_internal_interface(void) { return PA_INTERFACE; }
+
 int pa_paged_kv_write(const void *k, const void *v, const int32_t *slot_mapping, int64_t num_tokens,
                       void *key_cache, void *value_cache, int64_t num_blocks, int block_size,
                       int num_kv_heads, int head_dim, int dtype, void *stream) {

@@ -71,3 +71,40 @@ def test_module_of_another_python(built, tmp_path):
     copy = package(built, tmp_path)
     (copy / "_build" / built[1].replace(tag, "cpython-399-other")).write_text("no module")
     assert state_of(tmp_path) == "False []"
+
+
+FAKE = """
+#include <Python.h>
+static PyObject *interface(PyObject *self, PyObject *args) { return Py_BuildValue("KKK", 1ull, %s, 0ull); }
+static PyMethodDef methods[] = {{"%s", interface, METH_NOARGS, NULL}, {NULL, NULL, 0, NULL}};
+static PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pagedattn_binding", NULL, -1, methods};
+PyMODINIT_FUNC PyInit__pagedattn_binding(void) { return PyModule_Create(&module); }
+"""
+
+
+@pytest.mark.parametrize("library,name", [("2ull", "interface"), ("1ull", "interface"), ("1ull", "something_else")])
+def test_a_module_of_another_library(built, tmp_path, library, name):
+    """Built with another header than the library, calling another copy of it, or from before modules said so."""
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        pytest.skip("no Python.h")
+    copy = package(built, tmp_path)
+    (tmp_path / "fake.c").write_text(FAKE % (library, name))
+    subprocess.run(["gcc", "-shared", "-fPIC", "-I" + include, str(tmp_path / "fake.c"), "-o", str(copy / "_build" / built[1])],
+                   check=True)
+    last = state_of(tmp_path)
+    assert last.startswith("False") and built[1] in last
+
+
+def test_the_module_that_was_built(built, tmp_path):
+    """It is taken, and says the header's number."""
+    from __graft_entry__ import _build_module
+    if not os.path.exists(os.path.join(built[0], "_build", built[1])):
+        pytest.skip("no compiled module here")
+    copy = package(built, tmp_path)
+    os.symlink(os.path.join(built[0], "_build", built[1]), copy / "_build" / built[1])
+    assert state_of(tmp_path) == "True []"
+    import paged_kv_cache_261_gb300 as pa
+    pa._torch()
+    compiled, library, _ = pa._binding.interface()
+    assert compiled == library == int(_build_module().interface().split("=")[1][:-3], 16)

@@ -77,3 +77,40 @@ def test_looking_for_something_to_build_does_not_import_torch():
     assert r.returncode == 0, r.stderr
     import torch
     assert r.stdout.strip() == (torch.__version__ if torch.version.cuda else "None")
+
+
+@pytest.mark.parametrize("links", [True, False])
+def test_a_new_library_leaves_no_old_module_beside_it(monkeypatch, build, links):
+    """The module is linked before the library is replaced; those of the old one, for any torch, are gone."""
+    torch = pytest.importorskip("torch")
+    for f in (build.binding_path("1.0"), build.binding_path(torch.__version__), build.binding_path("1.0") + ".failed", build.LIB):
+        with open(f, "w") as h:
+            h.write("old")
+    monkeypatch.setattr(build, "_binding_command", lambda obj: ["g++", "-x", "c++", "-c", os.devnull, "-o", obj])
+
+    def link(obj, folder, to):
+        with open(build.LIB) as h:
+            assert h.read() == "old"
+        assert os.path.getsize(os.path.join(folder, "libpagedattn.so")) > 1000
+        if not links:
+            raise RuntimeError("does not link")
+        with open(to, "w") as h:
+            h.write("new")
+
+    monkeypatch.setattr(build, "_link_binding", link)
+    if links:
+        build.build_library(force=True)
+    else:
+        with pytest.warns(UserWarning, match="does not link"):
+            build.build_library(force=True)
+    path = build.binding_path(torch.__version__)
+    assert sorted(os.listdir(build.BUILD)) == sorted([os.path.basename(path) + ("" if links else ".failed"), "libpagedattn.so"])
+    assert os.path.getsize(build.LIB) > 1000
+
+
+def test_the_interface_is_the_header(monkeypatch, build, tmp_path):
+    a = build.interface()
+    other = tmp_path / "pagedattn.h"
+    other.write_text(open(build.HEADER).read() + "int pa_one_more(void);\n")
+    monkeypatch.setattr(build, "HEADER", str(other))
+    assert a.startswith("-DPA_INTERFACE=0x") and a.endswith("ull") and build.interface() != a
