@@ -12,7 +12,8 @@
 // turns, and its product with the position, modulo 2^64, the angle's fraction of a turn: whole
 // turns drop out exactly, whatever the position. The fraction, less its nearest quarter, is
 // short enough for float32 (an error of 2^-28 turns at most), and sincospif takes it.
-// The angle is off by position * inv_freq * 2^-52 and that, nothing else.
+// The angle is off by that, by position * inv_freq * 2^-52 (the quotient's two roundings) and by position * 2^-65 turns
+// (the fixed point's, 2^-34 turns at most).
 //
 // A CTA takes a few tokens: its threads first make the tokens' cosines and sines, in shared
 // memory, then take units of 16 channels, the 8 pairs of which lie in one thread for both kinds
@@ -40,11 +41,13 @@ constexpr int kMaxTokens = 8;                    // of a CTA
 // 1100 3.7, 3.5, 2000 5.8, 3.7).
 constexpr int64_t kManyTokens = 1200;
 
-// inv_freq radians as a number of 2^-64 turns, modulo one turn.
+// inv_freq radians as a number of 2^-64 turns, modulo one turn. Of a negative one the magnitude is taken and the
+// number negated: the rest of a small one less a whole turn would keep its bits from 2^-54 turns on alone.
 __device__ __forceinline__ uint64_t turn_step(double inv_freq) {
-    double turns = inv_freq * 0.15915494309189533577;      // 1 / (2 pi)
+    double turns = fabs(inv_freq) * 0.15915494309189533577;      // 1 / (2 pi)
     turns -= floor(turns);
-    return __double2ull_rn(turns * 18446744073709551616.0);
+    const uint64_t step = __double2ull_rn(turns * 18446744073709551616.0);
+    return inv_freq < 0.0 ? 0 - step : step;
 }
 // Cosine and sine of position * step.
 __device__ __forceinline__ float2 cos_sin(uint64_t step, int position) {
