@@ -1147,8 +1147,8 @@ int pa_paged_kv_write_fp8_block(const void *k, int64_t k_stride, const void *v, 
         return PA_ERR_INVALID_ARG;
     unsigned int *err = nullptr;
     if ((rc = error_word(&err)) != PA_OK) return rc;
-    return pa::launch_kv_write_fp8_block(k, v, k_stride, v_stride, src_dtype, slot_mapping, num_tokens, c, err,
-                                         static_cast<cudaStream_t>(stream)) == 0
+    return pa::launch_kv_write_fp8_block(k, v, k_stride, v_stride, src_dtype, slot_mapping, num_tokens, c,
+                                         device_sm_count(), err, static_cast<cudaStream_t>(stream)) == 0
                ? PA_OK
                : PA_ERR_CUDA;
 }
@@ -1166,7 +1166,7 @@ int pa_paged_kv_read_fp8_block(void *k, void *v, const int32_t *slot_mapping, in
     if (rc != PA_OK) return rc;
     unsigned int *err = nullptr;
     if ((rc = error_word(&err)) != PA_OK) return rc;
-    return pa::launch_kv_read_fp8_block(k, v, dst_dtype, slot_mapping, num_tokens, c, err,
+    return pa::launch_kv_read_fp8_block(k, v, dst_dtype, slot_mapping, num_tokens, c, device_sm_count(), err,
                                         static_cast<cudaStream_t>(stream)) == 0
                ? PA_OK
                : PA_ERR_CUDA;

@@ -22,12 +22,12 @@ struct Fp8BlockCache {
     int log2_block_size;
 };
 
-// k, v: rows of token t at k + t * k_stride elements.
+// k, v: rows of token t at k + t * k_stride elements. sms: the device's multiprocessors.
 int launch_kv_write_fp8_block(const void *k, const void *v, int64_t k_stride, int64_t v_stride, int src_dtype,
                               const int32_t *slot_mapping, int64_t num_tokens, const Fp8BlockCache &c,
-                              unsigned int *err, cudaStream_t stream);
+                              int sms, unsigned int *err, cudaStream_t stream);
 int launch_kv_read_fp8_block(void *k, void *v, int dst_dtype, const int32_t *slot_mapping, int64_t num_tokens,
-                             const Fp8BlockCache &c, unsigned int *err, cudaStream_t stream);
+                             const Fp8BlockCache &c, int sms, unsigned int *err, cudaStream_t stream);
 int launch_copy_scales_fp8_block(float2 *scales, const int32_t *pairs, int64_t num_pairs, int64_t num_blocks,
                                  int num_kv_heads, unsigned int *err, cudaStream_t stream);
 

@@ -42,11 +42,7 @@ template <int D> constexpr int kKeep = D / 32;
 constexpr int kMinScaleExp = -100;
 constexpr int kWriteCtas = 4;                    // of the scatter, on an SM (one less for float32 rows)
 constexpr int kColumn = 32;                      // tokens, a lane each, whose runs the scatter's CTAs take together
-// CTAs that it aims at where columns are few: as many as the device holds (8 kv heads, us
-// with three quarters, as many and one and a half times: single tokens of 1024 sequences 3.6, 3.0, 4.1, of 2048 5.0, 4.4,
-// 5.5; 2000 tokens of one 4.8, 3.6, 4.1, 50 of each of 40 5.6, 4.7, 5.8).
-constexpr int kSms = 152;
-constexpr int64_t kFillCtas = kSms * kWriteCtas;
+template <typename T> constexpr int kWriteCtasOf = kWriteCtas - (sizeof(T) == 4);
 // Channels per lane in reading: more where there are enough rows to fill the SMs all the same (us
 // with 8 and 32 channels, 8 kv heads: 100 tokens 1.4, 1.6; 700 1.9, 1.9; 1000 2.4, 2.1).
 constexpr int kFewChannels = 8, kManyChannels = 32;
@@ -184,7 +180,7 @@ __device__ __forceinline__ void reencode(uint4 *codes, int first, int step, int 
 // kColumn tokens of slot_mapping, so that their rows are read at the same time: the parts of all runs,
 // in order, are dealt to their warps in turn, and a warp finds its own without passing by the others.
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads, sizeof(T) == 4 ? kWriteCtas - 1 : kWriteCtas) void kv_write_fp8_block_kernel(const T *__restrict__ k, const T *__restrict__ v,
+__global__ __launch_bounds__(kThreads, kWriteCtasOf<T>) void kv_write_fp8_block_kernel(const T *__restrict__ k, const T *__restrict__ v,
                                                                       int64_t k_stride, int64_t v_stride,
                                                                       const int32_t *__restrict__ slots,
                                                                       int64_t num_tokens, const Fp8BlockCache c,
@@ -431,35 +427,39 @@ __global__ __launch_bounds__(kThreads) void copy_scales_kernel(float2 *scales, c
 
 template <typename T, int D>
 int write_t(const void *k, const void *v, int64_t ks, int64_t vs, const int32_t *slots, int64_t n,
-            const Fp8BlockCache &c, unsigned int *err, cudaStream_t s) {
+            const Fp8BlockCache &c, int sms, unsigned int *err, cudaStream_t s) {
     constexpr int kRows = 32 / (D / 16);               // of a warp
     // as many warps a team as hold a block's rows in registers
     int log2_team = 0;
     while (1 << log2_team < kWarps && kRows * kKeep<D> << log2_team < 1 << c.log2_block_size) ++log2_team;
     // CTAs of a column: a warp for each unit of runs of 8 (8 kv heads, us with half, as many and twice: 16,384 tokens,
     // blocks of 16 23.9, 21.5, 24.2; 8192, of 32 12.6, 10.8, 13.6; of 256, f32 32.4, 30.8, 36.7), or more where columns
-    // are few, up to a warp for each step that single tokens need.
+    // are few: as many as the device holds (us with three quarters, as many and one and a half times: single tokens of
+    // 1024 sequences 3.6, 3.0, 4.1, of 2048 5.0, 4.4, 5.5; 2000 tokens of one 4.8, 3.6, 4.1, 50 of each of 40 5.6, 4.7, 5.8;
+    // of f32, which fewer CTAs hold, as many and one and a third times: 3.8, 4.5, 6.1, 7.8, 6.3, 5.9, 7.0, 7.3), up
+    // to a warp for each step that single tokens need.
     const int Hk = c.num_kv_heads;
     const int64_t columns = (n + kColumn - 1) / kColumn;
     const int64_t for_runs = ((Hk << log2_team) + 1) / 2;
     const int64_t for_singles = ((2 * Hk + kRows - 1) / kRows * kColumn + kWarps - 1) / kWarps;
-    const int64_t ctas = std::max(for_runs, std::min(for_singles, kFillCtas / columns));
+    const int64_t ctas = std::max(for_runs, std::min(for_singles, (int64_t)sms * kWriteCtasOf<T> / columns));
     const int split = (int)std::max<int64_t>(1, std::min(ctas, INT32_MAX / columns));
     return launch_pdl(kv_write_fp8_block_kernel<T, D>, dim3((unsigned)(columns * split)), dim3(kThreads), 0, s,
                       (const T *)k, (const T *)v, ks, vs, slots, n, c, log2_team, split, err);
 }
 
 template <typename T, int D>
-int read_t(void *k, void *v, const int32_t *slots, int64_t n, const Fp8BlockCache &c, unsigned int *err,
+int read_t(void *k, void *v, const int32_t *slots, int64_t n, const Fp8BlockCache &c, int sms, unsigned int *err,
            cudaStream_t s) {
     const bool many = n * c.num_kv_heads >= kManyRows;
     const int pairs = kThreads / (D / (many ? kManyChannels : kFewChannels)) / 2;   // of a CTA
-    const int64_t ctas = (n * c.num_kv_heads + pairs - 1) / pairs, each = (ctas + kSms - 1) / kSms;
+    const int64_t ctas = (n * c.num_kv_heads + pairs - 1) / pairs, each = (ctas + sms - 1) / sms;
     // CTAs of a dependent start where the kernel before leaves room, and small ones crowd the SMs that it leaves
     // first. Where the SMs are not full anyway, they ask for shared memory that no more fit into than spread
     // evenly (read-backs after a scatter, us of both without and so: 2159 tokens of 4 kv heads of 64 channels, f32
     // 13.9, 6.9, bf16 9.5, 5.7; 2000 of 8 10.5, 9.6; 560 4.2, 4.2; not launched as a dependent: 7.2, 5.9, 9.0, 4.0, but 1 to 2 us
-    // more each outside a graph).
+    // more each outside a graph). (On another stream beside a decode, whose joining kernel waits in the rest of the SMs, a
+    // read-back comes at its end with shared memory or without: after 485 and 474 of 490 us.)
     const int smem = each < kFullCtas ? (int)(kSmemOfSm / each) - kSmemOfCta : 0;
     auto kern = many ? kv_read_fp8_block_kernel<T, D, kManyChannels> : kv_read_fp8_block_kernel<T, D, kFewChannels>;
     static bool attr_set[2][kMaxDevices] = {};
@@ -475,36 +475,36 @@ int read_t(void *k, void *v, const int32_t *slots, int64_t n, const Fp8BlockCach
 
 template <typename T>
 int write_d(const void *k, const void *v, int64_t ks, int64_t vs, const int32_t *slots, int64_t n,
-            const Fp8BlockCache &c, unsigned int *err, cudaStream_t s) {
-    return c.head_dim == 128 ? write_t<T, 128>(k, v, ks, vs, slots, n, c, err, s)
-                             : write_t<T, 64>(k, v, ks, vs, slots, n, c, err, s);
+            const Fp8BlockCache &c, int sms, unsigned int *err, cudaStream_t s) {
+    return c.head_dim == 128 ? write_t<T, 128>(k, v, ks, vs, slots, n, c, sms, err, s)
+                             : write_t<T, 64>(k, v, ks, vs, slots, n, c, sms, err, s);
 }
 template <typename T>
-int read_d(void *k, void *v, const int32_t *slots, int64_t n, const Fp8BlockCache &c, unsigned int *err,
+int read_d(void *k, void *v, const int32_t *slots, int64_t n, const Fp8BlockCache &c, int sms, unsigned int *err,
            cudaStream_t s) {
-    return c.head_dim == 128 ? read_t<T, 128>(k, v, slots, n, c, err, s) : read_t<T, 64>(k, v, slots, n, c, err, s);
+    return c.head_dim == 128 ? read_t<T, 128>(k, v, slots, n, c, sms, err, s) : read_t<T, 64>(k, v, slots, n, c, sms, err, s);
 }
 
 }  // namespace
 
 int launch_kv_write_fp8_block(const void *k, const void *v, int64_t k_stride, int64_t v_stride, int src_dtype,
                               const int32_t *slot_mapping, int64_t num_tokens, const Fp8BlockCache &c,
-                              unsigned int *err, cudaStream_t stream) {
+                              int sms, unsigned int *err, cudaStream_t stream) {
     switch (src_dtype) {
-    case PA_DTYPE_F32: return write_d<float>(k, v, k_stride, v_stride, slot_mapping, num_tokens, c, err, stream);
-    case PA_DTYPE_F16: return write_d<__half>(k, v, k_stride, v_stride, slot_mapping, num_tokens, c, err, stream);
+    case PA_DTYPE_F32: return write_d<float>(k, v, k_stride, v_stride, slot_mapping, num_tokens, c, sms, err, stream);
+    case PA_DTYPE_F16: return write_d<__half>(k, v, k_stride, v_stride, slot_mapping, num_tokens, c, sms, err, stream);
     case PA_DTYPE_BF16:
-        return write_d<__nv_bfloat16>(k, v, k_stride, v_stride, slot_mapping, num_tokens, c, err, stream);
+        return write_d<__nv_bfloat16>(k, v, k_stride, v_stride, slot_mapping, num_tokens, c, sms, err, stream);
     default: return -2;
     }
 }
 
 int launch_kv_read_fp8_block(void *k, void *v, int dst_dtype, const int32_t *slot_mapping, int64_t num_tokens,
-                             const Fp8BlockCache &c, unsigned int *err, cudaStream_t stream) {
+                             const Fp8BlockCache &c, int sms, unsigned int *err, cudaStream_t stream) {
     switch (dst_dtype) {
-    case PA_DTYPE_F32: return read_d<float>(k, v, slot_mapping, num_tokens, c, err, stream);
-    case PA_DTYPE_F16: return read_d<__half>(k, v, slot_mapping, num_tokens, c, err, stream);
-    case PA_DTYPE_BF16: return read_d<__nv_bfloat16>(k, v, slot_mapping, num_tokens, c, err, stream);
+    case PA_DTYPE_F32: return read_d<float>(k, v, slot_mapping, num_tokens, c, sms, err, stream);
+    case PA_DTYPE_F16: return read_d<__half>(k, v, slot_mapping, num_tokens, c, sms, err, stream);
+    case PA_DTYPE_BF16: return read_d<__nv_bfloat16>(k, v, slot_mapping, num_tokens, c, sms, err, stream);
     default: return -2;
     }
 }
