@@ -593,6 +593,9 @@ int pa_paged_kv_evict(int32_t *kept, int64_t kept_len, const float *mass, int64_
  * num_tokens), or when the stack is too short for its blocks (PA_DEVERR_FREE_BLOCKS); after
  * one of the last kind, no later request is served that needs a block. An id outside
  * [0, num_blocks) sets PA_DEVERR_BLOCK_ID; its tokens get slot -1, and a table -1 for it.
+ * A num_free[0] outside [0, free_capacity] is no stack's height: it sets PA_DEVERR_FREE_BLOCKS and counts as 0, so
+ * no request that needs a block is served and new_num_free[0] is 0 (in place, the stack's height is lost:
+ * rebuild the stack from the tables, or keep the two apart).
  *
  * new_context_lens may be context_lens and new_num_free num_free; no other array overlaps
  * another. Tables that share blocks (pa_alloc_fork) stay with the host allocator: this
@@ -617,7 +620,9 @@ int pa_paged_blocks_append(int32_t *block_tables, int max_blocks_per_seq, const 
  * new height. The tables stay as they are. A length outside [0, max_blocks_per_seq *
  * block_size] (PA_DEVERR_CONTEXT) or a full stack (PA_DEVERR_FREE_BLOCKS; then for every later
  * request that holds a block too) leaves a request unreleased; an id outside [0, num_blocks)
- * goes onto the stack as -1 (PA_DEVERR_BLOCK_ID). Aliasing and limits as
+ * goes onto the stack as -1 (PA_DEVERR_BLOCK_ID). A num_free[0] outside [0, free_capacity] sets
+ * PA_DEVERR_FREE_BLOCKS and counts as 0: the stack starts again with what this call gives back, written
+ * over its old entries from free_blocks[0] on. Aliasing and limits as
  * pa_paged_blocks_append; releasing a block twice is a caller error.
  */
 int pa_paged_blocks_release(const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,

@@ -991,7 +991,8 @@ def paged_blocks_append(block_tables, context_lens, query_lens, free_blocks, num
     query_start_loc [B + 1], slot_mapping [T] and positions [T] get the new tokens' starts, slots
     (-1: not served, or past the last token) and positions; new_context_lens and new_num_free
     (default: context_lens and num_free, in place) the lengths and the stack's height after the
-    step. All int32; block_tables [B, MB], num_free [1]."""
+    step. All int32; block_tables [B, MB], num_free [1]. A num_free outside [0, F] counts as 0 and
+    sets PA_DEVERR_FREE_BLOCKS."""
     if _binding is not None:
         rc = _binding.blocks_append(block_tables, context_lens, query_lens, free_blocks, num_free, query_start_loc,
                                     slot_mapping, positions, block_size, num_blocks, new_context_lens, new_num_free,
@@ -1048,7 +1049,8 @@ def paged_blocks_release(block_tables, context_lens, finished, free_blocks, num_
     """Give the blocks of every request b with finished[b] (torch.bool or uint8 [B]) back to the
     stack free_blocks[:num_free] and set its length to 0; its table stays as it is.
     new_context_lens and new_num_free: as paged_blocks_append. num_blocks (default: no bound): ids at
-    or above it are bad."""
+    or above it are bad. A num_free outside [0, F] counts as 0 and sets PA_DEVERR_FREE_BLOCKS: the
+    stack starts again, its old entries written over."""
     if _binding is not None:
         rc = _binding.blocks_release(block_tables, context_lens, finished, free_blocks, num_free, block_size,
                                      new_context_lens, new_num_free, num_blocks, stream)

@@ -84,7 +84,8 @@ __device__ __forceinline__ int owner(const int *first, int n, int x) {
     return lo;
 }
 
-// num_free, or 0 with an error where it cannot be the height of the stack.
+// num_free, or 0 with an error where it cannot be the height of the stack: which of its entries are free is
+// not known then, so it counts as empty.
 __device__ __forceinline__ int stack_height(const int32_t *num_free, int cap, bool report, unsigned int *err) {
     const int n = *num_free;
     if (n >= 0 && n <= cap) return n;
