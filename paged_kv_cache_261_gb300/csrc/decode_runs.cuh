@@ -135,7 +135,7 @@ __device__ __forceinline__ void zero_empty_rows(const DecodeParams &p, const int
 
 // Joins the partials of the rows that several runs share: M = max m_i, L = sum l_i
 // 2^(m_i - M), out = sum o_i 2^(m_i - M) / L. Warps per (query head, sequence), WPR: one where a
-// row has few partials, 4 or 16 (joined through shared memory) where it has many. A warp reads
+// row has few partials, 4, 16 or 32 (joined through shared memory) where it has many. A warp reads
 // 32 partials' pairs at once, one a lane, and then their outputs, kJoinBatch in flight.
 constexpr int kJoinWarps(int wpr) { return wpr < 4 ? 4 : wpr; }      // of a CTA
 constexpr int kJoinBatch = 8;
