@@ -31,8 +31,8 @@
 // cut into equal runs, one for each warp of the persistent grid (decode_runs.cuh). Warps share
 // nothing. Few rows of short contexts are too little work to cut so: there one to sixteen CTAs, a
 // cluster, take each row, its stages dealt to their warps in equal parts, and join the parts
-// through each other's shared memory, without a second kernel (row_cluster). Each warp fetches its own stages, one ahead and across rows, into its own ring: a
-// block of one kv head is one contiguous run for K and V each, so a stage is a few untiled bulk
+// through each other's shared memory, without a second kernel (row_cluster). Each warp fetches its own
+// stages, one ahead and across rows, into its own ring: a block of one kv head is one contiguous run for K and V each, so a stage is a few untiled bulk
 // copies, and its blocks' scales one 8-byte copy each, all on one mbarrier. (Boxes that TMA
 // swizzles, so that the lanes of a fragment do not meet on few banks, changed nothing: 52.9 and
 // 201.7 us on the two cases below.)
@@ -690,11 +690,11 @@ template <typename T, int D, int GT> struct RowCtas {
 // which costs about as much as a warp's stage, 1.6 us. So rows where no warp has more than one stage beyond what
 // runs would give it (and few at all: runs even out lengths below the bound). A cluster doubles while its CTAs
 // have stages and all clusters have room at once: 16 of eight CTAs, of which 14 have, are slower than runs.
-// us, runs and rows, of G 4 and D 128, by rows and stages of the longest: 8 and 2 5.7, 4.0; 8 and 10 5.6, 5.0;
-// 8 and 22 5.9, 5.1; 8 and 63 7.0, 5.6; 8 and 125 7.8, 7.0; 14 and 125 9.3, 7.5; 32 and 32 6.5, 5.7; 64 and 32 8.7, 6.7;
-// 64 and 63 10.7, 9.3; 96 and 32 9.5, 8.9; 128 and 4 6.5, 4.6; 128 and 32 10.7, 8.9; 144 and 54 13.4, 12.7; not taken: 128 and
-// 63 13.4, 13.9, 16 and 125 8.4, 12.1 (eight CTAs). Of sixteen CTAs, 7 have room: 1 and 250 8.0, 7.3; 4 and 250 8.9, 7.6; 7 and
-// 250 9.8, 8.4. 32 rows of 32 stages of G 16, f16: 9.5, 8.3.
+// us, runs and rows, of G 4 and D 128, by rows and the stages of each: 8 and 2 5.7, 4.0; 8 and 10 5.8, 5.2;
+// 8 and 22 5.9, 5.3; 8 and 63 7.5, 5.9; 8 and 125 8.1, 7.1; 14 and 125 10.1, 7.6; 32 and 32 6.8, 5.9; 64 and 32 9.2, 7.2;
+// 64 and 63 12.5, 10.7; 96 and 32 11.1, 9.8; 128 and 4 6.4, 4.8; 128 and 32 11.9, 10.7; 144 and 54 17.6, 15.8; not taken, with
+// weights as one f16 and up to that many stages: 128 and 63 13.4, 13.9, 16 and 125 8.4, 12.1 (eight CTAs). Of sixteen CTAs, 7
+// have room: 1 and 250 7.7, 7.4; 4 and 250 8.5, 7.7; 7 and 250 9.8, 8.3. 32 rows of 32 stages of G 16: 10.4, 8.3.
 int row_cluster(int64_t rows, int64_t stages, int sms, const int *room) {
     if (rows > room[0]) return 0;
     int i = 0;
