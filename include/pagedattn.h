@@ -732,10 +732,9 @@ size_t pa_decode_fp8_block_workspace_bytes(int num_seqs, int num_heads, int num_
  *   out[b,h,:] = sum_t softmax_t(scale * q[b,h,:] . K[b,t,h/G,:]) * V[b,t,h/G,:]
  *
  * with K and V the values held (code * scale, unrounded). The products of weights and V scales enter the
- * tensor cores as two f16 terms (22 bits; the softmax's sum takes the weights unrounded): each is off by 2^-23
- * of itself, or by 2^-33 of the context's largest weight times its largest V scale where that
- * is more, so V scales far apart cost the small ones their
- * precision; V scales below 2^-100 count as that for it. Values are below 2^90 in magnitude
+ * tensor cores as two f16 terms (22 bits; the softmax's sum takes the weights unrounded): each is off by
+ * 2^-23 of itself, or by 2^-32 of the context's largest weight times its largest V scale where that is more,
+ * so V scales far apart cost the small ones their precision; V scales below 2^-100 count as that for it. Values are below 2^90 in magnitude
  * and queries below 2^118 (times |scale|; beyond, a head's output may be NaN). q and out:
  * [num_seqs, num_heads, head_dim], PA_DTYPE_BF16 or PA_DTYPE_F16; num_heads / num_kv_heads <= 16.
  * Codes and scales past a context's end are never used, whatever they hold; a NaN code or scale
