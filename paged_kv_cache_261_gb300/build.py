@@ -117,7 +117,8 @@ def _no_binding(torch_version: str, why: Exception) -> None:
     before a source changes."""
     with open(binding_path(torch_version) + ".failed", "w") as f:
         f.write(f"{why}\n")
-    warnings.warn(f"the compiled module of the serving step's calls was not built; they go through ctypes. {why}")
+    warnings.warn("the compiled module of the serving step's calls was not built; they go through ctypes "
+                  f"(build.py --force tries again). {why}")
 
 
 def build_library(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
